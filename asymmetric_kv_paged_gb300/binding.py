@@ -19,6 +19,7 @@ ATTN_ERR_WORKSPACE = -3
 ATTN_ERR_CUDA = -4
 ATTN_KV_BF16 = 0
 ATTN_KV_FP8_E4M3 = 1
+ATTN_KV_FP4_E2M1 = 2
 
 EXPORTED = ("attn_plan", "attn_run_paged", "attn_run_phase", "attn_plan_destroy", "attn_get_device_error",
             "attn_status_string", "attn_plan_host", "attn_plan_info", "attn_plan_blocks",
@@ -26,7 +27,8 @@ EXPORTED = ("attn_plan", "attn_run_paged", "attn_run_phase", "attn_plan_destroy"
             "attn_plan_merge_ctas",
             "attn_debug_tc_gemm", "attn_debug_stamps",
             "attn_run_paged_no_workspace",
-            "attn_append_kv", "attn_plan_replayable", "attn_plan_replayable_host",
+            "attn_append_kv", "attn_append_kv_rope", "attn_read_kv", "attn_kv_row_bytes",
+            "attn_plan_replayable", "attn_plan_replayable_host",
             "attn_plan_replan_host", "attn_plan_fetch_device")
 
 
@@ -39,6 +41,12 @@ class attn_problem_t(ctypes.Structure):
                 ("has_sinks", ctypes.c_int32),
                 ("qo_indptr_host", ctypes.POINTER(ctypes.c_int32)),
                 ("seq_lens_host", ctypes.POINTER(ctypes.c_int32))]
+
+
+class attn_rope_t(ctypes.Structure):
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("max_pos", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("rot_offset", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 class AttnError(RuntimeError):
@@ -82,6 +90,10 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     L.attn_run_phase.argtypes = [vp, ctypes.c_int32] + L.attn_run_paged.argtypes[1:]
     L.attn_run_paged_no_workspace.argtypes = L.attn_run_paged.argtypes[:14] + [vp]
     L.attn_append_kv.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_float, ctypes.c_float, vp]
+    L.attn_append_kv_rope.argtypes = [vp, ctypes.POINTER(attn_rope_t)] + [vp] * 9 + \
+        [ctypes.c_float, ctypes.c_float, vp]
+    L.attn_read_kv.argtypes = [vp] * 6 + [ctypes.c_int64, vp, vp, ctypes.c_float, ctypes.c_float, vp]
+    L.attn_kv_row_bytes.argtypes = [ctypes.c_int, ctypes.c_int32, i32p]
     L.attn_plan_destroy.argtypes = [vp]
     L.attn_get_device_error.argtypes = [vp, vp, i32p]
     L.attn_status_string.argtypes = [ctypes.c_int]
@@ -114,6 +126,13 @@ def _check(status: int, what: str) -> None:
 
 def _ptr(t) -> int | None:
     return None if t is None else int(t.data_ptr())
+
+
+def _stream(stream) -> int:
+    if stream is None:
+        import torch
+        return torch.cuda.current_stream().cuda_stream
+    return int(getattr(stream, "cuda_stream", stream))
 
 
 class Plan:
@@ -266,6 +285,45 @@ def attn_append_kv(plan: Plan, k_new, v_new, k_cache, v_cache, page_table, seq_l
                                  _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens),
                                  _ptr(qo_indptr), float(k_scale), float(v_scale),
                                  ctypes.c_void_p(int(stream))), "attn_append_kv")
+
+
+def attn_kv_row_bytes(kv_dtype: int, head_dim: int) -> int:
+    """Bytes of one cached row of head_dim values of one KV head."""
+    n = ctypes.c_int32()
+    _check(load().attn_kv_row_bytes(int(kv_dtype), int(head_dim), ctypes.byref(n)), "attn_kv_row_bytes")
+    return n.value
+
+
+def make_rope(cos_sin, rot_dim: int, rot_offset: int = 0, interleaved: bool = False,
+              positions=None) -> attn_rope_t:
+    """The rotation of attn_append_kv_rope.  cos_sin: fp32 [max_pos, rot_dim] on the
+    device, cosines then sines; positions: int32 [total_q] on the device, or None for
+    the tokens' own.  The result keeps both tensors alive."""
+    r = attn_rope_t(_ptr(cos_sin), _ptr(positions), int(cos_sin.shape[0]), int(rot_dim),
+                    int(rot_offset), int(bool(interleaved)))
+    r.keep = (cos_sin, positions)
+    return r
+
+
+def attn_append_kv_rope(plan: Plan, rope: attn_rope_t, q, k_new, v_new, q_out, k_cache, v_cache,
+                        page_table, seq_lens, qo_indptr, k_scale: float = 1.0, v_scale: float = 1.0,
+                        stream=None) -> None:
+    """attn_append_kv with the keys rotated on the way, and the queries into q_out
+    (may be q; both None: no queries)."""
+    _check(load().attn_append_kv_rope(
+        plan.handle, ctypes.byref(rope), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(q_out), _ptr(k_cache),
+        _ptr(v_cache), _ptr(page_table), _ptr(seq_lens), _ptr(qo_indptr), k_scale, v_scale,
+        _stream(stream)), "attn_append_kv_rope")
+
+
+def attn_read_kv(plan: Plan, k_cache, v_cache, page_table, seq_lens, kv_indptr, k_out, v_out,
+                 k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
+    """Cached rows as bf16: the last kv_indptr[b + 1] - kv_indptr[b] positions of every
+    request b, into k_out [rows, Hkv, Dqk] and v_out [rows, Hkv, 128]."""
+    _check(load().attn_read_kv(
+        plan.handle, _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens), _ptr(kv_indptr),
+        int(k_out.shape[0]), _ptr(k_out), _ptr(v_out), k_scale, v_scale, _stream(stream)),
+        "attn_read_kv")
 
 
 def attn_get_device_error(plan: Plan) -> int:

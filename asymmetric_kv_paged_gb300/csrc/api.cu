@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "attn_paged.h"
+#include "e2m1.cuh"
 #include "kernels.hpp"
 #include "plan.hpp"
 #include "replan.hpp"
@@ -47,20 +48,22 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 // K (d = 192 or 128) or V (d = 128) cache as a 3D tensor [slots][Hkv][d]; boxes of
 // `rows` consecutive slots of one head: 64 bf16 columns with 128-byte swizzle
-// (the tensor-core operand layout), or whole raw E4M3 rows without swizzle.
-bool make_cache_map(CUtensorMap *map, const void *base, bool fp8, int d, int hkv, int64_t slots,
+// (the tensor-core operand layout), or whole raw rows of `row_bytes` bytes (E4M3,
+// E2M1 with its scales; row_bytes = 0 for bf16) without swizzle.
+bool make_cache_map(CUtensorMap *map, const void *base, int row_bytes, int d, int hkv, int64_t slots,
                     int rows) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t es = fp8 ? 1 : 2;
-  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)hkv, (cuuint64_t)slots};
-  const cuuint64_t strides[2] = {d * es, (cuuint64_t)hkv * d * es};
-  const cuuint32_t box[3] = {fp8 ? (cuuint32_t)d : 64u, 1u, (cuuint32_t)rows};
+  const bool raw = row_bytes > 0;
+  const cuuint64_t row = raw ? row_bytes : 2 * d;
+  const cuuint64_t dims[3] = {raw ? row : (cuuint64_t)d, (cuuint64_t)hkv, (cuuint64_t)slots};
+  const cuuint64_t strides[2] = {row, (cuuint64_t)hkv * row};
+  const cuuint32_t box[3] = {raw ? (cuuint32_t)row : 64u, 1u, (cuuint32_t)rows};
   const cuuint32_t estr[3] = {1u, 1u, 1u};
-  CUresult r = fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+  CUresult r = fn(map, raw ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                   const_cast<void *>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                  raw ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
                   // 128-byte promotion: a 256-byte one pulls in part of the neighbouring
                   // head's K row (rows are 384 bytes at offset g * 384), which measured
                   // 2% slower on the batched decode
@@ -253,22 +256,24 @@ static attn_status_t run_impl(attn_plan_t plan, int phases, bool allow_stage, co
   if (!std::isfinite(softmax_scale) || !std::isfinite(k_scale) || !std::isfinite(v_scale))
     return ATTN_ERR_INVALID_ARG;
   // the kernels take score maxima on unscaled dot products: the scale must be > 0
-  if (!(softmax_scale > 0.f) || (pr.kv_dtype == ATTN_KV_FP8_E4M3 && !(k_scale > 0.f)))
+  if (!(softmax_scale > 0.f) || (pr.kv_dtype != ATTN_KV_BF16 && !(k_scale > 0.f)))
     return ATTN_ERR_INVALID_ARG;
   const bool staged = allow_stage && hp.stage_rows > 0;
   const size_t need = staged ? hp.workspace_bytes : hp.partial_bytes;
   if (workspace_bytes < need || (need && !workspace)) return ATTN_ERR_WORKSPACE;
   if (!has_rows) return ATTN_OK;
 
-  const bool fp8 = pr.kv_dtype == ATTN_KV_FP8_E4M3;
+  const bool raw = pr.kv_dtype != ATTN_KV_BF16;    // E4M3 or E2M1 codes, with scales
+  const int k_row = raw ? akp::kv_row_bytes(pr.kv_dtype, pr.head_dim_qk) : 0;
+  const int v_row = raw ? akp::kv_row_bytes(pr.kv_dtype, akp::kDv) : 0;
   akp::RunArgs a{};
   a.q = q;
   a.k_cache = k_cache;
   a.v_cache = v_cache;
   a.page_table = page_table;
   a.sinks = sinks;
-  a.scale_log2 = softmax_scale * (fp8 ? k_scale : 1.f) * 1.4426950408889634f;
-  a.v_scale = fp8 ? v_scale : 1.f;
+  a.scale_log2 = softmax_scale * (raw ? k_scale : 1.f) * 1.4426950408889634f;
+  a.v_scale = raw ? v_scale : 1.f;
   a.out = out;
   a.lse_out = lse_out;
   a.part_o = static_cast<float *>(workspace);
@@ -290,13 +295,18 @@ static attn_status_t run_impl(attn_plan_t plan, int phases, bool allow_stage, co
   a.err = plan->dev.err;
 
   akp::TmaMaps maps{};
+  // the kernels read 4-bit rows in 16-byte pieces on every path
+  if (pr.kv_dtype == ATTN_KV_FP4_E2M1 &&
+      ((reinterpret_cast<uintptr_t>(k_cache) | reinterpret_cast<uintptr_t>(v_cache) |
+        reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) & 15))
+    return ATTN_ERR_INVALID_ARG;
   if ((phases & 1) && hp.use_tma && !hp.prefill) {
     if ((reinterpret_cast<uintptr_t>(k_cache) & 15) || (reinterpret_cast<uintptr_t>(v_cache) & 15))
       return ATTN_ERR_INVALID_ARG;
     const int64_t slots = (int64_t)pr.num_pages * pr.page_size;
     const int rows = pr.page_size >= akp::kKeyTile ? akp::kKeyTile : pr.page_size;
-    if (!make_cache_map(&maps.k, k_cache, fp8, pr.head_dim_qk, pr.num_kv_heads, slots, rows) ||
-        !make_cache_map(&maps.v, v_cache, fp8, akp::kDv, pr.num_kv_heads, slots, rows))
+    if (!make_cache_map(&maps.k, k_cache, k_row, pr.head_dim_qk, pr.num_kv_heads, slots, rows) ||
+        !make_cache_map(&maps.v, v_cache, v_row, akp::kDv, pr.num_kv_heads, slots, rows))
       return ATTN_ERR_CUDA;
   }
   int cur = -1;
@@ -340,10 +350,10 @@ static attn_status_t run_impl(attn_plan_t plan, int phases, bool allow_stage, co
     sa.page_size = pr.page_size;
     sa.pt_stride = pr.page_table_stride;
     sa.num_pages = pr.num_pages;
-    sa.fp8 = fp8;
+    sa.kv_dtype = pr.kv_dtype;
     if ((reinterpret_cast<uintptr_t>(ws) & 255) ||
-        !make_stage_map(&stage_maps.k, sa.k_stage, fp8, pr.head_dim_qk, hp.stage_rows) ||
-        !make_stage_map(&stage_maps.v, sa.v_stage, fp8, akp::kDv, hp.stage_rows))
+        !make_stage_map(&stage_maps.k, sa.k_stage, raw, pr.head_dim_qk, hp.stage_rows) ||
+        !make_stage_map(&stage_maps.v, sa.v_stage, raw, akp::kDv, hp.stage_rows))
       return ATTN_ERR_CUDA;
     if (akp::launch_kv_stage(sa, st) != cudaSuccess) return ATTN_ERR_CUDA;
   }
@@ -378,6 +388,16 @@ attn_status_t attn_run_phase(attn_plan_t plan, int32_t phase, const void *q,
   return run_impl(plan, phase == 0 ? 1 : 2, true, q, k_cache, v_cache, page_table, seq_lens,
                   qo_indptr, sinks, window, softmax_scale, k_scale, v_scale, out, lse_out,
                   workspace, workspace_bytes, stream);
+}
+
+attn_status_t attn_kv_row_bytes(attn_kv_dtype_t kv_dtype, int32_t head_dim, int32_t *bytes) {
+  if (!bytes) return ATTN_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (head_dim != akp::kDqk && head_dim != akp::kDqkSym) return ATTN_ERR_UNSUPPORTED;
+  const int n = akp::kv_row_bytes(kv_dtype, head_dim);
+  if (n == 0) return ATTN_ERR_UNSUPPORTED;
+  *bytes = n;
+  return ATTN_OK;
 }
 
 attn_status_t attn_get_device_error(attn_plan_t plan, void *workspace, int32_t *err) {

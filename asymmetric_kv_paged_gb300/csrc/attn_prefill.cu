@@ -5,7 +5,7 @@
 //
 // A row block holds up to 256 query rows of one (request, KV head), as two
 // 128-row Q tiles that share every 128-key K/V tile: each key tile is fetched
-// and (for FP8 caches) widened once per 256 rows, and each tcgen05.mma runs at
+// and (for FP8 and 4-bit caches) widened once per 256 rows, and each tcgen05.mma runs at
 // N = 128, the shape that keeps the tensor pipe at its full rate.
 //
 // Warp roles (512 threads, four warpgroups; registers are moved from the load
@@ -21,7 +21,7 @@
 //               page lookup of each key, K and V rows read from the cache with
 //               16-byte loads (one thread per key), widened in registers, and
 //               stored into the 128-byte-swizzled operand tiles.  (The MMAs of
-//               an FP8 cache run in fp16.)
+//               an FP8 or 4-bit cache run in fp16.)
 //   warp  12    TMEM allocation; one thread issues the MMAs of Q tile 0;
 //   warp  13    one thread issues the MMAs of Q tile 1;
 //   warps 14-15 idle (they complete the fourth warpgroup).
@@ -42,7 +42,7 @@
 #include <cmath>
 #include <cstdint>
 
-#include "e4m3.cuh"
+#include "e2m1.cuh"
 #include "kernels.hpp"
 #include "tc_common.cuh"
 
@@ -138,7 +138,7 @@ __device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
 }
 
 
-// FP8 caches: Q rows go to fp16 scaled by 2^sh, the power of two that puts
+// FP8 and 4-bit caches: Q rows go to fp16 scaled by 2^sh, the power of two that puts
 // the row's largest |q| in [2^14, 2^15) (bf16 exponent field e of that
 // maximum: sh = 141 - e, at most 126 for zero or subnormal rows).  Every bf16
 // element down to 2^-31 of the maximum is then exact in fp16.  The load warps
@@ -165,7 +165,10 @@ __device__ __forceinline__ int q_row_shift(const uint4 *row) {
 // issued by one thread of the load warps; else the load warps read the paged
 // caches themselves (plans without a scratch: replayable plans, runs without
 // a workspace).
-template <bool FP8, bool STAGED>
+// F16: the caches hold 8- or 4-bit values, so the operands are fp16.  E2M1: they
+// are 4-bit rows (a staging scratch holds fp16 rows either way, so only the
+// path that reads the caches itself tells the two apart).
+template <bool F16, bool E2M1, bool STAGED>
 __global__ void __launch_bounds__(kPThreads, 1)
     attn_prefill_kernel(const RunArgs args, const __grid_constant__ TmaMaps stage) {
   const RunArgs a = args;
@@ -232,7 +235,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
     // shared store: 8 distinct bank groups).
     const int lt = tid - 256;
     const int key = lt;
-    constexpr int kEs = FP8 ? 1 : 2;
+    // 16-byte chunks of a cache row
+    constexpr int KCH = E2M1 ? e2m1_row_bytes(kDqk) / 16 : kDqk / (F16 ? 16 : 8);
+    constexpr int VCH = E2M1 ? e2m1_row_bytes(kDv) / 16 : kDv / (F16 ? 16 : 8);
     const uint8_t *kc = static_cast<const uint8_t *>(a.k_cache);
     const uint8_t *vc = static_cast<const uint8_t *>(a.v_cache);
     // K-stream position: segment, tile, and the block fields a page lookup
@@ -268,8 +273,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
       bad_page |= (int)(in && !ok);
       return ok ? (int64_t)page * a.page_size + j % a.page_size : -1;
     };
-    auto row_ptr = [&](const uint8_t *cache, int64_t slot, int g, int d) {
-      return reinterpret_cast<const uint4 *>(cache + ((slot >= 0 ? slot : 0) * a.hkv + g) * (d * kEs));
+    auto row_ptr = [&](const uint8_t *cache, int64_t slot, int g, int nch) {
+      return reinterpret_cast<const uint4 *>(cache) + ((slot >= 0 ? slot : 0) * a.hkv + g) * nch;
     };
     // N 16-byte chunks of a row, from chunk c0; zeros for slot -1
     auto load = [&](uint4 *dst, int n, const uint4 *row, int64_t slot) {
@@ -283,19 +288,28 @@ __global__ void __launch_bounds__(kPThreads, 1)
                    "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                    : "memory");
     };
-    // E4M3 chunks (16 codes each) -> two fp16 chunks each (exact; one
-    // conversion instruction per pair of codes): Q.K^T and P.V run in fp16
-    // for FP8 caches (Q scaled per row, see stage_q; P keeps 11 mantissa bits)
-    auto put_fp8 = [&](uint32_t base, const uint4 *src, int n, bool to_bf16) {
+    // The row's n chunks -> fp16 chunks (exact; one conversion instruction per
+    // pair of codes, and one product with the block's scale for E2M1, whose
+    // scales are in the last chunk): Q.K^T and P.V run in fp16 for these caches
+    // (Q scaled per row, see stage_q; P keeps 11 mantissa bits)
+    auto put_row = [&](uint32_t base, const uint4 *src, int n) {
+      if constexpr (E2M1) {
+        const uint32_t sc[4] = {src[n - 1].x, src[n - 1].y, src[n - 1].z, src[n - 1].w};
 #pragma unroll
-      for (int i = 0; i < n; ++i) {
-        uint4 lo, hi;
-        if (to_bf16)
-          e4m3x16_to_bf16(src[i], lo, hi);
-        else
+        for (int i = 0; i + 1 < n; ++i) {
+          uint4 w[4];
+          e2m1x32_to_f16(src[i], i & 1 ? sc[i >> 1] >> 16 : sc[i >> 1], w);
+#pragma unroll
+          for (int u = 0; u < 4; ++u) put(base, 4 * i + u, w[u]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+          uint4 lo, hi;
           e4m3x16_to_f16(src[i], lo, hi);
-        put(base, 2 * i, lo);
-        put(base, 2 * i + 1, hi);
+          put(base, 2 * i, lo);
+          put(base, 2 * i + 1, hi);
+        }
       }
     };
     // Q rows of the cursor's block: row r of the block is Q tile r / 128, MMA
@@ -304,7 +318,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const BlockDesc bd = a.blocks[a.segs[seg].block];
       const int si = seg - seg_begin;
       if (si > 0 && !tc::mbar_wait_warp(&bars.q_empty, (si - 1) & 1, &abort_flag)) return false;
-      if constexpr (FP8) {
+      if constexpr (F16) {
         // Q.K^T runs in fp16 against K widened exactly from E4M3, each Q row
         // scaled by 2^sh (q_row_shift).  One thread per row (rows lt and
         // lt + 128): a pass for the shift, then one that scales, converts and
@@ -475,33 +489,32 @@ __global__ void __launch_bounds__(kPThreads, 1)
       auto head_of = [](int in) { return in & 0xFFFF; };
       auto starts = [](int in) { return ((in >> 16) & 1) != 0; };
       auto seg_of = [](int in) { return in >> 17; };
-      if constexpr (FP8) {
-        // raw E4M3 rows in registers: K of tile k, V of tile k-1 (20 x 16 bytes)
-        constexpr int KCH = kDqk / 16, VCH = kDv / 16;
+      if constexpr (F16) {
+        // raw rows in registers: K of tile k, V of tile k-1 (20 x 16 bytes of E4M3)
         uint4 kr[KCH], vr[VCH];
         int64_t v_slot = -1;
         int v_g = 0;
-        load(kr, KCH, row_ptr(kc, slot[0], head_of(info[0]), kDqk), slot[0]);
+        load(kr, KCH, row_ptr(kc, slot[0], head_of(info[0]), KCH), slot[0]);
         for (int k = 0; k <= total; ++k) {
           if (k < total) {
             if (starts(info[0]) && !stage_q(seg_of(info[0]))) break;
             const int s = k & 1;
             if (k >= 2 && !tc::mbar_wait_warp(&bars.k_empty[s], ((k >> 1) - 1) & 1, &abort_flag)) break;
-            put_fp8(sbase + kOffK + s * kKStage, kr, KCH, false);
+            put_row(sbase + kOffK + s * kKStage, kr, KCH);
             tc::fence_proxy_async_smem();
             tc::mbar_arrive_warp(&bars.k_full[s]);
-            if (k + 1 < total) load(kr, KCH, row_ptr(kc, slot[1], head_of(info[1]), kDqk), slot[1]);
+            if (k + 1 < total) load(kr, KCH, row_ptr(kc, slot[1], head_of(info[1]), KCH), slot[1]);
           }
           if (k >= 1) {
             if (k >= 2 && !tc::mbar_wait_warp(&bars.v_empty, (k - 2) & 1, &abort_flag)) break;
-            put_fp8(sbase + kOffV, vr, VCH, false);
+            put_row(sbase + kOffV, vr, VCH);
             tc::fence_proxy_async_smem();
             tc::mbar_arrive_warp(&bars.v_full);
           }
           if (k < total) {
             v_slot = slot[0];
             v_g = head_of(info[0]);
-            load(vr, VCH, row_ptr(vc, v_slot, v_g, kDv), v_slot);
+            load(vr, VCH, row_ptr(vc, v_slot, v_g, VCH), v_slot);
             shift(k);
           }
         }
@@ -514,7 +527,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         for (int k = 0; k <= total; ++k) {
           if (k < total) {
             if (starts(info[0]) && !stage_q(seg_of(info[0]))) break;
-            const uint4 *krow = row_ptr(kc, slot[0], head_of(info[0]), kDqk);
+            const uint4 *krow = row_ptr(kc, slot[0], head_of(info[0]), KCH);
             const int s = k & 1;
             load(buf, 12, krow, slot[0]);
             if (k >= 2 && !tc::mbar_wait_warp(&bars.k_empty[s], ((k >> 1) - 1) & 1, &abort_flag)) break;
@@ -528,7 +541,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             tc::mbar_arrive_warp(&bars.k_full[s]);
           }
           if (k >= 1) {
-            const uint4 *vrow = row_ptr(vc, v_slot, v_g, kDv);
+            const uint4 *vrow = row_ptr(vc, v_slot, v_g, VCH);
             load(buf, 8, vrow, v_slot);
             if (k >= 2 && !tc::mbar_wait_warp(&bars.v_empty, (k - 2) & 1, &abort_flag)) break;
   #pragma unroll
@@ -564,8 +577,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
     // slower on the chunked prefill).
     if ((tid & 31) == 0) {
       const int t = warp - kMmaWarp;
-      const uint32_t id_s = tc::idesc_f16(FP8 ? 0 : 1, 0, 0, kPM, kPN);     // fp16 for FP8 caches
-      const uint32_t id_pv = tc::idesc_f16(FP8 ? 0 : 1, 0, 1, kPM, kDv);   // P.V in fp16 for FP8 caches
+      const uint32_t id_s = tc::idesc_f16(F16 ? 0 : 1, 0, 0, kPM, kPN);     // fp16 for 8- and 4-bit caches
+      const uint32_t id_pv = tc::idesc_f16(F16 ? 0 : 1, 0, 1, kPM, kDv);   // P.V in fp16 for those too
       const uint32_t q_smem = sbase + t * kQTile;
       const uint32_t s_tmem = tmem + kPN * t;
       const uint32_t o_tmem = tmem + kTmemO + kDv * t;
@@ -678,7 +691,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           row_tok = bd.tok0 + flat / a.group;
           row_h = bd.g * a.group + flat % a.group;
           if (a.sinks) sink2 = a.sinks[row_h] * kLog2e;
-          if (FP8) {
+          if (F16) {
             // the scores of this row come from Q scaled by 2^sh (see q_row_shift)
             const int sh = q_row_shift(reinterpret_cast<const uint4 *>(
                 static_cast<const uint16_t *>(a.q) + ((int64_t)row_tok * a.hq + row_h) * kDqk));
@@ -752,7 +765,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           tc::ffma2(y0, y1, x0, x1, sc, nm);
           const float p0 = ex2(y0), p1 = ex2(y1);
           tc::fadd2(rs[0], rs[1], p0, p1);
-          pk[j >> 1] = FP8 ? f16_pair(p0, p1) : bf16_pair(p0, p1);
+          pk[j >> 1] = F16 ? f16_pair(p0, p1) : bf16_pair(p0, p1);
         }
       };
       exp_pack(s2, pk2, m_base == -INFINITY ? 0.f : -m_base, true);
@@ -811,7 +824,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             tc::ffma2(y0, y1, __uint_as_float(raw[h + j]), __uint_as_float(raw[h + j + 1]), sc, neg_m);
             const float p0 = ex2(y0), p1 = ex2(y1);
             tc::fadd2(rs[0], rs[1], p0, p1);
-            pk[j >> 1] = FP8 ? f16_pair(p0, p1) : bf16_pair(p0, p1);
+            pk[j >> 1] = F16 ? f16_pair(p0, p1) : bf16_pair(p0, p1);
           }
           tc::tmem_st8(s_addr + kPN / 2 + (c0 + h) / 2, pk);
         }
@@ -892,22 +905,29 @@ cudaError_t launch_attn_prefill(const HostPlan &hp, const RunArgs &a, const TmaM
   if (hp.num_ctas == 0) return cudaSuccess;
   const dim3 grid(hp.num_ctas), block(kPThreads);
   const TmaMaps none{};
-  const bool fp8 = hp.prob.kv_dtype == ATTN_KV_FP8_E4M3;
+  const bool f16 = hp.prob.kv_dtype != ATTN_KV_BF16;
   if (stage)
-    return fp8 ? launch_dependent(attn_prefill_kernel<true, true>, grid, block, kSmem, stream, a, *stage)
-               : launch_dependent(attn_prefill_kernel<false, true>, grid, block, kSmem, stream, a,
+    return f16 ? launch_dependent(attn_prefill_kernel<true, false, true>, grid, block, kSmem, stream, a,
+                                  *stage)
+               : launch_dependent(attn_prefill_kernel<false, false, true>, grid, block, kSmem, stream, a,
                                   *stage);
-  return fp8 ? launch_dependent(attn_prefill_kernel<true, false>, grid, block, kSmem, stream, a, none)
-             : launch_dependent(attn_prefill_kernel<false, false>, grid, block, kSmem, stream, a,
+  if (hp.prob.kv_dtype == ATTN_KV_FP4_E2M1)
+    return launch_dependent(attn_prefill_kernel<true, true, false>, grid, block, kSmem, stream, a, none);
+  return f16 ? launch_dependent(attn_prefill_kernel<true, false, false>, grid, block, kSmem, stream, a,
+                                none)
+             : launch_dependent(attn_prefill_kernel<false, false, false>, grid, block, kSmem, stream, a,
                                 none);
 }
 
 cudaError_t prepare_attn_prefill(const HostPlan &hp) {
-  const bool fp8 = hp.prob.kv_dtype == ATTN_KV_FP8_E4M3;
-  cudaError_t e = cudaFuncSetAttribute(fp8 ? attn_prefill_kernel<true, true> : attn_prefill_kernel<false, true>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const bool f16 = hp.prob.kv_dtype != ATTN_KV_BF16;
+  cudaError_t e = cudaFuncSetAttribute(
+      f16 ? attn_prefill_kernel<true, false, true> : attn_prefill_kernel<false, false, true>,
+      cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(fp8 ? attn_prefill_kernel<true, false> : attn_prefill_kernel<false, false>,
+    e = cudaFuncSetAttribute(hp.prob.kv_dtype == ATTN_KV_FP4_E2M1 ? attn_prefill_kernel<true, true, false>
+                             : f16                                ? attn_prefill_kernel<true, false, false>
+                                                                  : attn_prefill_kernel<false, false, false>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   return e;
 }

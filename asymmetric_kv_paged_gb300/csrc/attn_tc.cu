@@ -41,6 +41,7 @@
 #include <type_traits>
 
 #include "attn_paged_debug.h"
+#include "e2m1.cuh"
 #include "e4m3.cuh"
 #include "kernels.hpp"
 #include "stamps.cuh"
@@ -57,15 +58,17 @@ namespace {
 constexpr int kN = kKeyTile;                 // keys per tile (64)
 constexpr int kThreads = 11 * 32;
 constexpr int kBlk = kN * 128;               // one 64-column block of a 64-row tile: 8 KB
+// Element types of the caches (attn_kv_dtype_t).
+constexpr int kBf16 = ATTN_KV_BF16, kE4m3 = ATTN_KV_FP8_E4M3, kE2m1 = ATTN_KV_FP4_E2M1;
 // Tile sizes for query/key head dim DQK (192, or 128 for layers with a
 // symmetric head-dim pair; the value head dim is 128 either way).
-template <int DQK>
+template <int KV, int DQK>
 struct Dims {
   static_assert(DQK % 64 == 0, "the K tile is made of 64-column blocks");
   static constexpr int kOpK = (DQK / 64) * kBlk;       // K operand tile: 24 KB at 192
   static constexpr int kOpBytes = kOpK + 2 * kBlk;      // + V operand tile: 40 KB at 192
-  static constexpr int kRawK = kN * DQK;                // raw E4M3 K rows: 12 KB at 192
-  static constexpr int kRawBytes = kRawK + kN * kDv;    // + raw V rows: 20 KB at 192
+  static constexpr int kRawK = kN * kv_row_bytes(KV, DQK);   // raw K rows: 12 KB of E4M3 at 192, 7 KB of E2M1
+  static constexpr int kRawBytes = kRawK + kN * kv_row_bytes(KV, kDv);   // + raw V rows: 20 KB, 12 KB
 };
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 128;             // O: 128 fp32 columns
@@ -83,19 +86,20 @@ struct SlotBars {
 // Shared-memory layout for MR MMA rows (64 or 128): Q as three 64-column
 // blocks of MR rows (two buffers where they fit), the K/V operand ring, the
 // FP8 staging ring and the epilogue's copy-combine buffer.  P lives in TMEM.
-template <bool FP8, int MR, bool TMA, int DQK>
+template <int KV, int MR, bool TMA, int DQK>
 struct Layout {
-  static constexpr int kOpBytes = Dims<DQK>::kOpBytes;
-  static constexpr int kRawBytes = Dims<DQK>::kRawBytes;
+  static constexpr bool RAW = KV != kBf16;
+  static constexpr int kOpBytes = Dims<KV, DQK>::kOpBytes;
+  static constexpr int kRawBytes = Dims<KV, DQK>::kRawBytes;
   static constexpr int kQBlock = MR * 128;    // one 64-column block of Q
   static constexpr int kQBytes = (DQK / 64) * kQBlock;
   // Q is double-buffered where it fits (BF16, M = 64): the next segment's
   // rows are staged while the current one runs.
-  static constexpr int kQBufs = (!FP8 && MR == 64) ? 2 : 1;
+  static constexpr int kQBufs = (!RAW && MR == 64) ? 2 : 1;
   // copy-combine buffer of the epilogue: MR rows x 32 fp32 columns
   static constexpr int kCombBytes = MR * 32 * 4;
-  static constexpr int kOpStages = FP8 ? (MR == 64 ? 3 : 2) : (TMA || MR == 64 ? 4 : 3);
-  static constexpr int kRawStages = FP8 ? 3 : 0;
+  static constexpr int kOpStages = RAW ? (MR == 64 ? 3 : 2) : (TMA || MR == 64 ? 4 : 3);
+  static constexpr int kRawStages = RAW ? 3 : 0;
   static constexpr int kOffOp = kQBufs * kQBytes;
   static constexpr int kOffRaw = kOffOp + kOpStages * kOpBytes;
   static constexpr int kOffComb = kOffRaw + kRawStages * kRawBytes;
@@ -106,7 +110,7 @@ struct Layout {
   static constexpr int kOffSlotBars = kOffSlots + kSlotRing * kN * 8;
   static constexpr int kUsed = kOffSlotBars + (TMA ? 0 : (int)sizeof(SlotBars));
   static constexpr int kSmem = kUsed + 1024;  // room to align the base to 1024 B
-  static constexpr int kTmaStages = FP8 ? kRawStages : kOpStages;
+  static constexpr int kTmaStages = RAW ? kRawStages : kOpStages;
   // 227 KB per CTA, less the 2 KB of static shared memory.
   static_assert(kSmem + 2048 <= 227 * 1024, "shared memory layout too large");
 };
@@ -219,7 +223,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
 // row has one copy, and lanes l and l + 16 of a softmax warp share row
 // 16w + l % 16, each taking 32 of the tile's 64 key columns (the two-half
 // 16-lane TMEM shapes): every lane works, on half the columns.
-template <bool FP8, bool TMA, int MR, int DQK, bool HALF>
+template <int KV, bool TMA, int MR, int DQK, bool HALF>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const RunArgs args, const __grid_constant__ TmaMaps maps) {
   static_assert(!HALF || MR == 64, "two threads per row only with the M = 64 layout");
@@ -227,13 +231,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   // and a reference into kernel-parameter space would turn every field read
   // inside them into a memory load that the K/V stream keeps evicting.
   const RunArgs a = args;
-  using Lay = Layout<FP8, MR, TMA, DQK>;
+  using Lay = Layout<KV, MR, TMA, DQK>;
+  constexpr bool RAW = KV != kBf16;         // raw rows that the converter warps widen
   // this instantiation's query/key head dim and tile sizes
   constexpr int kDqk = DQK;
-  constexpr int kOpK = Dims<DQK>::kOpK;
-  constexpr int kOpBytes = Dims<DQK>::kOpBytes;
-  constexpr int kRawK = Dims<DQK>::kRawK;
-  constexpr int kRawBytes = Dims<DQK>::kRawBytes;
+  constexpr int kOpK = Dims<KV, DQK>::kOpK;
+  constexpr int kOpBytes = Dims<KV, DQK>::kOpBytes;
+  constexpr int kRawK = Dims<KV, DQK>::kRawK;
+  constexpr int kRawBytes = Dims<KV, DQK>::kRawBytes;
   constexpr int kRows = MR;                 // MMA rows (M)
   constexpr int kQBlock = Lay::kQBlock;
   constexpr int NS = Lay::kOpStages;
@@ -397,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int box = a.page_size >= kN ? kN : a.page_size;   // key rows per box
       const int nbox = kN / box;
       const int oob = a.num_pages * a.page_size;              // first slot past the pool
-      constexpr uint32_t kTileBytes = FP8 ? kRawBytes : kOpBytes;
+      constexpr uint32_t kTileBytes = RAW ? kRawBytes : kOpBytes;
       Cursor cur;
       cur.init(a.segs, a.blocks, head);
       for (int k = 0; k < total; ++k, cur.next()) {
@@ -420,21 +425,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (k == 0) AKP_STAMP(kStampLookup);
-        uint64_t *empty = FP8 ? &bars.tma_empty[t] : &bars.op_empty[t];
+        uint64_t *empty = RAW ? &bars.tma_empty[t] : &bars.op_empty[t];
         if (k >= NT && !tc::mbar_wait(empty, ((k / NT) - 1) & 1, &abort_flag)) break;
         // BF16: a tile with keys outside the block's range lands on edge_full, which
         // only the converters wait on (they zero those V rows); every other tile
         // lands on tma_full, which only the Q.K^T issuer waits on.
-        const bool edge = !FP8 && (key0 < bd.klo || key0 + kN > bd.khi);
+        const bool edge = !RAW && (key0 < bd.klo || key0 + kN > bd.khi);
         uint64_t *full = edge ? &bars.edge_full[t] : &bars.tma_full[t];
         mbar_expect_tx(full, kTileBytes);
-        const uint32_t dst = sbase + (FP8 ? Lay::kOffRaw + t * kRawBytes : Lay::kOffOp + t * kOpBytes);
+        const uint32_t dst = sbase + (RAW ? Lay::kOffRaw + t * kRawBytes : Lay::kOffOp + t * kOpBytes);
 #pragma unroll
         for (int i = 0; i < kN / 8; ++i) {
           if (i >= nbox) break;
-          if (FP8) {
-            tma_load_3d(dst + i * box * kDqk, &maps.k, 0, bd.g, slot[i], full);
-            tma_load_3d(dst + kRawK + i * box * kDv, &maps.v, 0, bd.g, slot[i], full);
+          if (RAW) {
+            tma_load_3d(dst + i * box * kv_row_bytes(KV, kDqk), &maps.k, 0, bd.g, slot[i], full);
+            tma_load_3d(dst + kRawK + i * box * kv_row_bytes(KV, kDv), &maps.v, 0, bd.g, slot[i], full);
           } else {
 #pragma unroll
             for (int c = 0; c < kDqk / 64; ++c)
@@ -502,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ct == 0 && c.si == 0) AKP_STAMP(kStampFirstQ);
       return true;
     };
-    if constexpr (FP8 && TMA) {
+    if constexpr (KV == kE4m3 && TMA) {
       // FP8 rows staged by TMA: [64 keys x 192 B] K then [64 keys x 128 B] V.
       // Both halves are read into registers and the raw stage goes back to
       // the TMA producer at once (after a proxy fence: the refill must not
@@ -566,6 +571,104 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::fence_proxy_async_smem();
         tc::mbar_arrive(&bars.v_full[s]);
       }
+    } else if constexpr (KV == kE2m1) {
+      // E2M1 rows (codes, then a scale per 16 values): one 16-byte chunk of
+      // codes and its two scales become 32 bfloat16 values, exactly.  With TMA
+      // the rows come from the raw stage, which goes back once they are in
+      // registers, and the operand stage's halves have barriers of their own
+      // as for E4M3; without, two threads per key read them from the cache
+      // (slots from the ring the producer warp fills).
+      constexpr int kKrow = kv_row_bytes(kE2m1, kDqk), kVrow = kv_row_bytes(kE2m1, kDv);
+      constexpr int kKch = kDqk / 32, kVch = kDv / 32;      // code chunks per row
+      constexpr int kPerK = kN * kKch / 128, kPerV = kN * kVch / 128;
+      // chunk u of this thread: the key within the tile and the chunk of its row
+      auto at = [&](int u, int nch, int &kk, int &ch) {
+        if (TMA) {
+          const int c = ct + u * 128;
+          kk = c / nch;
+          ch = c % nch;
+        } else {
+          kk = ct >> 1;
+          ch = (ct & 1) * (nch / 2) + u;
+        }
+      };
+      auto widen = [&](uint8_t *dst, int kk, int ch, bool keep, uint4 raw, uint32_t scales) {
+        uint4 w[4];
+        if (keep) e2m1x32_to_bf16(raw, scales, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c16 = 4 * ch + i;
+          *reinterpret_cast<uint4 *>(dst + (c16 >> 3) * kBlk + tc::sw128_offset(kk, c16 & 7)) =
+              keep ? w[i] : make_uint4(0u, 0u, 0u, 0u);
+        }
+      };
+      for (int k = 0; k < total; ++k, cur.next()) {
+        const BlockDesc &bd = cur.bd;
+        if (cur.first() && !stage_q(cur)) break;
+        const int s = k % NS;
+        const int key0 = cur.tile * kN;
+        uint4 bk[kPerK], bv[kPerV];
+        uint32_t sk[kPerK], sv[kPerV];
+        auto fetch = [&](const uint8_t *krow, const uint8_t *vrow, bool per_key, bool live) {
+#pragma unroll
+          for (int u = 0; u < kPerK; ++u) {
+            int kk, ch;
+            at(u, kKch, kk, ch);
+            const uint8_t *row = krow + (per_key ? 0 : kk * kKrow);
+            bk[u] = live ? *reinterpret_cast<const uint4 *>(row + ch * 16) : make_uint4(0u, 0u, 0u, 0u);
+            sk[u] = live ? *reinterpret_cast<const uint16_t *>(row + kDqk / 2 + ch * 2) : 0u;
+          }
+#pragma unroll
+          for (int u = 0; u < kPerV; ++u) {
+            int kk, ch;
+            at(u, kVch, kk, ch);
+            const uint8_t *row = vrow + (per_key ? 0 : kk * kVrow);
+            bv[u] = live ? *reinterpret_cast<const uint4 *>(row + ch * 16) : make_uint4(0u, 0u, 0u, 0u);
+            sv[u] = live ? *reinterpret_cast<const uint16_t *>(row + kDv / 2 + ch * 2) : 0u;
+          }
+        };
+        if constexpr (TMA) {
+          const int t = k % NT;
+          if (!tc::mbar_wait_warp(&bars.tma_full[t], (k / NT) & 1, &abort_flag)) break;
+          const uint8_t *raw = smem + Lay::kOffRaw + t * kRawBytes;
+          fetch(raw, raw + kRawK, false, true);
+          tc::fence_proxy_async_smem();
+          tc::mbar_arrive(&bars.tma_empty[t]);
+        } else {
+          constexpr int R = Lay::kSlotRing > 0 ? Lay::kSlotRing : 1;   // 0 in TMA kernels (unused)
+          const int r = k % R;
+          if (!tc::mbar_wait_warp(&slot_bars->full[r], (k / R) & 1, &abort_flag)) break;
+          const int64_t slot = reinterpret_cast<const int64_t *>(smem + Lay::kOffSlots)[r * kN + (ct >> 1)];
+          tc::mbar_arrive(&slot_bars->empty[r]);
+          const int64_t srow = (slot >= 0 ? slot : 0) * a.hkv + bd.g;
+          fetch(kc + srow * kKrow, vc + srow * kVrow, true, slot >= 0);
+        }
+        uint8_t *dst = smem + Lay::kOffOp + s * kOpBytes;
+        uint64_t *kfree = TMA ? &bars.k_empty[s] : &bars.op_empty[s];
+        if (k >= NS && !tc::mbar_wait_warp(kfree, ((k / NS) - 1) & 1, &abort_flag)) break;
+#pragma unroll
+        for (int u = 0; u < kPerK; ++u) {
+          int kk, ch;
+          at(u, kKch, kk, ch);
+          const int j = key0 + kk;
+          widen(dst, kk, ch, j >= bd.klo && j < bd.khi, bk[u], sk[u]);
+        }
+        if (TMA) {
+          tc::fence_proxy_async_smem();
+          tc::mbar_arrive(&bars.op_full[s]);
+          if (k >= NS && !tc::mbar_wait_warp(&bars.op_empty[s], ((k / NS) - 1) & 1, &abort_flag))
+            break;
+        }
+#pragma unroll
+        for (int u = 0; u < kPerV; ++u) {
+          int kk, ch;
+          at(u, kVch, kk, ch);
+          const int j = key0 + kk;
+          widen(dst + kOpK, kk, ch, j >= bd.klo && j < bd.khi, bv[u], sv[u]);
+        }
+        tc::fence_proxy_async_smem();
+        tc::mbar_arrive(TMA ? &bars.v_full[s] : &bars.op_full[s]);
+      }
     } else {
     uint32_t edge_parity = 0;   // BF16 + TMA: completed edge tiles per stage (one bit each)
     for (int k = 0; k < total; ++k, cur.next()) {
@@ -574,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int s = k % NS;
       const int key0 = cur.tile * kN;
       uint8_t *op = smem + Lay::kOffOp + s * kOpBytes;
-      if (TMA && !FP8) {
+      if (TMA && !RAW) {
         // BF16 tile landed by TMA in operand layout.  Interior tiles go straight
         // to the Q.K^T issuer; on edge tiles zero the V rows outside the range first.
         if (key0 >= bd.klo && key0 + kN <= bd.khi) continue;
@@ -595,6 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::mbar_arrive(&bars.op_full[s]);
         continue;
       }
+      constexpr bool FP8 = KV == kE4m3;
       constexpr int kEs = FP8 ? 1 : 2;
       constexpr int kKch = kDqk * kEs / 16;  // source 16-byte chunks per K row
       constexpr int kVch = kDv * kEs / 16;
@@ -675,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int qb = cs.si % QB;
         if (cs.first() && !tc::mbar_wait(&bars.q_full[qb], (cs.si / QB) & 1, &abort_flag)) break;
         bool ok;
-        if (TMA && !FP8) {
+        if (TMA && !RAW) {
           if (key0 < cs.bd.klo || key0 + kN > cs.bd.khi) {
             ok = tc::mbar_wait(&bars.op_full[s], (edge_parity >> s) & 1, &abort_flag);
             edge_parity ^= 1u << s;
@@ -700,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc::mma_commit(&bars.s_full[b]);
         if (ks == 0) AKP_STAMP(kStampFirstQK);
-        if (FP8 && TMA) tc::mma_commit(&bars.k_empty[s]);
+        if (RAW && TMA) tc::mma_commit(&bars.k_empty[s]);
         if (cs.last()) tc::mma_commit(&bars.q_empty[qb]);
       }
       tc::mma_commit(&bars.final_done);
@@ -717,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = kp % NS;
         const bool first = cp.first();
         if (!tc::mbar_wait(&bars.p_full[b], (kp >> 1) & 1, &abort_flag)) break;
-        if (FP8 && TMA && !tc::mbar_wait(&bars.v_full[s], (kp / NS) & 1, &abort_flag)) break;
+        if (RAW && TMA && !tc::mbar_wait(&bars.v_full[s], (kp / NS) & 1, &abort_flag)) break;
         // the first P.V of a segment overwrites O: the epilogue of the
         // previous segment must have read it
         if (first && cp.si > 0 && !tc::mbar_wait(&bars.o_free, (cp.si - 1) & 1, &abort_flag))
@@ -1175,50 +1279,54 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <bool FP8, bool TMA, int MR, int DQK, bool HALF>
+template <int KV, bool TMA, int MR, int DQK, bool HALF>
 cudaError_t launch_one(const HostPlan &hp, const RunArgs &a, const TmaMaps &m, cudaStream_t st) {
-  return launch_dependent(attn_tc_kernel<FP8, TMA, MR, DQK, HALF>, dim3(hp.num_ctas),
-                          dim3(kThreads), Layout<FP8, MR, TMA, DQK>::kSmem, st, a, m);
+  return launch_dependent(attn_tc_kernel<KV, TMA, MR, DQK, HALF>, dim3(hp.num_ctas),
+                          dim3(kThreads), Layout<KV, MR, TMA, DQK>::kSmem, st, a, m);
 }
 
-template <bool FP8, bool TMA, int MR, int DQK, bool HALF>
+template <int KV, bool TMA, int MR, int DQK, bool HALF>
 cudaError_t prepare_one() {
-  return cudaFuncSetAttribute(attn_tc_kernel<FP8, TMA, MR, DQK, HALF>,
+  return cudaFuncSetAttribute(attn_tc_kernel<KV, TMA, MR, DQK, HALF>,
                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Layout<FP8, MR, TMA, DQK>::kSmem);
+                              Layout<KV, MR, TMA, DQK>::kSmem);
 }
 
-template <int MR, int DQK, bool HALF>
+template <int KV, int MR, int DQK, bool HALF>
 cudaError_t launch_rows(const HostPlan &hp, const RunArgs &a, const TmaMaps &m, cudaStream_t st) {
-  const bool fp8 = hp.prob.kv_dtype == ATTN_KV_FP8_E4M3;
-  if (hp.use_tma)
-    return fp8 ? launch_one<true, true, MR, DQK, HALF>(hp, a, m, st)
-               : launch_one<false, true, MR, DQK, HALF>(hp, a, m, st);
-  return fp8 ? launch_one<true, false, MR, DQK, HALF>(hp, a, m, st)
-             : launch_one<false, false, MR, DQK, HALF>(hp, a, m, st);
+  return hp.use_tma ? launch_one<KV, true, MR, DQK, HALF>(hp, a, m, st)
+                    : launch_one<KV, false, MR, DQK, HALF>(hp, a, m, st);
 }
 
-template <int MR, int DQK, bool HALF>
+template <int KV, int MR, int DQK, bool HALF>
 cudaError_t prepare_rows(const HostPlan &hp) {
-  const bool fp8 = hp.prob.kv_dtype == ATTN_KV_FP8_E4M3;
-  if (hp.use_tma)
-    return fp8 ? prepare_one<true, true, MR, DQK, HALF>() : prepare_one<false, true, MR, DQK, HALF>();
-  return fp8 ? prepare_one<true, false, MR, DQK, HALF>() : prepare_one<false, false, MR, DQK, HALF>();
+  return hp.use_tma ? prepare_one<KV, true, MR, DQK, HALF>() : prepare_one<KV, false, MR, DQK, HALF>();
 }
 
 // M = 64 plans whose blocks all have more than 32 rows run the two-threads-
 // per-row instantiation.
-template <int DQK>
+template <int KV, int DQK>
 cudaError_t launch_dqk(const HostPlan &hp, const RunArgs &a, const TmaMaps &m, cudaStream_t st) {
-  if (hp.block_rows != 64) return launch_rows<128, DQK, false>(hp, a, m, st);
-  return hp.one_copy ? launch_rows<64, DQK, true>(hp, a, m, st)
-                     : launch_rows<64, DQK, false>(hp, a, m, st);
+  if (hp.block_rows != 64) return launch_rows<KV, 128, DQK, false>(hp, a, m, st);
+  return hp.one_copy ? launch_rows<KV, 64, DQK, true>(hp, a, m, st)
+                     : launch_rows<KV, 64, DQK, false>(hp, a, m, st);
 }
 
-template <int DQK>
+template <int KV, int DQK>
 cudaError_t prepare_dqk(const HostPlan &hp) {
-  if (hp.block_rows != 64) return prepare_rows<128, DQK, false>(hp);
-  return hp.one_copy ? prepare_rows<64, DQK, true>(hp) : prepare_rows<64, DQK, false>(hp);
+  if (hp.block_rows != 64) return prepare_rows<KV, 128, DQK, false>(hp);
+  return hp.one_copy ? prepare_rows<KV, 64, DQK, true>(hp) : prepare_rows<KV, 64, DQK, false>(hp);
+}
+
+template <int KV>
+cudaError_t launch_kv(const HostPlan &hp, const RunArgs &a, const TmaMaps &m, cudaStream_t st) {
+  return hp.prob.head_dim_qk == kDqkSym ? launch_dqk<KV, kDqkSym>(hp, a, m, st)
+                                        : launch_dqk<KV, kDqk>(hp, a, m, st);
+}
+
+template <int KV>
+cudaError_t prepare_kv(const HostPlan &hp) {
+  return hp.prob.head_dim_qk == kDqkSym ? prepare_dqk<KV, kDqkSym>(hp) : prepare_dqk<KV, kDqk>(hp);
 }
 
 }  // namespace
@@ -1231,12 +1339,21 @@ bool tc_tma_page_size(int32_t page_size, int32_t num_pages) {
 cudaError_t launch_attn_tc(const HostPlan &hp, const RunArgs &a, const TmaMaps &m,
                            cudaStream_t stream) {
   if (hp.num_ctas == 0) return cudaSuccess;
-  return hp.prob.head_dim_qk == kDqkSym ? launch_dqk<kDqkSym>(hp, a, m, stream)
-                                        : launch_dqk<kDqk>(hp, a, m, stream);
+  switch (hp.prob.kv_dtype) {
+    case ATTN_KV_BF16: return launch_kv<kBf16>(hp, a, m, stream);
+    case ATTN_KV_FP8_E4M3: return launch_kv<kE4m3>(hp, a, m, stream);
+    case ATTN_KV_FP4_E2M1: return launch_kv<kE2m1>(hp, a, m, stream);
+  }
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t prepare_attn_tc(const HostPlan &hp) {
-  return hp.prob.head_dim_qk == kDqkSym ? prepare_dqk<kDqkSym>(hp) : prepare_dqk<kDqk>(hp);
+  switch (hp.prob.kv_dtype) {
+    case ATTN_KV_BF16: return prepare_kv<kBf16>(hp);
+    case ATTN_KV_FP8_E4M3: return prepare_kv<kE4m3>(hp);
+    case ATTN_KV_FP4_E2M1: return prepare_kv<kE2m1>(hp);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace akp

@@ -63,7 +63,7 @@ struct StageArgs {
   int32_t *err;
   int64_t tiles;             // all units' tiles
   int32_t num_units, dqk, hkv, page_size, pt_stride, num_pages;
-  bool fp8;
+  int32_t kv_dtype;          // attn_kv_dtype_t
 };
 cudaError_t launch_kv_stage(const StageArgs &a, cudaStream_t stream);
 
@@ -94,6 +94,12 @@ attn_status_t run_paged_unstaged(attn_plan_t plan, const void *q, const void *k_
                                  const float *sinks, int32_t window, float softmax_scale,
                                  float k_scale, float v_scale, void *out, float *lse_out,
                                  void *workspace, size_t workspace_bytes, void *stream);
+// New tokens' rows into the caches, rotated when `rope` is given (kv_rope.cu):
+// attn_append_kv_rope, and attn_append_kv of 4-bit caches (rope, q, q_out NULL).
+attn_status_t append_rows(attn_plan_t plan, const attn_rope_t *rope, const void *q, const void *k_new,
+                          const void *v_new, void *q_out, void *k_cache, void *v_cache,
+                          const int32_t *page_table, const int32_t *seq_lens, const int32_t *qo_indptr,
+                          float k_scale, float v_scale, void *stream);
 // Log-sum-exp merge of multi-split blocks.
 cudaError_t launch_merge(const HostPlan &hp, const RunArgs &a, cudaStream_t stream);
 

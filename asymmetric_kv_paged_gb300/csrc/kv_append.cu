@@ -9,6 +9,8 @@
 // FP8 E4M3 KV cache with a per-tensor scale stores its entries (model card
 // MiMo-V2.6-Flash-RL-FP8KV-W4A8-2x-RTX-PRO-6000, "What the kernels do").
 //
+// (4-bit caches are appended by kv_rope.cu, whose threads own whole scale blocks.)
+//
 // One thread per 16-byte chunk of a source row (8 bf16 values): a row of K is
 // 24 chunks, a row of V 16; the thread finds its request by binary search in
 // qo_indptr.  The kernel streams its bytes once (HBM-bound for large appends,
@@ -20,6 +22,7 @@
 #include <cstdint>
 
 #include "attn_paged.h"
+#include "kernels.hpp"
 #include "plan.hpp"
 
 namespace akp {
@@ -126,6 +129,9 @@ extern "C" attn_status_t attn_append_kv(attn_plan_t plan, const void *k_new, con
   if (!plan || plan->device < 0) return ATTN_ERR_INVALID_ARG;
   const akp::HostPlan &hp = plan->host;
   const attn_problem_t &pr = hp.prob;
+  if (pr.kv_dtype == ATTN_KV_FP4_E2M1)          // a scale per 16 values: kv_rope.cu
+    return akp::append_rows(plan, nullptr, nullptr, k_new, v_new, nullptr, k_cache, v_cache, page_table,
+                            seq_lens, qo_indptr, k_scale, v_scale, stream);
   const int64_t total_q = hp.qo_indptr.back();
   if (total_q == 0) return ATTN_OK;
   if (!k_new || !v_new || !k_cache || !v_cache || !page_table || !seq_lens || !qo_indptr)

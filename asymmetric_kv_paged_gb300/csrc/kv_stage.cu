@@ -10,7 +10,7 @@
 // the paged layout of the MiMo-V2.6-Flash-RL model card, "What the kernels
 // do"): BF16 rows are copied bit for bit, E4M3 codes are widened exactly to
 // fp16 (every E4M3 value is an fp16 value; the scale stays outside, as in the
-// attention kernels).  Keys outside [klo, khi) are written as zeros: the
+// attention kernels), E2M1 codes with their block scales likewise (e2m1.cuh).  Keys outside [klo, khi) are written as zeros: the
 // kernel masks them, and zeros keep P.V free of whatever the pool holds
 // there.  A page id outside the pool is read as zeros and reported in bit 1
 // of the plan's error word, as the attention kernels do.
@@ -24,7 +24,7 @@
 
 #include <cstdint>
 
-#include "e4m3.cuh"
+#include "e2m1.cuh"
 #include "kernels.hpp"
 
 namespace akp {
@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kStageThreads = 256;
 
-template <bool FP8>
+template <int KV>
 __global__ void __launch_bounds__(kStageThreads) stage_kernel(const StageArgs a) {
   // Launched as a programmatic dependent of the stream's previous kernel (a
   // KV append writes the caches read here): wait for it before reading them.
@@ -42,13 +42,13 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const StageArgs a)
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   __shared__ int64_t s_slot[kStageTile];
   __shared__ StageUnit s_unit;
-  // 16-byte chunks of a source row: E4M3 rows hold 16 codes per chunk, BF16 8 values
-  constexpr int kCodes = FP8 ? 16 : 8;
+  // 16-byte chunks of a source row: E2M1 rows hold 32 codes per chunk (their
+  // scales, in the chunk behind the last, come with each), E4M3 16, BF16 8 values
+  constexpr int kCodes = KV == ATTN_KV_FP4_E2M1 ? 32 : KV == ATTN_KV_FP8_E4M3 ? 16 : 8;
   const int kch = a.dqk / kCodes, vch = kDv / kCodes;
   const int chunks = kch + vch;
   const uint8_t *kc = static_cast<const uint8_t *>(a.k_cache);
   const uint8_t *vc = static_cast<const uint8_t *>(a.v_cache);
-  constexpr int kEs = FP8 ? 1 : 2;
   for (int64_t t = blockIdx.x; t < a.tiles; t += gridDim.x) {
     if (threadIdx.x == 0) {
       // the unit of tile t: the last one with tile_off <= t
@@ -83,13 +83,19 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const StageArgs a)
       const int cc = is_k ? c : c - kch;
       const int d = is_k ? a.dqk : kDv;
       const int64_t slot = s_slot[key];
+      const int row_bytes = KV == ATTN_KV_FP4_E2M1 ? e2m1_row_bytes(d) : KV == ATTN_KV_FP8_E4M3 ? d : 2 * d;
+      const uint8_t *src = (is_k ? kc : vc) + ((slot >= 0 ? slot : 0) * a.hkv + u.g) * (int64_t)row_bytes;
       uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-      if (slot >= 0)
-        raw = __ldg(reinterpret_cast<const uint4 *>((is_k ? kc : vc) +
-                                                    (slot * a.hkv + u.g) * (int64_t)(d * kEs)) +
-                    cc);
+      if (slot >= 0) raw = __ldg(reinterpret_cast<const uint4 *>(src) + cc);
       uint4 *dst = reinterpret_cast<uint4 *>((is_k ? a.k_stage : a.v_stage) + (row0 + key) * d);
-      if (FP8) {
+      if (KV == ATTN_KV_FP4_E2M1) {
+        uint32_t scales = 0u;
+        if (slot >= 0) scales = __ldg(reinterpret_cast<const uint16_t *>(src + d / 2) + cc);
+        uint4 w[4];
+        e2m1x32_to_f16(raw, scales, w);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) dst[4 * cc + q] = w[q];
+      } else if (KV == ATTN_KV_FP8_E4M3) {
         uint4 lo, hi;
         e4m3x16_to_f16(raw, lo, hi);
         dst[2 * cc] = lo;
@@ -107,11 +113,12 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const StageArgs a)
 cudaError_t launch_kv_stage(const StageArgs &a, cudaStream_t stream) {
   if (a.tiles == 0) return cudaSuccess;
   const int64_t grid = a.tiles < 152 * 8 ? a.tiles : 152 * 8;
-  if (a.fp8)
-    return launch_dependent(stage_kernel<true>, dim3((unsigned)grid), dim3(kStageThreads), 0,
-                            stream, a);
-  return launch_dependent(stage_kernel<false>, dim3((unsigned)grid), dim3(kStageThreads), 0,
-                          stream, a);
+  const dim3 blocks((unsigned)grid), threads(kStageThreads);
+  if (a.kv_dtype == ATTN_KV_FP4_E2M1)
+    return launch_dependent(stage_kernel<ATTN_KV_FP4_E2M1>, blocks, threads, 0, stream, a);
+  if (a.kv_dtype == ATTN_KV_FP8_E4M3)
+    return launch_dependent(stage_kernel<ATTN_KV_FP8_E4M3>, blocks, threads, 0, stream, a);
+  return launch_dependent(stage_kernel<ATTN_KV_BF16>, blocks, threads, 0, stream, a);
 }
 
 }  // namespace akp

@@ -95,7 +95,9 @@ attn_status_t build_host_plan(const attn_problem_t *p, int32_t num_sms, HostPlan
   if ((p->head_dim_qk != kDqk && p->head_dim_qk != kDqkSym) || p->head_dim_v != kDv)
     return ATTN_ERR_UNSUPPORTED;
   if (p->num_q_heads % p->num_kv_heads != 0) return ATTN_ERR_UNSUPPORTED;
-  if (p->kv_dtype != ATTN_KV_BF16 && p->kv_dtype != ATTN_KV_FP8_E4M3) return ATTN_ERR_UNSUPPORTED;
+  if (p->kv_dtype != ATTN_KV_BF16 && p->kv_dtype != ATTN_KV_FP8_E4M3 &&
+      p->kv_dtype != ATTN_KV_FP4_E2M1)
+    return ATTN_ERR_UNSUPPORTED;
 
   HostPlan hp;
   hp.prob = *p;

@@ -11,6 +11,9 @@ import torch
 from . import binding as B
 
 
+KV_DTYPES = {"bf16": B.ATTN_KV_BF16, "fp8": B.ATTN_KV_FP8_E4M3, "fp4": B.ATTN_KV_FP4_E2M1}
+
+
 def _dev(a: np.ndarray, device, dtype=None) -> torch.Tensor:
     t = torch.from_numpy(np.ascontiguousarray(a))
     if dtype is not None:
@@ -45,7 +48,7 @@ class DeviceWorkload:
         return B.make_problem(
             batch=w.batch, num_q_heads=w.hq, num_kv_heads=w.hkv, page_size=w.page_size,
             num_pages=w.num_pages, page_table_stride=w.page_table.shape[1],
-            kv_dtype=B.ATTN_KV_BF16 if w.kv_dtype == "bf16" else B.ATTN_KV_FP8_E4M3,
+            kv_dtype=KV_DTYPES[w.kv_dtype],
             window=w.window, has_sinks=w.sinks is not None, qo_indptr=w.qo_indptr,
             seq_lens=w.seq_lens, head_dim_qk=w.dqk)
 

@@ -13,9 +13,11 @@ Recipe (numpy PCG64, ``default_rng(seed)``), draw order fixed:
   * fp8 K/V: float32 N(0,1) draws, per-tensor scale = amax / 448, codes are
     RNE(x / scale) in OCP E4M3 (torch's float8_e4m3fn cast; no overflow because
     |x / scale| <= 448).
+  * fp4 K/V: the same draws as 4-bit rows (E2M1 codes, an E4M3 scale per 16
+    values), per-tensor scale = amax / (6 * 448).
   * Only slots that some query can see get values.  Every other slot (the tail
     of a last page, keys left of a sliding window, pages nobody references) holds
-    NaN: bf16 0x7FC0, fp8 0x7F.  Unused page-table columns point at a page no
+    NaN: bf16 0x7FC0, fp8 0x7F, fp4 rows of 0xFF (NaN scales).  Unused page-table columns point at a page no
     request owns (all NaN), so a kernel that reads past a request's pages
     produces NaN instead of touching memory outside the pool.
 The five named workloads mirror the pages' shapes: the 1.2M-slot pools and page
@@ -80,6 +82,49 @@ def e4m3_codes(x: np.ndarray) -> np.ndarray:
     return t.to(torch.float8_e4m3fn).view(torch.uint8).numpy().copy()
 
 
+E2M1_VALUES = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], np.float32)
+FP4_TOP = 6.0 * 448.0                    # largest code times largest block scale
+
+
+def fp4_row_bytes(d: int) -> int:
+    """Bytes of a 4-bit row of d values: codes, block scales, padding to 16."""
+    return (d // 2 + d // 16 + 15) // 16 * 16
+
+
+def fp4_rows(x: np.ndarray) -> np.ndarray:
+    """float32 [..., d] -> 4-bit rows uint8 [..., fp4_row_bytes(d)]: per 16 values the
+    scale E4M3(amax / 6), then the E2M1 code of each quotient, nearest even."""
+    x = np.asarray(x, np.float32)
+    d = x.shape[-1]
+    y = x.reshape(x.shape[:-1] + (d // 16, 16))
+    scale = e4m3_codes(np.minimum(np.abs(y).max(-1) / np.float32(6.0), np.float32(448.0)))
+    import torch
+    s = torch.from_numpy(scale).view(torch.float8_e4m3fn).float().numpy()[..., None]
+    a = np.divide(np.abs(y), s, out=np.zeros_like(y), where=s > 0)
+    # borders between neighbouring codes; a tie goes to the even code
+    code = (a > 0.25).astype(np.uint8)
+    for border, even_above in ((0.75, True), (1.25, False), (1.75, True), (2.5, False), (3.5, True),
+                               (5.0, False)):
+        code += (a >= border) if even_above else (a > border)
+    code |= np.signbit(y).astype(np.uint8) << 3
+    code = code.reshape(x.shape)
+    out = np.zeros(x.shape[:-1] + (fp4_row_bytes(d),), np.uint8)
+    out[..., :d // 2] = code[..., 0::2] | (code[..., 1::2] << 4)
+    out[..., d // 2:d // 2 + d // 16] = scale
+    return out
+
+
+def fp4_values(rows: np.ndarray, d: int) -> np.ndarray:
+    """4-bit rows -> float32 [..., d], exact (codes times block scales)."""
+    import torch
+    rows = np.asarray(rows, np.uint8)
+    code = np.stack([rows[..., :d // 2] & 15, rows[..., :d // 2] >> 4], -1).reshape(rows.shape[:-1] + (d,))
+    v = np.where(code & 8, -E2M1_VALUES[code & 7], E2M1_VALUES[code & 7])
+    s = np.ascontiguousarray(rows[..., d // 2:d // 2 + d // 16])
+    s = torch.from_numpy(s).view(torch.float8_e4m3fn).float().numpy()
+    return v * np.repeat(s, 16, axis=-1)
+
+
 @dataclass
 class Workload:
     name: str
@@ -88,13 +133,13 @@ class Workload:
     page_size: int
     num_pages: int
     window: int
-    kv_dtype: str                    # "bf16" | "fp8"
+    kv_dtype: str                    # "bf16" | "fp8" | "fp4"
     qo_indptr: np.ndarray            # int32 [B+1]
     seq_lens: np.ndarray             # int32 [B]
     page_table: np.ndarray           # int32 [B, stride]
     q: np.ndarray                    # uint16 (bf16 bits) [total_q, Hq, Dqk] (Dqk 192 or 128)
-    k_cache: np.ndarray              # uint16 | uint8 [num_pages, P, Hkv, Dqk]
-    v_cache: np.ndarray              # uint16 | uint8 [num_pages, P, Hkv, 128]
+    k_cache: np.ndarray              # uint16 | uint8 [num_pages, P, Hkv, Dqk (fp4: row bytes)]
+    v_cache: np.ndarray              # uint16 | uint8 [num_pages, P, Hkv, 128 (fp4: row bytes)]
     sinks: np.ndarray | None         # float32 [Hq] or None
     softmax_scale: float
     k_scale: float = 1.0
@@ -111,7 +156,12 @@ class Workload:
         return int(self.qo_indptr[-1])
 
     def host_arrays(self) -> dict:
-        return dict(q=self.q, k_cache=self.k_cache, v_cache=self.v_cache,
+        """The problem as host arrays; 4-bit caches as the bf16 values their rows
+        stand for (exact: at most 6 significant bits)."""
+        k, v = self.k_cache, self.v_cache
+        if self.kv_dtype == "fp4":
+            k, v = bf16_bits(fp4_values(k, self.dqk)), bf16_bits(fp4_values(v, DV))
+        return dict(q=self.q, k_cache=k, v_cache=v,
                     qo_indptr=self.qo_indptr, seq_lens=self.seq_lens,
                     page_table=self.page_table, sinks=self.sinks, window=self.window,
                     softmax_scale=self.softmax_scale, k_scale=self.k_scale,
@@ -190,6 +240,15 @@ def make_workload(seed: int, seq_lens, n_per_req, hq: int, hkv: int, page_size: 
         v_scale = float(np.float32(v_amax / 448.0)) or 1.0
         k_cache[slots] = e4m3_codes(k_vals / np.float32(k_scale))
         v_cache[slots] = e4m3_codes(v_vals / np.float32(v_scale))
+    elif kv_dtype == "fp4":
+        k_cache = np.full((nslot, hkv * fp4_row_bytes(dqk)), 0xFF, dtype=np.uint8)
+        v_cache = np.full((nslot, hkv * fp4_row_bytes(DV)), 0xFF, dtype=np.uint8)
+        k_amax = float(np.abs(k_vals).max()) if k_vals.size else 1.0
+        v_amax = float(np.abs(v_vals).max()) if v_vals.size else 1.0
+        k_scale = float(np.float32(k_amax / FP4_TOP)) or 1.0
+        v_scale = float(np.float32(v_amax / FP4_TOP)) or 1.0
+        k_cache[slots] = fp4_rows((k_vals / np.float32(k_scale)).reshape(-1, hkv, dqk)).reshape(slots.size, k_cache.shape[1])
+        v_cache[slots] = fp4_rows((v_vals / np.float32(v_scale)).reshape(-1, hkv, DV)).reshape(slots.size, v_cache.shape[1])
     else:
         raise ValueError(kv_dtype)
     del k_vals, v_vals
@@ -200,8 +259,8 @@ def make_workload(seed: int, seq_lens, n_per_req, hq: int, hkv: int, page_size: 
     return Workload(name=name, hq=hq, hkv=hkv, page_size=page_size, num_pages=num_pages,
                     window=window, kv_dtype=kv_dtype, qo_indptr=qo_indptr,
                     seq_lens=seq.astype(np.int32), page_table=page_table, q=q,
-                    k_cache=k_cache.reshape(num_pages, page_size, hkv, dqk),
-                    v_cache=v_cache.reshape(num_pages, page_size, hkv, DV),
+                    k_cache=k_cache.reshape(num_pages, page_size, hkv, -1),
+                    v_cache=v_cache.reshape(num_pages, page_size, hkv, -1),
                     sinks=sink_arr, softmax_scale=float(softmax_scale),
                     k_scale=k_scale, v_scale=v_scale, dqk=dqk)
 

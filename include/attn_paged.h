@@ -61,9 +61,31 @@ typedef enum {
 
 typedef enum {
     ATTN_KV_BF16 = 0,      /* K/V elements are bfloat16 */
-    ATTN_KV_FP8_E4M3 = 1   /* K/V elements are OCP FP8 E4M3 codes; value =
+    ATTN_KV_FP8_E4M3 = 1,  /* K/V elements are OCP FP8 E4M3 codes; value =
                               decoded code * k_scale (resp. v_scale) */
+    ATTN_KV_FP4_E2M1 = 2   /* K/V rows are records of E2M1 codes with an E4M3
+                              scale per 16 values (see below) */
 } attn_kv_dtype_t;
+
+/*
+ * 4-bit caches (ATTN_KV_FP4_E2M1).  The row of d values (d = 192 or 128) of
+ * one KV head is a record of attn_kv_row_bytes bytes, 112 for d = 192 and 80
+ * for d = 128, so the caches are uint8 [num_pages, P, Hkv, 112 or 80] and
+ * [num_pages, P, Hkv, 80]:
+ *   bytes [0, d/2)           OCP FP4 E2M1 codes (sign, 2 exponent bits, bias 1,
+ *                            1 mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6);
+ *                            element 2i is the low nibble of byte i;
+ *   bytes [d/2, d/2 + d/16)  E4M3 block scales, block c = elements [16c, 16c + 16);
+ *   the rest                 padding up to a multiple of 16 (written as zeros,
+ *                            never read).
+ *   value = code * block scale * k_scale (resp. v_scale).
+ * code * block scale has at most 6 significant bits, so the kernels widen it
+ * exactly.  A block scale of 0x7F or 0xFF (NaN) makes its block NaN.
+ */
+
+/* Bytes of one cached row of head_dim (192 or 128) values of one KV head.
+ * Errors: INVALID_ARG (bytes NULL), UNSUPPORTED (type or head dim). */
+attn_status_t attn_kv_row_bytes(attn_kv_dtype_t kv_dtype, int32_t head_dim, int32_t *bytes);
 
 typedef struct attn_plan_s *attn_plan_t;
 
@@ -140,7 +162,8 @@ attn_status_t attn_plan_replayable(const attn_problem_t *bounds, int device, att
  * Run the planned attention on `stream`.
  *   q            bf16 [total_q, Hq, Dqk], row-major, contiguous (Dqk = the
  *                plan's head_dim_qk: 192 or 128).
- *   k_cache      [num_pages, P, Hkv, Dqk] of bf16 or E4M3 bytes.
+ *   k_cache      [num_pages, P, Hkv, Dqk] of bf16 or E4M3 bytes, or 4-bit
+ *                records (above); 16-byte aligned.
  *   v_cache      [num_pages, P, Hkv, 128] of the same type.
  *   page_table   int32 [B, page_table_stride]; entries at or beyond
  *                ceil(seq_lens[b] / P) are never read, and with a window
@@ -164,7 +187,7 @@ attn_status_t attn_plan_replayable(const attn_problem_t *bounds, int device, att
  *   window       must equal the plan's window.
  *   softmax_scale, k_scale, v_scale  as in the operation above (the kv scales
  *                are ignored for bf16 caches and should be 1).  All finite;
- *                softmax_scale > 0, and k_scale > 0 for an FP8 cache.
+ *                softmax_scale > 0, and k_scale > 0 for an FP8 or 4-bit cache.
  *   out          bf16 [total_q, Hq, 128].
  *   lse_out      fp32 [total_q, Hq] natural-log denominators, or NULL.
  *   workspace    device scratch of at least workspace_bytes (may be NULL when
@@ -172,18 +195,18 @@ attn_status_t attn_plan_replayable(const attn_problem_t *bounds, int device, att
  * Slots of the caches that no query can see are never read, so they may hold
  * anything (NaN included).  Queries keep their full bf16 range for either
  * cache type.  Plans whose row blocks hold at most 128 rows (decode, verify)
- * widen E4M3 elements exactly to bf16 and form every product as bf16 x bf16
- * with fp32 accumulation.  Plans with larger blocks (chunked prefill) run
- * Q.K^T on an FP8 cache in fp16: each query row is multiplied by the power of
+ * widen E4M3 and E2M1 elements exactly to bf16 and form every product as
+ * bf16 x bf16 with fp32 accumulation.  Plans with larger blocks (chunked
+ * prefill) run Q.K^T on an FP8 or 4-bit cache in fp16: each query row is multiplied by the power of
  * two that puts its largest |q| in [2^14, 2^15) (exact; every element down to
- * 2^-31 of that maximum stays exact in fp16), E4M3 is widened exactly to
+ * 2^-31 of that maximum stays exact in fp16), the cache is widened exactly to
  * fp16, and the scores are divided by the same power of two in fp32; P.V
  * is fp16 x fp16 with fp32 accumulation.  The E4M3 NaN codes (0x7F, 0xFF) in
  * a visible slot read as +-480 on the decode/verify plans and stay NaN on the
- * prefill plans.
+ * prefill plans; NaN block scales of a 4-bit cache are NaN on every plan.
  * Prefill plans that are not replayable first gather the keys their blocks
- * read into a staging scratch in the workspace (16-bit rows: E4M3 widened
- * exactly to fp16, BF16 copied; (Dqk + 128) * 2 bytes per key of each KV
+ * read into a staging scratch in the workspace (16-bit rows: E4M3 and
+ * E2M1 widened exactly to fp16, BF16 copied; (Dqk + 128) * 2 bytes per key of each KV
  * head, over whole 128-key tiles), which the prefill kernel loads as TMA
  * tiles; attn_plan's workspace size includes it.
  * Runs of one plan must be ordered on one stream (they share the plan's
@@ -226,11 +249,16 @@ attn_status_t attn_run_phase(attn_plan_t plan, int32_t phase, const void *q,
  *                rounding to nearest even with saturation to +-448, which is
  *                how an FP8 E4M3 KV cache with a per-tensor scale stores its
  *                entries (model card MiMo-V2.6-Flash-RL-FP8KV-W4A8-2x-RTX-PRO-
- *                6000, "What the kernels do"); V likewise with v_scale.
+ *                6000, "What the kernels do"); V likewise with v_scale;
+ *   4-bit caches: y = k_new / k_scale (fp32, IEEE); the scale of each 16
+ *                consecutive values is E4M3(max|y| / 6), nearest even,
+ *                saturating at 448 (NaN when the block holds a NaN); the codes
+ *                are E2M1(y / scale), the quotient in fp32, nearest even,
+ *                saturating at +-6, signed zeros where the scale is zero.
  *   k_new, v_new bf16 [total_q][Hkv][Dqk] and [total_q][Hkv][128], contiguous.
  *   k_cache, v_cache, page_table, seq_lens, qo_indptr: as for attn_run_paged
  *                (device copies equal to the plan's host arrays).
- *   k_scale, v_scale  finite and > 0 for FP8 caches; ignored for BF16.
+ *   k_scale, v_scale  finite and > 0 for FP8 and 4-bit caches; ignored for BF16.
  * Only the written slots change.  A page id outside [0, num_pages) is not
  * dereferenced: that token's rows are skipped and the plan's device error
  * word records it (bit 0).  With a replayable plan seq_lens may change between
@@ -242,6 +270,77 @@ attn_status_t attn_append_kv(attn_plan_t plan, const void *k_new, const void *v_
                              void *k_cache, void *v_cache, const int32_t *page_table,
                              const int32_t *seq_lens, const int32_t *qo_indptr, float k_scale,
                              float v_scale, void *stream);
+
+/*
+ * The rotation that attn_append_kv_rope applies.
+ *   cos_sin      device fp32 [max_pos][rot_dim], contiguous, 16-byte aligned: row
+ *                p holds the cosines c_i of position p's rot_dim / 2 angles,
+ *                then their sines s_i.
+ *   positions    device int32 [total_q], the row of cos_sin for each new token,
+ *                or NULL: the token's own position seq_lens[b] - n_b + t.
+ *   rot_dim      rotated dims, a multiple of 16; rot_offset: the first of them,
+ *                a multiple of 8; rot_offset + rot_dim <= Dqk.
+ *   interleaved  0: dim i is paired with dim i + rot_dim / 2; nonzero: dim 2i
+ *                with dim 2i + 1 (i < rot_dim / 2, counted from rot_offset).
+ * Pair i of a row, (x1, x2), becomes (x1 c_i - x2 s_i, x2 c_i + x1 s_i).
+ */
+typedef struct {
+    const float *cos_sin;
+    const int32_t *positions;
+    int32_t max_pos, rot_dim, rot_offset, interleaved;
+} attn_rope_t;
+
+/*
+ * attn_append_kv with the position rotation on the way: the keys are rotated
+ * before they are stored, and the queries in the same launch, so that the step
+ * from the projections to attn_run_paged is this one kernel.
+ *   rope         the rotation (host struct, copied by the call).
+ *   q, q_out     bf16 [total_q][Hq][Dqk], contiguous: q_out receives the rows of
+ *                q rotated, other dims copied.  q_out == q rotates in place
+ *                (only the rotated dims are then touched); otherwise the two
+ *                must not overlap.  Both NULL: no queries.
+ *   others       as for attn_append_kv (any cache type of the plan).
+ * The rotation is fp32, every product, sum and difference rounded to nearest on
+ * its own, from the bf16 inputs and the fp32 table; the result is rounded once,
+ * to bf16 (q_out, BF16 caches) or as attn_append_kv stores an fp32 value (FP8
+ * and 4-bit caches).  Dims that are not rotated keep their bits in q_out and in
+ * BF16 caches.  V is not rotated.
+ * A position outside [0, max_pos) is not looked up: nothing of that token is
+ * written (neither K, V nor its q_out rows) and bit 3 of the plan's device error
+ * word is set.  Bad page ids and lengths are skipped as by attn_append_kv (bits
+ * 0 and 2); that token's q_out rows are still written if its position is good.
+ * Runs on `stream`; no allocation, no synchronisation; can be captured.
+ * Errors: INVALID_ARG (also pointers that are not 16-byte aligned, q and q_out
+ * not given together, a range outside the head), UNSUPPORTED (rot_dim or
+ * rot_offset not a multiple of 16 or 8), CUDA.
+ */
+attn_status_t attn_append_kv_rope(attn_plan_t plan, const attn_rope_t *rope, const void *q,
+                                  const void *k_new, const void *v_new, void *q_out,
+                                  void *k_cache, void *v_cache, const int32_t *page_table,
+                                  const int32_t *seq_lens, const int32_t *qo_indptr,
+                                  float k_scale, float v_scale, void *stream);
+
+/*
+ * Read cached rows back as bf16, the values a cache of any type stands for.
+ *   kv_indptr    device int32 [B+1], kv_indptr[0] = 0, non-decreasing: output
+ *                rows [kv_indptr[b], kv_indptr[b+1]) are the last so many
+ *                positions of request b, in order (with qo_indptr: its new
+ *                tokens; with the lengths' prefix sums: all its keys).
+ *   rows         kv_indptr[B]; rows past it are written as zeros (bit 2).
+ *   seq_lens     device int32 [B], any lengths within the page table's rows.
+ *   k_out, v_out bf16 [rows][Hkv][Dqk] and [rows][Hkv][128], contiguous.
+ *   k_scale, v_scale  as for attn_append_kv.
+ * BF16 rows are copied; FP8 and 4-bit values are decoded exactly, multiplied by
+ * the tensor's scale in fp32 and rounded to bf16.  A position before 0 or outside
+ * its page-table row is written as zeros and sets bit 2 of the plan's device
+ * error word, a page id outside the pool likewise with bit 0.
+ * Runs on `stream`; no allocation, no synchronisation; can be captured.
+ * Errors: INVALID_ARG (also pointers that are not 16-byte aligned), CUDA.
+ */
+attn_status_t attn_read_kv(attn_plan_t plan, const void *k_cache, const void *v_cache,
+                           const int32_t *page_table, const int32_t *seq_lens,
+                           const int32_t *kv_indptr, int64_t rows, void *k_out, void *v_out,
+                           float k_scale, float v_scale, void *stream);
 
 /*
  * Size of the library-owned scratch used by attn_run_paged_no_workspace.
@@ -292,7 +391,8 @@ attn_status_t attn_plan_destroy(attn_plan_t plan);
  * id outside [0, num_pages) was met.  Bit 1: a pipeline wait of the attention
  * kernel gave up after its time limit (the affected rows are not valid).
  * Bit 2: a run length outside a replayable plan's bounds (clamped), or an
- * appended position outside its page-table row (skipped).  The workspace
+ * appended or read position outside its page-table row (skipped, or read as
+ * zeros).  Bit 3: a rotation position outside its table (skipped).  The workspace
  * argument is unused and may be NULL.
  */
 attn_status_t attn_get_device_error(attn_plan_t plan, void *workspace, int32_t *err);

@@ -58,6 +58,100 @@ def bf16_to_f32(bits: np.ndarray) -> np.ndarray:
     return (np.asarray(bits, np.uint16).astype(np.uint32) << 16).view(np.float32)
 
 
+# the eight E2M1 magnitudes, in code order (even codes have an even mantissa)
+_E2M1_VALUES = np.array([m * 0.5 if e == 0 else (1 + m * 0.5) * 2.0 ** (e - 1)
+                         for e in range(4) for m in range(2)], dtype=np.float64)
+
+
+def e2m1_encode(x: float) -> int:
+    """Nearest E2M1 code to x, ties to even mantissa, saturating at 6."""
+    sign = 8 if np.signbit(x) else 0
+    d = np.abs(_E2M1_VALUES - min(abs(float(x)), 6.0))
+    best = np.flatnonzero(d == d.min())
+    if best.size > 1:
+        best = best[(best & 1) == 0]
+    return sign | int(best[0])
+
+
+def fp4_row(x: np.ndarray, scale: float) -> np.ndarray:
+    """One 4-bit cache row (codes, block scales, zero padding) of the fp32 row x:
+    y = x / scale; per 16 values the block scale E4M3(max|y| / 6), then the E2M1
+    code of y / block scale; every quotient the fp32 IEEE one."""
+    d = x.size
+    out = np.zeros((d // 2 + d // 16 + 15) // 16 * 16, np.uint8)
+    with np.errstate(over="ignore", invalid="ignore"):
+        y = (x.astype(np.float32) / np.float32(scale)).astype(np.float32)
+        for c in range(d // 16):
+            blk = y[16 * c:16 * c + 16]
+            code = e4m3_encode(np.abs(blk).max() / np.float32(6.0))
+            out[d // 2 + c] = code
+            s = np.float32(e4m3_decode(code))
+            if np.isnan(s):                      # the codes under a NaN scale mean nothing
+                continue
+            q = blk / s if s > 0 else np.copysign(np.float32(0), blk)
+            codes = [e2m1_encode(v) for v in q]
+            for i in range(8):
+                out[8 * c + i] = codes[2 * i] | codes[2 * i + 1] << 4
+    return out
+
+
+def fp4_row_values(row: np.ndarray, d: int) -> np.ndarray:
+    """The float64 values a 4-bit row stands for, from the format's bit fields."""
+    out = np.empty(d)
+    for i in range(d):
+        code = (int(row[i // 2]) >> (4 * (i % 2))) & 15
+        v = _E2M1_VALUES[code & 7] * (-1.0 if code & 8 else 1.0)
+        out[i] = v * e4m3_decode(int(row[d // 2 + i // 16]))
+    return out
+
+
+def rotate(x: np.ndarray, cos_sin: np.ndarray, rot: int, off: int, interleaved: bool) -> np.ndarray:
+    """fp32 rows x [..., d] rotated by the table rows cos_sin [..., rot]: pair i is dims
+    (off + i, off + rot/2 + i), or (off + 2i, off + 2i + 1); every product, sum and
+    difference is one fp32 operation."""
+    x = np.array(x, np.float32)
+    half = rot // 2
+    c, s = np.float32(cos_sin[..., :half]), np.float32(cos_sin[..., half:])
+    i = np.arange(half)
+    a, b = (off + 2 * i, off + 2 * i + 1) if interleaved else (off + i, off + half + i)
+    x1, x2 = x[..., a].copy(), x[..., b].copy()
+    x[..., a] = (x1 * c) - (x2 * s)
+    x[..., b] = (x2 * c) + (x1 * s)
+    return x
+
+
+def f32_to_bf16(x: np.ndarray) -> np.ndarray:
+    """bf16 bits of fp32 values, nearest even."""
+    u = np.ascontiguousarray(x, np.float32).view(np.uint32).astype(np.uint64)
+    r = ((u + 0x7FFF + ((u >> 16) & 1)) >> 16).astype(np.uint16)
+    return np.where(np.isnan(x), np.uint16(0x7FFF), r)
+
+
+def append_rows(rows_k, rows_v, k_cache, v_cache, page_table, seq_lens, qo_indptr, kv_dtype: str,
+                k_scale: float = 1.0, v_scale: float = 1.0):
+    """append_kv for fp32 rows [total_q, Hkv, D] (rotated keys) into a cache of any
+    type; returns the caches after it."""
+    kc, vc = np.array(k_cache, copy=True), np.array(v_cache, copy=True)
+    num_pages, P = kc.shape[0], kc.shape[1]
+
+    def stored(row, scale):                      # [Hkv, D] fp32 -> [Hkv, row]
+        if kv_dtype == "bf16":
+            return f32_to_bf16(row)
+        if kv_dtype == "fp8":
+            return np.vectorize(e4m3_encode, otypes=[np.uint8])(row / np.float32(scale))
+        return np.stack([fp4_row(r, scale) for r in row])
+
+    for b in range(len(seq_lens)):
+        q0, q1 = int(qo_indptr[b]), int(qo_indptr[b + 1])
+        for t in range(q0, q1):
+            i = int(seq_lens[b]) - (q1 - t)
+            page = int(page_table[b][i // P])
+            if 0 <= page < num_pages:
+                kc[page, i % P] = stored(rows_k[t], k_scale)
+                vc[page, i % P] = stored(rows_v[t], v_scale)
+    return kc, vc
+
+
 def append_kv(k_new, v_new, k_cache, v_cache, page_table, seq_lens, qo_indptr,
               kv_dtype: str, k_scale: float = 1.0, v_scale: float = 1.0):
     """Returns (k_cache, v_cache) after the append, as new arrays, and the number
