@@ -151,7 +151,9 @@ attn_status_t upload(attn_plan_s *p) {
     e = cudaMemcpy(p->dev.seq_bounds, hp.seq_lens.data(), hp.seq_lens.size() * sizeof(int32_t),
                    cudaMemcpyHostToDevice);
   if (e == cudaSuccess) e = cudaMemset(p->dev.err, 0, e_bytes);
-  if (e == cudaSuccess) e = hp.prefill ? akp::prepare_attn_prefill(hp) : akp::prepare_attn_tc(hp);
+  if (e == cudaSuccess) e = hp.prefill    ? akp::prepare_attn_prefill(hp)
+        : hp.fp4_rows ? akp::prepare_attn_fp4(hp)
+                      : akp::prepare_attn_tc(hp);
   if (e != cudaSuccess) {
     free_device(p);
     return ATTN_ERR_CUDA;
@@ -177,6 +179,7 @@ static attn_status_t plan_host(const attn_problem_t *problem, int32_t num_sms, b
     return st;
   }
   p->host.use_tma = akp::tc_tma_page_size(problem->page_size, problem->num_pages);
+  p->host.fp4_rows = akp::fp4_register_rows(p->host);
   *plan = p;
   return ATTN_OK;
 }
@@ -358,8 +361,9 @@ static attn_status_t run_impl(attn_plan_t plan, int phases, bool allow_stage, co
     if (akp::launch_kv_stage(sa, st) != cudaSuccess) return ATTN_ERR_CUDA;
   }
   if (phases & 1) {
-    const cudaError_t le = hp.prefill ? akp::launch_attn_prefill(hp, a, staged ? &stage_maps : nullptr, st)
-                                      : akp::launch_attn_tc(hp, a, maps, st);
+    const cudaError_t le = hp.prefill    ? akp::launch_attn_prefill(hp, a, staged ? &stage_maps : nullptr, st)
+                           : hp.fp4_rows ? akp::launch_attn_fp4(hp, a, maps, st)
+                                         : akp::launch_attn_tc(hp, a, maps, st);
     if (le != cudaSuccess) return ATTN_ERR_CUDA;
   }
   if ((phases & 2) && akp::launch_merge(hp, a, st) != cudaSuccess) return ATTN_ERR_CUDA;

@@ -1,0 +1,682 @@
+// Split-KV attention over a 4-bit cache for row blocks of at most 16 query rows
+// (decode, and a few draft tokens on small groups).
+//
+// At these sizes a key's 192 bytes feed at most 16 rows, and what bounds the
+// tcgen05 kernel (attn_tc.cu) is not the tensor pipe but shared memory: its
+// operands have to be 16-bit tiles there, so every 4-bit tile would be read,
+// written four times as wide, and read again (128 KB of shared-memory traffic
+// for 12 KB of cache: ~1000 cycles a 64-key tile, where HBM delivers one in
+// ~580).  Here the codes go from the TMA ring straight into registers, are
+// widened there, and feed register-operand MMAs (m16n8k16, fp16, fp32
+// accumulation).  Both products are computed transposed, so that the padded
+// side is the 8-row granule and not 64 rows of MMA:
+//   S^T (keys x rows) = K (16 keys x 16 dims) . Q^T (16 dims x 8 rows),
+//   O^T (dv x rows)   = V^T (16 dv x 16 keys) . P^T (16 keys x 8 rows).
+// The order of a contraction's index is free, so lanes take what is
+// contiguous in the cache: lane (g, t) (g = lane / 4, t = lane % 4) of a K
+// operand owns the whole 16-code blocks t, t + 4, t + 8 of keys g and g + 8
+// (Q's fragments use the same order), and of a V operand the block g of keys 2t,
+// 2t + 1, 2t + 8, 2t + 9; a lane needs one scale per 8-byte load.  V^T wants two
+// keys in one register: the nibbles of two keys are interleaved into bytes
+// first (one shift and one bit-select per four pairs), and the byte's one
+// conversion then yields the pair.  P^T comes out of S^T's accumulators with an
+// 8x8 transpose (movmatrix).
+//
+// Codes times scales are exact in fp16 (e2m1.cuh).  Q rows are scaled by the power
+// of two that puts the row's largest |q| in [2^14, 2^15) (exact down to 2^-31 of
+// it) and the scores divided by it in fp32.  P is held in fp16 relative to the
+// running maximum times 2^7, so that weights down to 2^-21 of the maximum keep
+// 11 bits and none above 2^-32 is lost; the maximum may grow by 2^8 before O is
+// rescaled (P <= 2^15).  Row sums are fp32, of the weights before rounding.
+//
+// Warps: kConsumers consumer warps, then the producer warps.  A unit of work is
+// half a 64-key tile (32 keys); unit u of the CTA belongs to consumer u %
+// kConsumers, which keeps running maxima, sums and O of its own for the whole
+// segment, so nothing is shared between tiles.  At the end of a segment the
+// consumers' partials are combined through shared memory.  With page sizes TMA
+// can tile, one producer warp looks up to 32 pages at once and issues a K and
+// a V box per page piece; otherwise four or eight producer warps gather rows
+// through registers, a tile per warp in flight.
+// Every wait is bounded in time, as in attn_tc.cu.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "e2m1.cuh"
+#include "kernels.hpp"
+#include "tc_common.cuh"
+
+namespace akp {
+namespace {
+
+constexpr int kN = kKeyTile;
+constexpr int kConsumers = 8;
+constexpr int kUnitKeys = 32;
+constexpr int kUnits = kN / kUnitKeys;        // units per tile
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kGrow = 8.0f;                 // base-2 growth of a maximum before O is rescaled
+constexpr float kLift = 7.0f;                 // P is held times 2^kLift
+constexpr int kCombStride = 130;              // floats per row of the combine buffer (see flush)
+
+template <int DQK>
+struct Tile {
+  static constexpr int kKrow = e2m1_row_bytes(DQK), kVrow = e2m1_row_bytes(kDv);
+  static constexpr int kKBytes = kN * kKrow;
+  static constexpr int kBytes = kKBytes + kN * kVrow;       // 12 KB at 192
+  static constexpr int kChunks = (kKrow + kVrow) / 16;      // 16-byte chunks per key
+};
+
+template <int DQK, int NB, bool TMA>
+struct Cfg {
+  static constexpr int kProducers = TMA ? 1 : NB == 1 ? 8 : 4;
+  static constexpr int kThreads = (kConsumers + kProducers) * 32;
+  static constexpr int kStages = NB == 1 ? 14 : 11;
+  static constexpr int kOffComb = kStages * Tile<DQK>::kBytes;
+  static constexpr int kSmem = kOffComb + kConsumers * NB * 8 * kCombStride * 4 + 1024;
+  static_assert(kSmem + 2048 <= 227 * 1024, "shared memory layout too large");
+};
+
+struct FBars {
+  uint64_t full[16], empty[16];
+  uint64_t sync;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&h);
+}
+
+// c (16 x 8, fp32) += a (16 x 16, fp16) . b (16 x 8, fp16)
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8x8 transpose of 16-bit elements held as one row per four lanes.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t lo16) {
+  uint32_t p;
+  asm("{\n .reg .b16 l, u;\n mov.b32 {l, u}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}\n" : "=r"(p) : "r"(lo16));
+  return p;
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int c1, int c2, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(c1), "r"(c2), "r"(tc::smem_u32(bar))
+      : "memory");
+}
+
+// Walks the CTA's tiles in order (as in attn_tc.cu).
+struct Walk {
+  const SegDesc *segs;
+  const BlockDesc *blocks;
+  int seg, seg_end, tile;
+  SegDesc sd;
+  BlockDesc bd;
+  __device__ void init(const RunArgs &a, const CtaHead &h) {
+    segs = a.segs;
+    blocks = a.blocks;
+    seg = h.seg_begin;
+    seg_end = h.seg_end;
+    sd = h.seg;
+    bd = h.blk;
+    tile = sd.tile_begin;
+  }
+  __device__ void next() {
+    if (++tile == sd.tile_end && seg + 1 < seg_end) {
+      ++seg;
+      sd = segs[seg];
+      bd = blocks[sd.block];
+      tile = sd.tile_begin;
+    }
+  }
+};
+
+template <int DQK, int NB, bool TMA>
+__global__ void __launch_bounds__(Cfg<DQK, NB, TMA>::kThreads, 1)
+    attn_fp4_kernel(const RunArgs args, const __grid_constant__ TmaMaps maps) {
+  const RunArgs a = args;
+  using C = Cfg<DQK, NB, TMA>;
+  using T = Tile<DQK>;
+  constexpr int NS = C::kStages;
+  constexpr int NJ = DQK / 64;                 // K blocks per lane
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t *smem = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
+  __shared__ FBars bars;
+  __shared__ int abort_flag;
+  __shared__ float sm_m[kConsumers][NB * 8], sm_l[kConsumers][NB * 8];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // programmatic dependent: see attn_tc.cu
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  const CtaHead head = a.cta_heads[blockIdx.x];
+  if (head.seg_begin >= head.seg_end) return;
+  const int total = head.total;
+  if (tid == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < NS; ++s) {
+      tc::mbar_init(&bars.full[s], 1);
+      tc::mbar_init(&bars.empty[s], kUnits);
+    }
+    tc::mbar_init(&bars.sync, kConsumers);
+    tc::fence_mbar_init();
+  }
+  __syncthreads();
+
+  if (warp >= kConsumers) {
+    Walk cur;
+    cur.init(a, head);
+    if constexpr (TMA) {
+      // ---------------------------------------------------------- TMA producer
+      // One lane per (tile, box): up to 32 page lookups in one round trip.
+      const int box = a.page_size >= kN ? kN : a.page_size;
+      const int nbox = kN / box, batch = 32 / nbox;
+      const int oob = a.num_pages * a.page_size;      // first slot past the pool: zero fill
+      const int mine = lane / nbox, bx = lane % nbox;
+      const uint32_t sbase = tc::smem_u32(smem);
+      bool ok = true;
+      for (int k0 = 0; k0 < total && ok; k0 += batch) {
+        const int cnt = min(batch, total - k0);
+        int slot = oob, g = 0, pt_idx = -1, j = 0, b = 0;
+        for (int u = 0; u < cnt; ++u, cur.next()) {
+          if (u == mine) {
+            j = cur.tile * kN + bx * box;
+            g = cur.bd.g;
+            b = cur.bd.b;
+            if (j + box > cur.bd.klo && j < cur.bd.khi) pt_idx = j / a.page_size;
+          }
+        }
+        if (pt_idx >= 0) {
+          const int32_t page = __ldg(a.page_table + (int64_t)b * a.pt_stride + pt_idx);
+          if (page >= 0 && page < a.num_pages)
+            slot = page * a.page_size + j % a.page_size;
+          else
+            atomicOr(a.err, 1);
+        }
+        for (int u = 0; u < cnt; ++u) {
+          const int k = k0 + u, s = k % NS;
+          if (k >= NS && !tc::mbar_wait_warp(&bars.empty[s], ((k / NS) - 1) & 1, &abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) tc::mbar_arrive_expect_tx(&bars.full[s], T::kBytes);
+          __syncwarp();
+          if (u == mine) {
+            const uint32_t dst = sbase + s * T::kBytes;
+            tma_load_3d(dst + bx * box * T::kKrow, &maps.k, g, slot, &bars.full[s]);
+            tma_load_3d(dst + T::kKBytes + bx * box * T::kVrow, &maps.v, g, slot, &bars.full[s]);
+          }
+        }
+      }
+    } else {
+      // ---------------------------------------------------------- gather
+      // Producer p takes tiles p, p + kProducers, ...; two lanes per key, 16
+      // keys at a time, each lane half of the key's 16-byte chunks (K's, then
+      // V's).  The slots of its next tile are looked up before the current
+      // tile's rows are waited for.
+      constexpr int PW = C::kProducers, HC = T::kChunks / 2;
+      static_assert(T::kChunks % 2 == 0, "two lanes share a key's chunks");
+      const int p = warp - kConsumers;
+      const int part = lane & 1;
+      const uint8_t *kc = static_cast<const uint8_t *>(a.k_cache);
+      const uint8_t *vc = static_cast<const uint8_t *>(a.v_cache);
+      for (int i = 0; i < p && i < total; ++i) cur.next();
+      int64_t slot[4];
+      int g = 0;
+      auto lookup = [&]() {
+        g = cur.bd.g;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int j = cur.tile * kN + q * 16 + (lane >> 1);
+          slot[q] = -1;
+          if (j >= cur.bd.klo && j < cur.bd.khi) {
+            const int32_t page = __ldg(a.page_table + (int64_t)cur.bd.b * a.pt_stride + j / a.page_size);
+            if (page >= 0 && page < a.num_pages)
+              slot[q] = (int64_t)page * a.page_size + j % a.page_size;
+            else
+              atomicOr(a.err, 1);
+          }
+        }
+      };
+      if (p < total) lookup();
+      for (int k = p; k < total; k += PW) {
+        uint4 r[4][HC];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t row = (slot[q] >= 0 ? slot[q] : 0) * a.hkv + g;
+          const uint4 *krow = reinterpret_cast<const uint4 *>(kc + row * T::kKrow);
+          const uint4 *vrow = reinterpret_cast<const uint4 *>(vc + row * T::kVrow);
+#pragma unroll
+          for (int u = 0; u < HC; ++u) {
+            const int c = part * HC + u;
+            r[q][u] = make_uint4(0u, 0u, 0u, 0u);
+            if (slot[q] >= 0) r[q][u] = __ldg(c < T::kKrow / 16 ? krow + c : vrow + (c - T::kKrow / 16));
+          }
+        }
+        if (k + PW < total) {
+          for (int i = 0; i < PW; ++i) cur.next();
+          lookup();
+        }
+        const int s = k % NS;
+        if (k >= NS && !tc::mbar_wait_warp(&bars.empty[s], ((k / NS) - 1) & 1, &abort_flag)) break;
+        uint8_t *dst = smem + s * T::kBytes;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int key = q * 16 + (lane >> 1);
+#pragma unroll
+          for (int u = 0; u < HC; ++u) {
+            const int c = part * HC + u;
+            uint8_t *d = c < T::kKrow / 16 ? dst + key * T::kKrow + c * 16
+                                           : dst + T::kKBytes + key * T::kVrow + (c - T::kKrow / 16) * 16;
+            *reinterpret_cast<uint4 *>(d) = r[q][u];
+          }
+        }
+        tc::mbar_arrive_warp(&bars.full[s]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ consumers
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t qf[NB][NJ * 4][2];
+    float o[8][NB][4];
+    float m[NB][2], l[NB][2], sc[NB][2];
+    int row_lo[NB][2], row_hi[NB][2];
+    uint32_t sync_phase = 0;
+    auto group_sync = [&]() -> bool {
+      tc::mbar_arrive_warp(&bars.sync);
+      const bool ok = __all_sync(0xffffffffu, tc::mbar_wait_spin(&bars.sync, sync_phase, &abort_flag));
+      sync_phase ^= 1;
+      return ok;
+    };
+    SegDesc sd = head.seg;
+    BlockDesc bd = head.blk;
+    int k0 = 0;                                // the segment's first tile among the CTA's
+    bool alive = true;
+    for (int seg = head.seg_begin; seg < head.seg_end && alive; ++seg) {
+      if (seg > head.seg_begin) {
+        sd = a.segs[seg];
+        bd = a.blocks[sd.block];
+      }
+      const int u_end = (k0 + sd.tile_end - sd.tile_begin) * kUnits;
+      // this warp's first unit of the segment
+      int u = k0 * kUnits;
+      u += (warp - u % kConsumers + kConsumers) % kConsumers;
+      const bool has = u < u_end;
+      // ---- rows: Q fragments (scaled to fp16), score scales, visible keys
+      const int i_first = bd.L - bd.n + bd.row0 / a.group;
+      const int i_last = bd.L - bd.n + (bd.row0 + bd.nrows - 1) / a.group;
+      // keys every row sees
+      const int all_lo = a.window > 0 ? max(0, i_last - a.window + 1) : 0, all_hi = i_first + 1;
+      if (has) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const int r = nb * 8 + g;
+          uint32_t e = 0;
+          const bool live = r < bd.nrows;
+          const int flat = bd.row0 + (live ? r : 0);
+          const uint2 *src = reinterpret_cast<const uint2 *>(
+              static_cast<const uint16_t *>(a.q) +
+              ((int64_t)(bd.tok0 + flat / a.group) * a.hq + bd.g * a.group + flat % a.group) * DQK);
+#pragma unroll
+          for (int i = 0; i < NJ * 4; ++i) {
+            const uint2 v = live ? __ldg(src + (t + 4 * (i >> 2)) * 4 + (i & 3)) : make_uint2(0u, 0u);
+            qf[nb][i][0] = v.x;
+            qf[nb][i][1] = v.y;
+            e = max(e, max(max((v.x >> 7) & 0xFFu, (v.x >> 23) & 0xFFu),
+                           max((v.y >> 7) & 0xFFu, (v.y >> 23) & 0xFFu)));
+          }
+          e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
+          e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
+          const int sh = min(141 - (int)e, 126);
+          const float f = __int_as_float((sh + 127) << 23);
+#pragma unroll
+          for (int i = 0; i < NJ * 4; ++i)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t w = qf[nb][i][x];
+              qf[nb][i][x] = f16_pair(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
+            }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int shr = __shfl_sync(0xffffffffu, sh, (2 * t + x) * 4);
+            sc[nb][x] = a.scale_log2 * __int_as_float((127 - shr) << 23);
+            // rows past the block have zero queries and are never written:
+            // any range does for them
+            const int rr = min(nb * 8 + 2 * t + x, bd.nrows - 1);
+            const int i = bd.L - bd.n + (bd.row0 + rr) / a.group;
+            row_hi[nb][x] = i + 1;
+            row_lo[nb][x] = a.window > 0 ? max(0, i - a.window + 1) : 0;
+            m[nb][x] = -INFINITY;
+            l[nb][x] = 0.f;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[i][nb][x] = 0.f;
+      }
+#pragma unroll 1
+      for (; u < u_end; u += kConsumers) {
+        const int k = u / kUnits, s = k % NS;
+        const int key0 = (sd.tile_begin + k - k0) * kN + (u % kUnits) * kUnitKeys;
+        if (!tc::mbar_wait_warp(&bars.full[s], (k / NS) & 1, &abort_flag)) {
+          alive = false;
+          break;
+        }
+        const uint8_t *kt = smem + s * T::kBytes + (u % kUnits) * kUnitKeys * T::kKrow;
+        const uint8_t *vt = smem + s * T::kBytes + T::kKBytes + (u % kUnits) * kUnitKeys * T::kVrow;
+        // ---- S^T = K . Q^T for 2 x 16 keys
+        float sacc[2][NB][4];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) sacc[mt][nb][x] = 0.f;
+          const uint8_t *r0 = kt + (mt * 16 + g) * T::kKrow, *r1 = r0 + 8 * T::kKrow;
+          const uint4 w0 = *reinterpret_cast<const uint4 *>(r0 + DQK / 2);      // the rows' scales
+          const uint4 w1 = *reinterpret_cast<const uint4 *>(r1 + DQK / 2);
+          const uint32_t ws0[3] = {w0.x, w0.y, w0.z}, ws1[3] = {w1.x, w1.y, w1.z};
+#pragma unroll
+          for (int j = 0; j < NJ; ++j) {
+            const uint2 c0 = *reinterpret_cast<const uint2 *>(r0 + 8 * (t + 4 * j));
+            const uint2 c1 = *reinterpret_cast<const uint2 *>(r1 + 8 * (t + 4 * j));
+            // byte t of each row's scale word -> both rows' scales, doubled up
+            const uint32_t p2 = e4m3x2_to_f16(__byte_perm(ws0[j], ws1[j], t | (t + 4) << 4));
+            const uint32_t s0 = __byte_perm(p2, 0u, 0x1010), s1 = __byte_perm(p2, 0u, 0x3232);
+            uint32_t h0[8], h1[8];
+            {
+              uint32_t x[4];
+              e2m1x8_to_f16(c0.x, x);
+              h0[0] = x[0], h0[1] = x[1], h0[2] = x[2], h0[3] = x[3];
+              e2m1x8_to_f16(c0.y, x);
+              h0[4] = x[0], h0[5] = x[1], h0[6] = x[2], h0[7] = x[3];
+              e2m1x8_to_f16(c1.x, x);
+              h1[0] = x[0], h1[1] = x[1], h1[2] = x[2], h1[3] = x[3];
+              e2m1x8_to_f16(c1.y, x);
+              h1[4] = x[0], h1[5] = x[1], h1[6] = x[2], h1[7] = x[3];
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t a0 = mul_f16x2(h0[2 * q], s0), a2 = mul_f16x2(h0[2 * q + 1], s0);
+              const uint32_t a1 = mul_f16x2(h1[2 * q], s1), a3 = mul_f16x2(h1[2 * q + 1], s1);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+                mma16816(sacc[mt][nb], a0, a1, a2, a3, qf[nb][4 * j + q][0], qf[nb][4 * j + q][1]);
+            }
+          }
+        }
+        // ---- softmax: base-2 scores, the running maximum, P in fp16
+        const bool full = key0 >= all_lo && key0 + kUnitKeys <= all_hi;
+        float lm[NB][2];
+        bool grow = false;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float v = sacc[mt][nb][2 * h + x] * sc[nb][x];
+                if (!full) {
+                  const int j = key0 + mt * 16 + h * 8 + g;
+                  if (j < row_lo[nb][x] || j >= row_hi[nb][x]) v = -INFINITY;
+                }
+                sacc[mt][nb][2 * h + x] = v;
+                mx = fmaxf(mx, v);
+              }
+            lm[nb][x] = mx;
+            grow |= mx > m[nb][x] + kGrow;
+          }
+        if (__any_sync(0xffffffffu, grow)) {
+          float alpha[NB][2];
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              float mx = lm[nb][x];
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+              const bool up = mx > m[nb][x] + kGrow;       // also from -inf
+              alpha[nb][x] = up ? ex2(m[nb][x] - mx) : 1.f;
+              if (up) m[nb][x] = mx;
+              l[nb][x] *= alpha[nb][x];
+            }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) o[i][nb][x] *= alpha[nb][x & 1];
+        }
+        uint32_t pf[2][NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const float n0 = m[nb][0] == -INFINITY ? 0.f : kLift - m[nb][0];
+          const float n1 = m[nb][1] == -INFINITY ? 0.f : kLift - m[nb][1];
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float p0 = ex2(sacc[mt][nb][2 * h] + n0), p1 = ex2(sacc[mt][nb][2 * h + 1] + n1);
+              l[nb][0] += p0;
+              l[nb][1] += p1;
+              pf[mt][nb][h] = transpose8(f16_pair(p0, p1));
+            }
+        }
+        // ---- O^T += V^T . P^T
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          const uint8_t *vr = vt + (mt * 16 + 2 * t) * T::kVrow + 8 * g;
+          const uint8_t *vs = vt + (mt * 16 + 2 * t) * T::kVrow + kDv / 2 + g;
+          uint2 c[4];                                      // keys 2t, 2t + 1, 2t + 8, 2t + 9
+          uint32_t sb[4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int kk = (y & 1) + 8 * (y >> 1);
+            c[y] = *reinterpret_cast<const uint2 *>(vr + kk * T::kVrow);
+            sb[y] = vs[kk * T::kVrow];
+          }
+          if (!full) {
+            // keys outside the block's range may hold anything: NaN scales to zero
+            const int j0 = key0 + mt * 16 + 2 * t;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int j = j0 + (y & 1) + 8 * (y >> 1);
+              if (j < bd.klo || j >= bd.khi) sb[y] = 0u;
+            }
+          }
+          const uint32_t sA = e4m3x2_to_f16(sb[0] | sb[1] << 8), sB = e4m3x2_to_f16(sb[2] | sb[3] << 8);
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {                    // eight codes of each key
+            const uint32_t k0w = w ? c[0].y : c[0].x, k1w = w ? c[1].y : c[1].x;
+            const uint32_t k2w = w ? c[2].y : c[2].x, k3w = w ? c[3].y : c[3].x;
+            constexpr uint32_t L4 = 0x0F0F0F0Fu;
+            uint32_t eA[4], oA[4], eB[4], oB[4];
+            e2m1x8_to_f16((k0w & L4) | ((k1w << 4) & ~L4), eA);      // even codes, (key, key + 1)
+            e2m1x8_to_f16(((k0w >> 4) & L4) | (k1w & ~L4), oA);      // odd codes
+            e2m1x8_to_f16((k2w & L4) | ((k3w << 4) & ~L4), eB);
+            e2m1x8_to_f16(((k2w >> 4) & L4) | (k3w & ~L4), oB);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t a0 = mul_f16x2(eA[i], sA), a1 = mul_f16x2(oA[i], sA);
+              const uint32_t a2 = mul_f16x2(eB[i], sB), a3 = mul_f16x2(oB[i], sB);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb)
+                mma16816(o[4 * w + i][nb], a0, a1, a2, a3, pf[mt][nb][0], pf[mt][nb][1]);
+            }
+          }
+        }
+        if (TMA) tc::fence_proxy_async_smem();   // the refill must not overtake these reads
+        tc::mbar_arrive_warp(&bars.empty[s]);
+      }
+      if (!alive) break;
+
+      // ---- end of the segment: this warp's partial, then the common result.
+      // Row r of the buffer starts at r * 130 and the pair of dv (16g + 2i, + 1)
+      // sits at 16g + ((2i + 2(g / 2)) & 15): the 16 lanes of a half-warp write 32
+      // different banks.
+      float *comb = reinterpret_cast<float *>(smem + C::kOffComb);
+      if (has) {
+        float *dst = comb + warp * (NB * 8 * kCombStride);
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            float sum = l[nb][x];
+            sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+            const int r = nb * 8 + 2 * t + x;
+            if (g == 0) {
+              sm_m[warp][r] = m[nb][x];
+              sm_l[warp][r] = sum;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<float2 *>(dst + r * kCombStride + 16 * g + ((2 * i + 2 * (g >> 1)) & 15)) =
+                  make_float2(o[i][nb][x], o[i][nb][2 + x]);
+          }
+      } else if (lane < NB * 8) {
+        sm_m[warp][lane] = -INFINITY;
+      }
+      if (!group_sync()) break;
+      // warp w combines rows w and w + 8: lane owns dv 4 lane .. 4 lane + 3
+      for (int r = warp; r < bd.nrows; r += kConsumers) {
+        const int flat = bd.row0 + r;
+        const int tok = bd.tok0 + flat / a.group, h = bd.g * a.group + flat % a.group;
+        const float sink2 = a.sinks && bd.num_splits == 1 ? __ldg(a.sinks + h) * kLog2e : -INFINITY;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, sm_m[w][r]);
+        float Lsum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int gg = lane >> 2;
+        const int p0 = 16 * gg + ((4 * (lane & 3) + 2 * (gg >> 1)) & 15);
+        const int p1 = 16 * gg + ((4 * (lane & 3) + 2 + 2 * (gg >> 1)) & 15);
+        if (M != -INFINITY) {
+#pragma unroll
+          for (int w = 0; w < kConsumers; ++w) {
+            const float mw = sm_m[w][r];
+            if (mw == -INFINITY) continue;             // nothing written by this warp
+            const float f = exp2f(mw - M);
+            const float *src = comb + (w * NB * 8 + r) * kCombStride;
+            const float2 x = *reinterpret_cast<const float2 *>(src + p0);
+            const float2 y = *reinterpret_cast<const float2 *>(src + p1);
+            Lsum += f * sm_l[w][r];
+            acc.x += f * x.x;
+            acc.y += f * x.y;
+            acc.z += f * y.x;
+            acc.w += f * y.y;
+          }
+        }
+        // O and the sums are both 2^kLift times what they stand for
+        const float inv_lift = 0.0078125f;              // 2^-kLift
+        if (bd.num_splits == 1) {
+          const float MM = fmaxf(M, sink2);
+          float scale = 0.f, lse = -INFINITY;
+          if (MM != -INFINITY) {
+            const float fm = exp2f(M - MM) * inv_lift;
+            const float Z = Lsum * fm + exp2f(sink2 - MM);
+            scale = fm * a.v_scale / Z;
+            lse = (MM + log2f(Z)) * kLn2;
+          }
+          __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * scale, acc.y * scale);
+          __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * scale, acc.w * scale);
+          uint2 w2;
+          w2.x = *reinterpret_cast<uint32_t *>(&lo);
+          w2.y = *reinterpret_cast<uint32_t *>(&hi);
+          *(reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + ((int64_t)tok * a.hq + h) * kDv) + lane) = w2;
+          if (a.lse_out && lane == 0) a.lse_out[(int64_t)tok * a.hq + h] = lse;
+        } else {
+          const int prow = bd.part_row_base + sd.split * bd.nrows + r;
+          const float scale = Lsum == 0.f ? 0.f : a.v_scale / Lsum;      // a NaN stays one
+          reinterpret_cast<float4 *>(a.part_o + (int64_t)prow * kDv)[lane] =
+              make_float4(acc.x * scale, acc.y * scale, acc.z * scale, acc.w * scale);
+          if (lane == 0) a.part_lse[prow] = Lsum == 0.f ? -INFINITY : M + log2f(Lsum * inv_lift);
+        }
+      }
+      k0 += sd.tile_end - sd.tile_begin;
+      // the buffer is free for the next segment once every warp has read it
+      if (seg + 1 < head.seg_end && !group_sync()) break;
+    }
+  }
+  __syncthreads();
+  if (tid == 0 && abort_flag) atomicOr(a.err, 2);
+}
+
+template <int DQK, int NB, bool TMA>
+cudaError_t launch_one(const HostPlan &hp, const RunArgs &a, const TmaMaps &m, cudaStream_t st) {
+  using C = Cfg<DQK, NB, TMA>;
+  return launch_dependent(attn_fp4_kernel<DQK, NB, TMA>, dim3(hp.num_ctas), dim3(C::kThreads), C::kSmem, st, a, m);
+}
+
+template <int DQK, int NB, bool TMA>
+cudaError_t prepare_one() {
+  return cudaFuncSetAttribute(attn_fp4_kernel<DQK, NB, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Cfg<DQK, NB, TMA>::kSmem);
+}
+
+template <int DQK, int NB>
+cudaError_t launch_nb(const HostPlan &hp, const RunArgs &a, const TmaMaps &m, cudaStream_t st) {
+  return hp.use_tma ? launch_one<DQK, NB, true>(hp, a, m, st) : launch_one<DQK, NB, false>(hp, a, m, st);
+}
+
+template <int DQK, int NB>
+cudaError_t prepare_nb(const HostPlan &hp) {
+  return hp.use_tma ? prepare_one<DQK, NB, true>() : prepare_one<DQK, NB, false>();
+}
+
+}  // namespace
+
+int32_t fp4_register_rows(const HostPlan &hp) {
+  if (hp.prob.kv_dtype != ATTN_KV_FP4_E2M1 || hp.prefill) return 0;
+  int32_t rows = 8;
+  for (const BlockDesc &b : hp.blocks) {
+    if (b.nrows > 16) return 0;
+    if (b.nrows > 8) rows = 16;
+  }
+  return rows;
+}
+
+cudaError_t launch_attn_fp4(const HostPlan &hp, const RunArgs &a, const TmaMaps &m, cudaStream_t st) {
+  if (hp.num_ctas == 0) return cudaSuccess;
+  const bool one = hp.fp4_rows == 8;
+  if (hp.prob.head_dim_qk == kDqkSym)
+    return one ? launch_nb<kDqkSym, 1>(hp, a, m, st) : launch_nb<kDqkSym, 2>(hp, a, m, st);
+  return one ? launch_nb<kDqk, 1>(hp, a, m, st) : launch_nb<kDqk, 2>(hp, a, m, st);
+}
+
+cudaError_t prepare_attn_fp4(const HostPlan &hp) {
+  const bool one = hp.fp4_rows == 8;
+  if (hp.prob.head_dim_qk == kDqkSym) return one ? prepare_nb<kDqkSym, 1>(hp) : prepare_nb<kDqkSym, 2>(hp);
+  return one ? prepare_nb<kDqk, 1>(hp) : prepare_nb<kDqk, 2>(hp);
+}
+
+}  // namespace akp

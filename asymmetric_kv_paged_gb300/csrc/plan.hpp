@@ -73,6 +73,9 @@ struct HostPlan {
   int32_t block_rows = 128;      // 64 or 128 (the MMA M), or 256 (prefill kernel)
   int32_t key_tile = kKeyTile;   // keys per tile: 64, or 128 for the prefill kernel
   bool prefill = false;          // block_rows == 256: attn_prefill.cu runs the plan
+  // rows per block of the register-operand 4-bit kernel (attn_fp4.cu): 8 or 16;
+  // 0: attn_tc.cu or attn_prefill.cu runs the plan
+  int32_t fp4_rows = 0;
   bool one_copy = false;         // every block has more than block_rows / 2 rows
   int32_t num_sms = 0, num_ctas = 0, threads = 0;
   std::vector<BlockDesc> blocks;
