@@ -333,6 +333,7 @@ static attn_status_t run_impl(attn_plan_t plan, int phases, bool allow_stage, co
     r.group = hp.group;
     r.window = pr.window;
     r.key_tile = hp.key_tile;
+    r.lockstep = hp.lockstep;
     if (akp::launch_replan(r, st) != cudaSuccess) return ATTN_ERR_CUDA;
   }
   akp::TmaMaps stage_maps{};

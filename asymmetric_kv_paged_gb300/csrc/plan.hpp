@@ -76,6 +76,9 @@ struct HostPlan {
   // rows per block of the register-operand 4-bit kernel (attn_fp4.cu): 8 or 16;
   // 0: attn_tc.cu or attn_prefill.cu runs the plan
   int32_t fp4_rows = 0;
+  // KV heads dealt alike, CTA c working on head c % lockstep (4-bit plans;
+  // 1: one deal over all blocks), see planner.cpp
+  int32_t lockstep = 1;
   bool one_copy = false;         // every block has more than block_rows / 2 rows
   int32_t num_sms = 0, num_ctas = 0, threads = 0;
   std::vector<BlockDesc> blocks;

@@ -136,14 +136,28 @@ attn_status_t build_host_plan(const attn_problem_t *p, int32_t num_sms, HostPlan
   const int32_t tile = hp.key_tile;
   const int32_t G = hp.group;
 
-  // Row blocks.
+  // Rows of a 4-bit cache are 112 and 80 bytes: a head's row ends inside the
+  // 64-byte units that DRAM is read in, which the next head's row shares.  A KV
+  // head is therefore dealt like every other one, to CTAs of its own
+  // (CTA c works on head c % Hkv), so that the heads of a slot are read at the
+  // same time and the shared units come out of L2: with heads dealt one after
+  // the other a ragged decode batch read 325 MB for 221 MB of rows.  Not where
+  // dividing the CTAs among the heads leaves more than an eighth of them idle.
+  const int32_t H = p->num_kv_heads;
+  if (p->kv_dtype == ATTN_KV_FP4_E2M1 && !hp.prefill && H <= num_sms &&
+      8 * (num_sms % H) <= num_sms)
+    hp.lockstep = H;
+
+  // Row blocks, in (request, KV head) order; by KV head first in lockstep plans.
   int64_t total_tiles = 0;
+  const int32_t outer = hp.lockstep > 1 ? H : 1;
+  for (int32_t g0 = 0; g0 < outer; ++g0)
   for (int32_t b = 0; b < p->batch; ++b) {
     const int32_t n = hp.qo_indptr[b + 1] - hp.qo_indptr[b];
     const int32_t L = hp.seq_lens[b];
     if (n == 0) continue;
     const int32_t R = n * G;
-    for (int32_t g = 0; g < p->num_kv_heads; ++g) {
+    for (int32_t g = outer > 1 ? g0 : 0; g < (outer > 1 ? g0 + 1 : H); ++g) {
       for (int32_t row0 = 0; row0 < R; row0 += rows_per_block) {
         BlockDesc bd{};
         bd.b = b;
@@ -177,7 +191,7 @@ attn_status_t build_host_plan(const attn_problem_t *p, int32_t num_sms, HostPlan
   // CTAs, so rounding never piles up on the last one; a block remainder of at
   // most `slack` tiles (1/32 of a share; two for prefill plans) stays on the
   // current CTA rather than becoming a split of its own.
-  const int64_t nb = (int64_t)hp.blocks.size();
+  const int64_t nb_all = (int64_t)hp.blocks.size();
   constexpr int64_t kWholeBlockTiles = 8;
   // A CTA that goes on to a further segment pays for the switch (the finished
   // segment's epilogue, the next block's Q) with this many tiles of its share:
@@ -185,9 +199,13 @@ attn_status_t build_host_plan(const attn_problem_t *p, int32_t num_sms, HostPlan
   // (on the batched decode 4 tiles measured ~1.5% faster than 3, 5 and 6 no
   // better than 4).
   constexpr int64_t kSegSwitchTiles = 4;
+  // The deal of a lockstep plan is that of its first head's blocks over the
+  // head's CTAs, repeated for every head.
+  const int64_t nb = nb_all / hp.lockstep;
+  const int32_t sms = num_sms / hp.lockstep;
   if (nb > 0) {
     const int64_t min_tiles = 2;
-    int64_t remaining = total_tiles;
+    int64_t remaining = total_tiles / hp.lockstep;
     int32_t cta = -1;
     int64_t room = 0, target = 0, slack = 0;
     bool charge = false;          // this CTA's share pays for its segment switches
@@ -199,13 +217,13 @@ attn_status_t build_host_plan(const attn_problem_t *p, int32_t num_sms, HostPlan
       while (t0 < tend) {
         if (room <= 0) {
           ++cta;
-          const int64_t ctas_left = std::max<int64_t>(1, (int64_t)num_sms - cta);
+          const int64_t ctas_left = std::max<int64_t>(1, (int64_t)sms - cta);
           target = std::max<int64_t>(min_tiles, (remaining + ctas_left - 1) / ctas_left);
           // Large shares count the switches still ahead (about one per block
           // not yet begun) as work, so that the CTAs after a switch are not
           // left with the tiles the switching ones gave up; shares of a few
           // tiles, where most CTAs switch, stay even in tiles.
-          charge = cta + 1 < num_sms && target >= 8 * kSegSwitchTiles;
+          charge = cta + 1 < sms && target >= 8 * kSegSwitchTiles;
           if (charge)
             target = (remaining + kSegSwitchTiles * (nb - bi - 1) + ctas_left - 1) / ctas_left;
           // A prefill tile (128 keys x 256 rows) costs far more than the
@@ -221,7 +239,7 @@ attn_status_t build_host_plan(const attn_problem_t *p, int32_t num_sms, HostPlan
         // to the next one.  For such a block a split's extra segment and merge
         // cost more than the room left unused.
         const bool whole = t0 == bd.klo / tile && left <= kWholeBlockTiles &&
-                           left <= 2 * target && nb - bi <= (int64_t)num_sms - cta - 1;
+                           left <= 2 * target && nb - bi <= (int64_t)sms - cta - 1;
         if (whole && room < target && left > room + slack) {
           room = 0;
           continue;
@@ -240,12 +258,32 @@ attn_status_t build_host_plan(const attn_problem_t *p, int32_t num_sms, HostPlan
     }
     hp.num_ctas = cta + 1;
   }
+  if (hp.lockstep > 1) {
+    const int32_t heads = hp.lockstep;
+    const std::vector<SegDesc> segs = hp.segs;
+    const std::vector<int32_t> ctas = hp.seg_cta;
+    hp.segs.clear();
+    hp.seg_cta.clear();
+    for (size_t s0 = 0, s1; s0 < segs.size(); s0 = s1) {      // one CTA of the first head
+      for (s1 = s0; s1 < segs.size() && ctas[s1] == ctas[s0];) ++s1;
+      for (int32_t h = 0; h < heads; ++h)
+        for (size_t s = s0; s < s1; ++s) {
+          SegDesc sd = segs[s];
+          sd.block += (int32_t)(h * nb);
+          hp.segs.push_back(sd);
+          hp.seg_cta.push_back(ctas[s] * heads + h);
+        }
+    }
+    for (int32_t h = 1; h < heads; ++h)
+      for (int64_t bi = 0; bi < nb; ++bi) hp.blocks[h * nb + bi].num_splits = hp.blocks[bi].num_splits;
+    hp.num_ctas *= heads;
+  }
   hp.cta_seg_begin.assign(hp.num_ctas + 1, 0);
   for (size_t s = 0; s < hp.segs.size(); ++s) hp.cta_seg_begin[hp.seg_cta[s] + 1]++;
   for (int32_t c = 0; c < hp.num_ctas; ++c) hp.cta_seg_begin[c + 1] += hp.cta_seg_begin[c];
 
   // Partials and merge items for multi-split blocks.
-  for (int64_t bi = 0; bi < nb; ++bi) {
+  for (int64_t bi = 0; bi < nb_all; ++bi) {
     BlockDesc &bd = hp.blocks[bi];
     bd.part_row_base = -1;
     if (bd.num_splits > 1) {
@@ -281,7 +319,8 @@ attn_status_t build_replayable_plan(const attn_problem_t *p, int32_t num_sms, Ho
   }
   if (max_tiles >= INT32_MAX / 2) return ATTN_ERR_UNSUPPORTED;
   hp.replayable = true;
-  hp.num_ctas = (int32_t)std::min<int64_t>(num_sms, max_tiles);
+  // (in a lockstep plan every head has the same tiles, and gets the same CTAs)
+  hp.num_ctas = (int32_t)std::min<int64_t>(num_sms, max_tiles) / hp.lockstep * hp.lockstep;
   hp.seg_capacity = nb + hp.num_ctas;
   // a multi-split block keeps nrows partial rows per split, and there are at
   // most nb + num_ctas - 1 segments in all
@@ -319,7 +358,7 @@ int32_t replan_host(HostPlan *hp, const int32_t *seq_lens) {
     start[bi + 1] = start[bi] + block_tile_count(klo, khi, hp->key_tile);
   }
   const int64_t T = start[nb];
-  const int64_t ctas = std::min<int64_t>(T, hp->num_ctas);
+  const int64_t ctas = working_ctas(T, hp->num_ctas, hp->lockstep);
   const int32_t charge = switch_charge(T, ctas);
   const int64_t P = T + (int64_t)charge * nb;
   const int32_t *st = start.data();
@@ -328,11 +367,12 @@ int32_t replan_host(HostPlan *hp, const int32_t *seq_lens) {
   hp->cta_seg_begin.assign(hp->num_ctas + 1, 0);
   for (int32_t c = 0; c < hp->num_ctas; ++c) {
     if (c < ctas) {
-      const int64_t a = share_begin(c, P, ctas), e = share_begin(c + 1, P, ctas);
+      const int32_t sh = cta_share(c, ctas, hp->lockstep);
+      const int64_t a = share_begin(sh, P, ctas), e = share_begin(sh + 1, P, ctas);
       for (int32_t bi = block_at(st, nb, a, charge); bi < nb && block_pos(st, bi, charge) < e;
            ++bi) {
         const SegDesc sd = share_segment(bi, hp->blocks[bi], block_pos(st, bi, charge),
-                                         block_pos(st, bi + 1, charge), a, e, c, P, ctas,
+                                         block_pos(st, bi + 1, charge), a, e, sh, P, ctas,
                                          hp->key_tile, charge);
         if (sd.tile_end == sd.tile_begin) continue;   // the share ends in the block's charge
         hp->segs.push_back(sd);

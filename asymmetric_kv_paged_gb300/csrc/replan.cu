@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kReplanThreads, 1) replan_kernel(const ReplanA
   __syncthreads();
   cta_exclusive_scan(r.tile_start, r.nb);
   const int64_t T = r.tile_start[r.nb];
-  const int64_t ctas = T < r.num_ctas ? T : r.num_ctas;
+  const int64_t ctas = working_ctas(T, r.num_ctas, r.lockstep);
   const int32_t charge = switch_charge(T, ctas);
   const int64_t P = T + (int64_t)charge * r.nb;     // global positions
 
@@ -92,12 +92,13 @@ __global__ void __launch_bounds__(kReplanThreads, 1) replan_kernel(const ReplanA
   for (int32_t c = tid; c < r.num_ctas; c += kReplanThreads) {
     int32_t cnt = 0;
     if (c < ctas) {
-      const int64_t a = share_begin(c, P, ctas), e = share_begin(c + 1, P, ctas);
+      const int32_t sh = cta_share(c, ctas, r.lockstep);
+      const int64_t a = share_begin(sh, P, ctas), e = share_begin(sh + 1, P, ctas);
       for (int32_t bi = block_at(r.tile_start, r.nb, a, charge); bi < r.nb; ++bi) {
         const int64_t gs = block_pos(r.tile_start, bi, charge);
         if (gs >= e) break;
         const SegDesc sd =
-            share_segment(bi, r.blocks[bi], gs, block_pos(r.tile_start, bi + 1, charge), a, e, c,
+            share_segment(bi, r.blocks[bi], gs, block_pos(r.tile_start, bi + 1, charge), a, e, sh,
                           P, ctas, r.key_tile, charge);
         cnt += sd.tile_end > sd.tile_begin;
       }
@@ -108,13 +109,14 @@ __global__ void __launch_bounds__(kReplanThreads, 1) replan_kernel(const ReplanA
   cta_exclusive_scan(r.cta_seg_begin, r.num_ctas);
 
   for (int32_t c = tid; c < ctas; c += kReplanThreads) {
-    const int64_t a = share_begin(c, P, ctas), e = share_begin(c + 1, P, ctas);
+    const int32_t sh = cta_share(c, ctas, r.lockstep);
+    const int64_t a = share_begin(sh, P, ctas), e = share_begin(sh + 1, P, ctas);
     int32_t s = r.cta_seg_begin[c];
     for (int32_t bi = block_at(r.tile_start, r.nb, a, charge); bi < r.nb; ++bi) {
       const int64_t gs = block_pos(r.tile_start, bi, charge);
       if (gs >= e) break;
       const SegDesc sd =
-          share_segment(bi, r.blocks[bi], gs, block_pos(r.tile_start, bi + 1, charge), a, e, c, P,
+          share_segment(bi, r.blocks[bi], gs, block_pos(r.tile_start, bi + 1, charge), a, e, sh, P,
                         ctas, r.key_tile, charge);
       if (sd.tile_end > sd.tile_begin) r.segs[s++] = sd;
     }

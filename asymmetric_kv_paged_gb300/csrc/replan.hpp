@@ -10,8 +10,9 @@
 //   - its tiles take the global positions [start[bi], start[bi+1]) of the
 //     exclusive prefix sum `start` of the tile counts (T = start[nb] tiles);
 //   - with C' = min(C, T) working CTAs, CTA c takes positions
-//     [c*P/C', (c+1)*P/C') (equal shares, rounded down), so a block is cut
-//     wherever a share ends and each piece is one segment.  On shares of 32
+//     [c*P/C', (c+1)*P/C') (equal shares, rounded down; in a lockstep plan,
+//     whose blocks come head by head, the share of CTA c is the one of its
+//     place among the CTAs of head c % heads), so a block is cut wherever a share ends and each piece is one segment.  On shares of 32
 //     tiles or more every block is first given `charge` positions without a
 //     tile (P = T + charge * nb): the CTA whose share reaches into a block
 //     pays for its epilogue and Q staging with that much less work, as in the
@@ -56,6 +57,19 @@ AKP_HD int32_t switch_charge(int64_t T, int64_t ctas) {
 // earlier block (the block's tiles start `charge` positions later).
 AKP_HD int64_t block_pos(const int32_t *start, int32_t bi, int32_t charge) {
   return (int64_t)start[bi] + (int64_t)charge * bi;
+}
+
+// CTAs that get a share of T tiles: a multiple of `heads` (every head of a
+// lockstep plan has T / heads tiles).
+AKP_HD int64_t working_ctas(int64_t T, int64_t num_ctas, int32_t heads) {
+  const int64_t c = T < num_ctas ? T : num_ctas;
+  return c / heads * heads;
+}
+
+// The share of CTA c: c itself, or, with the heads in lockstep, share c / heads
+// of head c % heads (the head's shares lie together, as its blocks do).
+AKP_HD int32_t cta_share(int32_t c, int64_t ctas, int32_t heads) {
+  return (int32_t)((c % heads) * (ctas / heads) + c / heads);
 }
 
 // First global position of CTA c's share (c = ctas gives the total P).
@@ -128,7 +142,7 @@ struct ReplanArgs {
   const int32_t *seq_lens;     // [B] lengths of this run (caller's device array)
   const int32_t *seq_bounds;   // [B] upper bounds the plan was built for
   int32_t *err;                // device error word (bit 4: a length out of bounds)
-  int32_t nb, num_ctas, group, window, key_tile;
+  int32_t nb, num_ctas, group, window, key_tile, lockstep;
 };
 
 }  // namespace akp

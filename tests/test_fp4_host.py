@@ -83,14 +83,38 @@ def test_row_bytes():
     assert B.load().attn_kv_row_bytes(0, 192, None) == B.ATTN_ERR_INVALID_ARG
 
 
-def test_fp4_plans_share_the_schedule_of_other_types():
-    segs = []
-    for kv in (B.ATTN_KV_FP8_E4M3, B.ATTN_KV_FP4_E2M1):
-        prob, keep = B.make_problem(batch=3, num_q_heads=16, num_kv_heads=2, page_size=16, num_pages=900,
-                                    page_table_stride=300, kv_dtype=kv, window=0, has_sinks=False,
-                                    qo_indptr=[0, 1, 9, 10], seq_lens=[4000, 900, 77])
-        segs.append(B.attn_plan_segments(B.attn_plan_host(prob, 152, keep)))
-    assert np.array_equal(*segs)
+@pytest.mark.parametrize("hkv", [1, 2, 3, 8, 40])
+@pytest.mark.parametrize("num_sms", [1, 7, 152])
+def test_fp4_plans_cover_every_key_once_with_the_heads_in_lockstep(hkv, num_sms):
+    """The schedule invariants of every plan, static and replayable; where the heads
+    divide the CTAs well, CTA c works on head c % heads, on the same tiles as its
+    neighbours."""
+    from test_abi_host import _check_plan
+    for seq, n in (([4000, 900, 77], [1, 8, 1]), ([37], [1]), ([700, 5, 900, 64], [1, 0, 1, 1])):
+        w = W.make_workload(0, seq, n, hq=2 * hkv, hkv=hkv, page_size=16, pages_in_order=True)
+        prob, keep = B.make_problem(
+            batch=w.batch, num_q_heads=w.hq, num_kv_heads=hkv, page_size=16, num_pages=w.num_pages,
+            page_table_stride=w.page_table.shape[1], kv_dtype=B.ATTN_KV_FP4_E2M1, window=0,
+            has_sinks=False, qo_indptr=w.qo_indptr, seq_lens=w.seq_lens)
+        together = hkv > 1 and hkv <= num_sms and 8 * (num_sms % hkv) <= num_sms
+        for replayable in (False, True):
+            plan = (B.attn_plan_replayable_host if replayable else B.attn_plan_host)(prob, num_sms, keep)
+            for lens in ([w.seq_lens, np.maximum(w.seq_lens // 3, n)] if replayable else [w.seq_lens]):
+                w2 = W.Workload(**{**w.__dict__, "seq_lens": np.asarray(lens, np.int32)})
+                if replayable:
+                    assert B.attn_plan_replan_host(plan, lens) == 0
+                info = _check_plan(plan, w2, num_sms, replayable)
+                if not together:
+                    continue
+                segs, blocks = B.attn_plan_segments(plan), B.attn_plan_blocks(plan)
+                work = {}
+                for cta, blk, t0, t1, split in segs.tolist():
+                    b, g, row0 = blocks[blk][:3].tolist()
+                    assert g == cta % hkv
+                    work.setdefault(cta, []).append((b, row0, t0, t1, split))
+                assert info["ctas"] % hkv == 0
+                for c in range(info["ctas"]):
+                    assert work.get(c) == work.get(c - c % hkv)
 
 
 def test_host_plans_and_null_arguments_are_refused():
