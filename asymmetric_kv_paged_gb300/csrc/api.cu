@@ -307,7 +307,8 @@ static attn_status_t run_impl(attn_plan_t plan, int phases, bool allow_stage, co
     if ((reinterpret_cast<uintptr_t>(k_cache) & 15) || (reinterpret_cast<uintptr_t>(v_cache) & 15))
       return ATTN_ERR_INVALID_ARG;
     const int64_t slots = (int64_t)pr.num_pages * pr.page_size;
-    const int rows = pr.page_size >= akp::kKeyTile ? akp::kKeyTile : pr.page_size;
+    // keys per box: a whole tile, or a unit of the register-operand 4-bit kernel
+    const int rows = std::min(pr.page_size, hp.fp4_rows ? akp::kFp4UnitKeys : akp::kKeyTile);
     if (!make_cache_map(&maps.k, k_cache, k_row, pr.head_dim_qk, pr.num_kv_heads, slots, rows) ||
         !make_cache_map(&maps.v, v_cache, v_row, akp::kDv, pr.num_kv_heads, slots, rows))
       return ATTN_ERR_CUDA;

@@ -29,14 +29,16 @@
 // 11 bits and none above 2^-32 is lost; the maximum may grow by 2^8 before O is
 // rescaled (P <= 2^15).  Row sums are fp32, of the weights before rounding.
 //
-// Warps: kConsumers consumer warps, then the producer warps.  A unit of work is
-// half a 64-key tile (32 keys); unit u of the CTA belongs to consumer u %
-// kConsumers, which keeps running maxima, sums and O of its own for the whole
-// segment, so nothing is shared between tiles.  At the end of a segment the
-// consumers' partials are combined through shared memory.  With page sizes TMA
-// can tile, one producer warp looks up to 32 pages at once and issues a K and
-// a V box per page piece; otherwise four or eight producer warps gather rows
-// through registers, a tile per warp in flight.
+// A unit of work is half a 64-key tile (32 keys); unit u of the CTA belongs to
+// warp u % kWarps, which keeps running maxima, sums and O of its own for the
+// whole segment, so nothing is shared between tiles; at the end of a segment
+// the warps' partials are combined through shared memory.  Each warp also
+// fetches its own units, into a ring of its own, a few units ahead: it alone
+// fills, waits for and frees the ring's stages, in order, so that no barrier
+// phase can be mistaken for another and no warp ever waits for another one's
+// data.  With page sizes TMA can tile a unit is one K and one V box per page
+// piece, issued by a lane each after up to 32 page lookups in one round trip;
+// otherwise its rows are gathered with 16-byte asynchronous copies.
 // Every wait is bounded in time, as in attn_tc.cu.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -52,35 +54,33 @@ namespace akp {
 namespace {
 
 constexpr int kN = kKeyTile;
-constexpr int kConsumers = 8;
-constexpr int kUnitKeys = 32;
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kUnitKeys = kFp4UnitKeys;
 constexpr int kUnits = kN / kUnitKeys;        // units per tile
+constexpr int kDepth = 3;                     // units in a warp's ring
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.0f;                 // base-2 growth of a maximum before O is rescaled
 constexpr float kLift = 7.0f;                 // P is held times 2^kLift
-constexpr int kCombStride = 130;              // floats per row of the combine buffer (see flush)
+constexpr int kCombStride = 130;              // floats per row of the combine buffer (see its use)
 
 template <int DQK>
-struct Tile {
+struct Unit {
   static constexpr int kKrow = e2m1_row_bytes(DQK), kVrow = e2m1_row_bytes(kDv);
-  static constexpr int kKBytes = kN * kKrow;
-  static constexpr int kBytes = kKBytes + kN * kVrow;       // 12 KB at 192
-  static constexpr int kChunks = (kKrow + kVrow) / 16;      // 16-byte chunks per key
+  static constexpr int kKBytes = kUnitKeys * kKrow;
+  static constexpr int kBytes = kKBytes + kUnitKeys * kVrow;      // 6 KB at 192
 };
 
-template <int DQK, int NB, bool TMA>
+template <int DQK, int NB>
 struct Cfg {
-  static constexpr int kProducers = TMA ? 1 : NB == 1 ? 8 : 4;
-  static constexpr int kThreads = (kConsumers + kProducers) * 32;
-  static constexpr int kStages = NB == 1 ? 14 : 11;
-  static constexpr int kOffComb = kStages * Tile<DQK>::kBytes;
-  static constexpr int kSmem = kOffComb + kConsumers * NB * 8 * kCombStride * 4 + 1024;
-  static_assert(kSmem + 2048 <= 227 * 1024, "shared memory layout too large");
+  static constexpr int kOffComb = kWarps * kDepth * Unit<DQK>::kBytes;
+  static constexpr int kSmem = kOffComb + kWarps * NB * 8 * kCombStride * 4 + 1024;
+  static_assert(kSmem + 3072 <= 227 * 1024, "shared memory layout too large");
 };
 
 struct FBars {
-  uint64_t full[16], empty[16];
+  uint64_t full[kWarps][kDepth];
   uint64_t sync;
 };
 
@@ -126,45 +126,26 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
       : "memory");
 }
 
-// Walks the CTA's tiles in order (as in attn_tc.cu).
-struct Walk {
-  const SegDesc *segs;
-  const BlockDesc *blocks;
-  int seg, seg_end, tile;
-  SegDesc sd;
-  BlockDesc bd;
-  __device__ void init(const RunArgs &a, const CtaHead &h) {
-    segs = a.segs;
-    blocks = a.blocks;
-    seg = h.seg_begin;
-    seg_end = h.seg_end;
-    sd = h.seg;
-    bd = h.blk;
-    tile = sd.tile_begin;
-  }
-  __device__ void next() {
-    if (++tile == sd.tile_end && seg + 1 < seg_end) {
-      ++seg;
-      sd = segs[seg];
-      bd = blocks[sd.block];
-      tile = sd.tile_begin;
-    }
-  }
+// The page pieces ("boxes") of a warp's units, up to 32 looked up at a time:
+// lane i holds box i % nbox of the batch's unit i / nbox.  A page id is loaded when
+// its batch is looked up, one batch ahead, and first used when that becomes the
+// current one.
+struct Boxes {
+  int32_t page, off, g;      // page id, first slot in the page (-1: no visible key in the box), KV head
 };
 
 template <int DQK, int NB, bool TMA>
-__global__ void __launch_bounds__(Cfg<DQK, NB, TMA>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     attn_fp4_kernel(const RunArgs args, const __grid_constant__ TmaMaps maps) {
   const RunArgs a = args;
-  using C = Cfg<DQK, NB, TMA>;
-  using T = Tile<DQK>;
-  constexpr int NS = C::kStages;
+  using C = Cfg<DQK, NB>;
+  using T = Unit<DQK>;
   constexpr int NJ = DQK / 64;                 // K blocks per lane
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
   __shared__ FBars bars;
   __shared__ int abort_flag;
-  __shared__ float sm_m[kConsumers][NB * 8], sm_l[kConsumers][NB * 8];
+  __shared__ float sm_m[kWarps][NB * 8], sm_l[kWarps][NB * 8];
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // programmatic dependent: see attn_tc.cu
@@ -172,131 +153,131 @@ __global__ void __launch_bounds__(Cfg<DQK, NB, TMA>::kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const CtaHead head = a.cta_heads[blockIdx.x];
   if (head.seg_begin >= head.seg_end) return;
-  const int total = head.total;
+  const int total_units = head.total * kUnits;
   if (tid == 0) {
     abort_flag = 0;
-    for (int s = 0; s < NS; ++s) {
-      tc::mbar_init(&bars.full[s], 1);
-      tc::mbar_init(&bars.empty[s], kUnits);
-    }
-    tc::mbar_init(&bars.sync, kConsumers);
+    for (int w = 0; w < kWarps; ++w)
+      for (int d = 0; d < kDepth; ++d) tc::mbar_init(&bars.full[w][d], 1);
+    tc::mbar_init(&bars.sync, kWarps);
     tc::fence_mbar_init();
   }
   __syncthreads();
 
-  if (warp >= kConsumers) {
-    Walk cur;
-    cur.init(a, head);
+  // ------------------------------------------------------------ fetching
+  // This warp's units are warp, warp + kWarps, ... of the CTA; its n-th unit goes
+  // to stage n % kDepth of its ring.
+  const int my_units = total_units > warp ? (total_units - warp + kWarps - 1) / kWarps : 0;
+  uint8_t *ring = smem + warp * (kDepth * T::kBytes);
+  const uint32_t ring_addr = tc::smem_u32(ring);
+  const int box = TMA ? min(a.page_size, kUnitKeys) : 1;
+  const int nbox = TMA ? kUnitKeys / box : 32;            // boxes per unit (TMA: 1, 2 or 4)
+  const int batch = TMA ? 32 / nbox : 1;                  // units per lookup
+  const int mine = lane / nbox, bx = lane % nbox;
+  int lk_seg = head.seg_begin, lk_at = warp, lk_next = 0; // where the next lookup starts
+  SegDesc lk_sd = head.seg;
+  BlockDesc lk_bd = head.blk;
+  auto lookup = [&]() -> Boxes {
+    Boxes r{0, -1, 0};
+    const int cnt = min(batch, my_units - lk_next);
+    lk_next += batch;
+    if (cnt <= 0) return r;
+    // the lane's unit: past whole segments first (the batch's last unit is where
+    // the next batch goes on from; its segment and block stay in registers)
+    int sg = lk_seg, at = lk_at + min(mine, cnt - 1) * kWarps;
+    SegDesc sd = lk_sd;
+    while (at >= (sd.tile_end - sd.tile_begin) * kUnits && sg + 1 < head.seg_end) {
+      at -= (sd.tile_end - sd.tile_begin) * kUnits;
+      sd = a.segs[++sg];
+    }
+    int b = lk_bd.b, klo = lk_bd.klo, khi = lk_bd.khi;
+    r.g = lk_bd.g;
+    if (sd.block != lk_sd.block) {
+      const BlockDesc bd = a.blocks[sd.block];
+      b = bd.b;
+      klo = bd.klo;
+      khi = bd.khi;
+      r.g = bd.g;
+    }
+    const int j = sd.tile_begin * kN + at * kUnitKeys + bx * box;
+    if (mine < cnt && j + box > klo && j < khi) {
+      r.page = __ldg(a.page_table + (int64_t)b * a.pt_stride + j / a.page_size);
+      r.off = j % a.page_size;
+    }
+    const int last = __shfl_sync(0xffffffffu, sg, 31);
+    lk_at = __shfl_sync(0xffffffffu, at, 31) + kWarps;
+    if (last != lk_seg) {
+      lk_seg = last;
+      lk_sd = a.segs[last];
+      lk_bd = a.blocks[lk_sd.block];
+    }
+    return r;
+  };
+  // the batch's first slots, -1 where nothing is to be read (ids outside the pool
+  // are reported, and read as zeros)
+  auto resolve = [&](const Boxes &b) -> int64_t {
+    if (b.off < 0) return -1;
+    if (b.page < 0 || b.page >= a.num_pages) {
+      atomicOr(a.err, 1);
+      return -1;
+    }
+    return (int64_t)b.page * a.page_size + b.off;
+  };
+  Boxes nxt = lookup();
+  int64_t slot = resolve(nxt);
+  int cur_g = nxt.g;
+  nxt = lookup();
+  int issued = 0;
+  auto issue = [&]() {
+    const int d = issued % kDepth, u = issued & (batch - 1);
+    const uint32_t dst = ring_addr + d * T::kBytes;
     if constexpr (TMA) {
-      // ---------------------------------------------------------- TMA producer
-      // One lane per (tile, box): up to 32 page lookups in one round trip.
-      const int box = a.page_size >= kN ? kN : a.page_size;
-      const int nbox = kN / box, batch = 32 / nbox;
-      const int oob = a.num_pages * a.page_size;      // first slot past the pool: zero fill
-      const int mine = lane / nbox, bx = lane % nbox;
-      const uint32_t sbase = tc::smem_u32(smem);
-      bool ok = true;
-      for (int k0 = 0; k0 < total && ok; k0 += batch) {
-        const int cnt = min(batch, total - k0);
-        int slot = oob, g = 0, pt_idx = -1, j = 0, b = 0;
-        for (int u = 0; u < cnt; ++u, cur.next()) {
-          if (u == mine) {
-            j = cur.tile * kN + bx * box;
-            g = cur.bd.g;
-            b = cur.bd.b;
-            if (j + box > cur.bd.klo && j < cur.bd.khi) pt_idx = j / a.page_size;
-          }
-        }
-        if (pt_idx >= 0) {
-          const int32_t page = __ldg(a.page_table + (int64_t)b * a.pt_stride + pt_idx);
-          if (page >= 0 && page < a.num_pages)
-            slot = page * a.page_size + j % a.page_size;
-          else
-            atomicOr(a.err, 1);
-        }
-        for (int u = 0; u < cnt; ++u) {
-          const int k = k0 + u, s = k % NS;
-          if (k >= NS && !tc::mbar_wait_warp(&bars.empty[s], ((k / NS) - 1) & 1, &abort_flag)) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) tc::mbar_arrive_expect_tx(&bars.full[s], T::kBytes);
-          __syncwarp();
-          if (u == mine) {
-            const uint32_t dst = sbase + s * T::kBytes;
-            tma_load_3d(dst + bx * box * T::kKrow, &maps.k, g, slot, &bars.full[s]);
-            tma_load_3d(dst + T::kKBytes + bx * box * T::kVrow, &maps.v, g, slot, &bars.full[s]);
-          }
-        }
+      uint64_t *bar = &bars.full[warp][d];
+      if (lane == 0) tc::mbar_arrive_expect_tx(bar, T::kBytes);
+      __syncwarp();
+      if (mine == u) {
+        // a box without a visible key reads past the pool: zero fill
+        const int first = slot >= 0 ? (int)slot : a.num_pages * a.page_size;
+        tma_load_3d(dst + bx * box * T::kKrow, &maps.k, cur_g, first, bar);
+        tma_load_3d(dst + T::kKBytes + bx * box * T::kVrow, &maps.v, cur_g, first, bar);
       }
     } else {
-      // ---------------------------------------------------------- gather
-      // Producer p takes tiles p, p + kProducers, ...; two lanes per key, 16
-      // keys at a time, each lane half of the key's 16-byte chunks (K's, then
-      // V's).  The slots of its next tile are looked up before the current
-      // tile's rows are waited for.
-      constexpr int PW = C::kProducers, HC = T::kChunks / 2;
-      static_assert(T::kChunks % 2 == 0, "two lanes share a key's chunks");
-      const int p = warp - kConsumers;
-      const int part = lane & 1;
-      const uint8_t *kc = static_cast<const uint8_t *>(a.k_cache);
-      const uint8_t *vc = static_cast<const uint8_t *>(a.v_cache);
-      for (int i = 0; i < p && i < total; ++i) cur.next();
-      int64_t slot[4];
-      int g = 0;
-      auto lookup = [&]() {
-        g = cur.bd.g;
+      // lane i holds key i's slot; the lanes copy the unit's 16-byte chunks in
+      // order (a row's neighbouring chunks by neighbouring lanes); keys without
+      // a slot are filled with zeros
+      const int64_t row = slot >= 0 ? slot * a.hkv + cur_g : -1;
+      auto rows = [&](const void *cache, int row_bytes, uint32_t to) {
+        const int nch = row_bytes / 16;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int j = cur.tile * kN + q * 16 + (lane >> 1);
-          slot[q] = -1;
-          if (j >= cur.bd.klo && j < cur.bd.khi) {
-            const int32_t page = __ldg(a.page_table + (int64_t)cur.bd.b * a.pt_stride + j / a.page_size);
-            if (page >= 0 && page < a.num_pages)
-              slot[q] = (int64_t)page * a.page_size + j % a.page_size;
-            else
-              atomicOr(a.err, 1);
-          }
+        for (int i = 0; i < nch; ++i) {
+          const int c = i * 32 + lane, key = c / nch, ch = c % nch;
+          const int64_t s = __shfl_sync(0xffffffffu, row, key);
+          const uint8_t *src = static_cast<const uint8_t *>(cache) + (s >= 0 ? s : 0) * row_bytes + ch * 16;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(to + c * 16), "l"(src),
+                       "r"(s >= 0 ? 16 : 0)
+                       : "memory");
         }
       };
-      if (p < total) lookup();
-      for (int k = p; k < total; k += PW) {
-        uint4 r[4][HC];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int64_t row = (slot[q] >= 0 ? slot[q] : 0) * a.hkv + g;
-          const uint4 *krow = reinterpret_cast<const uint4 *>(kc + row * T::kKrow);
-          const uint4 *vrow = reinterpret_cast<const uint4 *>(vc + row * T::kVrow);
-#pragma unroll
-          for (int u = 0; u < HC; ++u) {
-            const int c = part * HC + u;
-            r[q][u] = make_uint4(0u, 0u, 0u, 0u);
-            if (slot[q] >= 0) r[q][u] = __ldg(c < T::kKrow / 16 ? krow + c : vrow + (c - T::kKrow / 16));
-          }
-        }
-        if (k + PW < total) {
-          for (int i = 0; i < PW; ++i) cur.next();
-          lookup();
-        }
-        const int s = k % NS;
-        if (k >= NS && !tc::mbar_wait_warp(&bars.empty[s], ((k / NS) - 1) & 1, &abort_flag)) break;
-        uint8_t *dst = smem + s * T::kBytes;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int key = q * 16 + (lane >> 1);
-#pragma unroll
-          for (int u = 0; u < HC; ++u) {
-            const int c = part * HC + u;
-            uint8_t *d = c < T::kKrow / 16 ? dst + key * T::kKrow + c * 16
-                                           : dst + T::kKBytes + key * T::kVrow + (c - T::kKrow / 16) * 16;
-            *reinterpret_cast<uint4 *>(d) = r[q][u];
-          }
-        }
-        tc::mbar_arrive_warp(&bars.full[s]);
-      }
+      rows(a.k_cache, T::kKrow, dst);
+      rows(a.v_cache, T::kVrow, dst + T::kKBytes);
     }
-  } else {
-    // ------------------------------------------------------------ consumers
+    ++issued;
+    if ((issued & (batch - 1)) == 0) {
+      slot = resolve(nxt);
+      cur_g = nxt.g;
+      nxt = lookup();
+    }
+  };
+  // every stage but one is filled ahead; without TMA each fill is one group of
+  // asynchronous copies, empty past the last unit, so that their count is fixed
+  auto fill = [&]() {
+    if (issued < my_units) issue();
+    if (!TMA) asm volatile("cp.async.commit_group;\n" ::: "memory");
+  };
+  for (int i = 0; i < kDepth - 1; ++i) fill();
+  int done = 0;                                // units this warp has finished
+
+  {
+    // ------------------------------------------------------------ attention
     const int g = lane >> 2, t = lane & 3;
     uint32_t qf[NB][NJ * 4][2];
     float o[8][NB][4];
@@ -311,17 +292,16 @@ __global__ void __launch_bounds__(Cfg<DQK, NB, TMA>::kThreads, 1)
     };
     SegDesc sd = head.seg;
     BlockDesc bd = head.blk;
-    int k0 = 0;                                // the segment's first tile among the CTA's
+    int u0 = 0;                                // the segment's first unit among the CTA's
     bool alive = true;
     for (int seg = head.seg_begin; seg < head.seg_end && alive; ++seg) {
       if (seg > head.seg_begin) {
         sd = a.segs[seg];
         bd = a.blocks[sd.block];
       }
-      const int u_end = (k0 + sd.tile_end - sd.tile_begin) * kUnits;
+      const int u_end = u0 + (sd.tile_end - sd.tile_begin) * kUnits;
       // this warp's first unit of the segment
-      int u = k0 * kUnits;
-      u += (warp - u % kConsumers + kConsumers) % kConsumers;
+      int u = u0 + (warp - u0 % kWarps + kWarps) % kWarps;
       const bool has = u < u_end;
       // ---- rows: Q fragments (scaled to fp16), score scales, visible keys
       const int i_first = bd.L - bd.n + bd.row0 / a.group;
@@ -379,15 +359,20 @@ __global__ void __launch_bounds__(Cfg<DQK, NB, TMA>::kThreads, 1)
             for (int x = 0; x < 4; ++x) o[i][nb][x] = 0.f;
       }
 #pragma unroll 1
-      for (; u < u_end; u += kConsumers) {
-        const int k = u / kUnits, s = k % NS;
-        const int key0 = (sd.tile_begin + k - k0) * kN + (u % kUnits) * kUnitKeys;
-        if (!tc::mbar_wait_warp(&bars.full[s], (k / NS) & 1, &abort_flag)) {
-          alive = false;
-          break;
+      for (; u < u_end; u += kWarps) {
+        const int d = done % kDepth;
+        const int key0 = sd.tile_begin * kN + (u - u0) * kUnitKeys;
+        fill();                                   // the stage freed by the previous unit
+        if constexpr (TMA) {
+          if (!tc::mbar_wait_warp(&bars.full[warp][d], (done / kDepth) & 1, &abort_flag)) {
+            alive = false;
+            break;
+          }
+        } else {
+          asm volatile("cp.async.wait_group %0;\n" ::"n"(kDepth - 1) : "memory");
+          __syncwarp();
         }
-        const uint8_t *kt = smem + s * T::kBytes + (u % kUnits) * kUnitKeys * T::kKrow;
-        const uint8_t *vt = smem + s * T::kBytes + T::kKBytes + (u % kUnits) * kUnitKeys * T::kVrow;
+        const uint8_t *kt = ring + d * T::kBytes, *vt = kt + T::kKBytes;
         // ---- S^T = K . Q^T for 2 x 16 keys
         float sacc[2][NB][4];
 #pragma unroll
@@ -533,8 +518,9 @@ __global__ void __launch_bounds__(Cfg<DQK, NB, TMA>::kThreads, 1)
             }
           }
         }
+        ++done;
         if (TMA) tc::fence_proxy_async_smem();   // the refill must not overtake these reads
-        tc::mbar_arrive_warp(&bars.empty[s]);
+        __syncwarp();
       }
       if (!alive) break;
 
@@ -568,13 +554,13 @@ __global__ void __launch_bounds__(Cfg<DQK, NB, TMA>::kThreads, 1)
       }
       if (!group_sync()) break;
       // warp w combines rows w and w + 8: lane owns dv 4 lane .. 4 lane + 3
-      for (int r = warp; r < bd.nrows; r += kConsumers) {
+      for (int r = warp; r < bd.nrows; r += kWarps) {
         const int flat = bd.row0 + r;
         const int tok = bd.tok0 + flat / a.group, h = bd.g * a.group + flat % a.group;
         const float sink2 = a.sinks && bd.num_splits == 1 ? __ldg(a.sinks + h) * kLog2e : -INFINITY;
         float M = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < kConsumers; ++w) M = fmaxf(M, sm_m[w][r]);
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w][r]);
         float Lsum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         const int gg = lane >> 2;
@@ -582,7 +568,7 @@ __global__ void __launch_bounds__(Cfg<DQK, NB, TMA>::kThreads, 1)
         const int p1 = 16 * gg + ((4 * (lane & 3) + 2 + 2 * (gg >> 1)) & 15);
         if (M != -INFINITY) {
 #pragma unroll
-          for (int w = 0; w < kConsumers; ++w) {
+          for (int w = 0; w < kWarps; ++w) {
             const float mw = sm_m[w][r];
             if (mw == -INFINITY) continue;             // nothing written by this warp
             const float f = exp2f(mw - M);
@@ -622,10 +608,19 @@ __global__ void __launch_bounds__(Cfg<DQK, NB, TMA>::kThreads, 1)
           if (lane == 0) a.part_lse[prow] = Lsum == 0.f ? -INFINITY : M + log2f(Lsum * inv_lift);
         }
       }
-      k0 += sd.tile_end - sd.tile_begin;
+      u0 = u_end;
       // the buffer is free for the next segment once every warp has read it
       if (seg + 1 < head.seg_end && !group_sync()) break;
     }
+  }
+  if constexpr (TMA) {
+    // after a give-up, the copies still in flight land before the CTA ends (a
+    // bounded wait of its own that ignores the abort)
+    int no_abort = 0;
+    for (; done < issued; ++done)
+      tc::mbar_wait(&bars.full[warp][done % kDepth], (done / kDepth) & 1, &no_abort, 100000000ull);
+  } else {
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
   }
   __syncthreads();
   if (tid == 0 && abort_flag) atomicOr(a.err, 2);
@@ -633,14 +628,13 @@ __global__ void __launch_bounds__(Cfg<DQK, NB, TMA>::kThreads, 1)
 
 template <int DQK, int NB, bool TMA>
 cudaError_t launch_one(const HostPlan &hp, const RunArgs &a, const TmaMaps &m, cudaStream_t st) {
-  using C = Cfg<DQK, NB, TMA>;
-  return launch_dependent(attn_fp4_kernel<DQK, NB, TMA>, dim3(hp.num_ctas), dim3(C::kThreads), C::kSmem, st, a, m);
+  return launch_dependent(attn_fp4_kernel<DQK, NB, TMA>, dim3(hp.num_ctas), dim3(kThreads), Cfg<DQK, NB>::kSmem, st, a, m);
 }
 
 template <int DQK, int NB, bool TMA>
 cudaError_t prepare_one() {
   return cudaFuncSetAttribute(attn_fp4_kernel<DQK, NB, TMA>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Cfg<DQK, NB, TMA>::kSmem);
+                              Cfg<DQK, NB>::kSmem);
 }
 
 template <int DQK, int NB>

@@ -13,6 +13,7 @@ constexpr int kDqk = 192;       // query/key head dim
 constexpr int kDqkSym = 128;    // query/key head dim of the symmetric pair 128/128
 constexpr int kDv = 128;        // value head dim
 constexpr int kKeyTile = 64;    // keys per pipeline tile (decode / verify kernel)
+constexpr int kFp4UnitKeys = 32;  // keys a warp of attn_fp4.cu takes at a time
 constexpr int kPrefillKeyTile = 128;   // keys per tile of the prefill kernel
 
 // Query rows per row block.  A block packs up to block_rows query rows of one
