@@ -54,11 +54,8 @@ namespace akp {
 namespace {
 
 constexpr int kN = kKeyTile;
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kUnitKeys = kFp4UnitKeys;
 constexpr int kUnits = kN / kUnitKeys;        // units per tile
-constexpr int kDepth = 3;                     // units in a warp's ring
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.0f;                 // base-2 growth of a maximum before O is rescaled
@@ -74,13 +71,16 @@ struct Unit {
 
 template <int DQK, int NB>
 struct Cfg {
+  static constexpr int kWarps = NB == 1 ? 12 : 8;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kDepth = NB == 1 ? 2 : 3;     // units in a warp's ring
   static constexpr int kOffComb = kWarps * kDepth * Unit<DQK>::kBytes;
   static constexpr int kSmem = kOffComb + kWarps * NB * 8 * kCombStride * 4 + 1024;
   static_assert(kSmem + 3072 <= 227 * 1024, "shared memory layout too large");
 };
 
 struct FBars {
-  uint64_t full[kWarps][kDepth];
+  uint64_t full[12][3];
   uint64_t sync;
 };
 
@@ -135,11 +135,12 @@ struct Boxes {
 };
 
 template <int DQK, int NB, bool TMA>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<DQK, NB>::kThreads, 1)
     attn_fp4_kernel(const RunArgs args, const __grid_constant__ TmaMaps maps) {
   const RunArgs a = args;
   using C = Cfg<DQK, NB>;
   using T = Unit<DQK>;
+  constexpr int kWarps = C::kWarps, kDepth = C::kDepth;
   constexpr int NJ = DQK / 64;                 // K blocks per lane
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int DQK, int NB, bool TMA>
 cudaError_t launch_one(const HostPlan &hp, const RunArgs &a, const TmaMaps &m, cudaStream_t st) {
-  return launch_dependent(attn_fp4_kernel<DQK, NB, TMA>, dim3(hp.num_ctas), dim3(kThreads), Cfg<DQK, NB>::kSmem, st, a, m);
+  return launch_dependent(attn_fp4_kernel<DQK, NB, TMA>, dim3(hp.num_ctas), dim3(Cfg<DQK, NB>::kThreads), Cfg<DQK, NB>::kSmem, st, a, m);
 }
 
 template <int DQK, int NB, bool TMA>
