@@ -34,6 +34,7 @@
 // Every wait is bounded in time; a broken invariant ends the kernel with bit 1
 // of the plan's error word set instead of hanging the GPU.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include <cmath>
@@ -204,6 +205,11 @@ __device__ __forceinline__ uint32_t cvt_pair(float lo, float hi) {
   return *reinterpret_cast<uint32_t *>(&h);
 }
 
+__device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&h);
+}
+
 __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(tc::smem_u32(bar)),
                "r"(bytes)
@@ -233,6 +239,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const RunArgs a = args;
   using Lay = Layout<KV, MR, TMA, DQK>;
   constexpr bool RAW = KV != kBf16;         // raw rows that the converter warps widen
+  // 4-bit caches: the MMAs are fp16 (codes convert to it in one instruction),
+  // Q rows scaled into its range, P held times 2^kLift (attn_fp4.cu says why)
+  constexpr bool F16 = KV == kE2m1;
+  constexpr float kLift = F16 ? 7.f : 0.f, kUnlift = F16 ? 0.0078125f : 1.f;
   // this instantiation's query/key head dim and tile sizes
   constexpr int kDqk = DQK;
   constexpr int kOpK = Dims<KV, DQK>::kOpK;
@@ -249,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ float sm_m[128], sm_l[128];
+  __shared__ int8_t sm_shift[F16 ? 4 : 1][F16 ? MR : 1];     // Q row shifts, per segment
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -471,6 +482,62 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (c.si >= QB && !tc::mbar_wait_warp(&bars.q_empty[qb], ((c.si / QB) - 1) & 1, &abort_flag))
         return false;
       uint8_t *qs = smem + qb * Lay::kQBytes;
+      if constexpr (F16) {
+        // Rows scaled by the power of two that puts their largest |q| in [2^14,
+        // 2^15) (exact down to 2^-31 of it); the softmax divides the row's scores
+        // by it.  128 / kRows threads per row, which agree on its maximum.
+        constexpr int kPer = kDqk / 8 * kRows / 128;       // chunks of a thread
+        constexpr int kHalfRow = 128 / kRows;
+        const int rows_pad16 = rows_pad_for<kRows>(bd.nrows, c.sd.tile_end - c.sd.tile_begin);
+        const int p = ct / kHalfRow, part = ct % kHalfRow, r = p % rows_pad16;
+        const bool live = r < bd.nrows;
+        const int flat = bd.row0 + (live ? r : 0);
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            static_cast<const uint16_t *>(a.q) +
+            ((int64_t)(bd.tok0 + flat / a.group) * a.hq + bd.g * a.group + flat % a.group) * kDqk);
+        constexpr int kBatch = kPer <= 12 ? kPer : 8;
+        uint32_t e = 0;
+        uint4 v[kBatch];
+        auto load = [&](int i0) {
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u)
+            v[u] = live ? __ldg(src + part * kPer + i0 + u) : make_uint4(0u, 0u, 0u, 0u);
+        };
+#pragma unroll 1
+        for (int i0 = 0; i0 < kPer; i0 += kBatch) {
+          load(i0);
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u) {
+            const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) e = max(e, max((w[q] >> 7) & 0xFFu, (w[q] >> 23) & 0xFFu));
+          }
+        }
+        if (kHalfRow == 2) e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
+        const int sh = min(141 - (int)e, 126);
+        const float f = __int_as_float((sh + 127) << 23);
+        // read by the row's softmax thread once per segment, at its first tile;
+        // the stage of segment si + 3 waits for a Q.K^T that waits for that
+        if (part == 0) sm_shift[c.si & 3][p] = sh;
+#pragma unroll 1
+        for (int i0 = 0; i0 < kPer; i0 += kBatch) {
+          if (kBatch < kPer) load(i0);
+#pragma unroll
+          for (int u = 0; u < kBatch; ++u) {
+            const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+            uint32_t h[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              h[q] = f16_pair(__uint_as_float(w[q] << 16) * f, __uint_as_float(w[q] & 0xFFFF0000u) * f);
+            const int ch = part * kPer + i0 + u;
+            *reinterpret_cast<uint4 *>(qs + (ch >> 3) * kQBlock + tc::sw128_offset(p, ch & 7)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        }
+        tc::fence_proxy_async_smem();
+        tc::mbar_arrive(&bars.q_full[qb]);
+        return true;
+      }
       const int rows_pad = rows_pad_for<kRows>(bd.nrows, c.sd.tile_end - c.sd.tile_begin);
       constexpr int kQch = kDqk / 8;       // 16-byte chunks per Q row
       constexpr int kIters = kRows * kQch / 128;
@@ -573,86 +640,70 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if constexpr (KV == kE2m1) {
       // E2M1 rows (codes, then a scale per 16 values): one 16-byte chunk of
-      // codes and its two scales become 32 bfloat16 values, exactly.  With TMA
-      // the rows come from the raw stage, which goes back once they are in
-      // registers, and the operand stage's halves have barriers of their own
-      // as for E4M3; without, two threads per key read them from the cache
-      // (slots from the ring the producer warp fills).
+      // codes and its two scales become 32 fp16 values, exactly (one conversion
+      // per pair and one product with the scale; these plans' MMAs are fp16).
+      // A thread owns key ct % 64 and every other chunk of its row, so that the
+      // 16-byte accesses of 8 neighbouring lanes, to rows of 112, 80 and 128
+      // bytes, fall into 8 different bank groups.  With TMA the rows come from the
+      // raw stage, which goes back once they are in registers, and the operand
+      // stage's halves have barriers of their own as for E4M3; without, they are
+      // read from the cache (slots from the ring the producer warp fills).
       constexpr int kKrow = kv_row_bytes(kE2m1, kDqk), kVrow = kv_row_bytes(kE2m1, kDv);
-      constexpr int kKch = kDqk / 32, kVch = kDv / 32;      // code chunks per row
-      constexpr int kPerK = kN * kKch / 128, kPerV = kN * kVch / 128;
-      // chunk u of this thread: the key within the tile and the chunk of its row
-      auto at = [&](int u, int nch, int &kk, int &ch) {
-        if (TMA) {
-          const int c = ct + u * 128;
-          kk = c / nch;
-          ch = c % nch;
-        } else {
-          kk = ct >> 1;
-          ch = (ct & 1) * (nch / 2) + u;
-        }
-      };
-      auto widen = [&](uint8_t *dst, int kk, int ch, bool keep, uint4 raw, uint32_t scales) {
+      constexpr int kPerK = kDqk / 64, kPerV = kDv / 64;    // code chunks of a thread
+      const int kk = ct & 63, ch0 = ct >> 6;
+      auto widen = [&](uint8_t *dst, int ch, bool keep, uint4 raw, uint32_t scales) {
         uint4 w[4];
-        if (keep) e2m1x32_to_bf16(raw, scales, w);
+        if (!keep) scales = 0u;       // keys outside the block's range: finite codes times zero
+        e2m1x32_to_f16(raw, scales, w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int c16 = 4 * ch + i;
-          *reinterpret_cast<uint4 *>(dst + (c16 >> 3) * kBlk + tc::sw128_offset(kk, c16 & 7)) =
-              keep ? w[i] : make_uint4(0u, 0u, 0u, 0u);
+          *reinterpret_cast<uint4 *>(dst + (c16 >> 3) * kBlk + tc::sw128_offset(kk, c16 & 7)) = w[i];
         }
       };
       for (int k = 0; k < total; ++k, cur.next()) {
         const BlockDesc &bd = cur.bd;
         if (cur.first() && !stage_q(cur)) break;
         const int s = k % NS;
-        const int key0 = cur.tile * kN;
+        const int j = cur.tile * kN + kk;
+        const bool keep = j >= bd.klo && j < bd.khi;
         uint4 bk[kPerK], bv[kPerV];
         uint32_t sk[kPerK], sv[kPerV];
-        auto fetch = [&](const uint8_t *krow, const uint8_t *vrow, bool per_key, bool live) {
+        auto fetch = [&](const uint8_t *krow, const uint8_t *vrow, bool live) {
 #pragma unroll
           for (int u = 0; u < kPerK; ++u) {
-            int kk, ch;
-            at(u, kKch, kk, ch);
-            const uint8_t *row = krow + (per_key ? 0 : kk * kKrow);
-            bk[u] = live ? *reinterpret_cast<const uint4 *>(row + ch * 16) : make_uint4(0u, 0u, 0u, 0u);
-            sk[u] = live ? *reinterpret_cast<const uint16_t *>(row + kDqk / 2 + ch * 2) : 0u;
+            const int ch = ch0 + 2 * u;
+            bk[u] = live ? *reinterpret_cast<const uint4 *>(krow + ch * 16) : make_uint4(0u, 0u, 0u, 0u);
+            sk[u] = live ? *reinterpret_cast<const uint16_t *>(krow + kDqk / 2 + ch * 2) : 0u;
           }
 #pragma unroll
           for (int u = 0; u < kPerV; ++u) {
-            int kk, ch;
-            at(u, kVch, kk, ch);
-            const uint8_t *row = vrow + (per_key ? 0 : kk * kVrow);
-            bv[u] = live ? *reinterpret_cast<const uint4 *>(row + ch * 16) : make_uint4(0u, 0u, 0u, 0u);
-            sv[u] = live ? *reinterpret_cast<const uint16_t *>(row + kDv / 2 + ch * 2) : 0u;
+            const int ch = ch0 + 2 * u;
+            bv[u] = live ? *reinterpret_cast<const uint4 *>(vrow + ch * 16) : make_uint4(0u, 0u, 0u, 0u);
+            sv[u] = live ? *reinterpret_cast<const uint16_t *>(vrow + kDv / 2 + ch * 2) : 0u;
           }
         };
         if constexpr (TMA) {
           const int t = k % NT;
           if (!tc::mbar_wait_warp(&bars.tma_full[t], (k / NT) & 1, &abort_flag)) break;
           const uint8_t *raw = smem + Lay::kOffRaw + t * kRawBytes;
-          fetch(raw, raw + kRawK, false, true);
+          fetch(raw + kk * kKrow, raw + kRawK + kk * kVrow, true);
           tc::fence_proxy_async_smem();
           tc::mbar_arrive(&bars.tma_empty[t]);
         } else {
           constexpr int R = Lay::kSlotRing > 0 ? Lay::kSlotRing : 1;   // 0 in TMA kernels (unused)
           const int r = k % R;
           if (!tc::mbar_wait_warp(&slot_bars->full[r], (k / R) & 1, &abort_flag)) break;
-          const int64_t slot = reinterpret_cast<const int64_t *>(smem + Lay::kOffSlots)[r * kN + (ct >> 1)];
+          const int64_t slot = reinterpret_cast<const int64_t *>(smem + Lay::kOffSlots)[r * kN + kk];
           tc::mbar_arrive(&slot_bars->empty[r]);
           const int64_t srow = (slot >= 0 ? slot : 0) * a.hkv + bd.g;
-          fetch(kc + srow * kKrow, vc + srow * kVrow, true, slot >= 0);
+          fetch(kc + srow * kKrow, vc + srow * kVrow, slot >= 0);
         }
         uint8_t *dst = smem + Lay::kOffOp + s * kOpBytes;
         uint64_t *kfree = TMA ? &bars.k_empty[s] : &bars.op_empty[s];
         if (k >= NS && !tc::mbar_wait_warp(kfree, ((k / NS) - 1) & 1, &abort_flag)) break;
 #pragma unroll
-        for (int u = 0; u < kPerK; ++u) {
-          int kk, ch;
-          at(u, kKch, kk, ch);
-          const int j = key0 + kk;
-          widen(dst, kk, ch, j >= bd.klo && j < bd.khi, bk[u], sk[u]);
-        }
+        for (int u = 0; u < kPerK; ++u) widen(dst, ch0 + 2 * u, keep, bk[u], sk[u]);
         if (TMA) {
           tc::fence_proxy_async_smem();
           tc::mbar_arrive(&bars.op_full[s]);
@@ -660,12 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
         }
 #pragma unroll
-        for (int u = 0; u < kPerV; ++u) {
-          int kk, ch;
-          at(u, kVch, kk, ch);
-          const int j = key0 + kk;
-          widen(dst + kOpK, kk, ch, j >= bd.klo && j < bd.khi, bv[u], sv[u]);
-        }
+        for (int u = 0; u < kPerV; ++u) widen(dst + kOpK, ch0 + 2 * u, keep, bv[u], sv[u]);
         tc::fence_proxy_async_smem();
         tc::mbar_arrive(TMA ? &bars.v_full[s] : &bars.op_full[s]);
       }
@@ -764,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // as long as the tensor pipe takes to accept it, so with one issuer P.V of
     // tile k would queue behind the whole Q.K^T of tile k+1.
     if ((tid & 31) == 0) {
-      const uint32_t id_s = tc::idesc_f16(1, 0, 0, kRows, kN);
+      const uint32_t id_s = tc::idesc_f16(F16 ? 0 : 1, 0, 0, kRows, kN);
       Cursor cs;
       cs.init(a.segs, a.blocks, head);
       // BF16 + TMA: interior tiles are consumed straight off the TMA barrier;
@@ -813,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 10) {
     // ------------------------------------------------------------ O += P.V issuer
     if ((tid & 31) == 0) {
-      const uint32_t id_pv = tc::idesc_f16(1, 0, 1, kRows, kDv);
+      const uint32_t id_pv = tc::idesc_f16(F16 ? 0 : 1, 0, 1, kRows, kDv);
       Cursor cp;
       cp.init(a.segs, a.blocks, head);
       for (int kp = 0; kp < total; ++kp, cp.next()) {
@@ -857,6 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Cursor cur;
     cur.init(a.segs, a.blocks, head);
     float m_run = -INFINITY, l_run = 0.f;
+    float row_sc = 0.f;            // F16: the row's score scale
     int row_lo = 0, row_hi = 0, rr = 0, rows_pad = kRows, col0 = 0, off = 0, len = kN, nc = kN;
     int zero_pending = 0;
     int row_tok = 0, row_h = 0;
@@ -909,7 +956,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int j_hi = min(off + len, row_hi - key0);
       const uint32_t taddr = tmem + lane_base + b * kN + col0;
       const int nch = nc >> 4;
-      const float sc = a.scale_log2;
+      const float sc = F16 ? row_sc : a.scale_log2;
       // P buffer b is free once P.V of tile k-2 is done
       if (k >= 2 && !wait(&bars.pv_done[b], ((k - 2) >> 1) & 1))
         return false;
@@ -981,13 +1028,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::fadd2(rs[2], rs[3], p0, p1);
           else
             tc::fadd2(rs[0], rs[1], p0, p1);
-          pk[j / 2] = cvt_pair(p0, p1);
+          pk[j / 2] = F16 ? f16_pair(p0, p1) : cvt_pair(p0, p1);
         }
         tc::tmem_st8(pcol + 8 * (g0 + c), pk);
       };
 #pragma unroll 1
       for (int pass = 0;; ++pass) {
-        const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+        const float neg_m = m_run == -INFINITY ? 0.f : F16 ? kLift - m_run : -m_run;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           rs[i] = 0.f;
@@ -1016,7 +1063,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc::fadd2(rs[2], rs[3], p0, p1);
             else
               tc::fadd2(rs[0], rs[1], p0, p1);
-            pk[j / 2] = cvt_pair(p0, p1);
+            pk[j / 2] = F16 ? f16_pair(p0, p1) : cvt_pair(p0, p1);
           }
           tc::tmem_st_16x32bx2_x16<16>(pcol, pk);
         } else {
@@ -1106,6 +1153,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait(&bars.s_full[b], (k >> 1) & 1)) break;
       if (t == 0 && k == 0) AKP_STAMP(kStampFirstS);
       tc::tc_fence_after();
+      if (F16 && cur.first())
+        row_sc = a.scale_log2 * __int_as_float((127 - (pos >= 0 ? sm_shift[cur.si & 3][pos] : 0)) << 23);
       if (!tile_body(k)) break;
       tc::tc_fence_before();
       tc::mbar_arrive(&bars.p_full[b]);
@@ -1121,6 +1170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         valid = valid && half == 0;
       }
       tc::tc_fence_after();
+      if (F16) l_run *= kUnlift;
       const SegDesc &sd = cur.sd;
       const bool single = bd.num_splits == 1;
       if (rows_pad == kRows) {
@@ -1138,12 +1188,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float MM = fmaxf(m_run, sig);
             if (MM != -INFINITY) {
               const float Z = l_run * exp2f(m_run - MM) + exp2f(sig - MM);
-              scale_o = exp2f(m_run - MM) * a.v_scale / Z;
+              scale_o = exp2f(m_run - MM) * a.v_scale / Z * kUnlift;
               lse = (MM + log2f(Z)) * kLn2;
             }
           } else {
-            scale_o = l_run > 0.f ? a.v_scale / l_run : 0.f;
-            lse = l_run > 0.f ? m_run + log2f(l_run) : -INFINITY;
+            const bool any = F16 ? l_run != 0.f : l_run > 0.f;      // F16: a NaN stays one
+            scale_o = any ? a.v_scale / l_run * kUnlift : 0.f;
+            lse = any ? m_run + log2f(l_run) : -INFINITY;
           }
           const int prow = bd.part_row_base + sd.split * bd.nrows + pos;
 #pragma unroll
@@ -1210,11 +1261,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float MM = fmaxf(M, sink2);
             if (MM != -INFINITY) {
               const float Z = L * exp2f(M - MM) + exp2f(sink2 - MM);
-              f = mine * exp2f(m_run - MM) * a.v_scale / Z;
+              f = mine * exp2f(m_run - MM) * a.v_scale / Z * kUnlift;
               lse = (MM + log2f(Z)) * kLn2;
             }
-          } else if (L > 0.f) {
-            f = mine * exp2f(m_run - M) * a.v_scale / L;
+          } else if (F16 ? L != 0.f : L > 0.f) {
+            f = mine * exp2f(m_run - M) * a.v_scale / L * kUnlift;
             lse = M + log2f(L);
           }
           if (pos < rows_pad) {          // copy 0 writes the row's log-sum-exp
