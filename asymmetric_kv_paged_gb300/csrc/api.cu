@@ -179,7 +179,6 @@ static attn_status_t plan_host(const attn_problem_t *problem, int32_t num_sms, b
     return st;
   }
   p->host.use_tma = akp::tc_tma_page_size(problem->page_size, problem->num_pages);
-  p->host.fp4_rows = akp::fp4_register_rows(p->host);
   *plan = p;
   return ATTN_OK;
 }
@@ -335,6 +334,7 @@ static attn_status_t run_impl(attn_plan_t plan, int phases, bool allow_stage, co
     r.window = pr.window;
     r.key_tile = hp.key_tile;
     r.lockstep = hp.lockstep;
+    r.whole_range = hp.whole_range;
     if (akp::launch_replan(r, st) != cudaSuccess) return ATTN_ERR_CUDA;
   }
   akp::TmaMaps stage_maps{};

@@ -73,9 +73,14 @@ template <int DQK, int NB>
 struct Cfg {
   static constexpr int kWarps = NB == 1 ? 12 : 8;
   static constexpr int kThreads = kWarps * 32;
-  static constexpr int kDepth = NB == 1 ? 2 : 3;     // units in a warp's ring
-  static constexpr int kOffComb = kWarps * kDepth * Unit<DQK>::kBytes;
-  static constexpr int kSmem = kOffComb + kWarps * NB * 8 * kCombStride * 4 + 1024;
+  static constexpr int kDepth = NB == 2 ? 3 : 2;     // units in a warp's ring
+  // 32-row blocks: Q's fragments in shared memory (O alone takes 128 registers)
+  static constexpr bool kQsmem = NB > 2;
+  static constexpr int kQBytes = kQsmem ? NB * (DQK / 16) * 32 * 8 : 0;
+  static constexpr int kCombRows = NB > 2 ? 16 : NB * 8;     // rows combined at a time
+  static constexpr int kOffQ = kWarps * kDepth * Unit<DQK>::kBytes;
+  static constexpr int kOffComb = kOffQ + kQBytes;
+  static constexpr int kSmem = kOffComb + kWarps * kCombRows * kCombStride * 4 + 1024;
   static_assert(kSmem + 3072 <= 227 * 1024, "shared memory layout too large");
 };
 
@@ -147,6 +152,7 @@ __global__ void __launch_bounds__(Cfg<DQK, NB>::kThreads, 1)
   __shared__ FBars bars;
   __shared__ int abort_flag;
   __shared__ float sm_m[kWarps][NB * 8], sm_l[kWarps][NB * 8];
+  __shared__ __align__(8) float sm_sc[C::kQsmem ? NB * 8 : 2];     // the rows' score scales
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // programmatic dependent: see attn_tc.cu
@@ -280,10 +286,10 @@ __global__ void __launch_bounds__(Cfg<DQK, NB>::kThreads, 1)
   {
     // ------------------------------------------------------------ attention
     const int g = lane >> 2, t = lane & 3;
-    uint32_t qf[NB][NJ * 4][2];
+    uint32_t qf[C::kQsmem ? 1 : NB][NJ * 4][2];
     float o[8][NB][4];
-    float m[NB][2], l[NB][2], sc[NB][2];
-    int row_lo[NB][2], row_hi[NB][2];
+    float m[NB][2], l[NB][2], sc[C::kQsmem ? 1 : NB][2];
+    uint2 *qsm = reinterpret_cast<uint2 *>(smem + C::kOffQ);      // [NB][NJ * 4][32 lanes]
     uint32_t sync_phase = 0;
     auto group_sync = [&]() -> bool {
       tc::mbar_arrive_warp(&bars.sync);
@@ -309,45 +315,61 @@ __global__ void __launch_bounds__(Cfg<DQK, NB>::kThreads, 1)
       const int i_last = bd.L - bd.n + (bd.row0 + bd.nrows - 1) / a.group;
       // keys every row sees
       const int all_lo = a.window > 0 ? max(0, i_last - a.window + 1) : 0, all_hi = i_first + 1;
+      // Row group nb as B fragments of fp16, scaled; returns this lane's row's shift.
+      auto load_q = [&](int nb, uint32_t (&f)[NJ * 4][2]) -> int {
+        const int r = nb * 8 + g;
+        uint32_t e = 0;
+        const bool live = r < bd.nrows;
+        const int flat = bd.row0 + (live ? r : 0);
+        const uint2 *src = reinterpret_cast<const uint2 *>(
+            static_cast<const uint16_t *>(a.q) +
+            ((int64_t)(bd.tok0 + flat / a.group) * a.hq + bd.g * a.group + flat % a.group) * DQK);
+#pragma unroll
+        for (int i = 0; i < NJ * 4; ++i) {
+          const uint2 v = live ? __ldg(src + (t + 4 * (i >> 2)) * 4 + (i & 3)) : make_uint2(0u, 0u);
+          f[i][0] = v.x;
+          f[i][1] = v.y;
+          e = max(e, max(max((v.x >> 7) & 0xFFu, (v.x >> 23) & 0xFFu),
+                         max((v.y >> 7) & 0xFFu, (v.y >> 23) & 0xFFu)));
+        }
+        e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
+        e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
+        const int sh = min(141 - (int)e, 126);
+        const float up = __int_as_float((sh + 127) << 23);
+#pragma unroll
+        for (int i = 0; i < NJ * 4; ++i)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t w = f[i][x];
+            f[i][x] = f16_pair(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xFFFF0000u) * up);
+          }
+        return sh;
+      };
+      if constexpr (C::kQsmem) {
+        // warp nb stages row group nb for all warps (the previous segment's
+        // combine has ended: nobody reads the old fragments any more)
+        if (warp < NB) {
+          uint32_t f[NJ * 4][2];
+          const int sh = load_q(warp, f);
+#pragma unroll
+          for (int i = 0; i < NJ * 4; ++i) qsm[(warp * NJ * 4 + i) * 32 + lane] = make_uint2(f[i][0], f[i][1]);
+          if (t == 0) sm_sc[warp * 8 + g] = a.scale_log2 * __int_as_float((127 - sh) << 23);
+        }
+        if (!group_sync()) break;
+      }
       if (has) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          const int r = nb * 8 + g;
-          uint32_t e = 0;
-          const bool live = r < bd.nrows;
-          const int flat = bd.row0 + (live ? r : 0);
-          const uint2 *src = reinterpret_cast<const uint2 *>(
-              static_cast<const uint16_t *>(a.q) +
-              ((int64_t)(bd.tok0 + flat / a.group) * a.hq + bd.g * a.group + flat % a.group) * DQK);
-#pragma unroll
-          for (int i = 0; i < NJ * 4; ++i) {
-            const uint2 v = live ? __ldg(src + (t + 4 * (i >> 2)) * 4 + (i & 3)) : make_uint2(0u, 0u);
-            qf[nb][i][0] = v.x;
-            qf[nb][i][1] = v.y;
-            e = max(e, max(max((v.x >> 7) & 0xFFu, (v.x >> 23) & 0xFFu),
-                           max((v.y >> 7) & 0xFFu, (v.y >> 23) & 0xFFu)));
-          }
-          e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
-          e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
-          const int sh = min(141 - (int)e, 126);
-          const float f = __int_as_float((sh + 127) << 23);
-#pragma unroll
-          for (int i = 0; i < NJ * 4; ++i)
+          if constexpr (!C::kQsmem) {
+            const int sh = load_q(nb, qf[nb]);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const uint32_t w = qf[nb][i][x];
-              qf[nb][i][x] = f16_pair(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
+              const int shr = __shfl_sync(0xffffffffu, sh, (2 * t + x) * 4);
+              sc[nb][x] = a.scale_log2 * __int_as_float((127 - shr) << 23);
             }
+          }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const int shr = __shfl_sync(0xffffffffu, sh, (2 * t + x) * 4);
-            sc[nb][x] = a.scale_log2 * __int_as_float((127 - shr) << 23);
-            // rows past the block have zero queries and are never written:
-            // any range does for them
-            const int rr = min(nb * 8 + 2 * t + x, bd.nrows - 1);
-            const int i = bd.L - bd.n + (bd.row0 + rr) / a.group;
-            row_hi[nb][x] = i + 1;
-            row_lo[nb][x] = a.window > 0 ? max(0, i - a.window + 1) : 0;
             m[nb][x] = -INFINITY;
             l[nb][x] = 0.f;
           }
@@ -377,41 +399,54 @@ __global__ void __launch_bounds__(Cfg<DQK, NB>::kThreads, 1)
         // ---- S^T = K . Q^T for 2 x 16 keys
         float sacc[2][NB][4];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int x = 0; x < 4; ++x) sacc[mt][nb][x] = 0.f;
-          const uint8_t *r0 = kt + (mt * 16 + g) * T::kKrow, *r1 = r0 + 8 * T::kKrow;
-          const uint4 w0 = *reinterpret_cast<const uint4 *>(r0 + DQK / 2);      // the rows' scales
-          const uint4 w1 = *reinterpret_cast<const uint4 *>(r1 + DQK / 2);
-          const uint32_t ws0[3] = {w0.x, w0.y, w0.z}, ws1[3] = {w1.x, w1.y, w1.z};
+        const uint8_t *krow = kt + g * T::kKrow;       // keys g, g + 8, g + 16, g + 24
+        uint32_t ws[4][NJ];                            // their scales
 #pragma unroll
-          for (int j = 0; j < NJ; ++j) {
-            const uint2 c0 = *reinterpret_cast<const uint2 *>(r0 + 8 * (t + 4 * j));
-            const uint2 c1 = *reinterpret_cast<const uint2 *>(r1 + 8 * (t + 4 * j));
-            // byte t of each row's scale word -> both rows' scales, doubled up
-            const uint32_t p2 = e4m3x2_to_f16(__byte_perm(ws0[j], ws1[j], t | (t + 4) << 4));
-            const uint32_t s0 = __byte_perm(p2, 0u, 0x1010), s1 = __byte_perm(p2, 0u, 0x3232);
-            uint32_t h0[8], h1[8];
-            {
-              uint32_t x[4];
-              e2m1x8_to_f16(c0.x, x);
-              h0[0] = x[0], h0[1] = x[1], h0[2] = x[2], h0[3] = x[3];
-              e2m1x8_to_f16(c0.y, x);
-              h0[4] = x[0], h0[5] = x[1], h0[6] = x[2], h0[7] = x[3];
-              e2m1x8_to_f16(c1.x, x);
-              h1[0] = x[0], h1[1] = x[1], h1[2] = x[2], h1[3] = x[3];
-              e2m1x8_to_f16(c1.y, x);
-              h1[4] = x[0], h1[5] = x[1], h1[6] = x[2], h1[7] = x[3];
-            }
+        for (int y = 0; y < 4; ++y) {
+          const uint4 w = *reinterpret_cast<const uint4 *>(krow + 8 * y * T::kKrow + DQK / 2);
+          ws[y][0] = w.x;
+          ws[y][1] = w.y;
+          if (NJ > 2) ws[y][NJ - 1] = w.z;
+        }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const uint32_t a0 = mul_f16x2(h0[2 * q], s0), a2 = mul_f16x2(h0[2 * q + 1], s0);
-              const uint32_t a1 = mul_f16x2(h1[2 * q], s1), a3 = mul_f16x2(h1[2 * q + 1], s1);
+        for (int j = 0; j < NJ; ++j) {
+          uint32_t h[4][8], s[4];
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
-                mma16816(sacc[mt][nb], a0, a1, a2, a3, qf[nb][4 * j + q][0], qf[nb][4 * j + q][1]);
+          for (int y = 0; y < 4; ++y) {
+            const uint2 c = *reinterpret_cast<const uint2 *>(krow + 8 * y * T::kKrow + 8 * (t + 4 * j));
+            uint32_t x[4];
+            e2m1x8_to_f16(c.x, x);
+            h[y][0] = x[0], h[y][1] = x[1], h[y][2] = x[2], h[y][3] = x[3];
+            e2m1x8_to_f16(c.y, x);
+            h[y][4] = x[0], h[y][5] = x[1], h[y][6] = x[2], h[y][7] = x[3];
+          }
+#pragma unroll
+          for (int y = 0; y < 4; y += 2) {
+            // byte t of two rows' scale words -> both scales, doubled up
+            const uint32_t p2 = e4m3x2_to_f16(__byte_perm(ws[y][j], ws[y + 1][j], t | (t + 4) << 4));
+            s[y] = __byte_perm(p2, 0u, 0x1010);
+            s[y + 1] = __byte_perm(p2, 0u, 0x3232);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint2 qs[NB];
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+              qs[nb] = C::kQsmem ? qsm[(nb * NJ * 4 + 4 * j + q) * 32 + lane]
+                                 : make_uint2(qf[C::kQsmem ? 0 : nb][4 * j + q][0], qf[C::kQsmem ? 0 : nb][4 * j + q][1]);
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) {
+              const uint32_t a0 = mul_f16x2(h[2 * mt][2 * q], s[2 * mt]);
+              const uint32_t a2 = mul_f16x2(h[2 * mt][2 * q + 1], s[2 * mt]);
+              const uint32_t a1 = mul_f16x2(h[2 * mt + 1][2 * q], s[2 * mt + 1]);
+              const uint32_t a3 = mul_f16x2(h[2 * mt + 1][2 * q + 1], s[2 * mt + 1]);
+#pragma unroll
+              for (int nb = 0; nb < NB; ++nb) mma16816(sacc[mt][nb], a0, a1, a2, a3, qs[nb].x, qs[nb].y);
             }
           }
         }
@@ -424,14 +459,24 @@ __global__ void __launch_bounds__(Cfg<DQK, NB>::kThreads, 1)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             float mx = -INFINITY;
+            const float scx = C::kQsmem ? sm_sc[nb * 8 + 2 * t + x] : sc[C::kQsmem ? 0 : nb][x];
+            int row_lo = 0, row_hi = 0;
+            if (!full) {
+              // (rows past the block have zero queries and are never written: any
+              // range does for them)
+              const int rr = min(nb * 8 + 2 * t + x, bd.nrows - 1);
+              const int i = bd.L - bd.n + (bd.row0 + rr) / a.group;
+              row_hi = i + 1;
+              row_lo = a.window > 0 ? max(0, i - a.window + 1) : 0;
+            }
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                float v = sacc[mt][nb][2 * h + x] * sc[nb][x];
+                float v = sacc[mt][nb][2 * h + x] * scx;
                 if (!full) {
                   const int j = key0 + mt * 16 + h * 8 + g;
-                  if (j < row_lo[nb][x] || j >= row_hi[nb][x]) v = -INFINITY;
+                  if (j < row_lo || j >= row_hi) v = -INFINITY;
                 }
                 sacc[mt][nb][2 * h + x] = v;
                 mx = fmaxf(mx, v);
@@ -530,32 +575,39 @@ __global__ void __launch_bounds__(Cfg<DQK, NB>::kThreads, 1)
       // sits at 16g + ((2i + 2(g / 2)) & 15): the 16 lanes of a half-warp write 32
       // different banks.
       float *comb = reinterpret_cast<float *>(smem + C::kOffComb);
-      if (has) {
-        float *dst = comb + warp * (NB * 8 * kCombStride);
+      bool synced = true;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+      for (int nb0 = 0; nb0 < NB; nb0 += C::kCombRows / 8) {
+      if (nb0 > 0 && nb0 * 8 >= bd.nrows) break;
+      if (nb0 > 0 && !(synced = group_sync())) break;     // the previous rows have been read
+      if (has) {
+        float *dst = comb + warp * (C::kCombRows * kCombStride);
+#pragma unroll
+        for (int nc = 0; nc < C::kCombRows / 8; ++nc)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
+            const int nb = nb0 + nc;
             float sum = l[nb][x];
             sum += __shfl_xor_sync(0xffffffffu, sum, 4);
             sum += __shfl_xor_sync(0xffffffffu, sum, 8);
             sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-            const int r = nb * 8 + 2 * t + x;
+            const int r = 2 * t + x;
             if (g == 0) {
-              sm_m[warp][r] = m[nb][x];
-              sm_l[warp][r] = sum;
+              sm_m[warp][nb * 8 + r] = m[nb][x];
+              sm_l[warp][nb * 8 + r] = sum;
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<float2 *>(dst + r * kCombStride + 16 * g + ((2 * i + 2 * (g >> 1)) & 15)) =
+              *reinterpret_cast<float2 *>(dst + (nc * 8 + r) * kCombStride + 16 * g +
+                                          ((2 * i + 2 * (g >> 1)) & 15)) =
                   make_float2(o[i][nb][x], o[i][nb][2 + x]);
           }
-      } else if (lane < NB * 8) {
-        sm_m[warp][lane] = -INFINITY;
+      } else if (lane < C::kCombRows) {
+        sm_m[warp][nb0 * 8 + lane] = -INFINITY;
       }
-      if (!group_sync()) break;
-      // warp w combines rows w and w + 8: lane owns dv 4 lane .. 4 lane + 3
-      for (int r = warp; r < bd.nrows; r += kWarps) {
+      if (!(synced = group_sync())) break;
+      // a warp combines whole rows: lane owns dv 4 lane .. 4 lane + 3
+      for (int r = nb0 * 8 + warp; r < min(bd.nrows, nb0 * 8 + C::kCombRows); r += kWarps) {
         const int flat = bd.row0 + r;
         const int tok = bd.tok0 + flat / a.group, h = bd.g * a.group + flat % a.group;
         const float sink2 = a.sinks && bd.num_splits == 1 ? __ldg(a.sinks + h) * kLog2e : -INFINITY;
@@ -573,7 +625,7 @@ __global__ void __launch_bounds__(Cfg<DQK, NB>::kThreads, 1)
             const float mw = sm_m[w][r];
             if (mw == -INFINITY) continue;             // nothing written by this warp
             const float f = exp2f(mw - M);
-            const float *src = comb + (w * NB * 8 + r) * kCombStride;
+            const float *src = comb + (w * C::kCombRows + r - nb0 * 8) * kCombStride;
             const float2 x = *reinterpret_cast<const float2 *>(src + p0);
             const float2 y = *reinterpret_cast<const float2 *>(src + p1);
             Lsum += f * sm_l[w][r];
@@ -609,6 +661,8 @@ __global__ void __launch_bounds__(Cfg<DQK, NB>::kThreads, 1)
           if (lane == 0) a.part_lse[prow] = Lsum == 0.f ? -INFINITY : M + log2f(Lsum * inv_lift);
         }
       }
+      }
+      if (!synced) break;
       u0 = u_end;
       // the buffer is free for the next segment once every warp has read it
       if (seg + 1 < head.seg_end && !group_sync()) break;
@@ -648,30 +702,35 @@ cudaError_t prepare_nb(const HostPlan &hp) {
   return hp.use_tma ? prepare_one<DQK, NB, true>() : prepare_one<DQK, NB, false>();
 }
 
-}  // namespace
 
-int32_t fp4_register_rows(const HostPlan &hp) {
-  if (hp.prob.kv_dtype != ATTN_KV_FP4_E2M1 || hp.prefill) return 0;
-  int32_t rows = 8;
-  for (const BlockDesc &b : hp.blocks) {
-    if (b.nrows > 16) return 0;
-    if (b.nrows > 8) rows = 16;
+
+template <int DQK>
+cudaError_t launch_dqk(const HostPlan &hp, const RunArgs &a, const TmaMaps &m, cudaStream_t st) {
+  switch (hp.fp4_rows) {
+    case 8: return launch_nb<DQK, 1>(hp, a, m, st);
+    case 16: return launch_nb<DQK, 2>(hp, a, m, st);
+    default: return launch_nb<DQK, 4>(hp, a, m, st);
   }
-  return rows;
 }
+
+template <int DQK>
+cudaError_t prepare_dqk(const HostPlan &hp) {
+  switch (hp.fp4_rows) {
+    case 8: return prepare_nb<DQK, 1>(hp);
+    case 16: return prepare_nb<DQK, 2>(hp);
+    default: return prepare_nb<DQK, 4>(hp);
+  }
+}
+
+}  // namespace
 
 cudaError_t launch_attn_fp4(const HostPlan &hp, const RunArgs &a, const TmaMaps &m, cudaStream_t st) {
   if (hp.num_ctas == 0) return cudaSuccess;
-  const bool one = hp.fp4_rows == 8;
-  if (hp.prob.head_dim_qk == kDqkSym)
-    return one ? launch_nb<kDqkSym, 1>(hp, a, m, st) : launch_nb<kDqkSym, 2>(hp, a, m, st);
-  return one ? launch_nb<kDqk, 1>(hp, a, m, st) : launch_nb<kDqk, 2>(hp, a, m, st);
+  return hp.prob.head_dim_qk == kDqkSym ? launch_dqk<kDqkSym>(hp, a, m, st) : launch_dqk<kDqk>(hp, a, m, st);
 }
 
 cudaError_t prepare_attn_fp4(const HostPlan &hp) {
-  const bool one = hp.fp4_rows == 8;
-  if (hp.prob.head_dim_qk == kDqkSym) return one ? prepare_nb<kDqkSym, 1>(hp) : prepare_nb<kDqkSym, 2>(hp);
-  return one ? prepare_nb<kDqk, 1>(hp) : prepare_nb<kDqk, 2>(hp);
+  return hp.prob.head_dim_qk == kDqkSym ? prepare_dqk<kDqkSym>(hp) : prepare_dqk<kDqk>(hp);
 }
 
 }  // namespace akp

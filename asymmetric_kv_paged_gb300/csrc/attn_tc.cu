@@ -100,7 +100,7 @@ struct Layout {
   // copy-combine buffer of the epilogue: MR rows x 32 fp32 columns
   static constexpr int kCombBytes = MR * 32 * 4;
   static constexpr int kOpStages = RAW ? (MR == 64 ? 3 : 2) : (TMA || MR == 64 ? 4 : 3);
-  static constexpr int kRawStages = RAW ? 3 : 0;
+  static constexpr int kRawStages = KV == kE2m1 ? 4 : RAW ? 3 : 0;
   static constexpr int kOffOp = kQBufs * kQBytes;
   static constexpr int kOffRaw = kOffOp + kOpStages * kOpBytes;
   static constexpr int kOffComb = kOffRaw + kRawStages * kRawBytes;
@@ -667,28 +667,29 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = k % NS;
         const int j = cur.tile * kN + kk;
         const bool keep = j >= bd.klo && j < bd.khi;
-        uint4 bk[kPerK], bv[kPerV];
-        uint32_t sk[kPerK], sv[kPerV];
-        auto fetch = [&](const uint8_t *krow, const uint8_t *vrow, bool live) {
-#pragma unroll
-          for (int u = 0; u < kPerK; ++u) {
-            const int ch = ch0 + 2 * u;
-            bk[u] = live ? *reinterpret_cast<const uint4 *>(krow + ch * 16) : make_uint4(0u, 0u, 0u, 0u);
-            sk[u] = live ? *reinterpret_cast<const uint16_t *>(krow + kDqk / 2 + ch * 2) : 0u;
-          }
-#pragma unroll
-          for (int u = 0; u < kPerV; ++u) {
-            const int ch = ch0 + 2 * u;
-            bv[u] = live ? *reinterpret_cast<const uint4 *>(vrow + ch * 16) : make_uint4(0u, 0u, 0u, 0u);
-            sv[u] = live ? *reinterpret_cast<const uint16_t *>(vrow + kDv / 2 + ch * 2) : 0u;
-          }
-        };
         if constexpr (TMA) {
           const int t = k % NT;
           if (!tc::mbar_wait_warp(&bars.tma_full[t], (k / NT) & 1, &abort_flag)) break;
-          const uint8_t *raw = smem + Lay::kOffRaw + t * kRawBytes;
-          fetch(raw + kk * kKrow, raw + kRawK + kk * kVrow, true);
+          const uint8_t *krow = smem + Lay::kOffRaw + t * kRawBytes + kk * kKrow;
+          const uint8_t *vrow = smem + Lay::kOffRaw + t * kRawBytes + kRawK + kk * kVrow;
+          uint8_t *dst = smem + Lay::kOffOp + s * kOpBytes;
+          // rolled: a chunk's ~60 instructions stay in the instruction cache that
+          // three warp roles share
+          if (k >= NS && !tc::mbar_wait_warp(&bars.k_empty[s], ((k / NS) - 1) & 1, &abort_flag)) break;
+#pragma unroll 1
+          for (int ch = ch0; ch < kDqk / 32; ch += 2)
+            widen(dst, ch, keep, *reinterpret_cast<const uint4 *>(krow + ch * 16),
+                  *reinterpret_cast<const uint16_t *>(krow + kDqk / 2 + ch * 2));
           tc::fence_proxy_async_smem();
+          tc::mbar_arrive(&bars.op_full[s]);
+          if (k >= NS && !tc::mbar_wait_warp(&bars.op_empty[s], ((k / NS) - 1) & 1, &abort_flag)) break;
+          dst += kOpK;
+#pragma unroll 1
+          for (int ch = ch0; ch < kDv / 32; ch += 2)
+            widen(dst, ch, keep, *reinterpret_cast<const uint4 *>(vrow + ch * 16),
+                  *reinterpret_cast<const uint16_t *>(vrow + kDv / 2 + ch * 2));
+          tc::fence_proxy_async_smem();
+          tc::mbar_arrive(&bars.v_full[s]);
           tc::mbar_arrive(&bars.tma_empty[t]);
         } else {
           constexpr int R = Lay::kSlotRing > 0 ? Lay::kSlotRing : 1;   // 0 in TMA kernels (unused)
@@ -697,23 +698,30 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int64_t slot = reinterpret_cast<const int64_t *>(smem + Lay::kOffSlots)[r * kN + kk];
           tc::mbar_arrive(&slot_bars->empty[r]);
           const int64_t srow = (slot >= 0 ? slot : 0) * a.hkv + bd.g;
-          fetch(kc + srow * kKrow, vc + srow * kVrow, slot >= 0);
-        }
-        uint8_t *dst = smem + Lay::kOffOp + s * kOpBytes;
-        uint64_t *kfree = TMA ? &bars.k_empty[s] : &bars.op_empty[s];
-        if (k >= NS && !tc::mbar_wait_warp(kfree, ((k / NS) - 1) & 1, &abort_flag)) break;
+          const uint8_t *krow = kc + srow * kKrow, *vrow = vc + srow * kVrow;
+          uint4 bk[kPerK], bv[kPerV];
+          uint32_t sk[kPerK], sv[kPerV];
 #pragma unroll
-        for (int u = 0; u < kPerK; ++u) widen(dst, ch0 + 2 * u, keep, bk[u], sk[u]);
-        if (TMA) {
+          for (int u = 0; u < kPerK; ++u) {
+            const int ch = ch0 + 2 * u;
+            bk[u] = slot >= 0 ? *reinterpret_cast<const uint4 *>(krow + ch * 16) : make_uint4(0u, 0u, 0u, 0u);
+            sk[u] = slot >= 0 ? *reinterpret_cast<const uint16_t *>(krow + kDqk / 2 + ch * 2) : 0u;
+          }
+#pragma unroll
+          for (int u = 0; u < kPerV; ++u) {
+            const int ch = ch0 + 2 * u;
+            bv[u] = slot >= 0 ? *reinterpret_cast<const uint4 *>(vrow + ch * 16) : make_uint4(0u, 0u, 0u, 0u);
+            sv[u] = slot >= 0 ? *reinterpret_cast<const uint16_t *>(vrow + kDv / 2 + ch * 2) : 0u;
+          }
+          uint8_t *dst = smem + Lay::kOffOp + s * kOpBytes;
+          if (k >= NS && !tc::mbar_wait_warp(&bars.op_empty[s], ((k / NS) - 1) & 1, &abort_flag)) break;
+#pragma unroll
+          for (int u = 0; u < kPerK; ++u) widen(dst, ch0 + 2 * u, keep, bk[u], sk[u]);
+#pragma unroll
+          for (int u = 0; u < kPerV; ++u) widen(dst + kOpK, ch0 + 2 * u, keep, bv[u], sv[u]);
           tc::fence_proxy_async_smem();
           tc::mbar_arrive(&bars.op_full[s]);
-          if (k >= NS && !tc::mbar_wait_warp(&bars.op_empty[s], ((k / NS) - 1) & 1, &abort_flag))
-            break;
         }
-#pragma unroll
-        for (int u = 0; u < kPerV; ++u) widen(dst + kOpK, ch0 + 2 * u, keep, bv[u], sv[u]);
-        tc::fence_proxy_async_smem();
-        tc::mbar_arrive(TMA ? &bars.v_full[s] : &bars.op_full[s]);
       }
     } else {
     uint32_t edge_parity = 0;   // BF16 + TMA: completed edge tiles per stage (one bit each)

@@ -73,9 +73,8 @@ cudaError_t launch_attn_tc(const HostPlan &hp, const RunArgs &a, const TmaMaps &
                            cudaStream_t stream);
 // One-time per-device kernel attributes (dynamic shared memory limits).
 cudaError_t prepare_attn_tc(const HostPlan &hp);
-// Plans over a 4-bit cache whose blocks have at most 16 rows (hp.fp4_rows > 0):
-// attn_fp4.cu.  `maps` is read only when hp.use_tma.
-int32_t fp4_register_rows(const HostPlan &hp);
+// Plans over a 4-bit cache with hp.fp4_rows > 0: attn_fp4.cu.  `maps` is read
+// only when hp.use_tma.
 cudaError_t launch_attn_fp4(const HostPlan &hp, const RunArgs &a, const TmaMaps &maps,
                             cudaStream_t stream);
 cudaError_t prepare_attn_fp4(const HostPlan &hp);

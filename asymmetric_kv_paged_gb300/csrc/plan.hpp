@@ -14,6 +14,7 @@ constexpr int kDqkSym = 128;    // query/key head dim of the symmetric pair 128/
 constexpr int kDv = 128;        // value head dim
 constexpr int kKeyTile = 64;    // keys per pipeline tile (decode / verify kernel)
 constexpr int kFp4UnitKeys = 32;  // keys a warp of attn_fp4.cu takes at a time
+constexpr int kFp4MaxRows = 16;   // rows of a (request, KV head) that attn_fp4.cu takes
 constexpr int kPrefillKeyTile = 128;   // keys per tile of the prefill kernel
 
 // Query rows per row block.  A block packs up to block_rows query rows of one
@@ -74,12 +75,14 @@ struct HostPlan {
   int32_t block_rows = 128;      // 64 or 128 (the MMA M), or 256 (prefill kernel)
   int32_t key_tile = kKeyTile;   // keys per tile: 64, or 128 for the prefill kernel
   bool prefill = false;          // block_rows == 256: attn_prefill.cu runs the plan
-  // rows per block of the register-operand 4-bit kernel (attn_fp4.cu): 8 or 16;
-  // 0: attn_tc.cu or attn_prefill.cu runs the plan
+  // rows per block of the register-operand 4-bit kernel (attn_fp4.cu): 8, 16 or
+  // 32; 0: attn_tc.cu or attn_prefill.cu runs the plan
   int32_t fp4_rows = 0;
-  // KV heads dealt alike, CTA c working on head c % lockstep (4-bit plans;
-  // 1: one deal over all blocks), see planner.cpp
+  // KV heads (with 32-row blocks: row groups of KV heads) dealt alike, CTA c
+  // working on the c % lockstep-th (4-bit plans; 1: one deal over all blocks),
+  // see planner.cpp
   int32_t lockstep = 1;
+  bool whole_range = false;      // blocks take their request's whole key range
   bool one_copy = false;         // every block has more than block_rows / 2 rows
   int32_t num_sms = 0, num_ctas = 0, threads = 0;
   std::vector<BlockDesc> blocks;
