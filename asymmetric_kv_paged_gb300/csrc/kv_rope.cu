@@ -18,12 +18,15 @@
 // E2M1(y / block scale), nearest even, saturating at 6 (all zeros under a zero
 // scale; a block that holds a NaN gets the NaN scale).  Quotients are IEEE fp32.
 //
-// One thread per 16 consecutive values of a K or V row (a whole scale block)
-// and per rotated pair of 8-value chunks of a query row; the CTA's threads walk
-// the units of its tokens, so that the request, position and cache slot of a
-// token are looked up by every warp once, in three dependent loads (all of
-// qo_indptr at once, the length, the page).  Bound by HBM for large chunks and
-// by the launch and those loads for decode-sized ones.
+// A unit of work is 16 values: a scale block of a K or V row, or two 8-value
+// chunks of a query row (the two halves of eight rotated pairs; 16 interleaved
+// values; two chunks that are only copied).  Warps are the workers: each takes a
+// range of consecutive tokens and every S-th 32-unit step of them, S chosen so that
+// all SMs' warps have work (decode: a step or two each; long chunks: whole
+// tokens), so that the chain of dependent lookups (request, length, page) is
+// walked once per range and not once per step, and the query loop keeps four
+// steps' loads in flight.  Bound by HBM for large chunks (the queries are most of
+// the bytes), by the launch and the lookups for decode-sized ones.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -51,10 +54,10 @@ struct RopeAppendArgs {
   const int32_t *page_table, *seq_lens, *qo_indptr, *positions;
   const float *cos_sin;
   int32_t *err;
-  int32_t tokens, tok_per_cta, units;     // units: of one token
+  int32_t tokens, chunks, slices;         // token ranges, and warps sharing each (see the top)
   int32_t batch, hq, hkv, page_size, pt_stride, num_pages;
   int32_t max_pos, rot, rot_off;
-  int32_t q_units, q_pairs;               // per query row: all, and the rotated ones (first)
+  int32_t q_units, q_turned;              // units per query row: all, and the rotated ones (first)
   float k_scale, v_scale;
 };
 
@@ -187,8 +190,66 @@ __device__ __forceinline__ uint2 quantise16(const float (&v)[16], float tensor_s
   return make_uint2(out[0], out[1]);
 }
 
+// The request of consecutive rows of a prefix-sum array, in registers: found by a
+// search once, then only when a row lies past its end.
+struct Request {
+  int b = -1, first = 0, end = 0;      // rows [first, end)
+  __device__ __forceinline__ bool seek(const int32_t *indptr, int batch, int64_t row) {
+    if (b >= 0 && row < end) return false;
+    b = request_of(indptr, batch, row);
+    if (b < batch) {
+      first = __ldg(indptr + b);
+      end = __ldg(indptr + b + 1);
+    }
+    return true;
+  }
+};
+
+// 16 values of a K or V row into the cache.
+template <int KV, int ROPE, int D>
+__device__ __forceinline__ void append_unit(const RopeAppendArgs &a, const uint16_t *src, uint8_t *dst, int c,
+                                            const float *cs, float scale) {
+  const uint4 raw[2] = {__ldg(reinterpret_cast<const uint4 *>(src) + 2 * c),
+                        __ldg(reinterpret_cast<const uint4 *>(src) + 2 * c + 1)};
+  float v[2][8];
+  bool turned[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) turned[h] = rotated_chunk<ROPE>(a, src, 16 * c + 8 * h, cs, raw[h], v[h]);
+  if (KV == ATTN_KV_BF16) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) reinterpret_cast<uint4 *>(dst)[2 * c + h] = turned[h] ? pack8(v[h]) : raw[h];
+  } else if (KV == ATTN_KV_FP8_E4M3) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float *x = &v[e >> 1][4 * (e & 1)];
+      uint16_t lo, hi;
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n"
+          : "=h"(lo) : "f"(__fdiv_rn(x[1], scale)), "f"(__fdiv_rn(x[0], scale)));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n"
+          : "=h"(hi) : "f"(__fdiv_rn(x[3], scale)), "f"(__fdiv_rn(x[2], scale)));
+      w[e] = (uint32_t)lo | ((uint32_t)hi << 16);
+    }
+    reinterpret_cast<uint4 *>(dst)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    constexpr int kGroups = D / kE2m1Block, kPad = e2m1_row_bytes(D) - D / 2 - kGroups;
+    static_assert(kPad == 4 || kPad == 8, "4-bit row padding");
+    float x[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x[j] = v[j >> 3][j & 7];
+    uint32_t s;
+    reinterpret_cast<uint2 *>(dst)[c] = quantise16(x, scale, s);
+    dst[D / 2 + c] = (uint8_t)s;
+    if (c == kGroups - 1) {                // the row's padding
+      uint32_t *pad = reinterpret_cast<uint32_t *>(dst + D / 2 + kGroups);
+      pad[0] = 0u;
+      if (kPad > 4) pad[1] = 0u;
+    }
+  }
+}
+
 template <int KV, int ROPE, int DQK>
-__global__ void __launch_bounds__(kAppendThreads) rope_append_kernel(const RopeAppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, 4) rope_append_kernel(const RopeAppendArgs a) {
   // A programmatic dependent of the stream's previous kernel: nothing is read
   // or written before that kernel has completed.  The kernels that follow in a
   // serving step (device planner, attention) may be scheduled now; they wait
@@ -196,126 +257,118 @@ __global__ void __launch_bounds__(kAppendThreads) rope_append_kernel(const RopeA
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   constexpr int kKGroups = DQK / kE2m1Block;
-  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int worker = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+  const int chunk = worker / a.slices, slice = worker % a.slices;
+  if (chunk >= a.chunks) return;
   const int k_units = a.hkv * kKGroups, kv_units = k_units + a.hkv * kVGroups;
-  const int tok0 = blockIdx.x * a.tok_per_cta;
-  const int ntok = min(a.tok_per_cta, a.tokens - tok0);
-  // The CTA's units in token order; a warp takes 32 consecutive units of one
-  // token (the last step of a token may leave lanes idle).
-  const int steps = (a.units + 31) >> 5;
-  for (int w = warp; w < ntok * steps; w += kAppendThreads / 32) {
-    const int tok = tok0 + w / steps;
-    const int unit = (w % steps) * 32 + (threadIdx.x & 31);
-    const int b = request_of(a.qo_indptr, a.batch, tok);
-    const int q0 = __ldg(a.qo_indptr + b), n = __ldg(a.qo_indptr + b + 1) - q0;
-    const int64_t i = (int64_t)__ldg(a.seq_lens + b) - n + (tok - q0);
+  const int q_units = a.hq * a.q_units, stride = 32 * a.slices;
+  const int tok_end = (int)((int64_t)(chunk + 1) * a.tokens / a.chunks);
+  Request rq;
+  int64_t shift = 0;                         // position of token tok: tok + shift
+  for (int tok = (int)((int64_t)chunk * a.tokens / a.chunks); tok < tok_end; ++tok) {
+    if (rq.seek(a.qo_indptr, a.batch, tok)) shift = (int64_t)__ldg(a.seq_lens + rq.b) - rq.end;
+    const int64_t i = tok + shift;
     const float *cs = nullptr;
     if (ROPE != kNoRope) {
       const int64_t pos = a.positions ? (int64_t)__ldg(a.positions + tok) : i;
       if (pos < 0 || pos >= a.max_pos) {            // no row of the table: the token is skipped
-        if (unit == 0) atomicOr(a.err, 8);
+        if (slice == 0 && lane == 0) atomicOr(a.err, 8);
         continue;
       }
       cs = a.cos_sin + pos * a.rot;
     }
-    if (unit >= a.units) continue;
-    if (unit >= kv_units) {
-      // ---- a query row: rotated pairs of chunks first, then the chunks copied
-      const int r = unit - kv_units;
-      const int h = r / a.q_units, u = r % a.q_units;
-      const int64_t row = ((int64_t)tok * a.hq + h) * DQK;
-      const uint16_t *src = a.q + row;
-      uint16_t *dst = a.q_out + row;
-      if (u < a.q_pairs) {
-        const int half = a.rot >> 1;
-        if (ROPE == kPairs) {
-          const int d = a.rot_off + 8 * u;
-          float v[8];
-          unpack8(*reinterpret_cast<const uint4 *>(src + d), v);
-          rotate_pairs(v, cs + 4 * u, half);
-          *reinterpret_cast<uint4 *>(dst + d) = pack8(v);
+    // ---- K and V
+    int64_t slot = -1;
+    if (slice * 32 < kv_units) {
+      int bad = 0;
+      if (i < 0 || i / a.page_size >= a.pt_stride) {   // a length outside the table row
+        bad = 4;
+      } else {
+        const int32_t page = __ldg(a.page_table + (int64_t)rq.b * a.pt_stride + i / a.page_size);
+        if (page < 0 || page >= a.num_pages)
+          bad = 1;
+        else
+          slot = (int64_t)page * a.page_size + i % a.page_size;
+      }
+      if (bad && slice == 0 && lane == 0) atomicOr(a.err, bad);
+    }
+    if (slot >= 0) {
+      for (int unit = slice * 32 + lane; unit < kv_units; unit += stride) {
+        if (unit < k_units) {
+          const int g = unit / kKGroups, c = unit % kKGroups;
+          append_unit<KV, ROPE, DQK>(a, a.k_new + ((int64_t)tok * a.hkv + g) * DQK,
+                                     static_cast<uint8_t *>(a.k_cache) + (slot * a.hkv + g) * kv_row_bytes(KV, DQK),
+                                     c, cs, a.k_scale);
         } else {
-          // both chunks of the pair are read before either is written (q_out may be q)
-          const int d = a.rot_off + 8 * u;
-          float x1[8], x2[8], c[8], s[8], o1[8], o2[8];
-          unpack8(*reinterpret_cast<const uint4 *>(src + d), x1);
-          unpack8(*reinterpret_cast<const uint4 *>(src + d + half), x2);
-          load8f(cs + 8 * u, c);
-          load8f(cs + half + 8 * u, s);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            o1[j] = rot_sub(x1[j], c[j], x2[j], s[j]);
-            o2[j] = rot_add(x2[j], c[j], x1[j], s[j]);
-          }
-          *reinterpret_cast<uint4 *>(dst + d) = pack8(o1);
-          *reinterpret_cast<uint4 *>(dst + d + half) = pack8(o2);
+          const int g = (unit - k_units) / kVGroups, c = (unit - k_units) % kVGroups;
+          append_unit<KV, kNoRope, kDv>(a, a.v_new + ((int64_t)tok * a.hkv + g) * kDv,
+                                        static_cast<uint8_t *>(a.v_cache) + (slot * a.hkv + g) * kv_row_bytes(KV, kDv),
+                                        c, cs, a.v_scale);
         }
-      } else {
-        int d = 8 * (u - a.q_pairs);
-        if (d >= a.rot_off) d += a.rot;
-        *reinterpret_cast<uint4 *>(dst + d) = *reinterpret_cast<const uint4 *>(src + d);
-      }
-      continue;
-    }
-    // ---- 16 values of a K or V row
-    const bool is_k = unit < k_units;
-    const int r = is_k ? unit : unit - k_units;
-    const int groups = is_k ? kKGroups : kVGroups, D = is_k ? DQK : kDv;
-    const int g = r / groups, c = r % groups;
-    const uint16_t *src = (is_k ? a.k_new : a.v_new) + ((int64_t)tok * a.hkv + g) * D;
-    const uint4 raw[2] = {__ldg(reinterpret_cast<const uint4 *>(src) + 2 * c),
-                          __ldg(reinterpret_cast<const uint4 *>(src) + 2 * c + 1)};
-    if (i < 0 || i / a.page_size >= a.pt_stride) {   // a length outside the table row
-      if (unit == 0) atomicOr(a.err, 4);
-      continue;
-    }
-    const int32_t page = __ldg(a.page_table + (int64_t)b * a.pt_stride + i / a.page_size);
-    if (page < 0 || page >= a.num_pages) {
-      if (unit == 0) atomicOr(a.err, 1);
-      continue;
-    }
-    const int64_t crow = ((int64_t)page * a.page_size + i % a.page_size) * a.hkv + g;
-    uint8_t *dst = static_cast<uint8_t *>(is_k ? a.k_cache : a.v_cache) + crow * kv_row_bytes(KV, D);
-    float v[2][8];
-    bool turned[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (is_k) {
-        turned[h] = rotated_chunk<ROPE>(a, src, 16 * c + 8 * h, cs, raw[h], v[h]);
-      } else {
-        unpack8(raw[h], v[h]);
-        turned[h] = false;
       }
     }
-    const float scale = is_k ? a.k_scale : a.v_scale;
-    if (KV == ATTN_KV_BF16) {
+    // ---- the query rows: rotated units first in each row, then the copied ones
+    if constexpr (ROPE != kNoRope) {
+      const int half = a.rot >> 1;
+      const int64_t row0 = (int64_t)tok * a.hq * DQK;
+      constexpr int kAhead = 2;
+#pragma unroll 1
+      for (int u0 = slice * 32 + lane; u0 < q_units; u0 += kAhead * stride) {
+        uint4 x[kAhead][2];
+        int at[kAhead][2], un[kAhead];             // offsets in the token's rows, unit in the row
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        reinterpret_cast<uint4 *>(dst)[2 * c + h] = turned[h] ? pack8(v[h]) : raw[h];
-    } else if (KV == ATTN_KV_FP8_E4M3) {
-      uint32_t w[4];
+        for (int k = 0; k < kAhead; ++k) {
+          const int unit = u0 + k * stride;
+          un[k] = -1;
+          if (unit < q_units) {
+            const int h = unit / a.q_units, u = unit % a.q_units;
+            un[k] = u;
+            if (u < a.q_turned) {
+              at[k][0] = a.rot_off + (ROPE == kPairs ? 16 : 8) * u;
+              at[k][1] = at[k][0] + (ROPE == kPairs ? 8 : half);
+            } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float *x = &v[e >> 1][4 * (e & 1)];
-        uint16_t lo, hi;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n"
-            : "=h"(lo) : "f"(__fdiv_rn(x[1], scale)), "f"(__fdiv_rn(x[0], scale)));
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n"
-            : "=h"(hi) : "f"(__fdiv_rn(x[3], scale)), "f"(__fdiv_rn(x[2], scale)));
-        w[e] = (uint32_t)lo | ((uint32_t)hi << 16);
-      }
-      reinterpret_cast<uint4 *>(dst)[c] = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      float x[16];
+              for (int y = 0; y < 2; ++y) {
+                const int d = 16 * (u - a.q_turned) + 8 * y;
+                at[k][y] = d < a.rot_off ? d : d + a.rot;
+              }
+            }
+            at[k][0] += h * DQK;
+            at[k][1] += h * DQK;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) x[j] = v[j >> 3][j & 7];
-      uint32_t s;
-      reinterpret_cast<uint2 *>(dst)[c] = quantise16(x, scale, s);
-      dst[D / 2 + c] = (uint8_t)s;
-      if (c == groups - 1) {               // the row's padding
-        uint32_t *pad = reinterpret_cast<uint32_t *>(dst + D / 2 + groups);
-        pad[0] = 0u;
-        if (e2m1_row_bytes(D) - D / 2 - groups > 4) pad[1] = 0u;
+            for (int y = 0; y < 2; ++y) x[k][y] = *reinterpret_cast<const uint4 *>(a.q + row0 + at[k][y]);
+          }
+        }
+        // a unit's two chunks are read before either is written (q_out may be q)
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+          if (un[k] < 0) continue;
+          if (un[k] < a.q_turned) {
+            float x1[8], x2[8];
+            unpack8(x[k][0], x1);
+            unpack8(x[k][1], x2);
+            const float *c8 = cs + 8 * un[k];
+            if (ROPE == kPairs) {
+              rotate_pairs(x1, c8, half);
+              rotate_pairs(x2, c8 + 4, half);
+            } else {
+              float c[8], sn[8];
+              load8f(c8, c);
+              load8f(c8 + half, sn);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float y1 = x1[j], y2 = x2[j];
+                x1[j] = rot_sub(y1, c[j], y2, sn[j]);
+                x2[j] = rot_add(y2, c[j], y1, sn[j]);
+              }
+            }
+            x[k][0] = pack8(x1);
+            x[k][1] = pack8(x2);
+          }
+#pragma unroll
+          for (int y = 0; y < 2; ++y) *reinterpret_cast<uint4 *>(a.q_out + row0 + at[k][y]) = x[k][y];
+        }
       }
     }
   }
@@ -326,96 +379,101 @@ struct ReadArgs {
   const int32_t *page_table, *seq_lens, *kv_indptr;
   uint16_t *k_out, *v_out;
   int32_t *err;
-  int64_t rows;
-  int32_t rows_per_cta, units;
+  int32_t rows, chunks, slices;          // as for the append's tokens
   int32_t batch, hkv, page_size, pt_stride, num_pages;
   float k_scale, v_scale;
 };
 
-// Cached rows as bfloat16: one thread per 16 values, the rows of request b its
-// last kv_indptr[b + 1] - kv_indptr[b] positions.
+// 16 cached values as bfloat16.
+template <int KV, int D>
+__device__ __forceinline__ void read_unit(const uint8_t *src, int c, float scale, uint4 (&o)[2]) {
+  if (KV == ATTN_KV_BF16) {
+    o[0] = __ldg(reinterpret_cast<const uint4 *>(src) + 2 * c);
+    o[1] = __ldg(reinterpret_cast<const uint4 *>(src) + 2 * c + 1);
+    return;
+  }
+  uint32_t h[8];                           // 16 values as fp16 pairs, exact
+  if (KV == ATTN_KV_FP8_E4M3) {
+    uint4 lo, hi;
+    e4m3x16_to_f16(__ldg(reinterpret_cast<const uint4 *>(src) + c), lo, hi);
+    h[0] = lo.x; h[1] = lo.y; h[2] = lo.z; h[3] = lo.w;
+    h[4] = hi.x; h[5] = hi.y; h[6] = hi.z; h[7] = hi.w;
+  } else {
+    const uint2 q = __ldg(reinterpret_cast<const uint2 *>(src) + c);
+    uint32_t s0, s1, p[4], u[4];
+    e4m3_scales_f16(__ldg(src + D / 2 + c), s0, s1);
+    e2m1x8_to_f16(q.x, p);
+    e2m1x8_to_f16(q.y, u);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      h[e] = mul_f16x2(p[e], s0);
+      h[4 + e] = mul_f16x2(u[e], s0);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      asm("{\n .reg .b16 l, u;\n mov.b32 {l, u}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, u;\n}\n"
+          : "=f"(v[2 * j]), "=f"(v[2 * j + 1])
+          : "r"(h[4 * e + j]));
+      v[2 * j] = __fmul_rn(v[2 * j], scale);
+      v[2 * j + 1] = __fmul_rn(v[2 * j + 1], scale);
+    }
+    o[e] = pack8(v);
+  }
+}
+
+// Cached rows as bfloat16, 16 values a unit; the rows of request b are its last
+// kv_indptr[b + 1] - kv_indptr[b] positions.  Work is split as for the append.
 template <int KV, int DQK>
-__global__ void __launch_bounds__(kAppendThreads) read_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, 4) read_kernel(const ReadArgs a) {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   constexpr int kKGroups = DQK / kE2m1Block;
-  const int warp = threadIdx.x >> 5;
-  const int k_units = a.hkv * kKGroups;
-  const int steps = (a.units + 31) >> 5;
-  const int64_t row0 = (int64_t)blockIdx.x * a.rows_per_cta;
-  const int nrow = (int)min((int64_t)a.rows_per_cta, a.rows - row0);
-  for (int w = warp; w < nrow * steps; w += kAppendThreads / 32) {
-    const int64_t t = row0 + w / steps;
-    const int unit = (w % steps) * 32 + (threadIdx.x & 31);
-    const int b = request_of(a.kv_indptr, a.batch, t);
+  const int lane = threadIdx.x & 31;
+  const int worker = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+  const int chunk = worker / a.slices, slice = worker % a.slices;
+  if (chunk >= a.chunks) return;
+  const int k_units = a.hkv * kKGroups, kv_units = k_units + a.hkv * kVGroups;
+  const int row_end = (int)((int64_t)(chunk + 1) * a.rows / a.chunks);
+  Request rq;
+  int64_t shift = 0;
+  for (int row = (int)((int64_t)chunk * a.rows / a.chunks); row < row_end; ++row) {
+    if (rq.seek(a.kv_indptr, a.batch, row) && rq.b < a.batch)
+      shift = (int64_t)__ldg(a.seq_lens + rq.b) - rq.end;
     int64_t slot = -1;
-    int bad = 0;
-    if (b < a.batch) {
-      const int32_t r0 = __ldg(a.kv_indptr + b), r1 = __ldg(a.kv_indptr + b + 1);
-      const int64_t i = (int64_t)__ldg(a.seq_lens + b) - r1 + t;
-      if (t < r0 || i < 0 || i / a.page_size >= a.pt_stride) {
-        bad = 4;
-      } else {
-        const int32_t page = __ldg(a.page_table + (int64_t)b * a.pt_stride + i / a.page_size);
-        if (page >= 0 && page < a.num_pages)
-          slot = (int64_t)page * a.page_size + i % a.page_size;
-        else
-          bad = 1;
-      }
-    } else {
-      bad = 4;                                   // more rows than kv_indptr holds
-    }
-    if (bad && unit == 0) atomicOr(a.err, bad);
-    if (unit >= a.units) continue;
-    const bool is_k = unit < k_units;
-    const int r = is_k ? unit : unit - k_units;
-    const int groups = is_k ? kKGroups : kVGroups, D = is_k ? DQK : kDv;
-    const int g = r / groups, c = r % groups;
-    uint4 *dst = reinterpret_cast<uint4 *>((is_k ? a.k_out : a.v_out) + (t * a.hkv + g) * D) + 2 * c;
-    uint4 o[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-    if (slot >= 0) {
-      const uint8_t *src = static_cast<const uint8_t *>(is_k ? a.k_cache : a.v_cache) +
-                           (slot * a.hkv + g) * kv_row_bytes(KV, D);
-      const float scale = is_k ? a.k_scale : a.v_scale;
-      if (KV == ATTN_KV_BF16) {
-        o[0] = __ldg(reinterpret_cast<const uint4 *>(src) + 2 * c);
-        o[1] = __ldg(reinterpret_cast<const uint4 *>(src) + 2 * c + 1);
-      } else {
-        uint32_t h[8];                           // 16 values as fp16 pairs, exact
-        if (KV == ATTN_KV_FP8_E4M3) {
-          uint4 lo, hi;
-          e4m3x16_to_f16(__ldg(reinterpret_cast<const uint4 *>(src) + c), lo, hi);
-          h[0] = lo.x; h[1] = lo.y; h[2] = lo.z; h[3] = lo.w;
-          h[4] = hi.x; h[5] = hi.y; h[6] = hi.z; h[7] = hi.w;
-        } else {
-          const uint2 q = __ldg(reinterpret_cast<const uint2 *>(src) + c);
-          uint32_t s0, s1, p[4], u[4];
-          e4m3_scales_f16(src[D / 2 + c], s0, s1);
-          e2m1x8_to_f16(q.x, p);
-          e2m1x8_to_f16(q.y, u);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            h[e] = mul_f16x2(p[e], s0);
-            h[4 + e] = mul_f16x2(u[e], s0);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float v[8];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            asm("{\n .reg .b16 l, u;\n mov.b32 {l, u}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, u;\n}\n"
-                : "=f"(v[2 * j]), "=f"(v[2 * j + 1])
-                : "r"(h[4 * e + j]));
-            v[2 * j] = __fmul_rn(v[2 * j], scale);
-            v[2 * j + 1] = __fmul_rn(v[2 * j + 1], scale);
-          }
-          o[e] = pack8(v);
-        }
+    int bad = 4;                                  // more rows than kv_indptr holds, or no such position
+    if (rq.b < a.batch) {
+      const int64_t i = row + shift;
+      if (row >= rq.first && i >= 0 && i / a.page_size < a.pt_stride) {
+        const int32_t page = __ldg(a.page_table + (int64_t)rq.b * a.pt_stride + i / a.page_size);
+        bad = page >= 0 && page < a.num_pages ? 0 : 1;
+        if (!bad) slot = (int64_t)page * a.page_size + i % a.page_size;
       }
     }
-    dst[0] = o[0];
-    dst[1] = o[1];
+    if (bad && slice == 0 && lane == 0) atomicOr(a.err, bad);
+#pragma unroll 2
+    for (int unit = slice * 32 + lane; unit < kv_units; unit += 32 * a.slices) {
+      uint4 o[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
+      uint4 *dst;
+      if (unit < k_units) {
+        const int g = unit / kKGroups, c = unit % kKGroups;
+        dst = reinterpret_cast<uint4 *>(a.k_out + ((int64_t)row * a.hkv + g) * DQK) + 2 * c;
+        if (slot >= 0)
+          read_unit<KV, DQK>(static_cast<const uint8_t *>(a.k_cache) + (slot * a.hkv + g) * kv_row_bytes(KV, DQK),
+                             c, a.k_scale, o);
+      } else {
+        const int g = (unit - k_units) / kVGroups, c = (unit - k_units) % kVGroups;
+        dst = reinterpret_cast<uint4 *>(a.v_out + ((int64_t)row * a.hkv + g) * kDv) + 2 * c;
+        if (slot >= 0)
+          read_unit<KV, kDv>(static_cast<const uint8_t *>(a.v_cache) + (slot * a.hkv + g) * kv_row_bytes(KV, kDv),
+                             c, a.v_scale, o);
+      }
+      dst[0] = o[0];
+      dst[1] = o[1];
+    }
   }
 }
 
@@ -434,28 +492,31 @@ struct OnDevice {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Rows (tokens) a CTA takes: enough for each of its warps to have a step, and
-// no more than leave every SM a CTA.
-int rows_per_cta(int64_t rows, int units) {
-  const int steps = (units + 31) / 32;
-  int64_t per = std::max<int64_t>(1, (kAppendThreads / 32) / steps);
-  per = std::min<int64_t>(per, std::max<int64_t>(1, rows / 152));
-  return (int)std::max<int64_t>(per, (rows + INT32_MAX - 1) / INT32_MAX);
-}
+// Splits `rows` of `steps` 32-unit steps each among the warps that all SMs hold:
+// ranges of rows, and the warps that share a range's steps.
+struct Split {
+  int32_t chunks, slices;
+  unsigned ctas;
+  Split(int64_t rows, int64_t steps) {
+    constexpr int64_t kWarps = 152 * 4 * (kAppendThreads / 32);
+    slices = (int32_t)std::max<int64_t>(1, std::min(steps, kWarps / std::max<int64_t>(rows, 1)));
+    chunks = (int32_t)std::min<int64_t>(rows, std::max<int64_t>(1, kWarps / slices));
+    ctas = (unsigned)(((int64_t)chunks * slices + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
+  }
+};
 
 template <int KV, int ROPE>
-cudaError_t launch_append(const RopeAppendArgs &a, int dqk, cudaStream_t st) {
-  const dim3 grid((unsigned)((a.tokens + a.tok_per_cta - 1) / a.tok_per_cta));
+cudaError_t launch_append(const RopeAppendArgs &a, int dqk, dim3 grid, cudaStream_t st) {
   return dqk == kDqk ? launch_dependent(rope_append_kernel<KV, ROPE, kDqk>, grid, dim3(kAppendThreads), 0, st, a)
                      : launch_dependent(rope_append_kernel<KV, ROPE, kDqkSym>, grid, dim3(kAppendThreads), 0, st, a);
 }
 
 template <int ROPE>
-cudaError_t launch_append_kv(const RopeAppendArgs &a, int kv, int dqk, cudaStream_t st) {
+cudaError_t launch_append_kv(const RopeAppendArgs &a, int kv, int dqk, dim3 grid, cudaStream_t st) {
   switch (kv) {
-    case ATTN_KV_BF16: return launch_append<ATTN_KV_BF16, ROPE>(a, dqk, st);
-    case ATTN_KV_FP8_E4M3: return launch_append<ATTN_KV_FP8_E4M3, ROPE>(a, dqk, st);
-    default: return launch_append<ATTN_KV_FP4_E2M1, ROPE>(a, dqk, st);
+    case ATTN_KV_BF16: return launch_append<ATTN_KV_BF16, ROPE>(a, dqk, grid, st);
+    case ATTN_KV_FP8_E4M3: return launch_append<ATTN_KV_FP8_E4M3, ROPE>(a, dqk, grid, st);
+    default: return launch_append<ATTN_KV_FP4_E2M1, ROPE>(a, dqk, grid, st);
   }
 }
 
@@ -506,7 +567,8 @@ attn_status_t append_rows(attn_plan_t plan, const attn_rope_t *rope, const void 
   a.num_pages = pr.num_pages;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
-  a.units = pr.num_kv_heads * (pr.head_dim_qk / kE2m1Block + kVGroups);
+  const int64_t kv_units = (int64_t)pr.num_kv_heads * (pr.head_dim_qk / kE2m1Block + kVGroups);
+  int64_t q_units = 0;
   if (rope) {
     a.cos_sin = rope->cos_sin;
     a.positions = rope->positions;
@@ -516,19 +578,21 @@ attn_status_t append_rows(attn_plan_t plan, const attn_rope_t *rope, const void 
     if (q) {
       a.q = static_cast<const uint16_t *>(q);
       a.q_out = static_cast<uint16_t *>(q_out);
-      a.q_pairs = rope->interleaved ? rope->rot_dim / 8 : rope->rot_dim / 16;
+      a.q_turned = rope->rot_dim / 16;
       // in place, the dims that are not rotated stay where they are
-      a.q_units = a.q_pairs + (q == q_out ? 0 : (pr.head_dim_qk - rope->rot_dim) / 8);
-      a.units += pr.num_q_heads * a.q_units;
+      a.q_units = q == q_out ? a.q_turned : pr.head_dim_qk / 16;
+      q_units = (int64_t)pr.num_q_heads * a.q_units;
     }
   }
-  a.tok_per_cta = rows_per_cta(total_q, a.units);
+  const Split sp(total_q, (std::max(kv_units, q_units) + 31) / 32);
+  a.chunks = sp.chunks;
+  a.slices = sp.slices;
   OnDevice dev(plan->device);
   if (!dev.ok) return ATTN_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = !rope               ? launch_append_kv<kNoRope>(a, pr.kv_dtype, pr.head_dim_qk, st)
-                        : rope->interleaved ? launch_append_kv<kPairs>(a, pr.kv_dtype, pr.head_dim_qk, st)
-                                            : launch_append_kv<kHalves>(a, pr.kv_dtype, pr.head_dim_qk, st);
+  const cudaError_t e = !rope               ? launch_append_kv<kNoRope>(a, pr.kv_dtype, pr.head_dim_qk, dim3(sp.ctas), st)
+                        : rope->interleaved ? launch_append_kv<kPairs>(a, pr.kv_dtype, pr.head_dim_qk, dim3(sp.ctas), st)
+                                            : launch_append_kv<kHalves>(a, pr.kv_dtype, pr.head_dim_qk, dim3(sp.ctas), st);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -565,7 +629,7 @@ extern "C" attn_status_t attn_read_kv(attn_plan_t plan, const void *k_cache, con
   a.k_out = static_cast<uint16_t *>(k_out);
   a.v_out = static_cast<uint16_t *>(v_out);
   a.err = plan->dev.err;
-  a.rows = rows;
+  a.rows = (int32_t)rows;
   a.batch = pr.batch;
   a.hkv = pr.num_kv_heads;
   a.page_size = pr.page_size;
@@ -573,11 +637,12 @@ extern "C" attn_status_t attn_read_kv(attn_plan_t plan, const void *k_cache, con
   a.num_pages = pr.num_pages;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
-  a.units = pr.num_kv_heads * (pr.head_dim_qk / akp::kE2m1Block + akp::kVGroups);
-  a.rows_per_cta = akp::rows_per_cta(rows, a.units);
+  const akp::Split sp(rows, ((int64_t)pr.num_kv_heads * (pr.head_dim_qk / akp::kE2m1Block + akp::kVGroups) + 31) / 32);
+  a.chunks = sp.chunks;
+  a.slices = sp.slices;
   akp::OnDevice dev(plan->device);
   if (!dev.ok) return ATTN_ERR_CUDA;
-  const dim3 grid((unsigned)((rows + a.rows_per_cta - 1) / a.rows_per_cta)), block(akp::kAppendThreads);
+  const dim3 grid(sp.ctas), block(akp::kAppendThreads);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool wide = pr.head_dim_qk == akp::kDqk;
   cudaError_t e;
