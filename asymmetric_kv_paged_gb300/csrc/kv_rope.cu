@@ -18,15 +18,17 @@
 // E2M1(y / block scale), nearest even, saturating at 6 (all zeros under a zero
 // scale; a block that holds a NaN gets the NaN scale).  Quotients are IEEE fp32.
 //
-// A unit of work is 16 values: a scale block of a K or V row, or two 8-value
-// chunks of a query row (the two halves of eight rotated pairs; 16 interleaved
-// values; two chunks that are only copied).  Warps are the workers: each takes a
-// range of consecutive tokens and every S-th 32-unit step of them, S chosen so that
-// all SMs' warps have work (decode: a step or two each; long chunks: whole
-// tokens), so that the chain of dependent lookups (request, length, page) is
-// walked once per range and not once per step, and the query loop keeps four
-// steps' loads in flight.  Bound by HBM for large chunks (the queries are most of
-// the bytes), by the launch and the lookups for decode-sized ones.
+// A warp takes a whole row at a time (two of 128 values), a lane one 16-byte
+// chunk of 8 values of it: loads and stores of a row are contiguous, the partner
+// chunk of a rotated half comes from another lane by shuffle, a lane pair shares a
+// scale block, and the angles of a lane's dims are the same for every head of the
+// token, so that they are loaded once per token and stay in registers.  Each warp
+// owns a range of consecutive tokens and every S-th row step of them, S chosen so
+// that all SMs' warps have work (decode: a row each; long chunks: whole tokens),
+// which walks the chain of dependent lookups (request, length, page) once per
+// range and not once per row; the query loop keeps four rows' loads in flight.
+// Bound by HBM for large chunks (the queries are most of the bytes), by the launch
+// and the lookups for decode-sized ones.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -44,7 +46,6 @@ namespace akp {
 namespace {
 
 constexpr int kAppendThreads = 256;
-constexpr int kVGroups = kDv / kE2m1Block;
 enum { kNoRope = 0, kHalves = 1, kPairs = 2 };
 
 struct RopeAppendArgs {
@@ -57,7 +58,6 @@ struct RopeAppendArgs {
   int32_t tokens, chunks, slices;         // token ranges, and warps sharing each (see the top)
   int32_t batch, hq, hkv, page_size, pt_stride, num_pages;
   int32_t max_pos, rot, rot_off;
-  int32_t q_units, q_turned;              // units per query row: all, and the rotated ones (first)
   float k_scale, v_scale;
 };
 
@@ -100,56 +100,70 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ void load8f(const float *p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
+// What a lane's chunk does under the rotation, for the token at hand.
+template <int ROPE, int NC>
+struct Turn {
+  bool in = false;                // the chunk's dims are rotated
+  int partner = 0;                // kHalves: the lane with the other half's chunk
+  float c[ROPE == kHalves ? 8 : 4], s[ROPE == kHalves ? 8 : 4];
+  int at = 0;                     // first cosine of the chunk
+  float sign = 1.f;
 
-__device__ __forceinline__ float rot_sub(float a, float c, float b, float s) {
-  return __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-}
-__device__ __forceinline__ float rot_add(float a, float c, float b, float s) {
-  return __fadd_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-}
-
-// Interleaved pairs of one 8-value chunk, in place; cs points at the chunk's
-// first cosine, the sines are `half` further.
-__device__ __forceinline__ void rotate_pairs(float (&v)[8], const float *cs, int half) {
-  const float4 c4 = __ldg(reinterpret_cast<const float4 *>(cs));
-  const float4 s4 = __ldg(reinterpret_cast<const float4 *>(cs + half));
-  const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float x1 = v[2 * i], x2 = v[2 * i + 1];
-    v[2 * i] = rot_sub(x1, c[i], x2, s[i]);
-    v[2 * i + 1] = rot_add(x2, c[i], x1, s[i]);
+  __device__ __forceinline__ void place(const RopeAppendArgs &a, int lane) {
+    if (ROPE == kNoRope) return;
+    const int half = a.rot >> 1, r = 8 * (lane % NC) - a.rot_off;
+    in = r >= 0 && r < a.rot;
+    partner = lane;
+    if (ROPE == kHalves) {
+      const bool first = r < half;
+      at = first ? r : r - half;
+      sign = first ? -1.f : 1.f;            // x1 c - x2 s, x2 c + x1 s
+      if (in) partner = first ? lane + half / 8 : lane - half / 8;
+    } else {
+      at = r >> 1;
+    }
   }
-}
-
-// One 8-value chunk of a K row from dim d on, rotated if it lies in the rotated
-// dims (returns whether it does; `raw` is the chunk as it stands).
-template <int ROPE>
-__device__ __forceinline__ bool rotated_chunk(const RopeAppendArgs &a, const uint16_t *row, int d,
-                                              const float *cs, uint4 raw, float (&v)[8]) {
-  unpack8(raw, v);
-  if (ROPE == kNoRope || d < a.rot_off || d >= a.rot_off + a.rot) return false;
-  const int half = a.rot >> 1, r = d - a.rot_off;
-  if (ROPE == kPairs) {
-    rotate_pairs(v, cs + (r >> 1), half);
-  } else {
-    const bool first = r < half;
-    const int i = first ? r : r - half;
-    float w[8], c[8], s[8];
-    unpack8(__ldg(reinterpret_cast<const uint4 *>(row + (first ? d + half : d - half))), w);
-    load8f(cs + i, c);
-    load8f(cs + half + i, s);
+  __device__ __forceinline__ void angles(const RopeAppendArgs &a, int64_t pos) {
+    if (ROPE == kNoRope) return;
+    constexpr int N = ROPE == kHalves ? 2 : 1;
+    const float *row = a.cos_sin + pos * a.rot + at;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      v[j] = first ? rot_sub(v[j], c[j], w[j], s[j]) : rot_add(v[j], c[j], w[j], s[j]);
+    for (int p = 0; p < N; ++p) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+      if (in) {
+        x = __ldg(reinterpret_cast<const float4 *>(row) + p);
+        y = __ldg(reinterpret_cast<const float4 *>(row + (a.rot >> 1)) + p);
+      }
+      c[4 * p] = x.x, c[4 * p + 1] = x.y, c[4 * p + 2] = x.z, c[4 * p + 3] = x.w;
+      s[4 * p] = sign * y.x, s[4 * p + 1] = sign * y.y, s[4 * p + 2] = sign * y.z, s[4 * p + 3] = sign * y.w;
+    }
   }
-  return true;
-}
+  // v = the lane's chunk, rotated; every lane of the warp calls it (shuffles).
+  // Products and sums are rounded one by one (a - b s = a + b (-s) exactly).
+  __device__ __forceinline__ void apply(const uint4 raw, float (&v)[8]) const {
+    unpack8(raw, v);
+    if (ROPE == kHalves) {
+      uint4 o;
+      o.x = __shfl_sync(0xffffffffu, raw.x, partner);
+      o.y = __shfl_sync(0xffffffffu, raw.y, partner);
+      o.z = __shfl_sync(0xffffffffu, raw.z, partner);
+      o.w = __shfl_sync(0xffffffffu, raw.w, partner);
+      float w[8];
+      unpack8(o, w);
+      if (in)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(__fmul_rn(v[j], c[j]), __fmul_rn(w[j], s[j]));
+    } else if (ROPE == kPairs) {
+      if (in)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float x1 = v[2 * j], x2 = v[2 * j + 1];
+          v[2 * j] = __fsub_rn(__fmul_rn(x1, c[j]), __fmul_rn(x2, s[j]));
+          v[2 * j + 1] = __fadd_rn(__fmul_rn(x2, c[j]), __fmul_rn(x1, s[j]));
+        }
+    }
+  }
+};
 
 // One E4M3 code of a non-negative value (nearest even, saturating; NaN: 0x7F).
 __device__ __forceinline__ uint32_t e4m3_of(float x) {
@@ -158,36 +172,77 @@ __device__ __forceinline__ uint32_t e4m3_of(float x) {
   return r & 0xFFu;
 }
 
-// 16 values -> 16 E2M1 codes (8 bytes) and their E4M3 scale.
-__device__ __forceinline__ uint2 quantise16(const float (&v)[16], float tensor_scale, uint32_t &scale) {
-  float y[16], amax = 0.f;
-  bool nan = false;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    y[i] = __fdiv_rn(v[i], tensor_scale);
-    amax = fmaxf(amax, fabsf(y[i]));
-    nan |= y[i] != y[i];
+// Quotients v / s as the IEEE fp32 ones, or as values that round to the same E4M3
+// or E2M1 code.  With r the correctly rounded reciprocal of s, q = RN(v r) and the
+// exact remainder v - q s (one fused multiply-add), RN(q + remainder r) is the
+// correctly rounded quotient (Markstein's theorem) as long as nothing under- or
+// overflows: |v| <= 2^60 and s within 2^+-40 leave only quotients below 2^-60
+// unproven, which round to zero codes with v's sign either way.  Anything else
+// (also infinities and NaN) takes the division instruction sequence.
+struct Divisor {
+  float s, r;
+  bool plain;                     // s is in the range above
+  __device__ __forceinline__ explicit Divisor(float s_) : s(s_), r(1.f / s_) {
+    plain = s >= 0x1p-40f && s <= 0x1p40f;
   }
-  scale = nan ? 0x7Fu : e4m3_of(__fdiv_rn(amax, 6.f));
-  uint32_t h2, out[2] = {0u, 0u};
-  asm("{\n .reg .b16 s;\n cvt.u16.u32 s, %1;\n cvt.rn.f16x2.e4m3x2 %0, s;\n}\n" : "=r"(h2) : "r"(scale));
-  float s;
-  asm("{\n .reg .b16 l, u;\n mov.b32 {l, u}, %1;\n cvt.f32.f16 %0, l;\n}\n" : "=f"(s) : "r"(h2));
-  if (scale != 0u && !nan) {
+  __device__ __forceinline__ float plainly(float v) const {      // v's sign kept, also of zeros
+    const float q = v * r;
+    const float e = __fmaf_rn(__fmaf_rn(-q, s, v), r, q);
+    return __uint_as_float((__float_as_uint(e) & 0x7FFFFFFFu) | (__float_as_uint(v) & 0x80000000u));
+  }
+};
+
+// The largest magnitude of 8 values as fp32 bits (a NaN is above everything).
+__device__ __forceinline__ uint32_t top_bits(const float (&v)[8]) {
+  uint32_t t = 0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+  for (int j = 0; j < 8; ++j) t = max(t, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  return t;
+}
+constexpr uint32_t kPlainTop = 0x5D800000u;      // 2^60
+constexpr uint32_t kInfBits = 0x7F800000u;
+
+__device__ __forceinline__ void divide8(float (&v)[8], const Divisor &d, uint32_t top) {
+  if (d.plain && top <= kPlainTop) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = d.plainly(v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __fdiv_rn(v[j], d.s);
+  }
+}
+
+// A lane's 8 values of a 4-bit row (its scale block's other 8 are in lane ^ 1):
+// the codes (4 bytes) and the block's scale.  Every lane of the warp calls it.
+// Rounding is monotonic, so the largest quotient is the quotient of the largest.
+__device__ __forceinline__ uint32_t quantise8(float (&y)[8], const Divisor &tensor, uint32_t &scale) {
+  uint32_t top = top_bits(y);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  const bool nan = top > kInfBits;
+  const float amax = __fdiv_rn(__uint_as_float(top), tensor.s);
+  scale = nan ? 0x7Fu : e4m3_of(__fdiv_rn(amax, 6.f));
+  uint32_t out = 0u;
+  if (scale != 0u && !nan) {
+    divide8(y, tensor, top);
+    uint32_t h2;
+    asm("{\n .reg .b16 s;\n cvt.u16.u32 s, %1;\n cvt.rn.f16x2.e4m3x2 %0, s;\n}\n" : "=r"(h2) : "r"(scale));
+    float s;
+    asm("{\n .reg .b16 l, u;\n mov.b32 {l, u}, %1;\n cvt.f32.f16 %0, l;\n}\n" : "=f"(s) : "r"(h2));
+    divide8(y, Divisor(s), __float_as_uint(amax));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
       uint32_t b;
       asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n cvt.u32.u8 %0, t;\n}\n"
           : "=r"(b)
-          : "f"(__fdiv_rn(y[2 * i + 1], s)), "f"(__fdiv_rn(y[2 * i], s)));
-      out[i >> 2] |= b << (8 * (i & 3));
+          : "f"(y[2 * i + 1]), "f"(y[2 * i]));
+      out |= b << (8 * i);
     }
   } else {
-    // no value below half the smallest step keeps more than its sign
+    // under a zero scale every value is below half the smallest step: its sign stays
 #pragma unroll
-    for (int i = 0; i < 16; ++i) out[i >> 3] |= (__float_as_uint(y[i]) >> 31) << (4 * (i & 7) + 3);
+    for (int i = 0; i < 8; ++i) out |= (__float_as_uint(y[i]) >> 31) << (4 * i + 3);
   }
-  return make_uint2(out[0], out[1]);
+  return out;
 }
 
 // The request of consecutive rows of a prefix-sum array, in registers: found by a
@@ -205,45 +260,68 @@ struct Request {
   }
 };
 
-// 16 values of a K or V row into the cache.
-template <int KV, int ROPE, int D>
-__device__ __forceinline__ void append_unit(const RopeAppendArgs &a, const uint16_t *src, uint8_t *dst, int c,
-                                            const float *cs, float scale) {
-  const uint4 raw[2] = {__ldg(reinterpret_cast<const uint4 *>(src) + 2 * c),
-                        __ldg(reinterpret_cast<const uint4 *>(src) + 2 * c + 1)};
-  float v[2][8];
-  bool turned[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) turned[h] = rotated_chunk<ROPE>(a, src, 16 * c + 8 * h, cs, raw[h], v[h]);
+// Rows of D values as a warp takes them: RPW rows a step, lane % NC the chunk.
+template <int D>
+struct Lanes {
+  static constexpr int NC = D / 8, RPW = 32 / NC;
+};
+
+// The lane's chunk (v: rotated values, raw: as it stands) into a cached row.
+// Every lane of the warp calls it; `live` lanes have a chunk.
+template <int KV, int D>
+__device__ __forceinline__ void store_chunk(uint8_t *row, int ch, bool live, bool turned, const uint4 raw,
+                                            float (&v)[8], const Divisor &scale) {
   if (KV == ATTN_KV_BF16) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) reinterpret_cast<uint4 *>(dst)[2 * c + h] = turned[h] ? pack8(v[h]) : raw[h];
+    if (live) reinterpret_cast<uint4 *>(row)[ch] = turned ? pack8(v) : raw;
   } else if (KV == ATTN_KV_FP8_E4M3) {
-    uint32_t w[4];
+    divide8(v, scale, top_bits(v));
+    uint32_t w[2];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float *x = &v[e >> 1][4 * (e & 1)];
+    for (int e = 0; e < 2; ++e) {
       uint16_t lo, hi;
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n"
-          : "=h"(lo) : "f"(__fdiv_rn(x[1], scale)), "f"(__fdiv_rn(x[0], scale)));
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n"
-          : "=h"(hi) : "f"(__fdiv_rn(x[3], scale)), "f"(__fdiv_rn(x[2], scale)));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(lo) : "f"(v[4 * e + 1]), "f"(v[4 * e]));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(hi) : "f"(v[4 * e + 3]), "f"(v[4 * e + 2]));
       w[e] = (uint32_t)lo | ((uint32_t)hi << 16);
     }
-    reinterpret_cast<uint4 *>(dst)[c] = make_uint4(w[0], w[1], w[2], w[3]);
+    if (live) reinterpret_cast<uint2 *>(row)[ch] = make_uint2(w[0], w[1]);
   } else {
     constexpr int kGroups = D / kE2m1Block, kPad = e2m1_row_bytes(D) - D / 2 - kGroups;
     static_assert(kPad == 4 || kPad == 8, "4-bit row padding");
-    float x[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] = v[j >> 3][j & 7];
     uint32_t s;
-    reinterpret_cast<uint2 *>(dst)[c] = quantise16(x, scale, s);
-    dst[D / 2 + c] = (uint8_t)s;
-    if (c == kGroups - 1) {                // the row's padding
-      uint32_t *pad = reinterpret_cast<uint32_t *>(dst + D / 2 + kGroups);
-      pad[0] = 0u;
-      if (kPad > 4) pad[1] = 0u;
+    const uint32_t codes = quantise8(v, scale, s);
+    if (live) {
+      reinterpret_cast<uint32_t *>(row)[ch] = codes;
+      if (!(ch & 1)) row[D / 2 + ch / 2] = (uint8_t)s;
+      if (ch < kPad / 4) reinterpret_cast<uint32_t *>(row + D / 2 + kGroups)[ch] = 0u;
+    }
+  }
+}
+
+// The new rows of one token (K: D = DQK, rotated; V: D = 128, as they are):
+// every `slices`-th step from `slice` on, two steps' loads ahead.
+template <int KV, int ROPE, int D>
+__device__ __forceinline__ void append_rows_of(const uint16_t *src, uint8_t *dst, int heads, int slice, int slices,
+                                               const Turn<ROPE, Lanes<D>::NC> &turn, const Divisor &scale) {
+  constexpr int NC = Lanes<D>::NC, RPW = Lanes<D>::RPW, kAhead = 2;
+  const int lane = threadIdx.x & 31, sub = lane / NC, ch = lane % NC;
+  const int steps = (heads + RPW - 1) / RPW;
+#pragma unroll 1
+  for (int st0 = slice; st0 < steps; st0 += kAhead * slices) {
+    uint4 x[kAhead];
+    int h[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      h[k] = (st0 + k * slices) * RPW + sub;
+      if (sub >= RPW || h[k] >= heads) h[k] = -1;
+      x[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (h[k] >= 0) x[k] = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)h[k] * D) + ch);
+    }
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (st0 + k * slices >= steps) break;
+      float v[8];
+      turn.apply(x[k], v);
+      store_chunk<KV, D>(dst + (int64_t)max(h[k], 0) * kv_row_bytes(KV, D), ch, h[k] >= 0, turn.in, x[k], v, scale);
     }
   }
 }
@@ -256,31 +334,32 @@ __global__ void __launch_bounds__(kAppendThreads, 4) rope_append_kernel(const Ro
   // for this grid.
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  constexpr int kKGroups = DQK / kE2m1Block;
-  const int lane = threadIdx.x & 31;
+  constexpr int NC = Lanes<DQK>::NC, RPW = Lanes<DQK>::RPW;
+  const int lane = threadIdx.x & 31, sub = lane / NC, ch = lane % NC;
   const int worker = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
   const int chunk = worker / a.slices, slice = worker % a.slices;
   if (chunk >= a.chunks) return;
-  const int k_units = a.hkv * kKGroups, kv_units = k_units + a.hkv * kVGroups;
-  const int q_units = a.hq * a.q_units, stride = 32 * a.slices;
+  Turn<ROPE, NC> turn;
+  turn.place(a, lane);
+  const Turn<kNoRope, Lanes<kDv>::NC> as_is{};
+  const Divisor k_scale(a.k_scale), v_scale(a.v_scale);
   const int tok_end = (int)((int64_t)(chunk + 1) * a.tokens / a.chunks);
   Request rq;
   int64_t shift = 0;                         // position of token tok: tok + shift
   for (int tok = (int)((int64_t)chunk * a.tokens / a.chunks); tok < tok_end; ++tok) {
     if (rq.seek(a.qo_indptr, a.batch, tok)) shift = (int64_t)__ldg(a.seq_lens + rq.b) - rq.end;
     const int64_t i = tok + shift;
-    const float *cs = nullptr;
     if (ROPE != kNoRope) {
       const int64_t pos = a.positions ? (int64_t)__ldg(a.positions + tok) : i;
       if (pos < 0 || pos >= a.max_pos) {            // no row of the table: the token is skipped
         if (slice == 0 && lane == 0) atomicOr(a.err, 8);
         continue;
       }
-      cs = a.cos_sin + pos * a.rot;
+      turn.angles(a, pos);
     }
-    // ---- K and V
-    int64_t slot = -1;
-    if (slice * 32 < kv_units) {
+    // ---- K and V (a step of heads or fewer: the last slices may have none)
+    if (slice < a.hkv) {
+      int64_t slot = -1;
       int bad = 0;
       if (i < 0 || i / a.page_size >= a.pt_stride) {   // a length outside the table row
         bad = 4;
@@ -292,82 +371,41 @@ __global__ void __launch_bounds__(kAppendThreads, 4) rope_append_kernel(const Ro
           slot = (int64_t)page * a.page_size + i % a.page_size;
       }
       if (bad && slice == 0 && lane == 0) atomicOr(a.err, bad);
-    }
-    if (slot >= 0) {
-      for (int unit = slice * 32 + lane; unit < kv_units; unit += stride) {
-        if (unit < k_units) {
-          const int g = unit / kKGroups, c = unit % kKGroups;
-          append_unit<KV, ROPE, DQK>(a, a.k_new + ((int64_t)tok * a.hkv + g) * DQK,
-                                     static_cast<uint8_t *>(a.k_cache) + (slot * a.hkv + g) * kv_row_bytes(KV, DQK),
-                                     c, cs, a.k_scale);
-        } else {
-          const int g = (unit - k_units) / kVGroups, c = (unit - k_units) % kVGroups;
-          append_unit<KV, kNoRope, kDv>(a, a.v_new + ((int64_t)tok * a.hkv + g) * kDv,
-                                        static_cast<uint8_t *>(a.v_cache) + (slot * a.hkv + g) * kv_row_bytes(KV, kDv),
-                                        c, cs, a.v_scale);
-        }
+      if (slot >= 0) {
+        append_rows_of<KV, ROPE, DQK>(a.k_new + (int64_t)tok * a.hkv * DQK,
+                                      static_cast<uint8_t *>(a.k_cache) + slot * a.hkv * kv_row_bytes(KV, DQK),
+                                      a.hkv, slice, a.slices, turn, k_scale);
+        append_rows_of<KV, kNoRope, kDv>(a.v_new + (int64_t)tok * a.hkv * kDv,
+                                         static_cast<uint8_t *>(a.v_cache) + slot * a.hkv * kv_row_bytes(KV, kDv),
+                                         a.hkv, slice, a.slices, as_is, v_scale);
       }
     }
-    // ---- the query rows: rotated units first in each row, then the copied ones
+    // ---- the query rows; a row is read by its warp before it is written (q_out
+    // may be q: then only the rotated chunks move)
     if constexpr (ROPE != kNoRope) {
-      const int half = a.rot >> 1;
-      const int64_t row0 = (int64_t)tok * a.hq * DQK;
-      constexpr int kAhead = 2;
+      if (a.q) {
+        const bool moves = sub < RPW && (turn.in || a.q != a.q_out);
+        const int64_t row0 = (int64_t)tok * a.hq * DQK;
+        const int steps = (a.hq + RPW - 1) / RPW;
+        constexpr int kAhead = 4;
 #pragma unroll 1
-      for (int u0 = slice * 32 + lane; u0 < q_units; u0 += kAhead * stride) {
-        uint4 x[kAhead][2];
-        int at[kAhead][2], un[kAhead];             // offsets in the token's rows, unit in the row
+        for (int st0 = slice; st0 < steps; st0 += kAhead * a.slices) {
+          uint4 x[kAhead];
 #pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          const int unit = u0 + k * stride;
-          un[k] = -1;
-          if (unit < q_units) {
-            const int h = unit / a.q_units, u = unit % a.q_units;
-            un[k] = u;
-            if (u < a.q_turned) {
-              at[k][0] = a.rot_off + (ROPE == kPairs ? 16 : 8) * u;
-              at[k][1] = at[k][0] + (ROPE == kPairs ? 8 : half);
-            } else {
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const int d = 16 * (u - a.q_turned) + 8 * y;
-                at[k][y] = d < a.rot_off ? d : d + a.rot;
-              }
-            }
-            at[k][0] += h * DQK;
-            at[k][1] += h * DQK;
-#pragma unroll
-            for (int y = 0; y < 2; ++y) x[k][y] = *reinterpret_cast<const uint4 *>(a.q + row0 + at[k][y]);
-          }
-        }
-        // a unit's two chunks are read before either is written (q_out may be q)
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-          if (un[k] < 0) continue;
-          if (un[k] < a.q_turned) {
-            float x1[8], x2[8];
-            unpack8(x[k][0], x1);
-            unpack8(x[k][1], x2);
-            const float *c8 = cs + 8 * un[k];
-            if (ROPE == kPairs) {
-              rotate_pairs(x1, c8, half);
-              rotate_pairs(x2, c8 + 4, half);
-            } else {
-              float c[8], sn[8];
-              load8f(c8, c);
-              load8f(c8 + half, sn);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float y1 = x1[j], y2 = x2[j];
-                x1[j] = rot_sub(y1, c[j], y2, sn[j]);
-                x2[j] = rot_add(y2, c[j], y1, sn[j]);
-              }
-            }
-            x[k][0] = pack8(x1);
-            x[k][1] = pack8(x2);
+          for (int k = 0; k < kAhead; ++k) {
+            const int h = (st0 + k * a.slices) * RPW + sub;
+            x[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (moves && h < a.hq) x[k] = *(reinterpret_cast<const uint4 *>(a.q + row0 + (int64_t)h * DQK) + ch);
           }
 #pragma unroll
-          for (int y = 0; y < 2; ++y) *reinterpret_cast<uint4 *>(a.q_out + row0 + at[k][y]) = x[k][y];
+          for (int k = 0; k < kAhead; ++k) {
+            if (st0 + k * a.slices >= steps) break;
+            const int h = (st0 + k * a.slices) * RPW + sub;
+            float v[8];
+            turn.apply(x[k], v);
+            if (moves && h < a.hq)
+              *(reinterpret_cast<uint4 *>(a.q_out + row0 + (int64_t)h * DQK) + ch) = turn.in ? pack8(v) : x[k];
+          }
         }
       }
     }
@@ -384,59 +422,78 @@ struct ReadArgs {
   float k_scale, v_scale;
 };
 
-// 16 cached values as bfloat16.
+// The heads of one cached slot (cache == nullptr: zeros) as bfloat16 rows.
 template <int KV, int D>
-__device__ __forceinline__ void read_unit(const uint8_t *src, int c, float scale, uint4 (&o)[2]) {
-  if (KV == ATTN_KV_BF16) {
-    o[0] = __ldg(reinterpret_cast<const uint4 *>(src) + 2 * c);
-    o[1] = __ldg(reinterpret_cast<const uint4 *>(src) + 2 * c + 1);
-    return;
-  }
-  uint32_t h[8];                           // 16 values as fp16 pairs, exact
-  if (KV == ATTN_KV_FP8_E4M3) {
-    uint4 lo, hi;
-    e4m3x16_to_f16(__ldg(reinterpret_cast<const uint4 *>(src) + c), lo, hi);
-    h[0] = lo.x; h[1] = lo.y; h[2] = lo.z; h[3] = lo.w;
-    h[4] = hi.x; h[5] = hi.y; h[6] = hi.z; h[7] = hi.w;
-  } else {
-    const uint2 q = __ldg(reinterpret_cast<const uint2 *>(src) + c);
-    uint32_t s0, s1, p[4], u[4];
-    e4m3_scales_f16(__ldg(src + D / 2 + c), s0, s1);
-    e2m1x8_to_f16(q.x, p);
-    e2m1x8_to_f16(q.y, u);
+__device__ __forceinline__ void read_rows_of(const uint8_t *cache, uint16_t *out, int heads, int slice, int slices,
+                                             float scale) {
+  constexpr int NC = Lanes<D>::NC, RPW = Lanes<D>::RPW, kAhead = 4;
+  const int lane = threadIdx.x & 31, sub = lane / NC, ch = lane % NC;
+  const int steps = (heads + RPW - 1) / RPW;
+#pragma unroll 1
+  for (int st0 = slice; st0 < steps; st0 += kAhead * slices) {
+    uint4 x[kAhead];                       // raw: 16, 8 or 4 bytes, and a scale byte in .w
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      h[e] = mul_f16x2(p[e], s0);
-      h[4 + e] = mul_f16x2(u[e], s0);
+    for (int k = 0; k < kAhead; ++k) {
+      const int h = (st0 + k * slices) * RPW + sub;
+      x[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (cache && sub < RPW && h < heads) {
+        const uint8_t *row = cache + (int64_t)h * kv_row_bytes(KV, D);
+        if (KV == ATTN_KV_BF16) {
+          x[k] = __ldg(reinterpret_cast<const uint4 *>(row) + ch);
+        } else if (KV == ATTN_KV_FP8_E4M3) {
+          const uint2 r = __ldg(reinterpret_cast<const uint2 *>(row) + ch);
+          x[k].x = r.x;
+          x[k].y = r.y;
+        } else {
+          x[k].x = __ldg(reinterpret_cast<const uint32_t *>(row) + ch);
+          x[k].w = __ldg(row + D / 2 + ch / 2);
+        }
+      }
     }
-  }
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    float v[8];
+    for (int k = 0; k < kAhead; ++k) {
+      const int h = (st0 + k * slices) * RPW + sub;
+      if (sub >= RPW || h >= heads) continue;
+      uint4 o = x[k];
+      if (KV != ATTN_KV_BF16) {
+        uint32_t p[4];                     // 8 values as fp16 pairs, exact
+        if (KV == ATTN_KV_FP8_E4M3) {
+          uint4 lo, hi;
+          e4m3x16_to_f16(make_uint4(x[k].x, x[k].y, 0u, 0u), lo, hi);
+          p[0] = lo.x, p[1] = lo.y, p[2] = lo.z, p[3] = lo.w;
+        } else {
+          uint32_t s0, s1;
+          e4m3_scales_f16(x[k].w, s0, s1);
+          e2m1x8_to_f16(x[k].x, p);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      asm("{\n .reg .b16 l, u;\n mov.b32 {l, u}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, u;\n}\n"
-          : "=f"(v[2 * j]), "=f"(v[2 * j + 1])
-          : "r"(h[4 * e + j]));
-      v[2 * j] = __fmul_rn(v[2 * j], scale);
-      v[2 * j + 1] = __fmul_rn(v[2 * j + 1], scale);
+          for (int e = 0; e < 4; ++e) p[e] = mul_f16x2(p[e], s0);
+        }
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          asm("{\n .reg .b16 l, u;\n mov.b32 {l, u}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, u;\n}\n"
+              : "=f"(v[2 * e]), "=f"(v[2 * e + 1])
+              : "r"(p[e]));
+          v[2 * e] = __fmul_rn(v[2 * e], scale);
+          v[2 * e + 1] = __fmul_rn(v[2 * e + 1], scale);
+        }
+        o = pack8(v);
+      }
+      reinterpret_cast<uint4 *>(out + (int64_t)h * D)[ch] = o;
     }
-    o[e] = pack8(v);
   }
 }
 
-// Cached rows as bfloat16, 16 values a unit; the rows of request b are its last
-// kv_indptr[b + 1] - kv_indptr[b] positions.  Work is split as for the append.
+// Cached rows as bfloat16; the rows of request b are its last kv_indptr[b + 1] -
+// kv_indptr[b] positions.  Work is split as for the append.
 template <int KV, int DQK>
 __global__ void __launch_bounds__(kAppendThreads, 4) read_kernel(const ReadArgs a) {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  constexpr int kKGroups = DQK / kE2m1Block;
   const int lane = threadIdx.x & 31;
   const int worker = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
   const int chunk = worker / a.slices, slice = worker % a.slices;
   if (chunk >= a.chunks) return;
-  const int k_units = a.hkv * kKGroups, kv_units = k_units + a.hkv * kVGroups;
   const int row_end = (int)((int64_t)(chunk + 1) * a.rows / a.chunks);
   Request rq;
   int64_t shift = 0;
@@ -454,26 +511,11 @@ __global__ void __launch_bounds__(kAppendThreads, 4) read_kernel(const ReadArgs 
       }
     }
     if (bad && slice == 0 && lane == 0) atomicOr(a.err, bad);
-#pragma unroll 2
-    for (int unit = slice * 32 + lane; unit < kv_units; unit += 32 * a.slices) {
-      uint4 o[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-      uint4 *dst;
-      if (unit < k_units) {
-        const int g = unit / kKGroups, c = unit % kKGroups;
-        dst = reinterpret_cast<uint4 *>(a.k_out + ((int64_t)row * a.hkv + g) * DQK) + 2 * c;
-        if (slot >= 0)
-          read_unit<KV, DQK>(static_cast<const uint8_t *>(a.k_cache) + (slot * a.hkv + g) * kv_row_bytes(KV, DQK),
-                             c, a.k_scale, o);
-      } else {
-        const int g = (unit - k_units) / kVGroups, c = (unit - k_units) % kVGroups;
-        dst = reinterpret_cast<uint4 *>(a.v_out + ((int64_t)row * a.hkv + g) * kDv) + 2 * c;
-        if (slot >= 0)
-          read_unit<KV, kDv>(static_cast<const uint8_t *>(a.v_cache) + (slot * a.hkv + g) * kv_row_bytes(KV, kDv),
-                             c, a.v_scale, o);
-      }
-      dst[0] = o[0];
-      dst[1] = o[1];
-    }
+    const int64_t row_heads = slot * a.hkv;
+    read_rows_of<KV, DQK>(slot < 0 ? nullptr : static_cast<const uint8_t *>(a.k_cache) + row_heads * kv_row_bytes(KV, DQK),
+                          a.k_out + (int64_t)row * a.hkv * DQK, a.hkv, slice, a.slices, a.k_scale);
+    read_rows_of<KV, kDv>(slot < 0 ? nullptr : static_cast<const uint8_t *>(a.v_cache) + row_heads * kv_row_bytes(KV, kDv),
+                          a.v_out + (int64_t)row * a.hkv * kDv, a.hkv, slice, a.slices, a.v_scale);
   }
 }
 
@@ -492,7 +534,7 @@ struct OnDevice {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Splits `rows` of `steps` 32-unit steps each among the warps that all SMs hold:
+// Splits `rows` of `steps` row steps each among the warps that all SMs hold:
 // ranges of rows, and the warps that share a range's steps.
 struct Split {
   int32_t chunks, slices;
@@ -567,8 +609,7 @@ attn_status_t append_rows(attn_plan_t plan, const attn_rope_t *rope, const void 
   a.num_pages = pr.num_pages;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
-  const int64_t kv_units = (int64_t)pr.num_kv_heads * (pr.head_dim_qk / kE2m1Block + kVGroups);
-  int64_t q_units = 0;
+  int64_t steps = pr.num_kv_heads;          // row steps that can run side by side
   if (rope) {
     a.cos_sin = rope->cos_sin;
     a.positions = rope->positions;
@@ -578,13 +619,10 @@ attn_status_t append_rows(attn_plan_t plan, const attn_rope_t *rope, const void 
     if (q) {
       a.q = static_cast<const uint16_t *>(q);
       a.q_out = static_cast<uint16_t *>(q_out);
-      a.q_turned = rope->rot_dim / 16;
-      // in place, the dims that are not rotated stay where they are
-      a.q_units = q == q_out ? a.q_turned : pr.head_dim_qk / 16;
-      q_units = (int64_t)pr.num_q_heads * a.q_units;
+      steps = pr.num_q_heads;
     }
   }
-  const Split sp(total_q, (std::max(kv_units, q_units) + 31) / 32);
+  const Split sp(total_q, steps);
   a.chunks = sp.chunks;
   a.slices = sp.slices;
   OnDevice dev(plan->device);
@@ -637,7 +675,7 @@ extern "C" attn_status_t attn_read_kv(attn_plan_t plan, const void *k_cache, con
   a.num_pages = pr.num_pages;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
-  const akp::Split sp(rows, ((int64_t)pr.num_kv_heads * (pr.head_dim_qk / akp::kE2m1Block + akp::kVGroups) + 31) / 32);
+  const akp::Split sp(rows, pr.num_kv_heads);
   a.chunks = sp.chunks;
   a.slices = sp.slices;
   akp::OnDevice dev(plan->device);
