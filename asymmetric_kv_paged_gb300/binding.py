@@ -125,14 +125,25 @@ def _check(status: int, what: str) -> None:
 
 
 def _ptr(t) -> int | None:
-    return None if t is None else int(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> int:
-    if stream is None:
+_RAW_STREAM = None
+
+
+def _stream(stream, plan) -> int:
+    """The raw handle of `stream`, by default torch's current stream on the plan's
+    device (asked for without building a torch.cuda.Stream: 0.1 us for 3)."""
+    global _RAW_STREAM
+    if stream is not None:
+        return int(getattr(stream, "cuda_stream", stream))
+    if plan.device < 0:          # a host plan: the library refuses to run it
+        return 0
+    if _RAW_STREAM is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
-    return int(getattr(stream, "cuda_stream", stream))
+        _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda device: torch.cuda.current_stream(device).cuda_stream)
+    return _RAW_STREAM(plan.device)
 
 
 class Plan:
@@ -225,16 +236,11 @@ def attn_plan_destroy(plan: Plan) -> None:
 
 def _run_args(plan, q, k_cache, v_cache, page_table, seq_lens, qo_indptr, sinks, window,
               softmax_scale, k_scale, v_scale, out, lse_out, workspace, stream):
-    if stream is None:
-        import torch
-        stream = torch.cuda.current_stream().cuda_stream
-    elif hasattr(stream, "cuda_stream"):
-        stream = stream.cuda_stream
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     return (_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens),
             _ptr(qo_indptr), _ptr(sinks), int(window), float(softmax_scale), float(k_scale),
             float(v_scale), _ptr(out), _ptr(lse_out), _ptr(workspace), ws_bytes,
-            ctypes.c_void_p(int(stream)))
+            _stream(stream, plan))
 
 
 def attn_run_paged(plan: Plan, q, k_cache, v_cache, page_table, seq_lens, qo_indptr, sinks,
@@ -244,7 +250,7 @@ def attn_run_paged(plan: Plan, q, k_cache, v_cache, page_table, seq_lens, qo_ind
     current stream).  Pointer-only; nothing is synchronised."""
     args = _run_args(plan, q, k_cache, v_cache, page_table, seq_lens, qo_indptr, sinks, window,
                      softmax_scale, k_scale, v_scale, out, lse_out, workspace, stream)
-    _check(load().attn_run_paged(ctypes.c_void_p(plan.handle), *args), "attn_run_paged")
+    _check(load().attn_run_paged(plan.handle, *args), "attn_run_paged")
 
 
 def attn_run_phase(plan: Plan, phase: int, q, k_cache, v_cache, page_table, seq_lens,
@@ -253,7 +259,7 @@ def attn_run_phase(plan: Plan, phase: int, q, k_cache, v_cache, page_table, seq_
     """One of the two launches of attn_run_paged (0: split-KV kernel, 1: merge)."""
     args = _run_args(plan, q, k_cache, v_cache, page_table, seq_lens, qo_indptr, sinks, window,
                      softmax_scale, k_scale, v_scale, out, lse_out, workspace, stream)
-    _check(load().attn_run_phase(ctypes.c_void_p(plan.handle), int(phase), *args),
+    _check(load().attn_run_phase(plan.handle, int(phase), *args),
            "attn_run_phase")
 
 
@@ -268,23 +274,17 @@ def attn_run_paged_no_workspace(plan: Plan, q, k_cache, v_cache, page_table, seq
     args = _run_args(plan, q, k_cache, v_cache, page_table, seq_lens, qo_indptr, sinks, window,
                      softmax_scale, k_scale, v_scale, out, lse_out, None, stream)
     args = args[:13] + args[15:]        # drop the workspace pointer and size
-    _check(load().attn_run_paged_no_workspace(ctypes.c_void_p(plan.handle), *args),
+    _check(load().attn_run_paged_no_workspace(plan.handle, *args),
            "attn_run_paged_no_workspace")
 
 
 def attn_append_kv(plan: Plan, k_new, v_new, k_cache, v_cache, page_table, seq_lens, qo_indptr,
                    k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
     """Write the plan's new tokens' K/V rows into the paged caches (FP8 caches
-    get E4M3 codes of value / scale)."""
-    if stream is None:
-        import torch
-        stream = torch.cuda.current_stream().cuda_stream
-    elif hasattr(stream, "cuda_stream"):
-        stream = stream.cuda_stream
-    _check(load().attn_append_kv(ctypes.c_void_p(plan.handle), _ptr(k_new), _ptr(v_new),
-                                 _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens),
-                                 _ptr(qo_indptr), float(k_scale), float(v_scale),
-                                 ctypes.c_void_p(int(stream))), "attn_append_kv")
+    get E4M3 codes of value / scale, 4-bit ones E2M1 codes with block scales)."""
+    _check(load().attn_append_kv(plan.handle, _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
+                                 _ptr(page_table), _ptr(seq_lens), _ptr(qo_indptr), float(k_scale),
+                                 float(v_scale), _stream(stream, plan)), "attn_append_kv")
 
 
 def attn_kv_row_bytes(kv_dtype: int, head_dim: int) -> int:
@@ -312,8 +312,8 @@ def attn_append_kv_rope(plan: Plan, rope: attn_rope_t, q, k_new, v_new, q_out, k
     (may be q; both None: no queries)."""
     _check(load().attn_append_kv_rope(
         plan.handle, ctypes.byref(rope), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(q_out), _ptr(k_cache),
-        _ptr(v_cache), _ptr(page_table), _ptr(seq_lens), _ptr(qo_indptr), k_scale, v_scale,
-        _stream(stream)), "attn_append_kv_rope")
+        _ptr(v_cache), _ptr(page_table), _ptr(seq_lens), _ptr(qo_indptr), float(k_scale), float(v_scale),
+        _stream(stream, plan)), "attn_append_kv_rope")
 
 
 def attn_read_kv(plan: Plan, k_cache, v_cache, page_table, seq_lens, kv_indptr, k_out, v_out,
@@ -322,7 +322,7 @@ def attn_read_kv(plan: Plan, k_cache, v_cache, page_table, seq_lens, kv_indptr, 
     request b, into k_out [rows, Hkv, Dqk] and v_out [rows, Hkv, 128]."""
     _check(load().attn_read_kv(
         plan.handle, _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens), _ptr(kv_indptr),
-        int(k_out.shape[0]), _ptr(k_out), _ptr(v_out), k_scale, v_scale, _stream(stream)),
+        int(k_out.shape[0]), _ptr(k_out), _ptr(v_out), float(k_scale), float(v_scale), _stream(stream, plan)),
         "attn_read_kv")
 
 

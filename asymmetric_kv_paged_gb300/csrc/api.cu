@@ -17,17 +17,8 @@
 
 namespace {
 
-// Restores the caller's current device on scope exit.
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = false;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess) ok = true;
-  }
-  ~DeviceGuard() {
-    if (prev >= 0) cudaSetDevice(prev);
-  }
-};
+using akp::DeviceGuard;
+
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -312,9 +303,7 @@ static attn_status_t run_impl(attn_plan_t plan, int phases, bool allow_stage, co
         !make_cache_map(&maps.v, v_cache, v_row, akp::kDv, pr.num_kv_heads, slots, rows))
       return ATTN_ERR_CUDA;
   }
-  int cur = -1;
-  if (cudaGetDevice(&cur) != cudaSuccess) return ATTN_ERR_CUDA;
-  DeviceGuard guard(cur == plan->device ? cur : plan->device);
+  DeviceGuard guard(plan->device);
   if (!guard.ok) return ATTN_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if ((phases & 1) && hp.replayable) {
@@ -334,6 +323,7 @@ static attn_status_t run_impl(attn_plan_t plan, int phases, bool allow_stage, co
     r.window = pr.window;
     r.key_tile = hp.key_tile;
     r.lockstep = hp.lockstep;
+    r.min_tiles = hp.min_tiles;
     r.whole_range = hp.whole_range;
     if (akp::launch_replan(r, st) != cudaSuccess) return ATTN_ERR_CUDA;
   }

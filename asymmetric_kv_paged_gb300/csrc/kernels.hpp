@@ -7,6 +7,19 @@
 
 namespace akp {
 
+// Makes `dev` the current device, and the caller's again on scope exit.
+struct DeviceGuard {
+  int prev = -1;          // to go back to; -1: `dev` is the caller's own
+  bool ok = false;
+  explicit DeviceGuard(int dev) {
+    ok = cudaGetDevice(&prev) == cudaSuccess && (prev == dev || cudaSetDevice(dev) == cudaSuccess);
+    if (prev == dev) prev = -1;
+  }
+  ~DeviceGuard() {
+    if (prev >= 0) cudaSetDevice(prev);
+  }
+};
+
 struct RunArgs {
   const void *q;
   const void *k_cache;

@@ -297,35 +297,6 @@ __device__ __forceinline__ void store_chunk(uint8_t *row, int ch, bool live, boo
   }
 }
 
-// The new rows of one token (K: D = DQK, rotated; V: D = 128, as they are):
-// every `slices`-th step from `slice` on, two steps' loads ahead.
-template <int KV, int ROPE, int D>
-__device__ __forceinline__ void append_rows_of(const uint16_t *src, uint8_t *dst, int heads, int slice, int slices,
-                                               const Turn<ROPE, Lanes<D>::NC> &turn, const Divisor &scale) {
-  constexpr int NC = Lanes<D>::NC, RPW = Lanes<D>::RPW, kAhead = 2;
-  const int lane = threadIdx.x & 31, sub = lane / NC, ch = lane % NC;
-  const int steps = (heads + RPW - 1) / RPW;
-#pragma unroll 1
-  for (int st0 = slice; st0 < steps; st0 += kAhead * slices) {
-    uint4 x[kAhead];
-    int h[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      h[k] = (st0 + k * slices) * RPW + sub;
-      if (sub >= RPW || h[k] >= heads) h[k] = -1;
-      x[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (h[k] >= 0) x[k] = __ldg(reinterpret_cast<const uint4 *>(src + (int64_t)h[k] * D) + ch);
-    }
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (st0 + k * slices >= steps) break;
-      float v[8];
-      turn.apply(x[k], v);
-      store_chunk<KV, D>(dst + (int64_t)max(h[k], 0) * kv_row_bytes(KV, D), ch, h[k] >= 0, turn.in, x[k], v, scale);
-    }
-  }
-}
-
 template <int KV, int ROPE, int DQK>
 __global__ void __launch_bounds__(kAppendThreads, 4) rope_append_kernel(const RopeAppendArgs a) {
   // A programmatic dependent of the stream's previous kernel: nothing is read
@@ -334,19 +305,41 @@ __global__ void __launch_bounds__(kAppendThreads, 4) rope_append_kernel(const Ro
   // for this grid.
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  constexpr int NC = Lanes<DQK>::NC, RPW = Lanes<DQK>::RPW;
+  constexpr int NC = Lanes<DQK>::NC, RPW = Lanes<DQK>::RPW;           // K and query rows
+  constexpr int VNC = Lanes<kDv>::NC, VRPW = Lanes<kDv>::RPW;         // V rows
   const int lane = threadIdx.x & 31, sub = lane / NC, ch = lane % NC;
   const int worker = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
   const int chunk = worker / a.slices, slice = worker % a.slices;
   if (chunk >= a.chunks) return;
   Turn<ROPE, NC> turn;
   turn.place(a, lane);
-  const Turn<kNoRope, Lanes<kDv>::NC> as_is{};
   const Divisor k_scale(a.k_scale), v_scale(a.v_scale);
+  // a token's row steps: K's, then V's
+  const int k_steps = (a.hkv + RPW - 1) / RPW, kv_steps = k_steps + (a.hkv + VRPW - 1) / VRPW;
   const int tok_end = (int)((int64_t)(chunk + 1) * a.tokens / a.chunks);
   Request rq;
   int64_t shift = 0;                         // position of token tok: tok + shift
   for (int tok = (int)((int64_t)chunk * a.tokens / a.chunks); tok < tok_end; ++tok) {
+    // this lane's chunk of row step `st`, and its head (-1: no row of its own)
+    auto head_of = [&](int st) {
+      const bool is_k = st < k_steps;
+      const int h = is_k ? st * RPW + sub : (st - k_steps) * VRPW + lane / VNC;
+      return h < a.hkv && (!is_k || sub < RPW) ? h : -1;
+    };
+    auto load_step = [&](int st) {
+      uint4 x = make_uint4(0u, 0u, 0u, 0u);
+      if (st >= kv_steps) return x;
+      const int h = head_of(st);
+      if (h < 0) return x;
+      const int64_t row = (int64_t)tok * a.hkv + h;
+      return st < k_steps ? __ldg(reinterpret_cast<const uint4 *>(a.k_new + row * DQK) + ch)
+                          : __ldg(reinterpret_cast<const uint4 *>(a.v_new + row * kDv) + lane % VNC);
+    };
+    // the first four rows are on their way while the token is looked up
+    constexpr int kAhead = 4;
+    uint4 x[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) x[k] = load_step(slice + k * a.slices);
     if (rq.seek(a.qo_indptr, a.batch, tok)) shift = (int64_t)__ldg(a.seq_lens + rq.b) - rq.end;
     const int64_t i = tok + shift;
     if (ROPE != kNoRope) {
@@ -357,8 +350,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) rope_append_kernel(const Ro
       }
       turn.angles(a, pos);
     }
-    // ---- K and V (a step of heads or fewer: the last slices may have none)
-    if (slice < a.hkv) {
+    // ---- K and V
+    if (slice < kv_steps) {
       int64_t slot = -1;
       int bad = 0;
       if (i < 0 || i / a.page_size >= a.pt_stride) {   // a length outside the table row
@@ -372,12 +365,27 @@ __global__ void __launch_bounds__(kAppendThreads, 4) rope_append_kernel(const Ro
       }
       if (bad && slice == 0 && lane == 0) atomicOr(a.err, bad);
       if (slot >= 0) {
-        append_rows_of<KV, ROPE, DQK>(a.k_new + (int64_t)tok * a.hkv * DQK,
-                                      static_cast<uint8_t *>(a.k_cache) + slot * a.hkv * kv_row_bytes(KV, DQK),
-                                      a.hkv, slice, a.slices, turn, k_scale);
-        append_rows_of<KV, kNoRope, kDv>(a.v_new + (int64_t)tok * a.hkv * kDv,
-                                         static_cast<uint8_t *>(a.v_cache) + slot * a.hkv * kv_row_bytes(KV, kDv),
-                                         a.hkv, slice, a.slices, as_is, v_scale);
+        uint8_t *k_rows = static_cast<uint8_t *>(a.k_cache) + slot * a.hkv * kv_row_bytes(KV, DQK);
+        uint8_t *v_rows = static_cast<uint8_t *>(a.v_cache) + slot * a.hkv * kv_row_bytes(KV, kDv);
+        // rolled: the loaded rows move up, and a new one is loaded behind them
+#pragma unroll 1
+        for (int st = slice; st < kv_steps; st += a.slices) {
+          const uint4 raw = x[0];
+#pragma unroll
+          for (int k = 0; k + 1 < kAhead; ++k) x[k] = x[k + 1];
+          x[kAhead - 1] = load_step(st + kAhead * a.slices);
+          const int h = head_of(st);
+          float v[8];
+          if (st < k_steps) {
+            turn.apply(raw, v);
+            store_chunk<KV, DQK>(k_rows + (int64_t)max(h, 0) * kv_row_bytes(KV, DQK), ch, h >= 0, turn.in, raw, v,
+                                 k_scale);
+          } else {
+            unpack8(raw, v);
+            store_chunk<KV, kDv>(v_rows + (int64_t)max(h, 0) * kv_row_bytes(KV, kDv), lane % VNC, h >= 0, false, raw,
+                                 v, v_scale);
+          }
+        }
       }
     }
     // ---- the query rows; a row is read by its warp before it is written (q_out
@@ -387,10 +395,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) rope_append_kernel(const Ro
         const bool moves = sub < RPW && (turn.in || a.q != a.q_out);
         const int64_t row0 = (int64_t)tok * a.hq * DQK;
         const int steps = (a.hq + RPW - 1) / RPW;
-        constexpr int kAhead = 4;
 #pragma unroll 1
         for (int st0 = slice; st0 < steps; st0 += kAhead * a.slices) {
-          uint4 x[kAhead];
 #pragma unroll
           for (int k = 0; k < kAhead; ++k) {
             const int h = (st0 + k * a.slices) * RPW + sub;
@@ -519,19 +525,6 @@ __global__ void __launch_bounds__(kAppendThreads, 4) read_kernel(const ReadArgs 
   }
 }
 
-// Restores the caller's current device on scope exit.
-struct OnDevice {
-  int prev = -1;
-  bool ok = false;
-  explicit OnDevice(int dev) {
-    ok = cudaGetDevice(&prev) == cudaSuccess && (prev == dev || cudaSetDevice(dev) == cudaSuccess);
-    if (prev == dev) prev = -1;
-  }
-  ~OnDevice() {
-    if (prev >= 0) cudaSetDevice(prev);
-  }
-};
-
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // Splits `rows` of `steps` row steps each among the warps that all SMs hold:
@@ -609,7 +602,7 @@ attn_status_t append_rows(attn_plan_t plan, const attn_rope_t *rope, const void 
   a.num_pages = pr.num_pages;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
-  int64_t steps = pr.num_kv_heads;          // row steps that can run side by side
+  int64_t steps = 2 * (int64_t)pr.num_kv_heads;     // row steps that can run side by side
   if (rope) {
     a.cos_sin = rope->cos_sin;
     a.positions = rope->positions;
@@ -619,13 +612,13 @@ attn_status_t append_rows(attn_plan_t plan, const attn_rope_t *rope, const void 
     if (q) {
       a.q = static_cast<const uint16_t *>(q);
       a.q_out = static_cast<uint16_t *>(q_out);
-      steps = pr.num_q_heads;
+      steps = std::max<int64_t>(steps, pr.num_q_heads);
     }
   }
   const Split sp(total_q, steps);
   a.chunks = sp.chunks;
   a.slices = sp.slices;
-  OnDevice dev(plan->device);
+  DeviceGuard dev(plan->device);
   if (!dev.ok) return ATTN_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = !rope               ? launch_append_kv<kNoRope>(a, pr.kv_dtype, pr.head_dim_qk, dim3(sp.ctas), st)
@@ -678,7 +671,7 @@ extern "C" attn_status_t attn_read_kv(attn_plan_t plan, const void *k_cache, con
   const akp::Split sp(rows, pr.num_kv_heads);
   a.chunks = sp.chunks;
   a.slices = sp.slices;
-  akp::OnDevice dev(plan->device);
+  akp::DeviceGuard dev(plan->device);
   if (!dev.ok) return ATTN_ERR_CUDA;
   const dim3 grid(sp.ctas), block(akp::kAppendThreads);
   cudaStream_t st = static_cast<cudaStream_t>(stream);

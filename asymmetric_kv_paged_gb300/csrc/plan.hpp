@@ -82,6 +82,7 @@ struct HostPlan {
   // working on the c % lockstep-th (4-bit plans; 1: one deal over all blocks),
   // see planner.cpp
   int32_t lockstep = 1;
+  int32_t min_tiles = 1;         // replayable deals: least tiles of a share
   bool whole_range = false;      // blocks take their request's whole key range
   bool one_copy = false;         // every block has more than block_rows / 2 rows
   int32_t num_sms = 0, num_ctas = 0, threads = 0;

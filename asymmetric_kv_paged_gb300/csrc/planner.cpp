@@ -224,7 +224,12 @@ attn_status_t build_host_plan(const attn_problem_t *p, int32_t num_sms, HostPlan
   // most `slack` tiles (1/32 of a share; two for prefill plans) stays on the
   // current CTA rather than becoming a split of its own.
   const int64_t nb_all = (int64_t)hp.blocks.size();
-  constexpr int64_t kWholeBlockTiles = 8;
+  // (attn_fp4.cu's warps take half a tile each: six tiles, or four with eight warps,
+  // are one unit's time to a CTA, and less is a split for nothing; up to twice
+  // that a whole block costs less than a merge.)
+  const int64_t fp4_tiles = hp.fp4_rows == 8 ? 6 : 4;
+  const int64_t kWholeBlockTiles = hp.fp4_rows ? 2 * fp4_tiles : 8;
+  if (hp.fp4_rows) hp.min_tiles = (int32_t)fp4_tiles;
   // A CTA that goes on to a further segment pays for the switch (the finished
   // segment's epilogue, the next block's Q) with this many tiles of its share:
   // measured, two-segment CTAs otherwise ended ~3-5 us after the others
@@ -236,7 +241,7 @@ attn_status_t build_host_plan(const attn_problem_t *p, int32_t num_sms, HostPlan
   const int64_t nb = nb_all / hp.lockstep;
   const int32_t sms = num_sms / hp.lockstep;
   if (nb > 0) {
-    const int64_t min_tiles = 2;
+    const int64_t min_tiles = hp.fp4_rows ? fp4_tiles : 2;
     int64_t remaining = total_tiles / hp.lockstep;
     int32_t cta = -1;
     int64_t room = 0, target = 0, slack = 0;
@@ -390,7 +395,7 @@ int32_t replan_host(HostPlan *hp, const int32_t *seq_lens) {
     start[bi + 1] = start[bi] + block_tile_count(klo, khi, hp->key_tile);
   }
   const int64_t T = start[nb];
-  const int64_t ctas = working_ctas(T, hp->num_ctas, hp->lockstep);
+  const int64_t ctas = working_ctas(T, hp->num_ctas, hp->lockstep, hp->min_tiles);
   const int32_t charge = switch_charge(T, ctas);
   const int64_t P = T + (int64_t)charge * nb;
   const int32_t *st = start.data();

@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kReplanThreads, 1) replan_kernel(const ReplanA
   __syncthreads();
   cta_exclusive_scan(r.tile_start, r.nb);
   const int64_t T = r.tile_start[r.nb];
-  const int64_t ctas = working_ctas(T, r.num_ctas, r.lockstep);
+  const int64_t ctas = working_ctas(T, r.num_ctas, r.lockstep, r.min_tiles);
   const int32_t charge = switch_charge(T, ctas);
   const int64_t P = T + (int64_t)charge * r.nb;     // global positions
 

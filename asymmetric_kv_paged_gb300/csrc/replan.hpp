@@ -9,7 +9,7 @@
 //     planner (bottom-right causal alignment, optional window);
 //   - its tiles take the global positions [start[bi], start[bi+1]) of the
 //     exclusive prefix sum `start` of the tile counts (T = start[nb] tiles);
-//   - with C' = min(C, T) working CTAs, CTA c takes positions
+//   - with C' = min(C, T) working CTAs (4-bit plans: fewer, see min_tiles), CTA c takes positions
 //     [c*P/C', (c+1)*P/C') (equal shares, rounded down; in a lockstep plan,
 //     whose blocks come head by head, the share of CTA c is the one of its
 //     place among the CTAs of head c % heads), so a block is cut wherever a share ends and each piece is one segment.  On shares of 32
@@ -60,11 +60,13 @@ AKP_HD int64_t block_pos(const int32_t *start, int32_t bi, int32_t charge) {
   return (int64_t)start[bi] + (int64_t)charge * bi;
 }
 
-// CTAs that get a share of T tiles: a multiple of `heads` (every head of a
-// lockstep plan has T / heads tiles).
-AKP_HD int64_t working_ctas(int64_t T, int64_t num_ctas, int32_t heads) {
-  const int64_t c = T < num_ctas ? T : num_ctas;
-  return c / heads * heads;
+// CTAs that get a share of T tiles: as many for each of `heads` (every head of a
+// lockstep plan has T / heads tiles), with at least min_tiles tiles each where a
+// head has that many.
+AKP_HD int64_t working_ctas(int64_t T, int64_t num_ctas, int32_t heads, int32_t min_tiles) {
+  if (T == 0) return 0;
+  const int64_t most = num_ctas / heads, fit = T / heads / min_tiles;
+  return (fit < 1 ? 1 : fit < most ? fit : most) * heads;
 }
 
 // The share of CTA c: c itself, or, with the heads in lockstep, share c / heads
@@ -143,7 +145,7 @@ struct ReplanArgs {
   const int32_t *seq_lens;     // [B] lengths of this run (caller's device array)
   const int32_t *seq_bounds;   // [B] upper bounds the plan was built for
   int32_t *err;                // device error word (bit 4: a length out of bounds)
-  int32_t nb, num_ctas, group, window, key_tile, lockstep, whole_range;
+  int32_t nb, num_ctas, group, window, key_tile, lockstep, min_tiles, whole_range;
 };
 
 }  // namespace akp

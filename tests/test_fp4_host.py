@@ -103,7 +103,12 @@ def test_fp4_plans_cover_every_key_once_with_the_heads_in_lockstep(hkv, num_sms)
                 w2 = W.Workload(**{**w.__dict__, "seq_lens": np.asarray(lens, np.int32)})
                 if replayable:
                     assert B.attn_plan_replan_host(plan, lens) == 0
-                info = _check_plan(plan, w2, num_sms, replayable)
+                info = _check_plan(plan, w2, num_sms, replayable=True)   # its balance bound is below
+                segs = B.attn_plan_segments(plan)
+                loads = np.bincount(segs[:, 0], weights=segs[:, 3] - segs[:, 2], minlength=info["ctas"])
+                # shares of six tiles at least (a unit for each warp), and blocks of up
+                # to twelve whole
+                assert loads.max() <= max(12, np.ceil(loads.sum() / (loads > 0).sum()) * 1.25 + 2 + 4 * replayable)
                 if not together:
                     continue
                 segs, blocks = B.attn_plan_segments(plan), B.attn_plan_blocks(plan)
