@@ -286,6 +286,7 @@ static attn_status_t run_impl(attn_plan_t plan, int phases, bool allow_stage, co
   a.num_pages = pr.num_pages;
   a.window = pr.window;
   a.err = plan->dev.err;
+  a.replayed = hp.replayable;
 
   akp::TmaMaps maps{};
   // the kernels read 4-bit rows in 16-byte pieces on every path
@@ -324,7 +325,6 @@ static attn_status_t run_impl(attn_plan_t plan, int phases, bool allow_stage, co
     r.key_tile = hp.key_tile;
     r.lockstep = hp.lockstep;
     r.min_tiles = hp.min_tiles;
-    r.whole_range = hp.whole_range;
     if (akp::launch_replan(r, st) != cudaSuccess) return ATTN_ERR_CUDA;
   }
   akp::TmaMaps stage_maps{};

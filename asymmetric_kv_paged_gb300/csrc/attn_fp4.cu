@@ -32,7 +32,7 @@
 // A unit of work is half a 64-key tile (32 keys); unit u of the CTA belongs to
 // warp u % kWarps, which keeps running maxima, sums and O of its own for the
 // whole segment, so nothing is shared between tiles; at the end of a segment
-// the warps' partials are combined through shared memory.  Each warp also
+// the warps' partials are combined through shared memory  Each warp also
 // fetches its own units, into a ring of its own, a few units ahead: it alone
 // fills, waits for and frees the ring's stages, in order, so that no barrier
 // phase can be mistaken for another and no warp ever waits for another one's
@@ -78,14 +78,17 @@ struct Cfg {
   static constexpr bool kQsmem = NB > 2;
   static constexpr int kQBytes = kQsmem ? NB * (DQK / 16) * 32 * 8 : 0;
   static constexpr int kCombRows = NB > 2 ? 16 : NB * 8;     // rows combined at a time
+  // 8-row blocks: a warp's partial goes into its own ring's free stage
+  static constexpr bool kCombInRing = NB == 1;
   static constexpr int kOffQ = kWarps * kDepth * Unit<DQK>::kBytes;
   static constexpr int kOffComb = kOffQ + kQBytes;
-  static constexpr int kSmem = kOffComb + kWarps * kCombRows * kCombStride * 4 + 1024;
+  static constexpr int kSmem = kOffComb + (kCombInRing ? 0 : kWarps * kCombRows * kCombStride * 4) + 1024;
+  static_assert(!kCombInRing || kCombRows * kCombStride * 4 <= Unit<DQK>::kBytes, "partial larger than a stage");
   static_assert(kSmem + 3072 <= 227 * 1024, "shared memory layout too large");
 };
 
 struct FBars {
-  uint64_t full[12][3];
+  uint64_t full[16][3];
   uint64_t sync;
 };
 
@@ -156,9 +159,13 @@ __global__ void __launch_bounds__(Cfg<DQK, NB>::kThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // programmatic dependent: see attn_tc.cu
+  // (a plan that is not replayable never changes: its head record is read while the
+  // previous kernel ends)
+  CtaHead head;
+  if (!a.replayed) head = a.cta_heads[blockIdx.x];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  const CtaHead head = a.cta_heads[blockIdx.x];
+  if (a.replayed) head = a.cta_heads[blockIdx.x];
   if (head.seg_begin >= head.seg_end) return;
   const int total_units = head.total * kUnits;
   if (tid == 0) {
@@ -574,14 +581,44 @@ __global__ void __launch_bounds__(Cfg<DQK, NB>::kThreads, 1)
       // Row r of the buffer starts at r * 130 and the pair of dv (16g + 2i, + 1)
       // sits at 16g + ((2i + 2(g / 2)) & 15): the 16 lanes of a half-warp write 32
       // different banks.
-      float *comb = reinterpret_cast<float *>(smem + C::kOffComb);
+      // (the partials in the rings' stages: the one a warp freed last, which nothing is
+      // fetched into before the next segment)
+      auto part_of = [&](int w) -> float * {
+        if constexpr (C::kCombInRing) {
+          const int n = u_end > w ? (u_end - w + kWarps - 1) / kWarps : 1;      // units warp w has finished
+          return reinterpret_cast<float *>(smem + (w * kDepth + (n - 1) % kDepth) * T::kBytes);
+        } else {
+          return reinterpret_cast<float *>(smem + C::kOffComb) + w * (C::kCombRows * kCombStride);
+        }
+      };
+      // Row r of an uncut block: its normalised sum `acc` (of this lane's dv) and
+      // base-2 log-sum-exp; the sink joins here.
+      auto finish = [&](int r, float lse2, float4 acc) {
+        const int flat = bd.row0 + r;
+        const int tok = bd.tok0 + flat / a.group, h = bd.g * a.group + flat % a.group;
+        const float sink2 = a.sinks ? __ldg(a.sinks + h) * kLog2e : -INFINITY;
+        const float M = fmaxf(lse2, sink2);
+        float f = a.v_scale, lse = lse2 * kLn2;
+        if (sink2 != -INFINITY) {
+          const float w = exp2f(lse2 - M), Z = w + exp2f(sink2 - M);
+          f *= w / Z;
+          lse = (M + log2f(Z)) * kLn2;
+        }
+        __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * f, acc.y * f);
+        __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * f, acc.w * f);
+        uint2 w2;
+        w2.x = *reinterpret_cast<uint32_t *>(&lo);
+        w2.y = *reinterpret_cast<uint32_t *>(&hi);
+        *(reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + ((int64_t)tok * a.hq + h) * kDv) + lane) = w2;
+        if (a.lse_out && lane == 0) a.lse_out[(int64_t)tok * a.hq + h] = lse;
+      };
       bool synced = true;
 #pragma unroll
       for (int nb0 = 0; nb0 < NB; nb0 += C::kCombRows / 8) {
       if (nb0 > 0 && nb0 * 8 >= bd.nrows) break;
       if (nb0 > 0 && !(synced = group_sync())) break;     // the previous rows have been read
       if (has) {
-        float *dst = comb + warp * (C::kCombRows * kCombStride);
+        float *dst = part_of(warp);
 #pragma unroll
         for (int nc = 0; nc < C::kCombRows / 8; ++nc)
 #pragma unroll
@@ -606,13 +643,12 @@ __global__ void __launch_bounds__(Cfg<DQK, NB>::kThreads, 1)
         sm_m[warp][nb0 * 8 + lane] = -INFINITY;
       }
       if (!(synced = group_sync())) break;
-      // a warp combines whole rows: lane owns dv 4 lane .. 4 lane + 3
+      // a warp combines whole rows: lane owns dv 4 lane .. 4 lane + 3.  (Rolled loops:
+      // this runs once per segment, and its time is the fetch of its code.)
+#pragma unroll 1
       for (int r = nb0 * 8 + warp; r < min(bd.nrows, nb0 * 8 + C::kCombRows); r += kWarps) {
-        const int flat = bd.row0 + r;
-        const int tok = bd.tok0 + flat / a.group, h = bd.g * a.group + flat % a.group;
-        const float sink2 = a.sinks && bd.num_splits == 1 ? __ldg(a.sinks + h) * kLog2e : -INFINITY;
         float M = -INFINITY;
-#pragma unroll
+#pragma unroll 4
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w][r]);
         float Lsum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -620,12 +656,12 @@ __global__ void __launch_bounds__(Cfg<DQK, NB>::kThreads, 1)
         const int p0 = 16 * gg + ((4 * (lane & 3) + 2 * (gg >> 1)) & 15);
         const int p1 = 16 * gg + ((4 * (lane & 3) + 2 + 2 * (gg >> 1)) & 15);
         if (M != -INFINITY) {
-#pragma unroll
+#pragma unroll 4
           for (int w = 0; w < kWarps; ++w) {
             const float mw = sm_m[w][r];
             if (mw == -INFINITY) continue;             // nothing written by this warp
             const float f = exp2f(mw - M);
-            const float *src = comb + (w * C::kCombRows + r - nb0 * 8) * kCombStride;
+            const float *src = part_of(w) + (r - nb0 * 8) * kCombStride;
             const float2 x = *reinterpret_cast<const float2 *>(src + p0);
             const float2 y = *reinterpret_cast<const float2 *>(src + p1);
             Lsum += f * sm_l[w][r];
@@ -635,36 +671,24 @@ __global__ void __launch_bounds__(Cfg<DQK, NB>::kThreads, 1)
             acc.w += f * y.y;
           }
         }
-        // O and the sums are both 2^kLift times what they stand for
-        const float inv_lift = 0.0078125f;              // 2^-kLift
+        // O and the sums are both 2^kLift times what they stand for; a NaN stays one
+        const float scale = Lsum == 0.f ? 0.f : 1.f / Lsum;
+        const float lse = Lsum == 0.f ? -INFINITY : M + log2f(Lsum * 0.0078125f);
+        acc.x *= scale, acc.y *= scale, acc.z *= scale, acc.w *= scale;
         if (bd.num_splits == 1) {
-          const float MM = fmaxf(M, sink2);
-          float scale = 0.f, lse = -INFINITY;
-          if (MM != -INFINITY) {
-            const float fm = exp2f(M - MM) * inv_lift;
-            const float Z = Lsum * fm + exp2f(sink2 - MM);
-            scale = fm * a.v_scale / Z;
-            lse = (MM + log2f(Z)) * kLn2;
-          }
-          __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * scale, acc.y * scale);
-          __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * scale, acc.w * scale);
-          uint2 w2;
-          w2.x = *reinterpret_cast<uint32_t *>(&lo);
-          w2.y = *reinterpret_cast<uint32_t *>(&hi);
-          *(reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + ((int64_t)tok * a.hq + h) * kDv) + lane) = w2;
-          if (a.lse_out && lane == 0) a.lse_out[(int64_t)tok * a.hq + h] = lse;
+          finish(r, lse, acc);
         } else {
           const int prow = bd.part_row_base + sd.split * bd.nrows + r;
-          const float scale = Lsum == 0.f ? 0.f : a.v_scale / Lsum;      // a NaN stays one
-          reinterpret_cast<float4 *>(a.part_o + (int64_t)prow * kDv)[lane] =
-              make_float4(acc.x * scale, acc.y * scale, acc.z * scale, acc.w * scale);
-          if (lane == 0) a.part_lse[prow] = Lsum == 0.f ? -INFINITY : M + log2f(Lsum * inv_lift);
+          acc.x *= a.v_scale, acc.y *= a.v_scale, acc.z *= a.v_scale, acc.w *= a.v_scale;
+          reinterpret_cast<float4 *>(a.part_o + (int64_t)prow * kDv)[lane] = acc;
+          if (lane == 0) a.part_lse[prow] = lse;
         }
       }
       }
       if (!synced) break;
       u0 = u_end;
-      // the buffer is free for the next segment once every warp has read it
+      // the partials are free for the next segment once every warp has read them
+      if (C::kCombInRing && TMA) tc::fence_proxy_async_smem();
       if (seg + 1 < head.seg_end && !group_sync()) break;
     }
   }

@@ -39,6 +39,7 @@ struct RunArgs {
   const MergeItem *merge_items;
   int32_t hq, hkv, group, page_size, pt_stride, num_pages, window;
   int32_t *err;
+  int32_t replayed;      // the work list is rewritten by the device planner at every run
 };
 
 // Launch `kernel` as a programmatic dependent of the stream's previous kernel:

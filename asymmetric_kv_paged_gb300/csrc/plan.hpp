@@ -14,7 +14,7 @@ constexpr int kDqkSym = 128;    // query/key head dim of the symmetric pair 128/
 constexpr int kDv = 128;        // value head dim
 constexpr int kKeyTile = 64;    // keys per pipeline tile (decode / verify kernel)
 constexpr int kFp4UnitKeys = 32;  // keys a warp of attn_fp4.cu takes at a time
-constexpr int kFp4MaxRows = 16;   // rows of a (request, KV head) that attn_fp4.cu takes
+constexpr int kFp4MaxRows = 32;  // rows of a (request, KV head) that attn_fp4.cu takes
 constexpr int kPrefillKeyTile = 128;   // keys per tile of the prefill kernel
 
 // Query rows per row block.  A block packs up to block_rows query rows of one
@@ -78,12 +78,10 @@ struct HostPlan {
   // rows per block of the register-operand 4-bit kernel (attn_fp4.cu): 8, 16 or
   // 32; 0: attn_tc.cu or attn_prefill.cu runs the plan
   int32_t fp4_rows = 0;
-  // KV heads (with 32-row blocks: row groups of KV heads) dealt alike, CTA c
-  // working on the c % lockstep-th (4-bit plans; 1: one deal over all blocks),
-  // see planner.cpp
+  // KV heads dealt alike, CTA c working on head c % lockstep (4-bit plans;
+  // 1: one deal over all blocks), see planner.cpp
   int32_t lockstep = 1;
   int32_t min_tiles = 1;         // replayable deals: least tiles of a share
-  bool whole_range = false;      // blocks take their request's whole key range
   bool one_copy = false;         // every block has more than block_rows / 2 rows
   int32_t num_sms = 0, num_ctas = 0, threads = 0;
   std::vector<BlockDesc> blocks;

@@ -132,12 +132,11 @@ attn_status_t build_host_plan(const attn_problem_t *p, int32_t num_sms, HostPlan
   hp.block_rows = max_rows <= 64 ? 64 : max_rows <= 128 || p->head_dim_qk != kDqk ? 128 : 256;
   hp.prefill = hp.block_rows == 256;
   hp.key_tile = hp.prefill ? kPrefillKeyTile : kKeyTile;
-  // Up to 64 rows over a 4-bit cache run attn_fp4.cu, in blocks of at most 32
-  // rows (the register-operand kernel's limit).
-  if (p->kv_dtype == ATTN_KV_FP4_E2M1 && max_rows <= kFp4MaxRows) {
+  // Up to 32 rows over a 4-bit cache run attn_fp4.cu (measured against the tcgen05
+  // kernel, four requests of 46K keys: 8 rows 23 us and 126, 32 rows 43 us and 77;
+  // 64 rows as two groups of 32 74 us and 70).
+  if (p->kv_dtype == ATTN_KV_FP4_E2M1 && max_rows <= kFp4MaxRows)
     hp.fp4_rows = max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : 32;
-    if (max_rows > 16) hp.block_rows = 32;
-  }
   const int32_t rows_per_block = hp.block_rows;
   const int32_t tile = hp.key_tile;
   const int32_t G = hp.group;
@@ -147,47 +146,26 @@ attn_status_t build_host_plan(const attn_problem_t *p, int32_t num_sms, HostPlan
   // head is therefore dealt like every other one, to CTAs of its own
   // (CTA c works on head c % Hkv), so that the heads of a slot are read at the
   // same time and the shared units come out of L2: with heads dealt one after
-  // the other a ragged decode batch read 325 MB for 221 MB of rows.  The row
-  // groups of a head's block, which read the very same keys, likewise, when all
-  // requests have as many.  Not where dividing the CTAs like that leaves more
-  // than an eighth of them idle.
+  // the other a ragged decode batch read 325 MB for 221 MB of rows.  Not where
+  // dividing the CTAs like that leaves more than an eighth of them idle.
   const int32_t H = p->num_kv_heads;
-  auto groups_of = [&](int32_t b) {
-    return (int32_t)(((int64_t)(hp.qo_indptr[b + 1] - hp.qo_indptr[b]) * G + rows_per_block - 1) /
-                     rows_per_block);
-  };
-  int32_t row_groups = 0;                 // of every request with rows; 0: they differ
-  for (int32_t b = 0; b < p->batch; ++b) {
-    const int32_t r = groups_of(b);
-    if (r > 0) row_groups = row_groups == 0 || row_groups == r ? r : -1;
-    if (row_groups < 0) break;
-  }
-  auto divides = [&](int64_t k) { return k > 1 && k <= num_sms && 8 * (num_sms % k) <= num_sms; };
-  if (p->kv_dtype == ATTN_KV_FP4_E2M1 && !hp.prefill) {
-    if (row_groups > 1 && divides((int64_t)H * row_groups))
-      hp.lockstep = H * row_groups;
-    else if (divides(H))
-      hp.lockstep = H;
-  }
-  const int32_t split_heads = hp.lockstep > 1 ? H : 1;
-  const int32_t split_rows = hp.lockstep > H ? row_groups : 1;
-  hp.whole_range = split_rows > 1;
+  if (p->kv_dtype == ATTN_KV_FP4_E2M1 && !hp.prefill && H > 1 && H <= num_sms &&
+      8 * (num_sms % H) <= num_sms)
+    hp.lockstep = H;
 
-  // Row blocks, in (request, KV head, row) order; in lockstep plans by KV head
-  // (and row group) first.
+  // Row blocks, in (request, KV head, row) order; by KV head first in lockstep
+  // plans.
   int64_t total_tiles = 0;
-  for (int32_t outer = 0; outer < split_heads * split_rows; ++outer) {
-    const int32_t g_first = split_heads > 1 ? outer / split_rows : 0;
-    const int32_t g_end = split_heads > 1 ? g_first + 1 : H;
+  for (int32_t outer = 0; outer < hp.lockstep; ++outer) {
+    const int32_t g_first = hp.lockstep > 1 ? outer : 0;
+    const int32_t g_end = hp.lockstep > 1 ? outer + 1 : H;
     for (int32_t b = 0; b < p->batch; ++b) {
       const int32_t n = hp.qo_indptr[b + 1] - hp.qo_indptr[b];
       const int32_t L = hp.seq_lens[b];
       if (n == 0) continue;
       const int32_t R = n * G;
-      const int32_t r_first = split_rows > 1 ? outer % split_rows * rows_per_block : 0;
-      const int32_t r_end = split_rows > 1 ? std::min(R, r_first + rows_per_block) : R;
       for (int32_t g = g_first; g < g_end; ++g) {
-        for (int32_t row0 = r_first; row0 < r_end; row0 += rows_per_block) {
+        for (int32_t row0 = 0; row0 < R; row0 += rows_per_block) {
           BlockDesc bd{};
           bd.b = b;
           bd.g = g;
@@ -198,10 +176,8 @@ attn_status_t build_host_plan(const attn_problem_t *p, int32_t num_sms, HostPlan
           bd.tok0 = hp.qo_indptr[b];
           const int32_t t_first = row0 / G;
           const int32_t t_last = (row0 + bd.nrows - 1) / G;
-          // (row groups in lockstep all take the request's range, so that they have
-          // the same tiles; keys that a group's rows do not see are masked)
-          const int64_t i_first = split_rows > 1 ? (int64_t)L - n : (int64_t)L - n + t_first;
-          const int64_t i_last = split_rows > 1 ? (int64_t)L - 1 : (int64_t)L - n + t_last;
+          const int64_t i_first = (int64_t)L - n + t_first;
+          const int64_t i_last = (int64_t)L - n + t_last;
           int64_t lo = 0;
           if (p->window > 0) lo = std::max<int64_t>(0, i_first - p->window + 1);
           bd.klo = (int32_t)lo;
@@ -388,7 +364,7 @@ int32_t replan_host(HostPlan *hp, const int32_t *seq_lens) {
       L = L < bd.n ? bd.n : bound;
     }
     int32_t klo, khi;
-    block_keys(bd, L, hp->group, hp->prob.window, hp->whole_range, &klo, &khi);
+    block_keys(bd, L, hp->group, hp->prob.window, &klo, &khi);
     bd.L = L;
     bd.klo = klo;
     bd.khi = khi;

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kReplanThreads, 1) replan_kernel(const ReplanA
       L = L < bd.n ? bd.n : bound;
     }
     int32_t klo, khi;
-    block_keys(bd, L, r.group, r.window, r.whole_range != 0, &klo, &khi);
+    block_keys(bd, L, r.group, r.window, &klo, &khi);
     bd.L = L;
     bd.klo = klo;
     bd.khi = khi;

@@ -30,12 +30,11 @@
 
 namespace akp {
 
-// Key range of a block's rows (`whole`: of all its request's rows) for request
-// length L.
-AKP_HD void block_keys(const BlockDesc &bd, int32_t L, int32_t group, int32_t window, bool whole,
+// Key range of a block's rows for request length L.
+AKP_HD void block_keys(const BlockDesc &bd, int32_t L, int32_t group, int32_t window,
                        int32_t *klo, int32_t *khi) {
-  const int64_t i_first = (int64_t)L - bd.n + (whole ? 0 : bd.row0 / group);
-  const int64_t i_last = (int64_t)L - bd.n + (whole ? bd.n - 1 : (bd.row0 + bd.nrows - 1) / group);
+  const int64_t i_first = (int64_t)L - bd.n + bd.row0 / group;
+  const int64_t i_last = (int64_t)L - bd.n + (bd.row0 + bd.nrows - 1) / group;
   int64_t lo = 0;
   if (window > 0 && i_first - window + 1 > 0) lo = i_first - window + 1;
   *klo = (int32_t)lo;
@@ -145,7 +144,7 @@ struct ReplanArgs {
   const int32_t *seq_lens;     // [B] lengths of this run (caller's device array)
   const int32_t *seq_bounds;   // [B] upper bounds the plan was built for
   int32_t *err;                // device error word (bit 4: a length out of bounds)
-  int32_t nb, num_ctas, group, window, key_tile, lockstep, min_tiles, whole_range;
+  int32_t nb, num_ctas, group, window, key_tile, lockstep, min_tiles;
 };
 
 }  // namespace akp

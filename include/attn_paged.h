@@ -406,8 +406,7 @@ const char *attn_status_string(attn_status_t status);
  * attn_plan_host builds a plan on the host only, for a device with `num_sms`
  * SMs; it cannot be run.  attn_plan_info reports its shape:
  *   info[0] = number of row blocks, info[1] = number of work segments,
- *   info[2] = number of CTAs, info[3] = rows per block (64, 128 or 256; 32 for 17 to 64
- *   rows over a 4-bit cache),
+ *   info[2] = number of CTAs, info[3] = rows per block (64, 128 or 256),
  *   info[4] = key tile (keys per tile), info[5] = multi-split blocks,
  *   info[6] = workspace bytes (low 31 bits in info[6], high bits in info[7]).
  * attn_plan_blocks copies the blocks as 8 int32 each:
