@@ -81,6 +81,27 @@ __device__ __forceinline__ int request_of(const int32_t *indptr, int batch, int6
   return lo + n;
 }
 
+// Paired fp32 arithmetic: a * b and a * b + c, two of each in one instruction.  (A
+// paired addition behind a paired product is contracted into one rounding by the
+// assembler in spite of its .rn, measured on a quarter of random inputs: the
+// rotation's sums are scalar.)
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 d, a, b;\n"
+      " mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
 __device__ __forceinline__ void unpack8(const uint4 r, float (&v)[8]) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -152,14 +173,20 @@ struct Turn {
       unpack8(o, w);
       if (in)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __fadd_rn(__fmul_rn(v[j], c[j]), __fmul_rn(w[j], s[j]));
+        for (int j = 0; j < 8; j += 2) {
+          const float2 x = mul2(make_float2(v[j], v[j + 1]), make_float2(c[j], c[j + 1]));
+          const float2 y = mul2(make_float2(w[j], w[j + 1]), make_float2(s[j], s[j + 1]));
+          v[j] = __fadd_rn(x.x, y.x);
+          v[j + 1] = __fadd_rn(x.y, y.y);
+        }
     } else if (ROPE == kPairs) {
       if (in)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float x1 = v[2 * j], x2 = v[2 * j + 1];
-          v[2 * j] = __fsub_rn(__fmul_rn(x1, c[j]), __fmul_rn(x2, s[j]));
-          v[2 * j + 1] = __fadd_rn(__fmul_rn(x2, c[j]), __fmul_rn(x1, s[j]));
+          const float2 x = make_float2(v[2 * j], v[2 * j + 1]);
+          const float2 y = mul2(x, make_float2(c[j], c[j])), z = mul2(make_float2(x.y, x.x), make_float2(-s[j], s[j]));
+          v[2 * j] = __fadd_rn(y.x, z.x);
+          v[2 * j + 1] = __fadd_rn(y.y, z.y);
         }
     }
   }
@@ -185,10 +212,10 @@ struct Divisor {
   __device__ __forceinline__ explicit Divisor(float s_) : s(s_), r(1.f / s_) {
     plain = s >= 0x1p-40f && s <= 0x1p40f;
   }
-  __device__ __forceinline__ float plainly(float v) const {      // v's sign kept, also of zeros
-    const float q = v * r;
-    const float e = __fmaf_rn(__fmaf_rn(-q, s, v), r, q);
-    return __uint_as_float((__float_as_uint(e) & 0x7FFFFFFFu) | (__float_as_uint(v) & 0x80000000u));
+  // (zeros come out as +0)
+  __device__ __forceinline__ float2 plainly(float2 v) const {
+    const float2 rr = make_float2(r, r), q = mul2(v, rr);
+    return fma2(fma2(make_float2(-q.x, -q.y), make_float2(s, s), v), rr, q);
   }
 };
 
@@ -202,61 +229,108 @@ __device__ __forceinline__ uint32_t top_bits(const float (&v)[8]) {
 constexpr uint32_t kPlainTop = 0x5D800000u;      // 2^60
 constexpr uint32_t kInfBits = 0x7F800000u;
 
+// v / d with v's signs, zeros included.
 __device__ __forceinline__ void divide8(float (&v)[8], const Divisor &d, uint32_t top) {
   if (d.plain && top <= kPlainTop) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = d.plainly(v[j]);
+    for (int j = 0; j < 8; j += 2) {
+      const float2 x = make_float2(v[j], v[j + 1]), y = d.plainly(x);
+      v[j] = copysignf(y.x, x.x);
+      v[j + 1] = copysignf(y.y, x.y);
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = __fdiv_rn(v[j], d.s);
   }
 }
 
-// A lane's 8 values of a 4-bit row (its scale block's other 8 are in lane ^ 1):
-// the codes (4 bytes) and the block's scale.  Every lane of the warp calls it.
-// Rounding is monotonic, so the largest quotient is the quotient of the largest.
-__device__ __forceinline__ uint32_t quantise8(float (&y)[8], const Divisor &tensor, uint32_t &scale) {
-  uint32_t top = top_bits(y);
-  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  const bool nan = top > kInfBits;
-  const float amax = __fdiv_rn(__uint_as_float(top), tensor.s);
-  scale = nan ? 0x7Fu : e4m3_of(__fdiv_rn(amax, 6.f));
-  uint32_t out = 0u;
-  if (scale != 0u && !nan) {
-    divide8(y, tensor, top);
-    uint32_t h2;
-    asm("{\n .reg .b16 s;\n cvt.u16.u32 s, %1;\n cvt.rn.f16x2.e4m3x2 %0, s;\n}\n" : "=r"(h2) : "r"(scale));
-    float s;
-    asm("{\n .reg .b16 l, u;\n mov.b32 {l, u}, %1;\n cvt.f32.f16 %0, l;\n}\n" : "=f"(s) : "r"(h2));
-    divide8(y, Divisor(s), __float_as_uint(amax));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t b;
-      asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n cvt.u32.u8 %0, t;\n}\n"
-          : "=r"(b)
-          : "f"(y[2 * i + 1]), "f"(y[2 * i]));
-      out |= b << (8 * i);
-    }
-  } else {
-    // under a zero scale every value is below half the smallest step: its sign stays
-#pragma unroll
-    for (int i = 0; i < 8; ++i) out |= (__float_as_uint(y[i]) >> 31) << (4 * i + 3);
-  }
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  uint32_t h2;
+  asm("{\n .reg .b16 s;\n cvt.u16.u32 s, %1;\n cvt.rn.f16x2.e4m3x2 %0, s;\n}\n" : "=r"(h2) : "r"(code));
+  float s;
+  asm("{\n .reg .b16 l, u;\n mov.b32 {l, u}, %1;\n cvt.f32.f16 %0, l;\n}\n" : "=f"(s) : "r"(h2));
+  return s;
+}
+
+// Eight quotients -> eight E2M1 codes, element i in nibble i.
+__device__ __forceinline__ uint32_t e2m1_codes(const float (&y)[8]) {
+  uint32_t out;
+  asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      " mov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(out)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
   return out;
 }
 
-// The request of consecutive rows of a prefix-sum array, in registers: found by a
-// search once, then only when a row lies past its end.
+// A lane's 8 values of a 4-bit row (its scale block's other 8 are in lane ^ 1):
+// the codes (4 bytes) and the block's scale.  Every lane of the warp calls it.
+// Rounding is monotonic, so the largest quotient is the quotient of the largest.
+__device__ __forceinline__ uint32_t quantise8(const float (&v)[8], const Divisor &tensor, uint32_t &scale) {
+  uint32_t top = top_bits(v);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  float y[8];
+  if (tensor.plain && top <= kPlainTop && top >= 0x21800000u) {       // 2^-60: the largest quotient is exact
+    const float amax = tensor.plainly(make_float2(__uint_as_float(top), 0.f)).x;
+    const float q6 = amax * (1.f / 6.f);
+    scale = e4m3_of(__fmaf_rn(__fmaf_rn(-q6, 6.f, amax), 1.f / 6.f, q6));
+    if (scale != 0u) {
+      const Divisor block(e4m3_value(scale));
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const float2 x = block.plainly(tensor.plainly(make_float2(v[j], v[j + 1])));
+        y[j] = copysignf(x.x, v[j]);
+        y[j + 1] = copysignf(x.y, v[j + 1]);
+      }
+      return e2m1_codes(y);
+    }
+  } else {
+    // zeros, tiny or huge values, infinities, NaN (its block gets the NaN scale), odd
+    // tensor scales: by the division instruction sequence
+    const float amax = __fdiv_rn(__uint_as_float(top), tensor.s);
+    scale = top > kInfBits ? 0x7Fu : e4m3_of(__fdiv_rn(amax, 6.f));
+    if (scale != 0u && scale != 0x7Fu) {
+      const float s = e4m3_value(scale);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = __fdiv_rn(__fdiv_rn(v[j], tensor.s), s);
+      return e2m1_codes(y);
+    }
+  }
+  // under a zero scale every value is below half the smallest step: its sign stays
+  uint32_t out = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) out |= (__float_as_uint(v[i]) >> 31) << (4 * i + 3);
+  return out;
+}
+
+// The request of consecutive rows of a prefix-sum array, in registers: looked up
+// once, then only when a row lies past its end.  `shift`: the position of row t in
+// its request is t + shift (the last row is the request's last key).
 struct Request {
   int b = -1, first = 0, end = 0;      // rows [first, end)
-  __device__ __forceinline__ bool seek(const int32_t *indptr, int batch, int64_t row) {
-    if (b >= 0 && row < end) return false;
+  int64_t shift = 0;
+  __device__ __forceinline__ void seek(const int32_t *indptr, const int32_t *seq_lens, int batch, int64_t row) {
+    if (b >= 0 && row < end) return;
+    if (batch <= 32) {                 // everything in one round of loads, a request a lane
+      const int lane = threadIdx.x & 31;
+      int lo = 0, hi = 0, len = 0;
+      if (lane < batch) {
+        lo = __ldg(indptr + lane);
+        hi = __ldg(indptr + lane + 1);
+        len = __ldg(seq_lens + lane);
+      }
+      b = __popc(__ballot_sync(0xffffffffu, lane < batch && hi <= row));
+      first = __shfl_sync(0xffffffffu, lo, b & 31);
+      end = __shfl_sync(0xffffffffu, hi, b & 31);
+      shift = (int64_t)__shfl_sync(0xffffffffu, len, b & 31) - end;
+      return;
+    }
     b = request_of(indptr, batch, row);
     if (b < batch) {
       first = __ldg(indptr + b);
       end = __ldg(indptr + b + 1);
+      shift = (int64_t)__ldg(seq_lens + b) - end;
     }
-    return true;
   }
 };
 
@@ -318,7 +392,6 @@ __global__ void __launch_bounds__(kAppendThreads, 4) rope_append_kernel(const Ro
   const int k_steps = (a.hkv + RPW - 1) / RPW, kv_steps = k_steps + (a.hkv + VRPW - 1) / VRPW;
   const int tok_end = (int)((int64_t)(chunk + 1) * a.tokens / a.chunks);
   Request rq;
-  int64_t shift = 0;                         // position of token tok: tok + shift
   for (int tok = (int)((int64_t)chunk * a.tokens / a.chunks); tok < tok_end; ++tok) {
     // this lane's chunk of row step `st`, and its head (-1: no row of its own)
     auto head_of = [&](int st) {
@@ -340,8 +413,8 @@ __global__ void __launch_bounds__(kAppendThreads, 4) rope_append_kernel(const Ro
     uint4 x[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) x[k] = load_step(slice + k * a.slices);
-    if (rq.seek(a.qo_indptr, a.batch, tok)) shift = (int64_t)__ldg(a.seq_lens + rq.b) - rq.end;
-    const int64_t i = tok + shift;
+    rq.seek(a.qo_indptr, a.seq_lens, a.batch, tok);
+    const int64_t i = tok + rq.shift;
     if (ROPE != kNoRope) {
       const int64_t pos = a.positions ? (int64_t)__ldg(a.positions + tok) : i;
       if (pos < 0 || pos >= a.max_pos) {            // no row of the table: the token is skipped
@@ -502,14 +575,12 @@ __global__ void __launch_bounds__(kAppendThreads, 4) read_kernel(const ReadArgs 
   if (chunk >= a.chunks) return;
   const int row_end = (int)((int64_t)(chunk + 1) * a.rows / a.chunks);
   Request rq;
-  int64_t shift = 0;
   for (int row = (int)((int64_t)chunk * a.rows / a.chunks); row < row_end; ++row) {
-    if (rq.seek(a.kv_indptr, a.batch, row) && rq.b < a.batch)
-      shift = (int64_t)__ldg(a.seq_lens + rq.b) - rq.end;
+    rq.seek(a.kv_indptr, a.seq_lens, a.batch, row);
     int64_t slot = -1;
     int bad = 4;                                  // more rows than kv_indptr holds, or no such position
     if (rq.b < a.batch) {
-      const int64_t i = row + shift;
+      const int64_t i = row + rq.shift;
       if (row >= rq.first && i >= 0 && i / a.page_size < a.pt_stride) {
         const int32_t page = __ldg(a.page_table + (int64_t)rq.b * a.pt_stride + i / a.page_size);
         bad = page >= 0 && page < a.num_pages ? 0 : 1;
