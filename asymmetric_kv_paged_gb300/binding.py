@@ -282,9 +282,11 @@ def attn_append_kv(plan: Plan, k_new, v_new, k_cache, v_cache, page_table, seq_l
                    k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
     """Write the plan's new tokens' K/V rows into the paged caches (FP8 caches
     get E4M3 codes of value / scale, 4-bit ones E2M1 codes with block scales)."""
-    _check(load().attn_append_kv(plan.handle, _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache),
-                                 _ptr(page_table), _ptr(seq_lens), _ptr(qo_indptr), float(k_scale),
-                                 float(v_scale), _stream(stream, plan)), "attn_append_kv")
+    st = (_LIB or load()).attn_append_kv(
+        plan.handle, _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens),
+        _ptr(qo_indptr), float(k_scale), float(v_scale), _stream(stream, plan))
+    if st:
+        raise AttnError(st, "attn_append_kv")
 
 
 def attn_kv_row_bytes(kv_dtype: int, head_dim: int) -> int:
@@ -310,20 +312,22 @@ def attn_append_kv_rope(plan: Plan, rope: attn_rope_t, q, k_new, v_new, q_out, k
                         stream=None) -> None:
     """attn_append_kv with the keys rotated on the way, and the queries into q_out
     (may be q; both None: no queries)."""
-    _check(load().attn_append_kv_rope(
-        plan.handle, ctypes.byref(rope), _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(q_out), _ptr(k_cache),
-        _ptr(v_cache), _ptr(page_table), _ptr(seq_lens), _ptr(qo_indptr), float(k_scale), float(v_scale),
-        _stream(stream, plan)), "attn_append_kv_rope")
+    st = (_LIB or load()).attn_append_kv_rope(
+        plan.handle, rope, _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(q_out), _ptr(k_cache), _ptr(v_cache),
+        _ptr(page_table), _ptr(seq_lens), _ptr(qo_indptr), float(k_scale), float(v_scale), _stream(stream, plan))
+    if st:
+        raise AttnError(st, "attn_append_kv_rope")
 
 
 def attn_read_kv(plan: Plan, k_cache, v_cache, page_table, seq_lens, kv_indptr, k_out, v_out,
                  k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
     """Cached rows as bf16: the last kv_indptr[b + 1] - kv_indptr[b] positions of every
     request b, into k_out [rows, Hkv, Dqk] and v_out [rows, Hkv, 128]."""
-    _check(load().attn_read_kv(
+    st = (_LIB or load()).attn_read_kv(
         plan.handle, _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens), _ptr(kv_indptr),
-        int(k_out.shape[0]), _ptr(k_out), _ptr(v_out), float(k_scale), float(v_scale), _stream(stream, plan)),
-        "attn_read_kv")
+        k_out.shape[0], _ptr(k_out), _ptr(v_out), float(k_scale), float(v_scale), _stream(stream, plan))
+    if st:
+        raise AttnError(st, "attn_read_kv")
 
 
 def attn_get_device_error(plan: Plan) -> int:
