@@ -207,24 +207,29 @@ __device__ __forceinline__ uint32_t e4m3_of(float x) {
 // unproven, which round to zero codes with v's sign either way.  Anything else
 // (also infinities and NaN) takes the division instruction sequence.
 struct Divisor {
-  float s, r;
+  float s, r;                     // the divisor, RN(1 / s)
   bool plain;                     // s is in the range above
   __device__ __forceinline__ explicit Divisor(float s_) : s(s_), r(1.f / s_) {
     plain = s >= 0x1p-40f && s <= 0x1p40f;
   }
+  __device__ __forceinline__ Divisor(float s_, float r_) : s(s_), r(r_), plain(true) {}
   // (zeros come out as +0)
   __device__ __forceinline__ float2 plainly(float2 v) const {
     const float2 rr = make_float2(r, r), q = mul2(v, rr);
-    return fma2(fma2(make_float2(-q.x, -q.y), make_float2(s, s), v), rr, q);
+    return fma2(fma2(q, make_float2(-s, -s), v), rr, q);
   }
 };
 
+// max(|a|, |b|, |c|), NaN if one is.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;\n" : "=f"(d) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
+  return d;
+}
 // The largest magnitude of 8 values as fp32 bits (a NaN is above everything).
 __device__ __forceinline__ uint32_t top_bits(const float (&v)[8]) {
-  uint32_t t = 0u;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) t = max(t, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-  return t;
+  const float t = max3_abs(max3_abs(v[0], v[1], v[2]), max3_abs(v[3], v[4], v[5]), max3_abs(v[6], v[7], v[7]));
+  return __float_as_uint(t);
 }
 constexpr uint32_t kPlainTop = 0x5D800000u;      // 2^60
 constexpr uint32_t kInfBits = 0x7F800000u;
@@ -263,10 +268,24 @@ __device__ __forceinline__ uint32_t e2m1_codes(const float (&y)[8]) {
   return out;
 }
 
+// Per CTA: every finite E4M3 block scale with its correctly rounded reciprocal.
+struct ScaleTable {
+  float2 at[128];
+  __device__ __forceinline__ void fill() {
+    const int i = threadIdx.x;
+    if (i < 128) {
+      const float s = e4m3_value(i);
+      at[i] = make_float2(s, 1.f / s);
+    }
+    __syncthreads();
+  }
+};
+
 // A lane's 8 values of a 4-bit row (its scale block's other 8 are in lane ^ 1):
 // the codes (4 bytes) and the block's scale.  Every lane of the warp calls it.
 // Rounding is monotonic, so the largest quotient is the quotient of the largest.
-__device__ __forceinline__ uint32_t quantise8(const float (&v)[8], const Divisor &tensor, uint32_t &scale) {
+__device__ __forceinline__ uint32_t quantise8(const float (&v)[8], const Divisor &tensor, const ScaleTable &table,
+                                              uint32_t &scale) {
   uint32_t top = top_bits(v);
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
   float y[8];
@@ -275,7 +294,8 @@ __device__ __forceinline__ uint32_t quantise8(const float (&v)[8], const Divisor
     const float q6 = amax * (1.f / 6.f);
     scale = e4m3_of(__fmaf_rn(__fmaf_rn(-q6, 6.f, amax), 1.f / 6.f, q6));
     if (scale != 0u) {
-      const Divisor block(e4m3_value(scale));
+      const float2 sr = table.at[scale];
+      const Divisor block(sr.x, sr.y);
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         const float2 x = block.plainly(tensor.plainly(make_float2(v[j], v[j + 1])));
@@ -344,7 +364,7 @@ struct Lanes {
 // Every lane of the warp calls it; `live` lanes have a chunk.
 template <int KV, int D>
 __device__ __forceinline__ void store_chunk(uint8_t *row, int ch, bool live, bool turned, const uint4 raw,
-                                            float (&v)[8], const Divisor &scale) {
+                                            float (&v)[8], const Divisor &scale, const ScaleTable &table) {
   if (KV == ATTN_KV_BF16) {
     if (live) reinterpret_cast<uint4 *>(row)[ch] = turned ? pack8(v) : raw;
   } else if (KV == ATTN_KV_FP8_E4M3) {
@@ -362,7 +382,7 @@ __device__ __forceinline__ void store_chunk(uint8_t *row, int ch, bool live, boo
     constexpr int kGroups = D / kE2m1Block, kPad = e2m1_row_bytes(D) - D / 2 - kGroups;
     static_assert(kPad == 4 || kPad == 8, "4-bit row padding");
     uint32_t s;
-    const uint32_t codes = quantise8(v, scale, s);
+    const uint32_t codes = quantise8(v, scale, table, s);
     if (live) {
       reinterpret_cast<uint32_t *>(row)[ch] = codes;
       if (!(ch & 1)) row[D / 2 + ch / 2] = (uint8_t)s;
@@ -370,6 +390,53 @@ __device__ __forceinline__ void store_chunk(uint8_t *row, int ch, bool live, boo
     }
   }
 }
+
+// The rows of one kind (K or V: D values) of a token, every `slices`-th row step
+// from `slice` on.  One step's loads are ahead of the one at work, two where the row
+// is rotated: its step is the longer one and starts before the lookups.
+template <int KV, int ROPE, int D>
+struct RowSteps {
+  static constexpr int NC = Lanes<D>::NC, RPW = Lanes<D>::RPW, kAhead = ROPE == kNoRope ? 1 : 2;
+  const uint4 *src;                // this lane's chunk of its next row to load
+  int h, heads, step;              // that row's head; heads a step moves on
+  bool lane_in;
+  uint4 x[kAhead];
+
+  __device__ __forceinline__ uint4 next() {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (lane_in && h < heads) v = __ldg(src);
+    src += step * NC;
+    h += step;
+    return v;
+  }
+  __device__ __forceinline__ void start(const uint16_t *rows, int heads_, int slice, int slices) {
+    const int lane = threadIdx.x & 31, sub = lane / NC;
+    lane_in = sub < RPW;
+    heads = heads_;
+    step = slices * RPW;
+    h = slice * RPW + sub;
+    src = reinterpret_cast<const uint4 *>(rows + (int64_t)h * D) + lane % NC;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) x[k] = next();
+  }
+  __device__ __forceinline__ void store(uint8_t *rows, int slice, const Turn<ROPE, NC> &turn, const Divisor &scale,
+                                        const ScaleTable &table) {
+    const int lane = threadIdx.x & 31, ch = lane % NC;
+    int hs = slice * RPW + lane / NC;
+    uint8_t *dst = rows + (int64_t)hs * kv_row_bytes(KV, D);
+    for (int first = slice * RPW; first < heads; first += step) {
+      const uint4 raw = x[0];
+#pragma unroll
+      for (int k = 0; k + 1 < kAhead; ++k) x[k] = x[k + 1];
+      x[kAhead - 1] = next();
+      float v[8];
+      turn.apply(raw, v);
+      store_chunk<KV, D>(dst, ch, lane_in && hs < heads, turn.in, raw, v, scale, table);
+      dst += step * kv_row_bytes(KV, D);
+      hs += step;
+    }
+  }
+};
 
 template <int KV, int ROPE, int DQK>
 __global__ void __launch_bounds__(kAppendThreads, 4) rope_append_kernel(const RopeAppendArgs a) {
@@ -380,40 +447,29 @@ __global__ void __launch_bounds__(kAppendThreads, 4) rope_append_kernel(const Ro
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   constexpr int NC = Lanes<DQK>::NC, RPW = Lanes<DQK>::RPW;           // K and query rows
-  constexpr int VNC = Lanes<kDv>::NC, VRPW = Lanes<kDv>::RPW;         // V rows
   const int lane = threadIdx.x & 31, sub = lane / NC, ch = lane % NC;
   const int worker = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
   const int chunk = worker / a.slices, slice = worker % a.slices;
+  __shared__ ScaleTable table;
+  if (KV == ATTN_KV_FP4_E2M1) table.fill();
   if (chunk >= a.chunks) return;
   Turn<ROPE, NC> turn;
   turn.place(a, lane);
+  const Turn<kNoRope, Lanes<kDv>::NC> as_is{};
   const Divisor k_scale(a.k_scale), v_scale(a.v_scale);
-  // a token's row steps: K's, then V's
-  const int k_steps = (a.hkv + RPW - 1) / RPW, kv_steps = k_steps + (a.hkv + VRPW - 1) / VRPW;
   const int tok_end = (int)((int64_t)(chunk + 1) * a.tokens / a.chunks);
   Request rq;
   for (int tok = (int)((int64_t)chunk * a.tokens / a.chunks); tok < tok_end; ++tok) {
-    // this lane's chunk of row step `st`, and its head (-1: no row of its own)
-    auto head_of = [&](int st) {
-      const bool is_k = st < k_steps;
-      const int h = is_k ? st * RPW + sub : (st - k_steps) * VRPW + lane / VNC;
-      return h < a.hkv && (!is_k || sub < RPW) ? h : -1;
-    };
-    auto load_step = [&](int st) {
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (st >= kv_steps) return x;
-      const int h = head_of(st);
-      if (h < 0) return x;
-      const int64_t row = (int64_t)tok * a.hkv + h;
-      return st < k_steps ? __ldg(reinterpret_cast<const uint4 *>(a.k_new + row * DQK) + ch)
-                          : __ldg(reinterpret_cast<const uint4 *>(a.v_new + row * kDv) + lane % VNC);
-    };
-    // the first four rows are on their way while the token is looked up
-    constexpr int kAhead = 4;
-    uint4 x[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) x[k] = load_step(slice + k * a.slices);
+    // the first rows are on their way while the token is looked up
+    RowSteps<KV, ROPE, DQK> k_rows;
+    RowSteps<KV, kNoRope, kDv> v_rows;
+    k_rows.start(a.k_new + (int64_t)tok * a.hkv * DQK, a.hkv, slice, a.slices);
+    v_rows.start(a.v_new + (int64_t)tok * a.hkv * kDv, a.hkv, slice, a.slices);
     rq.seek(a.qo_indptr, a.seq_lens, a.batch, tok);
+    if (rq.b >= a.batch || tok < rq.first) {          // a row that qo_indptr does not hold
+      if (slice == 0 && lane == 0) atomicOr(a.err, 4);
+      continue;
+    }
     const int64_t i = tok + rq.shift;
     if (ROPE != kNoRope) {
       const int64_t pos = a.positions ? (int64_t)__ldg(a.positions + tok) : i;
@@ -424,7 +480,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) rope_append_kernel(const Ro
       turn.angles(a, pos);
     }
     // ---- K and V
-    if (slice < kv_steps) {
+    if (slice < a.hkv) {
       int64_t slot = -1;
       int bad = 0;
       if (i < 0 || i / a.page_size >= a.pt_stride) {   // a length outside the table row
@@ -438,27 +494,10 @@ __global__ void __launch_bounds__(kAppendThreads, 4) rope_append_kernel(const Ro
       }
       if (bad && slice == 0 && lane == 0) atomicOr(a.err, bad);
       if (slot >= 0) {
-        uint8_t *k_rows = static_cast<uint8_t *>(a.k_cache) + slot * a.hkv * kv_row_bytes(KV, DQK);
-        uint8_t *v_rows = static_cast<uint8_t *>(a.v_cache) + slot * a.hkv * kv_row_bytes(KV, kDv);
-        // rolled: the loaded rows move up, and a new one is loaded behind them
-#pragma unroll 1
-        for (int st = slice; st < kv_steps; st += a.slices) {
-          const uint4 raw = x[0];
-#pragma unroll
-          for (int k = 0; k + 1 < kAhead; ++k) x[k] = x[k + 1];
-          x[kAhead - 1] = load_step(st + kAhead * a.slices);
-          const int h = head_of(st);
-          float v[8];
-          if (st < k_steps) {
-            turn.apply(raw, v);
-            store_chunk<KV, DQK>(k_rows + (int64_t)max(h, 0) * kv_row_bytes(KV, DQK), ch, h >= 0, turn.in, raw, v,
-                                 k_scale);
-          } else {
-            unpack8(raw, v);
-            store_chunk<KV, kDv>(v_rows + (int64_t)max(h, 0) * kv_row_bytes(KV, kDv), lane % VNC, h >= 0, false, raw,
-                                 v, v_scale);
-          }
-        }
+        k_rows.store(static_cast<uint8_t *>(a.k_cache) + slot * a.hkv * kv_row_bytes(KV, DQK), slice, turn, k_scale,
+                     table);
+        v_rows.store(static_cast<uint8_t *>(a.v_cache) + slot * a.hkv * kv_row_bytes(KV, kDv), slice, as_is, v_scale,
+                     table);
       }
     }
     // ---- the query rows; a row is read by its warp before it is written (q_out
@@ -468,8 +507,10 @@ __global__ void __launch_bounds__(kAppendThreads, 4) rope_append_kernel(const Ro
         const bool moves = sub < RPW && (turn.in || a.q != a.q_out);
         const int64_t row0 = (int64_t)tok * a.hq * DQK;
         const int steps = (a.hq + RPW - 1) / RPW;
+        constexpr int kAhead = 4;
 #pragma unroll 1
         for (int st0 = slice; st0 < steps; st0 += kAhead * a.slices) {
+          uint4 x[kAhead];
 #pragma unroll
           for (int k = 0; k < kAhead; ++k) {
             const int h = (st0 + k * a.slices) * RPW + sub;
@@ -673,7 +714,7 @@ attn_status_t append_rows(attn_plan_t plan, const attn_rope_t *rope, const void 
   a.num_pages = pr.num_pages;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
-  int64_t steps = 2 * (int64_t)pr.num_kv_heads;     // row steps that can run side by side
+  int64_t steps = pr.num_kv_heads;          // row steps that can run side by side
   if (rope) {
     a.cos_sin = rope->cos_sin;
     a.positions = rope->positions;
