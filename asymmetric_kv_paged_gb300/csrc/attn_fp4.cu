@@ -631,7 +631,8 @@ __global__ void __launch_bounds__(Cfg<DQK, NB>::kThreads, 1)
             sum += __shfl_xor_sync(0xffffffffu, sum, 16);
             const int r = 2 * t + x;
             if (g == 0) {
-              sm_m[warp][nb * 8 + r] = m[nb][x];
+              // (nothing but NaN scores: no maximum, but the NaN sum counts)
+              sm_m[warp][nb * 8 + r] = sum != sum && m[nb][x] == -INFINITY ? 0.f : m[nb][x];
               sm_l[warp][nb * 8 + r] = sum;
             }
 #pragma unroll

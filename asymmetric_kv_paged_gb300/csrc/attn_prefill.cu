@@ -841,6 +841,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
       // ---------------- end of segment: normalise and write the rows
       if (!wait(&bars.pv_done[t], cdone & 1)) break;
       tc::tc_fence_after();
+      // a row that saw nothing but NaN scores has no maximum: its NaN sum stays
+      if (l_run != l_run && m_run == -INFINITY) m_run = 0.f;
       float scale_o = 0.f, lse = -INFINITY;
       if (single) {
         const float MM = fmaxf(m_run, sink2);
@@ -849,7 +851,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           scale_o = exp2f(m_run - MM) * a.v_scale / Z;
           lse = (MM + log2f(Z)) * kLn2;
         }
-      } else if (l_run > 0.f) {
+      } else if (l_run != 0.f) {
         scale_o = a.v_scale / l_run;
         lse = m_run + log2f(l_run);
       }

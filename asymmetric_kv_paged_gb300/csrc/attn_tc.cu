@@ -1188,7 +1188,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         valid = valid && half == 0;
       }
       tc::tc_fence_after();
-      if (F16) l_run *= kUnlift;
+      if (F16) {
+        l_run *= kUnlift;
+        // a row that saw nothing but NaN scores has no maximum: its NaN sum stays
+        if (l_run != l_run && m_run == -INFINITY) m_run = 0.f;
+      }
       const SegDesc &sd = cur.sd;
       const bool single = bd.num_splits == 1;
       if (rows_pad == kRows) {

@@ -10,7 +10,7 @@
 // E2M1 magnitudes are 0, 0.5, 1, 1.5, 2, 3, 4, 6 (code s e e m, exponent bias
 // 1).  code * scale has at most 2 + 4 significant bits, is a multiple of
 // 2^-10 and at most 2688, so it is exact in fp16 (11 bits, steps down to
-// 2^-24, up to 65504) and in bfloat16 (8 bits): the widening rounds nothing.
+// 2^-24, up to 65504): the widening rounds nothing.
 // The E4M3 NaN scales (0x7F, 0xFF) make their whole block NaN.
 #pragma once
 #include <cstdint>
@@ -44,22 +44,9 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&h)[4]) {
       : "r"(w));
 }
 
-// Byte permute with the selector's sign-replicate bits in effect (bit 3 of a
-// selector nibble spreads the selected byte's sign over the byte).
-__device__ __forceinline__ uint32_t prmt_sign(uint32_t a, uint32_t sel) {
-  uint32_t r;
-  asm("prmt.b32 %0, %1, %1, %2;\n" : "=r"(r) : "r"(a), "r"(sel));
-  return r;
-}
-
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
@@ -67,15 +54,6 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ void e4m3_scales_f16(uint32_t s, uint32_t &s0, uint32_t &s1) {
   uint32_t p;
   asm("{\n .reg .b16 l, u;\n mov.b32 {l, u}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}\n" : "=r"(p) : "r"(s));
-  s0 = __byte_perm(p, 0u, 0x1010);
-  s1 = __byte_perm(p, 0u, 0x3232);
-}
-
-// The same as bfloat16 (the NaN scales stay NaN).
-__device__ __forceinline__ void e4m3_scales_bf16(uint32_t s, uint32_t &s0, uint32_t &s1) {
-  uint32_t p = e4m3_pair_to_bf16x2(__byte_perm(s, 0u, 0x4140));
-  if ((s & 0x7Fu) == 0x7Fu) p |= 0x00007FFFu;
-  if ((s & 0x7F00u) == 0x7F00u) p |= 0x7FFF0000u;
   s0 = __byte_perm(p, 0u, 0x1010);
   s1 = __byte_perm(p, 0u, 0x3232);
 }
@@ -92,34 +70,6 @@ __device__ __forceinline__ void e2m1x32_to_f16(const uint4 raw, uint32_t scales,
     e2m1x8_to_f16(w[q], h);
     const uint32_t s = q < 2 ? s0 : s1;
     out[q] = make_uint4(mul_f16x2(h[0], s), mul_f16x2(h[1], s), mul_f16x2(h[2], s), mul_f16x2(h[3], s));
-  }
-}
-
-// The same as bfloat16.  There is no conversion instruction to bfloat16, so
-// the eight magnitudes are looked up byte by byte with byte permutes: each
-// nibble's low three bits select the high and the low byte of its bfloat16
-// value from two eight-byte tables, and its sign bit comes from a third permute
-// whose table bytes are 0x80 (a selector with bit 3 set replicates the byte's
-// sign: 0xFF, otherwise 0x80), shifted left once.
-__device__ __forceinline__ void e2m1x32_to_bf16(const uint4 raw, uint32_t scales, uint4 (&out)[4]) {
-  uint32_t s0, s1;
-  e4m3_scales_bf16(scales, s0, s1);
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const uint32_t s = q < 2 ? s0 : s1;
-    uint32_t h[4];
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const uint32_t c = half ? w[q] >> 16 : w[q];     // four codes in the low 16 bits
-      const uint32_t sel = c & 0x7777u;
-      const uint32_t lo = __byte_perm(0xC0800000u, 0xC0804000u, sel);
-      uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, sel);
-      hi |= (prmt_sign(0x80808080u, c) << 1) & 0x80808080u;
-      h[2 * half] = mul_bf16x2(__byte_perm(lo, hi, 0x5140), s);
-      h[2 * half + 1] = mul_bf16x2(__byte_perm(lo, hi, 0x7362), s);
-    }
-    out[q] = make_uint4(h[0], h[1], h[2], h[3]);
   }
 }
 

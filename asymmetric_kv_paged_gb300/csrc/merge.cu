@@ -41,9 +41,13 @@ __device__ __forceinline__ void combine(const RunArgs &a, int base, int nrows, i
       }
     }
     float Mn = M;
+    bool seen = false;                      // a NaN split has no maximum but counts
 #pragma unroll
-    for (int u = 0; u < kB; ++u) Mn = fmaxf(Mn, ls[u]);
-    if (Mn == -INFINITY) continue;          // nothing seen yet
+    for (int u = 0; u < kB; ++u) {
+      Mn = fmaxf(Mn, ls[u]);
+      seen |= ls[u] != -INFINITY;
+    }
+    if (Mn == -INFINITY && !seen) continue; // nothing seen yet
     if (M != -INFINITY) {
       const float c = exp2f(M - Mn);
       Z *= c;
@@ -101,7 +105,7 @@ __global__ void __launch_bounds__(32 * kMergeRowsPerCta, 3) merge_kernel(const R
   else
     combine<8>(a, base, bd.nrows, S, lane, M, Z, acc);
   float lse = -INFINITY;
-  if (M != -INFINITY) {
+  if (M != -INFINITY || Z != Z) {
     const float inv = 1.f / Z;
     acc.x *= inv;
     acc.y *= inv;

@@ -168,6 +168,54 @@ def test_nan_scale_is_nan_and_stays_where_it_is_seen(n, hq, P):
     assert np.all(np.isnan(got[hit])) and np.array_equal(got[~hit], ref[~hit])
 
 
+@pytest.mark.parametrize("P", [16, 1])
+@pytest.mark.parametrize("n,hq,seq", [(1, 8, 90), (1, 8, 9000), (2, 16, 9000), (4, 16, 9000), (8, 16, 9000), (16, 16, 300),
+                                      (16, 16, 9000), (200, 16, 300), (200, 16, 9000)])
+def test_nan_scale_of_a_key(n, hq, seq, P):
+    """A NaN block scale of a visible K row makes its score NaN: the rows of that KV
+    head that see the key are NaN, all others as without it (blocks of 4 to 256 rows,
+    whole and split)."""
+    w = W.make_workload(9, [seq + n, 70 + n], [n, n], hq=hq, hkv=2, page_size=P, kv_dtype="fp4")
+    clean = device(w)
+    clean.run()
+    key = seq - 1 + n // 2                                    # later queries see it, earlier ones do not
+    slot = int(w.page_table[0, key // P]) * P + key % P
+    w.k_cache.reshape(-1, 2, 112)[slot, 1, 96 + 5] = 0xFF
+    dw = device(w)
+    dw.run()
+    torch.cuda.synchronize()
+    got, ref = dw.out.float().cpu().numpy(), clean.out.float().cpu().numpy()
+    lse, ref_lse = dw.lse.cpu().numpy(), clean.lse.cpu().numpy()
+    hit = np.zeros(got.shape[:2], bool)
+    hit[key - seq:n, hq // 2:] = True
+    if key < seq:
+        hit[:n, hq // 2:] = True
+    assert hit.any() and np.all(np.isnan(got[hit])) and np.all(np.isnan(lse[hit]))
+    assert np.array_equal(got[~hit], ref[~hit]) and np.array_equal(lse[~hit], ref_lse[~hit])
+    assert err_word(dw) == 0
+
+
+@pytest.mark.parametrize("sinks", [False, True])
+@pytest.mark.parametrize("n,hq,seq", [(1, 8, 5), (1, 8, 9000), (2, 16, 9000), (4, 16, 9000), (8, 16, 9000), (16, 16, 100),
+                                      (16, 16, 9000), (200, 16, 200), (200, 16, 9000)])
+def test_rows_with_nan_scores_only(n, hq, seq, sinks):
+    """Every key of one KV head of a request is NaN: those rows are NaN, not empty."""
+    w = W.make_workload(10, [seq + n, 70 + n], [n, n], hq=hq, hkv=2, page_size=16, sinks=sinks, kv_dtype="fp4")
+    clean = device(w)
+    clean.run()
+    for key in range(seq + n):
+        slot = int(w.page_table[0, key // 16]) * 16 + key % 16
+        w.k_cache.reshape(-1, 2, 112)[slot, 0, 96] = 0x7F
+    dw = device(w)
+    dw.run()
+    torch.cuda.synchronize()
+    got, ref = dw.out.float().cpu().numpy(), clean.out.float().cpu().numpy()
+    hit = np.zeros(got.shape[:2], bool)
+    hit[:n, :hq // 2] = True
+    assert np.all(np.isnan(got[hit])) and np.all(np.isnan(dw.lse.cpu().numpy()[hit]))
+    assert np.array_equal(got[~hit], ref[~hit])
+
+
 def test_large_scores_and_long_tails():
     """Scores of hundreds: weights that differ by more than any 16-bit range, the
     maximum rising late, in one segment and across splits."""
