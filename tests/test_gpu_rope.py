@@ -62,6 +62,10 @@ CASES = [
     ("sym_fp4", "fp4", [90, 50, 20], [5, 0, 3], 8, 2, 64, 128, 128, 0, True, False),
     ("sym_bf16_g5", "bf16", [90, 33], [1, 33], 15, 3, 8, 128, 80, 48, False, False),
     ("many_requests", "fp4", [9] * 700, [1] * 700, 4, 1, 4, 192, 64, 0, False, False),
+    ("a_warp_of_requests", "fp4", list(range(3, 35)), [1, 3] * 16, 8, 2, 16, 192, 64, 0, False, False),
+    ("one_request_more", "bf16", list(range(3, 36)), [3, 1] * 16 + [2], 8, 2, 16, 192, 64, 64, True, False),
+    ("tokens_past_the_warps_fp4", "fp4", [2999, 3000, 7, 1], [2400, 2470, 0, 1], 2, 1, 16, 192, 64, 0, False, False),
+    ("tokens_past_the_warps_fp8", "fp8", [3000, 5, 2999], [2400, 4, 2500], 3, 1, 1, 128, 64, 64, True, True),
 ]
 
 
@@ -191,6 +195,31 @@ def test_bad_pages_positions_and_lengths_are_skipped(kv):
     zero = (bits(ko) == 0).all((1, 2)) & (bits(vo) == 0).all((1, 2))
     # rows: bad page; position -1; two rows past kv_indptr's last
     assert zero.tolist() == [False, False, True, True, False, False, True, True]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "fp4"])
+def test_tokens_that_the_layout_does_not_hold_are_skipped(kv):
+    """The device's qo_indptr ends two tokens early: those are reported, nothing of them
+    is written, the others as ever."""
+    from asymmetric_kv_paged_gb300 import binding as B
+    w, dw = setup(kv, [60, 50], [4, 3], hq=8, hkv=2, P=16)
+    rng = np.random.default_rng(4)
+    kn, vn = rows(rng, 7, 2, 192), rows(rng, 7, 2, 128)
+    tab = table(64, 64)
+    rope = B.make_rope(torch.from_numpy(tab).cuda(), 64, 0, False)
+    short = torch.tensor([0, 4, 5], dtype=torch.int32, device="cuda")
+    lens = np.array([60, 50])
+    pos = np.array([56, 57, 58, 59, 49])
+    k_rot = A.rotate(W.bf16_values(kn[:5]), tab[pos][:, None], 64, 0, False)
+    ref_k, ref_v = A.append_rows(k_rot, W.bf16_values(vn[:5]), w.k_cache, w.v_cache, w.page_table, lens,
+                                 np.array([0, 4, 5]), kv, w.k_scale, w.v_scale)
+    q_out = torch.zeros_like(dw.q)
+    B.attn_append_kv_rope(dw.plan, rope, dw.q, dev(kn), dev(vn), q_out, dw.k_cache, dw.v_cache, dw.page_table,
+                          dw.seq_lens, short, w.k_scale, w.v_scale)
+    torch.cuda.synchronize()
+    assert B.attn_get_device_error(dw.plan) == 4
+    same_caches(dw, ref_k, ref_v)
+    assert (bits(q_out) != 0).any((1, 2)).tolist() == [True] * 5 + [False] * 2
 
 
 def test_refusals():
