@@ -300,7 +300,14 @@ def make_rope(cos_sin, rot_dim: int, rot_offset: int = 0, interleaved: bool = Fa
               positions=None) -> attn_rope_t:
     """The rotation of attn_append_kv_rope.  cos_sin: fp32 [max_pos, rot_dim] on the
     device, cosines then sines; positions: int32 [total_q] on the device, or None for
-    the tokens' own.  The result keeps both tensors alive."""
+    the tokens' own.  The result keeps both tensors alive.  Shapes and types, which
+    the library cannot see, are checked here, once for all steps."""
+    import torch
+    if cos_sin.dim() != 2 or cos_sin.shape[1] != rot_dim or cos_sin.dtype != torch.float32 or \
+            not cos_sin.is_contiguous():
+        raise ValueError("cos_sin must be contiguous fp32 [max_pos, rot_dim]")
+    if positions is not None and (positions.dtype != torch.int32 or not positions.is_contiguous()):
+        raise ValueError("positions must be contiguous int32")
     r = attn_rope_t(_ptr(cos_sin), _ptr(positions), int(cos_sin.shape[0]), int(rot_dim),
                     int(rot_offset), int(bool(interleaved)))
     r.keep = (cos_sin, positions)

@@ -1,15 +1,14 @@
-// Split-KV attention over a 4-bit cache for row blocks of at most 16 query rows
+// Split-KV attention over a 4-bit cache for row blocks of at most 32 query rows
 // (decode, and a few draft tokens on small groups).
 //
-// At these sizes a key's 192 bytes feed at most 16 rows, and what bounds the
-// tcgen05 kernel (attn_tc.cu) is not the tensor pipe but shared memory: its
-// operands have to be 16-bit tiles there, so every 4-bit tile would be read,
-// written four times as wide, and read again (128 KB of shared-memory traffic
-// for 12 KB of cache: ~1000 cycles a 64-key tile, where HBM delivers one in
-// ~580).  Here the codes go from the TMA ring straight into registers, are
-// widened there, and feed register-operand MMAs (m16n8k16, fp16, fp32
-// accumulation).  Both products are computed transposed, so that the padded
-// side is the 8-row granule and not 64 rows of MMA:
+// At these sizes a key's 192 bytes feed few rows, and what bounds the tcgen05 kernel
+// (attn_tc.cu) is not the tensor pipe but getting there: its operands have to be
+// 16-bit tiles in shared memory, so every 4-bit tile is read, written four times as
+// wide, and read again, and a 64-key tile passes through four warp roles.  Here the
+// codes go from the TMA ring straight into registers, are widened there, and feed
+// register-operand MMAs (m16n8k16, fp16, fp32 accumulation).  Both products are
+// computed transposed, so that the padded side is the 8-row granule (1, 2 or 4 of
+// them: NB) and not 64 rows of MMA:
 //   S^T (keys x rows) = K (16 keys x 16 dims) . Q^T (16 dims x 8 rows),
 //   O^T (dv x rows)   = V^T (16 dv x 16 keys) . P^T (16 keys x 8 rows).
 // The order of a contraction's index is free, so lanes take what is
@@ -32,14 +31,23 @@
 // A unit of work is half a 64-key tile (32 keys); unit u of the CTA belongs to
 // warp u % kWarps, which keeps running maxima, sums and O of its own for the
 // whole segment, so nothing is shared between tiles; at the end of a segment
-// the warps' partials are combined through shared memory  Each warp also
-// fetches its own units, into a ring of its own, a few units ahead: it alone
+// the warps' partials are combined through shared memory.  Each warp also
+// fetches its own units, into a ring of its own, a unit or two ahead: it alone
 // fills, waits for and frees the ring's stages, in order, so that no barrier
 // phase can be mistaken for another and no warp ever waits for another one's
 // data.  With page sizes TMA can tile a unit is one K and one V box per page
 // piece, issued by a lane each after up to 32 page lookups in one round trip;
 // otherwise its rows are gathered with 16-byte asynchronous copies.
 // Every wait is bounded in time, as in attn_tc.cu.
+//
+// Measured (16 query heads on 2 KV heads unless said, merge included): a ragged
+// decode batch of 32 requests, 195 MB of rows, 50 us (3.9 TB/s, 0.58 of the copy rate;
+// fetching alone, without any arithmetic, takes 42.7 us, so what is left is the
+// fetch and the warps' issue slots, 70% busy); four requests of 46K keys 23 us with
+// 8 rows and 43 with 32 (there it is the latency of one warp's chain: 2 warps a
+// scheduler, 0.36 instructions a cycle); pages of one token, 16 rows, 109 MB, 54 us
+// (16-byte copies).  12 warps for 8 rows, 8 beyond: what the registers allow; 16 of
+// 128 registers took 54 us on the batch, a ring of three units 53.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -85,11 +93,11 @@ struct Cfg {
   static constexpr int kOffComb = kOffQ + kQBytes;
   static constexpr int kSmem = kOffComb + (kCombInRing ? 0 : kWarps * kCombRows * kCombStride * 4) + 1024;
   static_assert(!kCombInRing || kCombRows * kCombStride * 4 <= Unit<DQK>::kBytes, "partial larger than a stage");
-  static_assert(kSmem + 3072 <= 227 * 1024, "shared memory layout too large");
+  static_assert(kSmem + 3 * 1024 <= 227 * 1024, "shared memory layout too large");
 };
 
 struct FBars {
-  uint64_t full[16][3];
+  uint64_t full[12][3];       // [warp][stage of its ring]
   uint64_t sync;
 };
 
@@ -727,8 +735,6 @@ template <int DQK, int NB>
 cudaError_t prepare_nb(const HostPlan &hp) {
   return hp.use_tma ? prepare_one<DQK, NB, true>() : prepare_one<DQK, NB, false>();
 }
-
-
 
 template <int DQK>
 cudaError_t launch_dqk(const HostPlan &hp, const RunArgs &a, const TmaMaps &m, cudaStream_t st) {

@@ -18,19 +18,28 @@
 //              (HALF instantiations: lanes l and l+16 share row 16w + l%16,
 //              32 key columns each);
 //   warps 4-7  converters: stage Q per block; turn raw FP8 K/V tiles into
-//              exact bf16 operand tiles; zero V rows of keys outside the
+//              exact bf16 operand tiles and raw 4-bit ones into exact fp16
+//              ones (4-bit plans form both products in fp16, Q scaled per
+//              row by a power of two); zero V rows of keys outside the
 //              block's range on edge tiles (unused slots may hold NaN:
 //              sammysun0711/sglang PR #35, FlyPA V-tail masking); or, for
 //              page sizes TMA cannot tile, gather K/V rows themselves;
 //   warp  8    TMEM allocation; issues the S = Q.K^T MMAs (one thread);
-//   warp  9    TMA producer: page-table lookup, then 3D tensor-map loads of
-//              the K/V boxes (BF16: straight into the 128-byte swizzled
-//              operand layout; FP8: raw rows into a staging ring); for the
+//   warp  9    TMA producer: page-table lookups a tile ahead, a lane per box,
+//              then 3D tensor-map loads of the K/V boxes (BF16: straight into the
+//              128-byte swizzled operand layout; FP8 and 4-bit: raw rows into a
+//              staging ring); for the
 //              gather path, the page lookups into a ring of resolved slots;
 //   warp 10    issues the O += P.V MMAs (one thread).
 // A CTA starts from its head record (segment range, tile count, first segment
 // and block) and is launched as a programmatic dependent (griddepcontrol).
 // TMEM: S double buffer (2 x 64 columns), O (128 columns), P double buffer (2 x 32).
+// 4-bit caches come here with 33 to 128 rows a block (fewer run attn_fp4.cu): 64
+// rows over four requests of 46K keys, 67 MB of rows, take 51 us, about 1 us a
+// 64-key tile and CTA on top of ~14 us of launch, start and merge.  Left out one by
+// one, the conversion is worth 4 us, the softmax 5 and the 16 MMAs of a tile 9 (they
+// cost the same ~60 cycles whatever their N up to 128); barriers and fetch are the
+// remaining 20.
 // Every wait is bounded in time; a broken invariant ends the kernel with bit 1
 // of the plan's error word set instead of hanging the GPU.
 #include <cuda_bf16.h>

@@ -10,7 +10,8 @@
 // the paged layout of the MiMo-V2.6-Flash-RL model card, "What the kernels
 // do"): BF16 rows are copied bit for bit, E4M3 codes are widened exactly to
 // fp16 (every E4M3 value is an fp16 value; the scale stays outside, as in the
-// attention kernels), E2M1 codes with their block scales likewise (e2m1.cuh).  Keys outside [klo, khi) are written as zeros: the
+// attention kernels), E2M1 codes with their block scales likewise
+// (e2m1.cuh).  Keys outside [klo, khi) are written as zeros: the
 // kernel masks them, and zeros keep P.V free of whatever the pool holds
 // there.  A page id outside the pool is read as zeros and reported in bit 1
 // of the plan's error word, as the attention kernels do.

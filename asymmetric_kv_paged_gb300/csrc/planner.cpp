@@ -133,10 +133,23 @@ attn_status_t build_host_plan(const attn_problem_t *p, int32_t num_sms, HostPlan
   hp.prefill = hp.block_rows == 256;
   hp.key_tile = hp.prefill ? kPrefillKeyTile : kKeyTile;
   // Up to 32 rows over a 4-bit cache run attn_fp4.cu (measured against the tcgen05
-  // kernel, four requests of 46K keys: 8 rows 23 us and 126, 32 rows 43 us and 77;
-  // 64 rows as two groups of 32 74 us and 70).
-  if (p->kv_dtype == ATTN_KV_FP4_E2M1 && max_rows <= kFp4MaxRows)
-    hp.fp4_rows = max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : 32;
+  // kernel, four requests of 46K keys: 8 rows 23 us and 51, 32 rows 43 us and 59;
+  // 64 rows as two groups of 32 74 us and 51).  With 17 to 32 rows its start and
+  // end cost more than the other one's, which its tiles only win back from about
+  // three to an SM on: 16 requests of 500 keys 15.0 us and 11.6, of 1000 13.8 and
+  // 16.5, of 8000 40.7 and 53.9; up to 16 rows it is the faster one throughout (500
+  // keys 10.1 and 11.3, 1000 keys 9.7 and 15.8).
+  if (p->kv_dtype == ATTN_KV_FP4_E2M1 && max_rows <= kFp4MaxRows) {
+    int64_t tiles = 0;
+    for (int32_t b = 0; b < p->batch; ++b) {
+      const int64_t n = hp.qo_indptr[b + 1] - hp.qo_indptr[b], L = hp.seq_lens[b];
+      if (n == 0) continue;
+      const int64_t lo = p->window > 0 ? std::max<int64_t>(0, L - n - p->window + 1) : 0;
+      tiles += ((L - 1) / kKeyTile - lo / kKeyTile + 1) * p->num_kv_heads;
+    }
+    if (max_rows <= 16 || tiles >= 3 * (int64_t)num_sms)
+      hp.fp4_rows = max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : 32;
+  }
   const int32_t rows_per_block = hp.block_rows;
   const int32_t tile = hp.key_tile;
   const int32_t G = hp.group;

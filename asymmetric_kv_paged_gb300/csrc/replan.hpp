@@ -9,10 +9,11 @@
 //     planner (bottom-right causal alignment, optional window);
 //   - its tiles take the global positions [start[bi], start[bi+1]) of the
 //     exclusive prefix sum `start` of the tile counts (T = start[nb] tiles);
-//   - with C' = min(C, T) working CTAs (4-bit plans: fewer, see min_tiles), CTA c takes positions
-//     [c*P/C', (c+1)*P/C') (equal shares, rounded down; in a lockstep plan,
-//     whose blocks come head by head, the share of CTA c is the one of its
-//     place among the CTAs of head c % heads), so a block is cut wherever a share ends and each piece is one segment.  On shares of 32
+//   - with C' = min(C, T) working CTAs (4-bit plans: fewer, see min_tiles),
+//     CTA c takes positions [c*P/C', (c+1)*P/C') (equal shares, rounded down;
+//     in a lockstep plan, whose blocks come head by head, the share of CTA c is
+//     the one of its place among the CTAs of head c % heads), so a block is cut
+//     wherever a share ends and each piece is one segment.  On shares of 32
 //     tiles or more every block is first given `charge` positions without a
 //     tile (P = T + charge * nb): the CTA whose share reaches into a block
 //     pays for its epilogue and Q staging with that much less work, as in the

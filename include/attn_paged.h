@@ -193,17 +193,19 @@ attn_status_t attn_plan_replayable(const attn_problem_t *bounds, int device, att
  *   workspace    device scratch of at least workspace_bytes (may be NULL when
  *                the plan reported 0).  Its contents need no initialisation.
  * Slots of the caches that no query can see are never read, so they may hold
- * anything (NaN included).  Queries keep their full bf16 range for either
+ * anything (NaN included).  Queries keep their full bf16 range for every
  * cache type.  Plans whose row blocks hold at most 128 rows (decode, verify)
- * widen E4M3 and E2M1 elements exactly to bf16 and form every product as
- * bf16 x bf16 with fp32 accumulation.  Plans with larger blocks (chunked
- * prefill) run Q.K^T on an FP8 or 4-bit cache in fp16: each query row is multiplied by the power of
- * two that puts its largest |q| in [2^14, 2^15) (exact; every element down to
- * 2^-31 of that maximum stays exact in fp16), the cache is widened exactly to
- * fp16, and the scores are divided by the same power of two in fp32; P.V
- * is fp16 x fp16 with fp32 accumulation.  The E4M3 NaN codes (0x7F, 0xFF) in
- * a visible slot read as +-480 on the decode/verify plans and stay NaN on the
- * prefill plans; NaN block scales of a 4-bit cache are NaN on every plan.
+ * widen E4M3 elements exactly to bf16 and form every product as bf16 x bf16
+ * with fp32 accumulation.  Plans with larger blocks (chunked prefill) on an FP8
+ * cache, and every plan on a 4-bit cache, run in fp16: each query row is
+ * multiplied by the power of two that puts its largest |q| in [2^14, 2^15)
+ * (exact; every element down to 2^-31 of that maximum stays exact in fp16), the
+ * cache is widened exactly to fp16, and the scores are divided by the same power
+ * of two in fp32; P.V is fp16 x fp16 with fp32 accumulation.  The E4M3 NaN codes
+ * (0x7F, 0xFF) in a visible slot read as +-480 on the decode/verify plans and stay
+ * NaN on the prefill plans; a NaN block scale of a 4-bit cache is NaN on every
+ * plan: in a K row the key's score is NaN, and with it every row that sees the
+ * key; in a V row the block's 16 output dims are.
  * Prefill plans that are not replayable first gather the keys their blocks
  * read into a staging scratch in the workspace (16-bit rows: E4M3 and
  * E2M1 widened exactly to fp16, BF16 copied; (Dqk + 128) * 2 bytes per key of each KV

@@ -135,3 +135,15 @@ def test_host_plans_and_null_arguments_are_refused():
         assert L.attn_read_kv(p, 64, 64, 64, 64, 64, 1, 64, 64, 1.0, 1.0, None) == B.ATTN_ERR_INVALID_ARG
         assert L.attn_append_kv(p, *[64] * 7, 1.0, 1.0, None) == B.ATTN_ERR_INVALID_ARG
     assert L.attn_append_kv_rope(plan.handle, None, *one, 1.0, 1.0, None) == B.ATTN_ERR_INVALID_ARG
+
+
+def test_make_rope_checks_what_the_library_cannot_see():
+    torch = pytest.importorskip("torch")
+    tab = torch.zeros(10, 64)
+    assert (lambda r: (r.max_pos, r.rot_dim, r.rot_offset, r.interleaved))(B.make_rope(tab, 64, 8, True)) == (10, 64, 8, 1)
+    for bad in (tab.double(), tab[:, :32], tab.t(), tab.view(-1)):
+        with pytest.raises(ValueError):
+            B.make_rope(bad, 64)
+    for pos in (torch.zeros(4), torch.zeros(8, dtype=torch.int32)[::2], torch.zeros(4, dtype=torch.int64)):
+        with pytest.raises(ValueError):
+            B.make_rope(tab, 64, positions=pos)

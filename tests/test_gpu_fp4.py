@@ -82,6 +82,12 @@ CASES = [
     ("swa_decode", [700, 5000, 100], [1, 1, 1], 16, 2, 16, 128, True, 192),
     ("window_one", [300], [8], 8, 1, 16, 1, True, 192),
     ("swa_small_window_p3", [400, 90], [8, 2], 8, 2, 3, 5, True, 192),
+    # 17 to 32 rows, enough key tiles for the register kernel
+    ("rows32_p128", [12000, 5000, 130], [4, 3, 4], 16, 2, 128, 0, True, 192),
+    ("rows24_p1", [9000, 7000], [3, 2], 16, 2, 1, 0, False, 192),
+    ("rows32_d128_p16", [15500], [4], 16, 2, 16, 0, True, 128),
+    ("rows20_swa_p8", [700 + 37 * i for i in range(80)], [4, 1, 3, 2] * 20, 10, 2, 8, 200, True, 192),
+    ("rows32_p3_one_head", [30000], [2], 16, 1, 3, 0, False, 192),
     ("prefill_g16", [700], [300], 32, 2, 128, 0, False, 192),
     ("prefill_p1", [500], [130], 16, 2, 1, 0, True, 192),
     ("prefill_swa_p16", [900, 40], [400, 40], 16, 2, 16, 77, True, 192),
@@ -169,7 +175,8 @@ def test_nan_scale_is_nan_and_stays_where_it_is_seen(n, hq, P):
 
 
 @pytest.mark.parametrize("P", [16, 1])
-@pytest.mark.parametrize("n,hq,seq", [(1, 8, 90), (1, 8, 9000), (2, 16, 9000), (4, 16, 9000), (8, 16, 9000), (16, 16, 300),
+@pytest.mark.parametrize("n,hq,seq", [(1, 8, 90), (1, 8, 9000), (2, 16, 9000), (4, 16, 9000), (4, 16, 16000),
+                                      (8, 16, 9000), (16, 16, 300),
                                       (16, 16, 9000), (200, 16, 300), (200, 16, 9000)])
 def test_nan_scale_of_a_key(n, hq, seq, P):
     """A NaN block scale of a visible K row makes its score NaN: the rows of that KV
@@ -196,7 +203,8 @@ def test_nan_scale_of_a_key(n, hq, seq, P):
 
 
 @pytest.mark.parametrize("sinks", [False, True])
-@pytest.mark.parametrize("n,hq,seq", [(1, 8, 5), (1, 8, 9000), (2, 16, 9000), (4, 16, 9000), (8, 16, 9000), (16, 16, 100),
+@pytest.mark.parametrize("n,hq,seq", [(1, 8, 5), (1, 8, 9000), (2, 16, 9000), (4, 16, 9000), (4, 16, 16000),
+                                      (8, 16, 9000), (16, 16, 100),
                                       (16, 16, 9000), (200, 16, 200), (200, 16, 9000)])
 def test_rows_with_nan_scores_only(n, hq, seq, sinks):
     """Every key of one KV head of a request is NaN: those rows are NaN, not empty."""
@@ -265,6 +273,44 @@ def test_replayed_graph_follows_the_lengths():
         pb["seq_lens"] = np.array(lens, np.int32)
         check(pb, dw.out, dw.lse, str(lens))
     assert err_word(dw) == 0
+
+
+@pytest.mark.parametrize("n,seqs,runs", [
+    (2, [900, 200, 3000], ([900, 200, 3000], [2, 64, 66], [333, 199, 2999])),
+    (4, [12000, 5000, 130], ([12000, 5000, 130], [4, 4, 4], [11999, 64, 5], [65, 4999, 129])),
+    (8, [900, 200], ([900, 200], [8, 8], [65, 199]))])
+def test_replayed_graph_of_draft_tokens(n, seqs, runs):
+    w = build(("replay_draft", seqs, [n] * len(seqs), 16, 2, 128, 0, True, 192))
+    dw = device(w, replayable=True)
+    dw.run()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dw.run()
+    for lens in runs:
+        dw.seq_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        pb = w.host_arrays()
+        pb["seq_lens"] = np.array(lens, np.int32)
+        check(pb, dw.out, dw.lse, str(lens))
+    assert err_word(dw) == 0
+
+
+@pytest.mark.parametrize("n,L", [(2, 6000), (4, 16000)])
+def test_large_scores_of_draft_tokens(n, L):
+    """As test_large_scores_and_long_tails, same tolerance, for 16 and 32 rows."""
+    w = W.make_workload(13, [L], [n], hq=16, hkv=2, page_size=128, kv_dtype="fp4", q_std=8.0, k_std=3.0)
+    dw = device(w)
+    dw.run()
+    torch.cuda.synchronize()
+    ref, ref_lse = oracle.attn_paged(w.host_arrays())
+    mag = w.host_arrays()
+    mag["v_cache"] = mag["v_cache"] & 0x7FFF
+    a, _ = oracle.attn_paged(mag)
+    got = dw.out.float().cpu().numpy()
+    assert np.all(np.abs(got - ref) <= U * (a + np.abs(ref)) + 7e-3 * a + 1e-9)
+    assert np.abs(dw.lse.cpu().numpy() - ref_lse).max() <= 7e-3
 
 
 @pytest.mark.parametrize("n", [8, 100])

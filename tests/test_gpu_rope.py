@@ -231,8 +231,9 @@ def test_refusals():
     before = bits(dw.k_cache).copy()
 
     def call(rot=64, off=0, cs=tab, q=dw.q, q_out=dw.q, k=kn, kc=dw.k_cache, ks=1.0, pt=dw.page_table):
-        B.attn_append_kv_rope(dw.plan, B.make_rope(cs, rot, off), q, k, vn, q_out, kc, dw.v_cache, pt,
-                              dw.seq_lens, dw.qo_indptr, ks, 1.0)
+        rope = B.attn_rope_t(cs.data_ptr(), None, cs.shape[0], rot, off, 0)
+        B.attn_append_kv_rope(dw.plan, rope, q, k, vn, q_out, kc, dw.v_cache, pt, dw.seq_lens, dw.qo_indptr,
+                              ks, 1.0)
 
     I, S = B.ATTN_ERR_INVALID_ARG, B.ATTN_ERR_UNSUPPORTED
     for kw, status in ((dict(rot=24), S), (dict(rot=64, off=4), S), (dict(rot=0), I), (dict(rot=-16), I),
