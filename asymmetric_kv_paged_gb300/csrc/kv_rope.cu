@@ -26,16 +26,17 @@
 // owns a range of consecutive tokens and every S-th row step of them, S chosen so
 // that all SMs' warps have work (decode: a row each; long chunks: whole tokens),
 // which walks the chain of dependent lookups (request, length, page) once per
-// range and not once per row; the query loop keeps four rows' loads in flight.
+// range and not once per row; the query loop keeps the loads of the next four rows in
+// flight (two: 46.6 us on the first case below, six: 44.4 for the spilled registers).
 //
 // Measured (in a graph): 4096 tokens of 64 query and 4 KV heads rotated and
-// quantised to E4M3, 217 MB, 43 us (5.0 TB/s, 0.75 of the copy rate; 7.4 us of it
-// for K and V alone); 4098 tokens of 32 and 8 heads to 4 bits, 128 MB, 33.5 us, K
+// quantised to E4M3, 217 MB, 40.6 us (5.3 TB/s, 0.80 of the copy rate; 7.4 us of it
+// for K and V alone); 4098 tokens of 32 and 8 heads to 4 bits, 128 MB, 32.3 us, K
 // and V 16 (issue: a value's two quotients, block maximum and codes); 4095 tokens of
 // 4 heads to 4 bits, not rotated, 13.6 MB, 9.8 us.  A decode step's 32 tokens take
 // 3.4 us, 4.5 with rotation and queries: the launch and four dependent loads.  Four
 // CTAs of 64 registers an SM: three of 80 took 55 us on the first, five 12.3 us on
-// the third.
+// the third; twice as many, shorter warps' shares 10.9 us on the third.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -512,26 +513,35 @@ __global__ void __launch_bounds__(kAppendThreads, 4) rope_append_kernel(const Ro
     if constexpr (ROPE != kNoRope) {
       if (a.q) {
         const bool moves = sub < RPW && (turn.in || a.q != a.q_out);
-        const int64_t row0 = (int64_t)tok * a.hq * DQK;
         const int steps = (a.hq + RPW - 1) / RPW;
         constexpr int kAhead = 4;
+        const int h0 = slice * RPW + sub;
+        const int64_t at = ((int64_t)tok * a.hq + h0) * DQK + ch * 8;
+        const uint16_t *src = a.q + at;
+        uint16_t *dst = a.q_out + at;
+        const int stride = a.slices * RPW * DQK;
+        int h = h0, h_next = h0;
+        auto next = [&]() {
+          uint4 v = make_uint4(0u, 0u, 0u, 0u);
+          if (moves && h_next < a.hq) v = *reinterpret_cast<const uint4 *>(src);
+          h_next += a.slices * RPW;
+          src += stride;
+          return v;
+        };
+        uint4 x[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) x[k] = next();
 #pragma unroll 1
         for (int st0 = slice; st0 < steps; st0 += kAhead * a.slices) {
-          uint4 x[kAhead];
-#pragma unroll
-          for (int k = 0; k < kAhead; ++k) {
-            const int h = (st0 + k * a.slices) * RPW + sub;
-            x[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (moves && h < a.hq) x[k] = *(reinterpret_cast<const uint4 *>(a.q + row0 + (int64_t)h * DQK) + ch);
-          }
 #pragma unroll
           for (int k = 0; k < kAhead; ++k) {
             if (st0 + k * a.slices >= steps) break;
-            const int h = (st0 + k * a.slices) * RPW + sub;
             float v[8];
             turn.apply(x[k], v);
-            if (moves && h < a.hq)
-              *(reinterpret_cast<uint4 *>(a.q_out + row0 + (int64_t)h * DQK) + ch) = turn.in ? pack8(v) : x[k];
+            if (moves && h < a.hq) *reinterpret_cast<uint4 *>(dst) = turn.in ? pack8(v) : x[k];
+            x[k] = next();
+            h += a.slices * RPW;
+            dst += stride;
           }
         }
       }
