@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstring>
 #include <algorithm>
+#include <limits>
 #include <new>
 #include <vector>
 
@@ -265,7 +266,10 @@ static attn_status_t run_impl(attn_plan_t plan, int phases, bool allow_stage, co
   a.v_cache = v_cache;
   a.page_table = page_table;
   a.sinks = sinks;
-  a.scale_log2 = softmax_scale * (raw ? k_scale : 1.f) * 1.4426950408889634f;
+  // (a product that underflows to zero would make a masked score -inf * 0; with the
+  // smallest fp32 in its place no score of queries up to 2^100 moves by 1e-8)
+  a.scale_log2 = std::max(softmax_scale * (raw ? k_scale : 1.f) * 1.4426950408889634f,
+                          std::numeric_limits<float>::denorm_min());
   a.v_scale = raw ? v_scale : 1.f;
   a.out = out;
   a.lse_out = lse_out;

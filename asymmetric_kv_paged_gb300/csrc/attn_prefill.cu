@@ -695,7 +695,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             // the scores of this row come from Q scaled by 2^sh (see q_row_shift)
             const int sh = q_row_shift(reinterpret_cast<const uint4 *>(
                 static_cast<const uint16_t *>(a.q) + ((int64_t)row_tok * a.hq + row_h) * kDqk));
-            sc = a.scale_log2 * __int_as_float((127 - sh) << 23);
+            sc = tc::row_score_scale(a.scale_log2, sh);
           }
           const int i = bd.L - bd.n + flat / a.group;
           row_hi = i + 1;

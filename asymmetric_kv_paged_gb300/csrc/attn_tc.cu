@@ -1181,7 +1181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (t == 0 && k == 0) AKP_STAMP(kStampFirstS);
       tc::tc_fence_after();
       if (F16 && cur.first())
-        row_sc = a.scale_log2 * __int_as_float((127 - (pos >= 0 ? sm_shift[cur.si & 3][pos] : 0)) << 23);
+        row_sc = tc::row_score_scale(a.scale_log2, pos >= 0 ? sm_shift[cur.si & 3][pos] : 0);
       if (!tile_body(k)) break;
       tc::tc_fence_before();
       tc::mbar_arrive(&bars.p_full[b]);

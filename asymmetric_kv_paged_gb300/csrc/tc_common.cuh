@@ -147,6 +147,15 @@ __device__ __forceinline__ void fadd2(float &s0, float &s1, float x0, float x1) 
       : "f"(x0), "f"(x1));
 }
 
+// Base-2 score scale of a row whose queries went to fp16 times 2^sh: scale_log2
+// 2^-sh, but at least the smallest normal fp32.  The scores of such a row are below
+// 2^34 (|q| < 2^15, 4-bit |k| <= 2688, 192 products), so the bound moves none by more
+// than 2^-92, while a scale that underflowed to zero (sh = 126: a zero row) would
+// turn a masked -inf into NaN.
+__device__ __forceinline__ float row_score_scale(float scale_log2, int sh) {
+  return fmaxf(scale_log2 * __int_as_float((127 - sh) << 23), 0x1p-126f);
+}
+
 // ---------------------------------------------------------------- fences
 
 // Make this thread's generic-proxy shared-memory writes visible to the async
