@@ -24,7 +24,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "attn_tc.cu", "attn_fp4.cu", "attn_prefill.cu", "merge.cu", "replan.cu", "no_workspace.cu", "kv_append.cu",
            "kv_stage.cu", "kv_rope.cu",
            "tc_selftest.cu", "planner.cpp"]
-HEADERS = ["plan.hpp", "replan.hpp", "kernels.hpp", "tc_common.cuh", "e4m3.cuh", "e2m1.cuh", "stamps.cuh"]
+HEADERS = ["plan.hpp", "replan.hpp", "kernels.hpp", "tc_common.cuh", "e4m3.cuh", "e2m1.cuh", "fp4_nan.cuh",
+           "stamps.cuh"]
 
 
 def build_dir(stamps: bool = False) -> str:

@@ -94,12 +94,13 @@ attn_status_t upload(attn_plan_s *p) {
   const size_t h_bytes = align256(hp.cta_heads.size() * sizeof(akp::CtaHead));
   const size_t m_bytes = align256(hp.merge_items.size() * sizeof(akp::MergeItem));
   const size_t u_bytes = align256(hp.stage_units.size() * sizeof(akp::StageUnit));
+  const size_t n_bytes = hp.prob.kv_dtype == ATTN_KV_FP4_E2M1 ? align256((size_t)hp.stage_tiles) : 0;
   const size_t e_bytes = 256;
   // replayable plans: the length bounds and two scratch arrays of the planner
   const size_t r_bytes = hp.replayable ? align256(hp.seq_lens.size() * sizeof(int32_t)) +
                                              2 * align256((hp.blocks.size() + 1) * sizeof(int32_t))
                                        : 0;
-  const size_t total = b_bytes + s_bytes + c_bytes + m_bytes + e_bytes + r_bytes + h_bytes + u_bytes;
+  const size_t total = b_bytes + s_bytes + c_bytes + m_bytes + e_bytes + r_bytes + h_bytes + u_bytes + n_bytes;
   uint8_t *base = nullptr;
   if (cudaMalloc(&base, total) != cudaSuccess) return ATTN_ERR_CUDA;
   p->dev.blocks = reinterpret_cast<akp::BlockDesc *>(base);
@@ -112,6 +113,7 @@ attn_status_t upload(attn_plan_s *p) {
   if (!hp.stage_units.empty())
     p->dev.stage_units = reinterpret_cast<akp::StageUnit *>(base + b_bytes + s_bytes + c_bytes +
                                                             m_bytes + e_bytes + r_bytes + h_bytes);
+  if (n_bytes) p->dev.stage_nan = base + total - n_bytes;
   if (hp.replayable) {
     uint8_t *r = base + b_bytes + s_bytes + c_bytes + m_bytes + e_bytes;
     p->dev.seq_bounds = reinterpret_cast<int32_t *>(r);
@@ -290,6 +292,7 @@ static attn_status_t run_impl(attn_plan_t plan, int phases, bool allow_stage, co
   a.num_pages = pr.num_pages;
   a.window = pr.window;
   a.err = plan->dev.err;
+  a.stage_nan = plan->dev.stage_nan;
   a.replayed = hp.replayable;
 
   akp::TmaMaps maps{};
@@ -341,6 +344,7 @@ static attn_status_t run_impl(attn_plan_t plan, int phases, bool allow_stage, co
     sa.page_table = page_table;
     sa.k_stage = reinterpret_cast<uint16_t *>(ws);
     sa.v_stage = reinterpret_cast<uint16_t *>(ws + akp::stage_k_bytes(hp.stage_rows, pr.head_dim_qk));
+    sa.tile_nan = plan->dev.stage_nan;
     sa.err = plan->dev.err;
     sa.tiles = hp.stage_tiles;
     sa.num_units = (int32_t)hp.stage_units.size();

@@ -55,6 +55,7 @@
 #include <cstdint>
 
 #include "e2m1.cuh"
+#include "fp4_nan.cuh"
 #include "kernels.hpp"
 #include "tc_common.cuh"
 
@@ -163,6 +164,7 @@ __global__ void __launch_bounds__(Cfg<DQK, NB>::kThreads, 1)
   uint8_t *smem = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
   __shared__ FBars bars;
   __shared__ int abort_flag;
+  __shared__ int v_nan;           // a NaN V block of a unit cut by some row's range (fp4_nan.cuh)
   __shared__ float sm_m[kWarps][NB * 8], sm_l[kWarps][NB * 8];
   __shared__ __align__(8) float sm_sc[C::kQsmem ? NB * 8 : 2];     // the rows' score scales
 
@@ -179,6 +181,7 @@ __global__ void __launch_bounds__(Cfg<DQK, NB>::kThreads, 1)
   const int total_units = head.total * kUnits;
   if (tid == 0) {
     abort_flag = 0;
+    v_nan = 0;
     for (int w = 0; w < kWarps; ++w)
       for (int d = 0; d < kDepth; ++d) tc::mbar_init(&bars.full[w][d], 1);
     tc::mbar_init(&bars.sync, kWarps);
@@ -551,12 +554,19 @@ __global__ void __launch_bounds__(Cfg<DQK, NB>::kThreads, 1)
             sb[y] = vs[kk * T::kVrow];
           }
           if (!full) {
-            // keys outside the block's range may hold anything: NaN scales to zero
+            // keys outside the block's range may hold anything: NaN scales to zero, and
+            // those that only some rows see must not reach the others (fp4_nan.cuh)
             const int j0 = key0 + mt * 16 + 2 * t;
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
               const int j = j0 + (y & 1) + 8 * (y >> 1);
               if (j < bd.klo || j >= bd.khi) sb[y] = 0u;
+            }
+            const uint32_t nan = e4m3_nan_bytes(sb[0] | sb[1] << 8 | sb[2] << 16 | sb[3] << 24);
+            if (nan) {
+              v_nan = 1;
+#pragma unroll
+              for (int y = 0; y < 4; ++y) sb[y] &= ~(nan >> (8 * y));
             }
           }
           const uint32_t sA = e4m3x2_to_f16(sb[0] | sb[1] << 8), sB = e4m3x2_to_f16(sb[2] | sb[3] << 8);
@@ -713,6 +723,7 @@ __global__ void __launch_bounds__(Cfg<DQK, NB>::kThreads, 1)
   }
   __syncthreads();
   if (tid == 0 && abort_flag) atomicOr(a.err, 2);
+  if (v_nan) patch_nan_rows(a, kN, kUnitKeys);
 }
 
 template <int DQK, int NB, bool TMA>

@@ -24,7 +24,8 @@
 //               an FP8 or 4-bit cache run in fp16.)
 //   warp  12    TMEM allocation; one thread issues the MMAs of Q tile 0;
 //   warp  13    one thread issues the MMAs of Q tile 1;
-//   warps 14-15 idle (they complete the fourth warpgroup).
+//   warps 14-15 complete the fourth warpgroup (4-bit caches: warp 14 looks for NaN
+//               V blocks that the staging pass reported).
 // Shared memory: Q 2 x 48 KB, K 2 x 48 KB (double-buffered), V 32 KB.
 // TMEM (512 columns): S of Q tile t at columns [128t, 128t + 128), O of Q
 // tile t at [256 + 128t, 384 + 128t); P (16-bit pairs) overwrites the last 64
@@ -43,6 +44,7 @@
 #include <cstdint>
 
 #include "e2m1.cuh"
+#include "fp4_nan.cuh"
 #include "kernels.hpp"
 #include "tc_common.cuh"
 
@@ -166,8 +168,8 @@ __device__ __forceinline__ int q_row_shift(const uint4 *row) {
 // caches themselves (plans without a scratch: replayable plans, runs without
 // a workspace).
 // F16: the caches hold 8- or 4-bit values, so the operands are fp16.  E2M1: they
-// are 4-bit rows (a staging scratch holds fp16 rows either way, so only the
-// path that reads the caches itself tells the two apart).
+// are 4-bit rows (a staging scratch holds fp16 rows either way: there only what
+// NaN V blocks do to the rows tells the two apart, see fp4_nan.cuh).
 template <bool F16, bool E2M1, bool STAGED>
 __global__ void __launch_bounds__(kPThreads, 1)
     attn_prefill_kernel(const RunArgs args, const __grid_constant__ TmaMaps stage) {
@@ -177,6 +179,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
   __shared__ PBars bars;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
+  // E2M1: nonzero if there may be NaN V blocks to see to at a segment's end
+  // (fp4_nan.cuh).  Without the scratch the load warps report those of the cut tiles
+  // they meet.  The staging pass took all of them as zeros; warp 14 looks through the
+  // bytes that it left per tile and says zero if there are none.
+  __shared__ int v_nan;
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -197,6 +204,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
 
   if (tid == 0) {
     abort_flag = 0;
+    v_nan = E2M1 && STAGED;
     // a K or V stage is filled by the four load warps, or by one TMA issue
     constexpr uint32_t kFill = STAGED ? 1 : kLoadWarps;
     for (int i = 0; i < 2; ++i) {
@@ -244,6 +252,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     // needs (loaded from the plan when the stream enters a segment).
     struct KPos {
       int seg, tile, tile_end, b, g, klo, khi;
+      SharedKeys all;               // E2M1 only
     };
     auto kpos_load = [&](KPos &p, int seg) {
       const SegDesc sd = a.segs[seg];
@@ -255,6 +264,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       p.g = bd.g;
       p.klo = bd.klo;
       p.khi = bd.khi;
+      if (E2M1) p.all = SharedKeys(a, bd);
     };
     auto kpos_next = [&](KPos &p) {
       if (++p.tile == p.tile_end && p.seg + 1 < seg_end) kpos_load(p, p.seg + 1);
@@ -460,9 +470,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
       kpos_load(kp, seg_begin);
       int64_t slot[3];
       int info[3];
+      bool cut[3] = {false, false, false};      // E2M1: some row does not see all of the tile
       auto pack = [](int seg, bool first, int g) { return (seg << 17) | ((int)first << 16) | g; };
       slot[0] = lookup(kp);
       info[0] = pack(kp.seg, true, kp.g);
+      if (E2M1) cut[0] = kp.all.cut(kp.tile * kPN, kPN);
       for (int i = 1; i < 3; ++i) {
         slot[i] = -1;
         info[i] = 0;
@@ -471,6 +483,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           kpos_next(kp);
           slot[i] = lookup(kp);
           info[i] = pack(kp.seg, kp.seg != prev_seg, kp.g);
+          if (E2M1) cut[i] = kp.all.cut(kp.tile * kPN, kPN);
         }
       }
       auto shift = [&](int k) {    // tile k+1 becomes [0]; look up tile k+3 into [2]
@@ -478,12 +491,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
         info[0] = info[1];
         slot[1] = slot[2];
         info[1] = info[2];
+        cut[0] = cut[1];
+        cut[1] = cut[2];
         slot[2] = -1;
         if (k + 3 < total) {
           const int prev_seg = kp.seg;
           kpos_next(kp);
           slot[2] = lookup(kp);
           info[2] = pack(kp.seg, kp.seg != prev_seg, kp.g);
+          if (E2M1) cut[2] = kp.all.cut(kp.tile * kPN, kPN);
         }
       };
       auto head_of = [](int in) { return in & 0xFFFF; };
@@ -492,6 +508,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       if constexpr (F16) {
         // raw rows in registers: K of tile k, V of tile k-1 (20 x 16 bytes of E4M3)
         uint4 kr[KCH], vr[VCH];
+        bool v_cut = false;
         int64_t v_slot = -1;
         int v_g = 0;
         load(kr, KCH, row_ptr(kc, slot[0], head_of(info[0]), KCH), slot[0]);
@@ -507,6 +524,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
           if (k >= 1) {
             if (k >= 2 && !tc::mbar_wait_warp(&bars.v_empty, (k - 2) & 1, &abort_flag)) break;
+            if (E2M1 && v_cut) {
+              const uint32_t n0 = e4m3_nan_bytes(vr[VCH - 1].x), n1 = e4m3_nan_bytes(vr[VCH - 1].y);
+              if (n0 | n1) *static_cast<volatile int *>(&v_nan) = 1;
+              vr[VCH - 1].x &= ~n0;
+              vr[VCH - 1].y &= ~n1;
+            }
             put_row(sbase + kOffV, vr, VCH);
             tc::fence_proxy_async_smem();
             tc::mbar_arrive_warp(&bars.v_full);
@@ -515,6 +538,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
             v_slot = slot[0];
             v_g = head_of(info[0]);
             load(vr, VCH, row_ptr(vc, v_slot, v_g, VCH), v_slot);
+            v_cut = cut[0];
             shift(k);
           }
         }
@@ -563,7 +587,18 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
   } else if (warp >= kMmaWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n" ::: "memory");
-    if (warp > kMmaWarp + 1) goto done;   // warps 14-15: idle
+    if (warp > kMmaWarp + 1) {            // warp 14: see v_nan; warp 15: idle
+      if (E2M1 && STAGED && warp == kMmaWarp + 2) {
+        uint32_t any = 0u;
+        for (int sg = seg_begin; sg < seg_end; ++sg) {
+          const SegDesc sd = a.segs[sg];
+          const uint8_t *nan = a.stage_nan + a.blocks[sd.block].srow / kPN;
+          for (int x = sd.tile_begin + (tid & 31); x < sd.tile_end; x += 32) any |= __ldcg(nan + x);
+        }
+        if (!__any_sync(0xffffffffu, any != 0u) && (tid & 31) == 0) *static_cast<volatile int *>(&v_nan) = 0;
+      }
+      goto done;
+    }
     // ------------------------------------------------------------ MMA issuers
     // One thread per Q tile (warp 12: Q tile 0, warp 13: Q tile 1), so that the
     // two tiles' chains S_t -> softmax_t -> P_t.V -> next S_t never wait on
@@ -886,6 +921,23 @@ __global__ void __launch_bounds__(kPThreads, 1)
           a.part_lse[prow] = lse;
         }
       }
+      if constexpr (E2M1) {
+        // NaN V blocks, into what has been written of the row.  (This form is one of
+        // several that do the same; others, in registers or at the kernel's end, made
+        // the whole kernel 1 to 3% slower.)
+        if (valid && *static_cast<volatile int *>(&v_nan)) {
+          const BlockDesc bd = a.blocks[sd.block];
+          uint32_t dims;
+          if (STAGED)
+            dims = staged_nan_blocks(a, bd, sd.tile_begin, sd.tile_end, row_lo, row_hi);
+          else
+            dims = cut_nan_blocks(a, bd, max(row_lo, sd.tile_begin * kPN), min(row_hi, sd.tile_end * kPN), kPN);
+          if (single)
+            store_nan_blocks(dims, static_cast<uint16_t *>(a.out) + ((int64_t)row_tok * a.hq + row_h) * kDv, nullptr);
+          else
+            store_nan_blocks(dims, nullptr, a.part_o + (int64_t)prow * kDv);
+        }
+      }
       tc::tc_fence_before();
       tc::mbar_arrive_warp(&bars.o_free[t]);
     }
@@ -908,6 +960,8 @@ cudaError_t launch_attn_prefill(const HostPlan &hp, const RunArgs &a, const TmaM
   const dim3 grid(hp.num_ctas), block(kPThreads);
   const TmaMaps none{};
   const bool f16 = hp.prob.kv_dtype != ATTN_KV_BF16;
+  if (stage && hp.prob.kv_dtype == ATTN_KV_FP4_E2M1)
+    return launch_dependent(attn_prefill_kernel<true, true, true>, grid, block, kSmem, stream, a, *stage);
   if (stage)
     return f16 ? launch_dependent(attn_prefill_kernel<true, false, true>, grid, block, kSmem, stream, a,
                                   *stage)
@@ -923,9 +977,10 @@ cudaError_t launch_attn_prefill(const HostPlan &hp, const RunArgs &a, const TmaM
 
 cudaError_t prepare_attn_prefill(const HostPlan &hp) {
   const bool f16 = hp.prob.kv_dtype != ATTN_KV_BF16;
-  cudaError_t e = cudaFuncSetAttribute(
-      f16 ? attn_prefill_kernel<true, false, true> : attn_prefill_kernel<false, false, true>,
-      cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t e = cudaFuncSetAttribute(hp.prob.kv_dtype == ATTN_KV_FP4_E2M1 ? attn_prefill_kernel<true, true, true>
+                                       : f16                                ? attn_prefill_kernel<true, false, true>
+                                                                            : attn_prefill_kernel<false, false, true>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(hp.prob.kv_dtype == ATTN_KV_FP4_E2M1 ? attn_prefill_kernel<true, true, false>
                              : f16                                ? attn_prefill_kernel<true, false, false>

@@ -53,6 +53,7 @@
 #include "attn_paged_debug.h"
 #include "e2m1.cuh"
 #include "e4m3.cuh"
+#include "fp4_nan.cuh"
 #include "kernels.hpp"
 #include "stamps.cuh"
 #include "tc_common.cuh"
@@ -267,6 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Bars bars;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
+  __shared__ int v_nan;           // a NaN V block of a tile cut by some row's range (fp4_nan.cuh)
   __shared__ float sm_m[128], sm_l[128];
   __shared__ int8_t sm_shift[F16 ? 4 : 1][F16 ? MR : 1];     // Q row shifts, per segment
 
@@ -327,6 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     abort_flag = 0;
+    v_nan = 0;
     for (int s = 0; s < 4; ++s) {
       tc::mbar_init(&bars.tma_full[s], 1);
       tc::mbar_init(&bars.tma_empty[s], 128);
@@ -670,9 +673,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kKrow = kv_row_bytes(kE2m1, kDqk), kVrow = kv_row_bytes(kE2m1, kDv);
       constexpr int kPerK = kDqk / 64, kPerV = kDv / 64;    // code chunks of a thread
       const int kk = ct & 63, ch0 = ct >> 6;
-      auto widen = [&](uint8_t *dst, int ch, bool keep, uint4 raw, uint32_t scales) {
+      // (keys outside the block's range may hold anything: their scores are masked, so
+      // only their values are taken as zeros)
+      auto widen = [&](uint8_t *dst, int ch, uint4 raw, uint32_t scales) {
         uint4 w[4];
-        if (!keep) scales = 0u;       // keys outside the block's range: finite codes times zero
         e2m1x32_to_f16(raw, scales, w);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -685,19 +689,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (cur.first() && !stage_q(cur)) break;
         const int s = k % NS;
         const int j = cur.tile * kN + kk;
-        const bool keep = j >= bd.klo && j < bd.khi;
+        // V scales of a tile that some row sees only in part: keys outside the block's
+        // range to zero, and NaN ones, which are reported
+        const bool cut = SharedKeys(a, bd).cut(cur.tile * kN, kN);
+        auto clean = [&](uint32_t scales) -> uint32_t {
+          if (j < bd.klo || j >= bd.khi) return 0u;
+          const uint32_t nan = e4m3_nan_bytes(scales) & 0xFFFFu;
+          if (nan) *static_cast<volatile int *>(&v_nan) = 1;
+          return scales & ~nan;
+        };
         if constexpr (TMA) {
           const int t = k % NT;
           if (!tc::mbar_wait_warp(&bars.tma_full[t], (k / NT) & 1, &abort_flag)) break;
           const uint8_t *krow = smem + Lay::kOffRaw + t * kRawBytes + kk * kKrow;
-          const uint8_t *vrow = smem + Lay::kOffRaw + t * kRawBytes + kRawK + kk * kVrow;
+          uint8_t *vrow = smem + Lay::kOffRaw + t * kRawBytes + kRawK + kk * kVrow;
           uint8_t *dst = smem + Lay::kOffOp + s * kOpBytes;
+          // in the raw stage, ahead of the waits (in the loop below it costs 0.7 us of a
+          // verify step's 51)
+          if (cut)
+            for (int ch = ch0; ch < kDv / 32; ch += 2) {
+              uint16_t *scales = reinterpret_cast<uint16_t *>(vrow + kDv / 2 + ch * 2);
+              *scales = (uint16_t)clean(*scales);
+            }
           // rolled: a chunk's ~60 instructions stay in the instruction cache that
           // three warp roles share
           if (k >= NS && !tc::mbar_wait_warp(&bars.k_empty[s], ((k / NS) - 1) & 1, &abort_flag)) break;
 #pragma unroll 1
           for (int ch = ch0; ch < kDqk / 32; ch += 2)
-            widen(dst, ch, keep, *reinterpret_cast<const uint4 *>(krow + ch * 16),
+            widen(dst, ch, *reinterpret_cast<const uint4 *>(krow + ch * 16),
                   *reinterpret_cast<const uint16_t *>(krow + kDqk / 2 + ch * 2));
           tc::fence_proxy_async_smem();
           tc::mbar_arrive(&bars.op_full[s]);
@@ -705,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           dst += kOpK;
 #pragma unroll 1
           for (int ch = ch0; ch < kDv / 32; ch += 2)
-            widen(dst, ch, keep, *reinterpret_cast<const uint4 *>(vrow + ch * 16),
+            widen(dst, ch, *reinterpret_cast<const uint4 *>(vrow + ch * 16),
                   *reinterpret_cast<const uint16_t *>(vrow + kDv / 2 + ch * 2));
           tc::fence_proxy_async_smem();
           tc::mbar_arrive(&bars.v_full[s]);
@@ -735,9 +754,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t *dst = smem + Lay::kOffOp + s * kOpBytes;
           if (k >= NS && !tc::mbar_wait_warp(&bars.op_empty[s], ((k / NS) - 1) & 1, &abort_flag)) break;
 #pragma unroll
-          for (int u = 0; u < kPerK; ++u) widen(dst, ch0 + 2 * u, keep, bk[u], sk[u]);
+          for (int u = 0; u < kPerK; ++u) widen(dst, ch0 + 2 * u, bk[u], sk[u]);
 #pragma unroll
-          for (int u = 0; u < kPerV; ++u) widen(dst + kOpK, ch0 + 2 * u, keep, bv[u], sv[u]);
+          for (int u = 0; u < kPerV; ++u) widen(dst + kOpK, ch0 + 2 * u, bv[u], cut ? clean(sv[u]) : sv[u]);
           tc::fence_proxy_async_smem();
           tc::mbar_arrive(&bars.op_full[s]);
         }
@@ -1359,6 +1378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, kTmemCols);
   }
+  if (F16 && v_nan) patch_nan_rows(a, kN, kN);
 }
 
 template <int KV, bool TMA, int MR, int DQK, bool HALF>

@@ -39,6 +39,7 @@ struct RunArgs {
   const MergeItem *merge_items;
   int32_t hq, hkv, group, page_size, pt_stride, num_pages, window;
   int32_t *err;
+  const uint8_t *stage_nan;  // NaN V blocks of each staged tile (4-bit prefill plans)
   int32_t replayed;      // the work list is rewritten by the device planner at every run
 };
 
@@ -74,6 +75,7 @@ struct StageArgs {
   const void *k_cache, *v_cache;
   const int32_t *page_table;
   uint16_t *k_stage, *v_stage;
+  uint8_t *tile_nan;         // 4-bit caches: [tiles], the NaN V blocks of each
   int32_t *err;
   int64_t tiles;             // all units' tiles
   int32_t num_units, dqk, hkv, page_size, pt_stride, num_pages;

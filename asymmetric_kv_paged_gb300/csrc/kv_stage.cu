@@ -11,7 +11,8 @@
 // do"): BF16 rows are copied bit for bit, E4M3 codes are widened exactly to
 // fp16 (every E4M3 value is an fp16 value; the scale stays outside, as in the
 // attention kernels), E2M1 codes with their block scales likewise
-// (e2m1.cuh).  Keys outside [klo, khi) are written as zeros: the
+// (e2m1.cuh), except that a V block with a NaN scale is written as zeros and
+// reported in a byte per tile (fp4_nan.cuh).  Keys outside [klo, khi) are written as zeros: the
 // kernel masks them, and zeros keep P.V free of whatever the pool holds
 // there.  A page id outside the pool is read as zeros and reported in bit 1
 // of the plan's error word, as the attention kernels do.
@@ -26,6 +27,7 @@
 #include <cstdint>
 
 #include "e2m1.cuh"
+#include "fp4_nan.cuh"
 #include "kernels.hpp"
 
 namespace akp {
@@ -43,6 +45,7 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const StageArgs a)
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   __shared__ int64_t s_slot[kStageTile];
   __shared__ StageUnit s_unit;
+  __shared__ uint32_t s_nan;          // E2M1: the tile's NaN V blocks, a bit per 16 dims
   // 16-byte chunks of a source row: E2M1 rows hold 32 codes per chunk (their
   // scales, in the chunk behind the last, come with each), E4M3 16, BF16 8 values
   constexpr int kCodes = KV == ATTN_KV_FP4_E2M1 ? 32 : KV == ATTN_KV_FP8_E4M3 ? 16 : 8;
@@ -59,6 +62,7 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const StageArgs a)
         if (a.units[mid].tile_off <= t) lo = mid; else hi = mid - 1;
       }
       s_unit = a.units[lo];
+      s_nan = 0u;
     }
     __syncthreads();
     const StageUnit u = s_unit;
@@ -92,6 +96,9 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const StageArgs a)
       if (KV == ATTN_KV_FP4_E2M1) {
         uint32_t scales = 0u;
         if (slot >= 0) scales = __ldg(reinterpret_cast<const uint16_t *>(src + d / 2) + cc);
+        const uint32_t nan = is_k ? 0u : e4m3_nan_bytes(scales) & 0xFFFFu;
+        if (nan) atomicOr(&s_nan, ((nan & 1u) | (nan >> 7 & 2u)) << (2 * cc));
+        scales &= ~nan;
         uint4 w[4];
         e2m1x32_to_f16(raw, scales, w);
 #pragma unroll
@@ -106,6 +113,7 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(const StageArgs a)
       }
     }
     __syncthreads();   // s_slot and s_unit are rewritten for the next tile
+    if (KV == ATTN_KV_FP4_E2M1 && threadIdx.x == 0) a.tile_nan[t] = (uint8_t)s_nan;
   }
 }
 

@@ -205,7 +205,10 @@ attn_status_t attn_plan_replayable(const attn_problem_t *bounds, int device, att
  * (0x7F, 0xFF) in a visible slot read as +-480 on the decode/verify plans and stay
  * NaN on the prefill plans; a NaN block scale of a 4-bit cache is NaN on every
  * plan: in a K row the key's score is NaN, and with it every row that sees the
- * key; in a V row the block's 16 output dims are.
+ * key; in a V row the block's 16 output dims of every row that sees the key, and
+ * nothing else.  (A NaN or infinity in a V row of a BF16 cache, and a NaN of an
+ * E4M3 cache on prefill plans, also makes those dims NaN for rows that do not see
+ * the key when one of their key tiles holds it.)
  * Prefill plans that are not replayable first gather the keys their blocks
  * read into a staging scratch in the workspace (16-bit rows: E4M3 and
  * E2M1 widened exactly to fp16, BF16 copied; (Dqk + 128) * 2 bytes per key of each KV
