@@ -149,10 +149,11 @@ def _stream(stream, plan) -> int:
 class Plan:
     """Owns an attn_plan_t handle (destroyed with the object)."""
 
-    def __init__(self, handle: int, workspace_bytes: int, device: int, keep):
+    def __init__(self, handle: int, workspace_bytes: int, device: int, keep, total_q: int):
         self.handle = handle
         self.workspace_bytes = workspace_bytes
         self.device = device
+        self.total_q = total_q          # new tokens of the whole batch
         self._keep = keep
 
     def destroy(self) -> None:
@@ -181,19 +182,24 @@ def make_problem(batch, num_q_heads, num_kv_heads, page_size, num_pages, page_ta
     return p, (qo, sl)
 
 
+def _total_q(problem: attn_problem_t) -> int:
+    """Read once the library has accepted the problem."""
+    return problem.qo_indptr_host[problem.batch] if problem.batch > 0 else 0
+
+
 def attn_plan(problem: attn_problem_t, device: int, keep=None) -> Plan:
     h = ctypes.c_void_p()
     ws = ctypes.c_size_t()
     _check(load().attn_plan(ctypes.byref(problem), int(device), ctypes.byref(h), ctypes.byref(ws)),
            "attn_plan")
-    return Plan(h.value, ws.value, device, keep)
+    return Plan(h.value, ws.value, device, keep, _total_q(problem))
 
 
 def attn_plan_host(problem: attn_problem_t, num_sms: int, keep=None) -> Plan:
     h = ctypes.c_void_p()
     _check(load().attn_plan_host(ctypes.byref(problem), int(num_sms), ctypes.byref(h)),
            "attn_plan_host")
-    return Plan(h.value, 0, -1, keep)
+    return Plan(h.value, 0, -1, keep, _total_q(problem))
 
 
 def attn_plan_replayable(bounds: attn_problem_t, device: int, keep=None) -> Plan:
@@ -203,14 +209,14 @@ def attn_plan_replayable(bounds: attn_problem_t, device: int, keep=None) -> Plan
     ws = ctypes.c_size_t()
     _check(load().attn_plan_replayable(ctypes.byref(bounds), int(device), ctypes.byref(h),
                                        ctypes.byref(ws)), "attn_plan_replayable")
-    return Plan(h.value, ws.value, device, keep)
+    return Plan(h.value, ws.value, device, keep, _total_q(bounds))
 
 
 def attn_plan_replayable_host(bounds: attn_problem_t, num_sms: int, keep=None) -> Plan:
     h = ctypes.c_void_p()
     _check(load().attn_plan_replayable_host(ctypes.byref(bounds), int(num_sms), ctypes.byref(h)),
            "attn_plan_replayable_host")
-    return Plan(h.value, 0, -1, keep)
+    return Plan(h.value, 0, -1, keep, _total_q(bounds))
 
 
 def attn_plan_replan_host(plan: Plan, seq_lens) -> int:
@@ -318,7 +324,11 @@ def attn_append_kv_rope(plan: Plan, rope: attn_rope_t, q, k_new, v_new, q_out, k
                         page_table, seq_lens, qo_indptr, k_scale: float = 1.0, v_scale: float = 1.0,
                         stream=None) -> None:
     """attn_append_kv with the keys rotated on the way, and the queries into q_out
-    (may be q; both None: no queries)."""
+    (may be q; both None: no queries).  The rope's positions, where given, are
+    one per new token of the plan, or more."""
+    positions = rope.keep[1] if hasattr(rope, "keep") else None
+    if positions is not None and positions.numel() < plan.total_q:
+        raise ValueError(f"positions has {positions.numel()} entries for the plan's {plan.total_q} tokens")
     st = (_LIB or load()).attn_append_kv_rope(
         plan.handle, rope, _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(q_out), _ptr(k_cache), _ptr(v_cache),
         _ptr(page_table), _ptr(seq_lens), _ptr(qo_indptr), float(k_scale), float(v_scale), _stream(stream, plan))
@@ -330,6 +340,8 @@ def attn_read_kv(plan: Plan, k_cache, v_cache, page_table, seq_lens, kv_indptr, 
                  k_scale: float = 1.0, v_scale: float = 1.0, stream=None) -> None:
     """Cached rows as bf16: the last kv_indptr[b + 1] - kv_indptr[b] positions of every
     request b, into k_out [rows, Hkv, Dqk] and v_out [rows, Hkv, 128]."""
+    if k_out.shape[0] != v_out.shape[0]:
+        raise ValueError(f"k_out has {k_out.shape[0]} rows and v_out {v_out.shape[0]}")
     st = (_LIB or load()).attn_read_kv(
         plan.handle, _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens), _ptr(kv_indptr),
         k_out.shape[0], _ptr(k_out), _ptr(v_out), float(k_scale), float(v_scale), _stream(stream, plan))
