@@ -750,9 +750,11 @@ attn_status_t append_rows(attn_plan_t plan, const attn_rope_t *rope, const void 
   DeviceGuard dev(plan->device);
   if (!dev.ok) return ATTN_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = !rope               ? launch_append_kv<kNoRope>(a, pr.kv_dtype, pr.head_dim_qk, dim3(sp.ctas), st)
-                        : rope->interleaved ? launch_append_kv<kPairs>(a, pr.kv_dtype, pr.head_dim_qk, dim3(sp.ctas), st)
-                                            : launch_append_kv<kHalves>(a, pr.kv_dtype, pr.head_dim_qk, dim3(sp.ctas), st);
+  const dim3 grid(sp.ctas);
+  // (without a rotation only 4-bit caches come here: kv_append.cu)
+  const cudaError_t e = !rope               ? launch_append<ATTN_KV_FP4_E2M1, kNoRope>(a, pr.head_dim_qk, grid, st)
+                        : rope->interleaved ? launch_append_kv<kPairs>(a, pr.kv_dtype, pr.head_dim_qk, grid, st)
+                                            : launch_append_kv<kHalves>(a, pr.kv_dtype, pr.head_dim_qk, grid, st);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
