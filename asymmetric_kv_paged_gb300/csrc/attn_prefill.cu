@@ -174,6 +174,8 @@ template <bool F16, bool E2M1, bool STAGED>
 __global__ void __launch_bounds__(kPThreads, 1)
     attn_prefill_kernel(const RunArgs args, const __grid_constant__ TmaMaps stage) {
   const RunArgs a = args;
+  // P of 4-bit caches is held times 2^kLift (attn_fp4.cu says why)
+  constexpr float kLift = E2M1 ? 7.f : 0.f, kUnlift = E2M1 ? 0.0078125f : 1.f;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *smem = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
   __shared__ PBars bars;
@@ -786,7 +788,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       // is taken, so their exponents need not wait for a maximum pass.  Only
       // when the tile's maximum exceeds m_base by more than the threshold
       // (rare once the maximum has settled) is O rescaled and the pass redone
-      // from S, which is still in TMEM.  Until then P may exceed 1 (up to 2^8).
+      // from S, which is still in TMEM.  Until then P may exceed 2^kLift (by 2^8 at most).
       float m_base = m_run != -INFINITY ? m_run : m_lo;
       float rs[2] = {0.f, 0.f};
       float mh[2] = {-INFINITY, -INFINITY};
@@ -803,8 +805,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
           pk[j >> 1] = F16 ? f16_pair(p0, p1) : bf16_pair(p0, p1);
         }
       };
-      exp_pack(s2, pk2, m_base == -INFINITY ? 0.f : -m_base, true);
-      exp_pack(s3, pk3, m_base == -INFINITY ? 0.f : -m_base, true);
+      exp_pack(s2, pk2, m_base == -INFINITY ? 0.f : kLift - m_base, true);
+      exp_pack(s3, pk3, m_base == -INFINITY ? 0.f : kLift - m_base, true);
       const float m_tile = fmaxf(m_lo, fmaxf(mh[0], mh[1]) * sc);
       const bool need = m_tile > m_base + kRescaleThreshold;   // never for m_tile = -inf
       if (__any_sync(0xffffffffu, need)) {
@@ -836,8 +838,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
           mask32(s3, 96);
         }
         rs[0] = rs[1] = 0.f;
-        exp_pack(s2, pk2, m_base == -INFINITY ? 0.f : -m_base, false);
-        exp_pack(s3, pk3, m_base == -INFINITY ? 0.f : -m_base, false);
+        exp_pack(s2, pk2, m_base == -INFINITY ? 0.f : kLift - m_base, false);
+        exp_pack(s3, pk3, m_base == -INFINITY ? 0.f : kLift - m_base, false);
       }
       m_run = m_base;
       // P_t: key j's 16-bit value in the low (even j) or high half of TMEM
@@ -848,7 +850,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       tc::tmem_wait_st();
       tc::tc_fence_before();
       tc::mbar_arrive_warp(&bars.p_hi[t]);
-      const float neg_m = m_run == -INFINITY ? 0.f : -m_run;
+      const float neg_m = m_run == -INFINITY ? 0.f : kLift - m_run;
       auto exp32 = [&](const uint32_t (&raw)[32], int c0) {
 #pragma unroll
         for (int h = 0; h < 32; h += 16) {
@@ -876,6 +878,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       // ---------------- end of segment: normalise and write the rows
       if (!wait(&bars.pv_done[t], cdone & 1)) break;
       tc::tc_fence_after();
+      l_run *= kUnlift;
       // a row that saw nothing but NaN scores has no maximum: its NaN sum stays
       if (l_run != l_run && m_run == -INFINITY) m_run = 0.f;
       float scale_o = 0.f, lse = -INFINITY;
@@ -883,11 +886,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
         const float MM = fmaxf(m_run, sink2);
         if (MM != -INFINITY) {
           const float Z = l_run * exp2f(m_run - MM) + exp2f(sink2 - MM);
-          scale_o = exp2f(m_run - MM) * a.v_scale / Z;
+          scale_o = exp2f(m_run - MM) * a.v_scale / Z * kUnlift;
           lse = (MM + log2f(Z)) * kLn2;
         }
       } else if (l_run != 0.f) {
-        scale_o = a.v_scale / l_run;
+        scale_o = a.v_scale / l_run * kUnlift;
         lse = m_run + log2f(l_run);
       }
 #pragma unroll 1

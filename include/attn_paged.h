@@ -201,7 +201,10 @@ attn_status_t attn_plan_replayable(const attn_problem_t *bounds, int device, att
  * multiplied by the power of two that puts its largest |q| in [2^14, 2^15)
  * (exact; every element down to 2^-31 of that maximum stays exact in fp16), the
  * cache is widened exactly to fp16, and the scores are divided by the same power
- * of two in fp32; P.V is fp16 x fp16 with fp32 accumulation.  The E4M3 NaN codes
+ * of two in fp32; P.V is fp16 x fp16 with fp32 accumulation.  P is held relative to
+ * the running maximum, on 4-bit plans times 2^7: weights down to 2^-21 of the
+ * maximum keep fp16's 11 bits and none above 2^-32 is lost (FP8 prefill plans:
+ * 2^-14 and 2^-25).  The E4M3 NaN codes
  * (0x7F, 0xFF) in a visible slot read as +-480 on the decode/verify plans and stay
  * NaN on the prefill plans; a NaN block scale of a 4-bit cache is NaN on every
  * plan: in a K row the key's score is NaN, and with it every row that sees the

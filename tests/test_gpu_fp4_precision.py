@@ -52,10 +52,10 @@ def build(shape, fraction, light, heavy):
     return w
 
 
-def run(w):
+def run(w, **kw):
     from asymmetric_kv_paged_gb300 import binding as B
     from asymmetric_kv_paged_gb300.runner import DeviceWorkload
-    dw = DeviceWorkload(w)
+    dw = DeviceWorkload(w, **kw)
     dw.run()
     torch.cuda.synchronize()
     assert B.attn_get_device_error(dw.plan) == 0
@@ -93,14 +93,18 @@ def test_weights_that_cancel(shape):
         assert abs(off - want) > (2.0 ** -11 + 2.0 ** -13) * mag + 2.0 ** -8 * abs(want)
 
 
-@pytest.mark.parametrize("shape", [s for s in SHAPES if s[0] != "rows256"], ids=lambda s: s[0])
-def test_small_weights(shape):
+@pytest.mark.parametrize("shape", SHAPES, ids=[s[0] for s in SHAPES])
+def test_small_weights(shape, **kw):
     """Light weights of 2^-20 (1 + 2^-5.1), heavy values of zero: the result is the
     light keys' alone.  Without the factor of 2^7 that the weights are held with, fp16
     would have steps of 2^-24 there, and the nearest one is 2^-5.1 off."""
     fraction = 2.0 ** -20 * (1 + 2.0 ** -5.1)
     w = build(shape, fraction, (0x66, 0x38), (0x00, 0x38))
-    got, ref, a = run(w)
+    got, ref, a = run(w, **kw)
     bound = 2.0 ** -11 + 2.0 ** -13 + 2.0 ** -8              # the result is A
     assert np.all(np.abs(got - ref) <= bound * a)
     assert abs(float(np.float16(fraction)) / fraction - 1) > bound
+
+
+def test_small_weights_on_a_replayable_plan():
+    test_small_weights(SHAPES[-1], replayable=True)
