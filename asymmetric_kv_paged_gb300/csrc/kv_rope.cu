@@ -656,15 +656,17 @@ __global__ void __launch_bounds__(kAppendThreads, 4) read_kernel(const ReadArgs 
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// Splits `rows` of `steps` row steps each among the warps that all SMs hold:
-// ranges of rows, and the warps that share a range's steps.
+// Splits `rows` of `heads` rows of one kind each among the warps that all SMs hold
+// (four CTAs an SM): ranges of rows, and the warps that share a range's heads.  (A
+// step of 128-value rows takes two heads, so that with few rows some of the warps
+// have nothing to take.)
 struct Split {
   int32_t chunks, slices;
   unsigned ctas;
-  Split(int64_t rows, int64_t steps) {
-    constexpr int64_t kWarps = 152 * 4 * (kAppendThreads / 32);
-    slices = (int32_t)std::max<int64_t>(1, std::min(steps, kWarps / std::max<int64_t>(rows, 1)));
-    chunks = (int32_t)std::min<int64_t>(rows, std::max<int64_t>(1, kWarps / slices));
+  Split(int64_t rows, int64_t heads, int num_sms) {
+    const int64_t warps = (int64_t)num_sms * 4 * (kAppendThreads / 32);
+    slices = (int32_t)std::max<int64_t>(1, std::min(heads, warps / std::max<int64_t>(rows, 1)));
+    chunks = (int32_t)std::min<int64_t>(rows, std::max<int64_t>(1, warps / slices));
     ctas = (unsigned)(((int64_t)chunks * slices + kAppendThreads / 32 - 1) / (kAppendThreads / 32));
   }
 };
@@ -731,7 +733,7 @@ attn_status_t append_rows(attn_plan_t plan, const attn_rope_t *rope, const void 
   a.num_pages = pr.num_pages;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
-  int64_t steps = pr.num_kv_heads;          // row steps that can run side by side
+  int64_t heads = pr.num_kv_heads;
   if (rope) {
     a.cos_sin = rope->cos_sin;
     a.positions = rope->positions;
@@ -741,10 +743,10 @@ attn_status_t append_rows(attn_plan_t plan, const attn_rope_t *rope, const void 
     if (q) {
       a.q = static_cast<const uint16_t *>(q);
       a.q_out = static_cast<uint16_t *>(q_out);
-      steps = std::max<int64_t>(steps, pr.num_q_heads);
+      heads = std::max<int64_t>(heads, pr.num_q_heads);
     }
   }
-  const Split sp(total_q, steps);
+  const Split sp(total_q, heads, hp.num_sms);
   a.chunks = sp.chunks;
   a.slices = sp.slices;
   DeviceGuard dev(plan->device);
@@ -799,7 +801,7 @@ extern "C" attn_status_t attn_read_kv(attn_plan_t plan, const void *k_cache, con
   a.num_pages = pr.num_pages;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
-  const akp::Split sp(rows, pr.num_kv_heads);
+  const akp::Split sp(rows, pr.num_kv_heads, plan->host.num_sms);
   a.chunks = sp.chunks;
   a.slices = sp.slices;
   akp::DeviceGuard dev(plan->device);
