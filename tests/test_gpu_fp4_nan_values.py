@@ -141,3 +141,24 @@ def test_nan_value_block_without_a_workspace(shape):
     poison(w, evs)
     dw.v_cache.copy_(torch.from_numpy(w.v_cache))
     compare(w, evs, hq, *run(), ref, ref_lse)
+
+
+@pytest.mark.parametrize("value", [0x7FC0, 0x7F80, 0xFF80], ids=["nan", "inf", "-inf"])
+@pytest.mark.parametrize("shape", SHAPES, ids=[s[0] for s in SHAPES])
+def test_a_query_that_is_not_finite_stays_in_its_row(shape, value):
+    from asymmetric_kv_paged_gb300.runner import DeviceWorkload
+    name, seq, n, hq, P, dqk = shape
+    w = W.make_workload(34, seq, n, hq=hq, hkv=2, page_size=P, kv_dtype="fp4", name=name, dqk=dqk)
+    clean = DeviceWorkload(w)
+    clean.run()
+    ref, ref_lse = outputs(clean)
+    hit = np.zeros((w.total_q, hq), bool)
+    for t, h, d in ((0, 1, 5), (w.total_q - 1, hq - 1, dqk - 1), (w.total_q // 2, 0, 64)):
+        w.q[t, h, d] = value
+        hit[t, h] = True
+    dw = DeviceWorkload(w)
+    dw.run()
+    got, lse = outputs(dw)
+    if value == 0x7FC0:
+        assert np.all(np.isnan(got[hit])) and np.all(np.isnan(lse[hit]))
+    assert np.array_equal(got[~hit], ref[~hit]) and np.array_equal(lse[~hit], ref_lse[~hit])
