@@ -1,5 +1,6 @@
 // Split-KV attention over a 4-bit cache for row blocks of at most 32 query rows
-// (decode, and a few draft tokens on small groups).
+// (decode, and a few draft tokens on small groups; of 17 to 32 rows where the batch
+// has three key tiles an SM or more, see planner.cpp).
 //
 // At these sizes a key's 192 bytes feed few rows, and what bounds the tcgen05 kernel
 // (attn_tc.cu) is not the tensor pipe but getting there: its operands have to be
@@ -43,7 +44,7 @@
 // Measured (16 query heads on 2 KV heads unless said, merge included): a ragged
 // decode batch of 32 requests, 195 MB of rows, 50 us (3.9 TB/s, 0.58 of the copy rate;
 // fetching alone, without any arithmetic, takes 42.7 us, so what is left is the
-// fetch and the warps' issue slots, 70% busy); four requests of 46K keys 23 us with
+// fetch and the warps' issue slots, 58% busy); four requests of 46K keys 23 us with
 // 8 rows and 43 with 32 (there it is the latency of one warp's chain: 2 warps a
 // scheduler, 0.36 instructions a cycle); pages of one token, 16 rows, 109 MB, 54 us
 // (16-byte copies).  12 warps for 8 rows, 8 beyond: what the registers allow; 16 of

@@ -34,9 +34,10 @@
 // A CTA starts from its head record (segment range, tile count, first segment
 // and block) and is launched as a programmatic dependent (griddepcontrol).
 // TMEM: S double buffer (2 x 64 columns), O (128 columns), P double buffer (2 x 32).
-// 4-bit caches come here with 33 to 128 rows a block (fewer run attn_fp4.cu): 64
-// rows over four requests of 46K keys, 67 MB of rows, take 51 us, about 1 us a
-// 64-key tile and CTA on top of ~14 us of launch, start and merge.  Left out one by
+// 4-bit caches come here with 33 to 128 rows a block, and with 17 to 32 where the
+// batch has fewer than three key tiles an SM (the others run attn_fp4.cu): 64 rows
+// over four requests of 46K keys, 67 MB of rows, take 52 us, about 1 us a 64-key
+// tile and CTA on top of ~14 us of launch, start and merge.  Left out one by
 // one, the conversion is worth 4 us, the softmax 5 and the 16 MMAs of a tile 9 (they
 // cost the same ~60 cycles whatever their N up to 128); barriers and fetch are the
 // remaining 20.

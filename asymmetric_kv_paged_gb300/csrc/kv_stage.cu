@@ -14,7 +14,7 @@
 // (e2m1.cuh), except that a V block with a NaN scale is written as zeros and
 // reported in a byte per tile (fp4_nan.cuh).  Keys outside [klo, khi) are written as zeros: the
 // kernel masks them, and zeros keep P.V free of whatever the pool holds
-// there.  A page id outside the pool is read as zeros and reported in bit 1
+// there.  A page id outside the pool is read as zeros and reported in bit 0
 // of the plan's error word, as the attention kernels do.
 //
 // One CTA per 128-key tile (grid-stride): the tile's page lookups first (one

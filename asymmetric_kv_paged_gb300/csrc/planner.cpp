@@ -136,8 +136,8 @@ attn_status_t build_host_plan(const attn_problem_t *p, int32_t num_sms, HostPlan
   // kernel, four requests of 46K keys: 8 rows 23 us and 51, 32 rows 43 us and 59;
   // 64 rows as two groups of 32 74 us and 51).  With 17 to 32 rows its start and
   // end cost more than the other one's, which its tiles only win back from about
-  // three to an SM on: 16 requests of 500 keys 15.0 us and 11.6, of 1000 13.8 and
-  // 16.5, of 8000 40.7 and 53.9; up to 16 rows it is the faster one throughout (500
+  // three to an SM on: 16 requests of 500 keys 15.0 us and 11.6, of 1000 14.2 and
+  // 16.5, of 8000 41.6 and 53.9; up to 16 rows it is the faster one throughout (500
   // keys 10.1 and 11.3, 1000 keys 9.7 and 15.8).
   if (p->kv_dtype == ATTN_KV_FP4_E2M1 && max_rows <= kFp4MaxRows) {
     int64_t tiles = 0;

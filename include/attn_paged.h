@@ -132,6 +132,11 @@ typedef struct {
  * Synchronous; allocates device memory.  Errors: INVALID_ARG (NULL pointers,
  * inconsistent lengths), UNSUPPORTED (head dims), CUDA (device errors).
  * On error *plan is set to NULL.
+ * One attention kernel runs a whole plan, chosen by the most query rows that any
+ * request has per KV head (new tokens times Hq / Hkv).  A prompt chunk therefore
+ * takes the decode requests of its batch through the prefill kernel: on a 4-bit cache
+ * one 1,024-token chunk beside 31 decode requests (16/2 heads) takes 576 us as one
+ * plan, 240 and 65 as two.
  */
 attn_status_t attn_plan(const attn_problem_t *problem, int device, attn_plan_t *plan,
                         size_t *workspace_bytes);
@@ -212,6 +217,7 @@ attn_status_t attn_plan_replayable(const attn_problem_t *bounds, int device, att
  * nothing else.  (A NaN or infinity in a V row of a BF16 cache, and a NaN of an
  * E4M3 cache on prefill plans, also makes those dims NaN for rows that do not see
  * the key when one of their key tiles holds it.)
+ * On a 4-bit cache q, out and the caches must be 16-byte aligned (INVALID_ARG).
  * Prefill plans that are not replayable first gather the keys their blocks
  * read into a staging scratch in the workspace (16-bit rows: E4M3 and
  * E2M1 widened exactly to fp16, BF16 copied; (Dqk + 128) * 2 bytes per key of each KV
@@ -267,6 +273,7 @@ attn_status_t attn_run_phase(attn_plan_t plan, int32_t phase, const void *q,
  *   k_cache, v_cache, page_table, seq_lens, qo_indptr: as for attn_run_paged
  *                (device copies equal to the plan's host arrays).
  *   k_scale, v_scale  finite and > 0 for FP8 and 4-bit caches; ignored for BF16.
+ * With a 4-bit cache k_new, v_new and the caches must be 16-byte aligned.
  * Only the written slots change.  A page id outside [0, num_pages) is not
  * dereferenced: that token's rows are skipped and the plan's device error
  * word records it (bit 0).  With a replayable plan seq_lens may change between
