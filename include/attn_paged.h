@@ -224,7 +224,7 @@ attn_status_t attn_plan_replayable(const attn_problem_t *bounds, int device, att
  * head, over whole 128-key tiles), which the prefill kernel loads as TMA
  * tiles; attn_plan's workspace size includes it.
  * Runs of one plan must be ordered on one stream (they share the plan's
- * device error word); different plans are independent.
+ * device memory); different plans are independent.
  * Errors: INVALID_ARG, WORKSPACE, CUDA (launch errors; nothing is waited for).
  */
 attn_status_t attn_run_paged(attn_plan_t plan, const void *q, const void *k_cache,
