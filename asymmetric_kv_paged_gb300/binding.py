@@ -28,6 +28,8 @@ EXPORTED = ("attn_plan", "attn_run_paged", "attn_run_phase", "attn_plan_destroy"
             "attn_debug_tc_gemm", "attn_debug_stamps",
             "attn_run_paged_no_workspace",
             "attn_append_kv", "attn_append_kv_rope", "attn_read_kv", "attn_kv_row_bytes",
+            "attn_append_kv_mrope", "attn_bounds_row_bytes", "attn_update_bounds", "attn_read_bounds",
+            "attn_select_blocks", "attn_run_sparse",
             "attn_plan_replayable", "attn_plan_replayable_host",
             "attn_plan_replan_host", "attn_plan_fetch_device")
 
@@ -47,6 +49,16 @@ class attn_rope_t(ctypes.Structure):
     _fields_ = [("cos_sin", ctypes.c_void_p), ("positions", ctypes.c_void_p),
                 ("max_pos", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
                 ("rot_offset", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
+class attn_mrope_t(ctypes.Structure):
+    _fields_ = [("rope", attn_rope_t), ("num_axes", ctypes.c_int32),
+                ("pair_axis_host", ctypes.POINTER(ctypes.c_uint8)), ("position_delta", ctypes.c_void_p)]
+
+
+class attn_sparse_t(ctypes.Structure):
+    _fields_ = [("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
+                ("first_blocks", ctypes.c_int32), ("last_blocks", ctypes.c_int32)]
 
 
 class AttnError(RuntimeError):
@@ -94,6 +106,12 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         [ctypes.c_float, ctypes.c_float, vp]
     L.attn_read_kv.argtypes = [vp] * 6 + [ctypes.c_int64, vp, vp, ctypes.c_float, ctypes.c_float, vp]
     L.attn_kv_row_bytes.argtypes = [ctypes.c_int, ctypes.c_int32, i32p]
+    L.attn_append_kv_mrope.argtypes = [vp, ctypes.POINTER(attn_mrope_t)] + L.attn_append_kv_rope.argtypes[2:]
+    L.attn_bounds_row_bytes.argtypes = [ctypes.c_int32, i32p]
+    L.attn_update_bounds.argtypes = [vp, ctypes.c_int32] + [vp] * 5 + [ctypes.c_int64, vp]
+    L.attn_read_bounds.argtypes = [vp, ctypes.c_int32] + [vp] * 4 + [ctypes.c_int64, vp, vp]
+    L.attn_select_blocks.argtypes = [vp, ctypes.POINTER(attn_sparse_t)] + [vp] * 7
+    L.attn_run_sparse.argtypes = [vp, ctypes.POINTER(attn_sparse_t)] + [vp] * 8 + [ctypes.c_float] * 3 + [vp] * 3
     L.attn_plan_destroy.argtypes = [vp]
     L.attn_get_device_error.argtypes = [vp, vp, i32p]
     L.attn_status_string.argtypes = [ctypes.c_int]
@@ -149,11 +167,13 @@ def _stream(stream, plan) -> int:
 class Plan:
     """Owns an attn_plan_t handle (destroyed with the object)."""
 
-    def __init__(self, handle: int, workspace_bytes: int, device: int, keep, total_q: int):
+    def __init__(self, handle: int, workspace_bytes: int, device: int, keep, problem: attn_problem_t):
         self.handle = handle
         self.workspace_bytes = workspace_bytes
         self.device = device
-        self.total_q = total_q          # new tokens of the whole batch
+        self.total_q = _total_q(problem)         # new tokens of the whole batch
+        self.batch = problem.batch
+        self.kv_heads = problem.num_kv_heads
         self._keep = keep
 
     def destroy(self) -> None:
@@ -192,14 +212,14 @@ def attn_plan(problem: attn_problem_t, device: int, keep=None) -> Plan:
     ws = ctypes.c_size_t()
     _check(load().attn_plan(ctypes.byref(problem), int(device), ctypes.byref(h), ctypes.byref(ws)),
            "attn_plan")
-    return Plan(h.value, ws.value, device, keep, _total_q(problem))
+    return Plan(h.value, ws.value, device, keep, problem)
 
 
 def attn_plan_host(problem: attn_problem_t, num_sms: int, keep=None) -> Plan:
     h = ctypes.c_void_p()
     _check(load().attn_plan_host(ctypes.byref(problem), int(num_sms), ctypes.byref(h)),
            "attn_plan_host")
-    return Plan(h.value, 0, -1, keep, _total_q(problem))
+    return Plan(h.value, 0, -1, keep, problem)
 
 
 def attn_plan_replayable(bounds: attn_problem_t, device: int, keep=None) -> Plan:
@@ -209,14 +229,14 @@ def attn_plan_replayable(bounds: attn_problem_t, device: int, keep=None) -> Plan
     ws = ctypes.c_size_t()
     _check(load().attn_plan_replayable(ctypes.byref(bounds), int(device), ctypes.byref(h),
                                        ctypes.byref(ws)), "attn_plan_replayable")
-    return Plan(h.value, ws.value, device, keep, _total_q(bounds))
+    return Plan(h.value, ws.value, device, keep, bounds)
 
 
 def attn_plan_replayable_host(bounds: attn_problem_t, num_sms: int, keep=None) -> Plan:
     h = ctypes.c_void_p()
     _check(load().attn_plan_replayable_host(ctypes.byref(bounds), int(num_sms), ctypes.byref(h)),
            "attn_plan_replayable_host")
-    return Plan(h.value, 0, -1, keep, _total_q(bounds))
+    return Plan(h.value, 0, -1, keep, bounds)
 
 
 def attn_plan_replan_host(plan: Plan, seq_lens) -> int:
@@ -347,6 +367,134 @@ def attn_read_kv(plan: Plan, k_cache, v_cache, page_table, seq_lens, kv_indptr, 
         k_out.shape[0], _ptr(k_out), _ptr(v_out), float(k_scale), float(v_scale), _stream(stream, plan))
     if st:
         raise AttnError(st, "attn_read_kv")
+
+
+def _contiguous(name: str, t, dtype, shape=None) -> None:
+    """What the library cannot see of a tensor that it gets as a pointer."""
+    if t.dtype != dtype or not t.is_contiguous() or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must be contiguous {dtype}" + (f" {tuple(shape)}" if shape is not None else "") +
+                         f", not {t.dtype} {tuple(t.shape)}")
+
+
+def make_mrope(cos_sin, rot_dim: int, pair_axis, positions=None, position_delta=None, rot_offset: int = 0,
+               interleaved: bool = False) -> attn_mrope_t:
+    """The rotation of attn_append_kv_mrope: as make_rope, with the axis of every pair in
+    pair_axis (rot_dim / 2 numbers, see mrope_axes), positions int32 [num_axes, total_q]
+    on the device or None for the tokens' own, then shifted by position_delta (int32
+    [batch] on the device) where that is given."""
+    import torch
+    axes = [int(x) for x in pair_axis]
+    if len(axes) != rot_dim // 2 or min(axes, default=0) < 0 or max(axes, default=0) > 255:
+        raise ValueError(f"pair_axis must hold rot_dim / 2 = {rot_dim // 2} axes")
+    rope = make_rope(cos_sin, rot_dim, rot_offset, interleaved, None)
+    num_axes = max(axes, default=0) + 1
+    if positions is not None:
+        if positions.dim() != 2 or positions.shape[0] < num_axes:
+            raise ValueError(f"positions must be [num_axes, total_q] with {num_axes} axes or more")
+        _contiguous("positions", positions, torch.int32)
+        num_axes = positions.shape[0]
+        rope.positions = _ptr(positions)
+    if position_delta is not None:
+        _contiguous("position_delta", position_delta, torch.int32)
+    m = attn_mrope_t(rope, num_axes, (ctypes.c_uint8 * len(axes))(*axes), _ptr(position_delta))
+    m.keep = (cos_sin, positions, position_delta)
+    return m
+
+
+def mrope_axes(sections, in_turn: bool = False) -> list:
+    """pair_axis for sections[a] pairs of each axis a: one section after the other, or the
+    axes in turn until each has had its pairs."""
+    if not in_turn:
+        return [a for a, n in enumerate(sections) for _ in range(n)]
+    left, out = list(sections), []
+    while any(left):
+        for a in range(len(left)):
+            if left[a]:
+                left[a] -= 1
+                out.append(a)
+    return out
+
+
+def attn_append_kv_mrope(plan: Plan, mrope: attn_mrope_t, q, k_new, v_new, q_out, k_cache, v_cache,
+                         page_table, seq_lens, qo_indptr, k_scale: float = 1.0, v_scale: float = 1.0,
+                         stream=None) -> None:
+    """attn_append_kv_rope with positions of several axes."""
+    _, positions, delta = getattr(mrope, "keep", (None, None, None))
+    if positions is not None and positions.shape[1] != plan.total_q:
+        raise ValueError(f"positions has {positions.shape[1]} columns for the plan's {plan.total_q} tokens")
+    if delta is not None and delta.numel() < plan.batch:
+        raise ValueError(f"position_delta has {delta.numel()} entries for the plan's {plan.batch} requests")
+    st = (_LIB or load()).attn_append_kv_mrope(
+        plan.handle, mrope, _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(q_out), _ptr(k_cache), _ptr(v_cache),
+        _ptr(page_table), _ptr(seq_lens), _ptr(qo_indptr), float(k_scale), float(v_scale), _stream(stream, plan))
+    if st:
+        raise AttnError(st, "attn_append_kv_mrope")
+
+
+def make_sparse(block_size: int, num_blocks: int, first_blocks: int = 1, last_blocks: int = 1) -> attn_sparse_t:
+    """How attn_select_blocks chooses: num_blocks blocks of block_size keys per (token, KV
+    head), the first_blocks and last_blocks always among them."""
+    return attn_sparse_t(int(block_size), int(num_blocks), int(first_blocks), int(last_blocks))
+
+
+def attn_bounds_row_bytes(head_dim: int) -> int:
+    """Bytes of one block's bounds for one KV head: the last dimension of the bounds array,
+    uint8 [num_pages, page_size / block_size, Hkv, bytes]."""
+    n = ctypes.c_int32()
+    _check(load().attn_bounds_row_bytes(int(head_dim), ctypes.byref(n)), "attn_bounds_row_bytes")
+    return n.value
+
+
+def attn_update_bounds(plan: Plan, block_size: int, k_cache, bounds, page_table, seq_lens, kv_indptr,
+                       rows: int, stream=None) -> None:
+    """Bounds of the blocks that the last kv_indptr[b + 1] - kv_indptr[b] positions of every
+    request b complete; rows = kv_indptr[batch]."""
+    st = (_LIB or load()).attn_update_bounds(
+        plan.handle, int(block_size), _ptr(k_cache), _ptr(bounds), _ptr(page_table), _ptr(seq_lens),
+        _ptr(kv_indptr), int(rows), _stream(stream, plan))
+    if st:
+        raise AttnError(st, "attn_update_bounds")
+
+
+def attn_read_bounds(plan: Plan, block_size: int, bounds, page_table, seq_lens, block_indptr, out,
+                     stream=None) -> None:
+    """The bounds as bf16: the last block_indptr[b + 1] - block_indptr[b] complete blocks of
+    every request b, into out [rows, Hkv, 2, Dqk] (upper, lower)."""
+    st = (_LIB or load()).attn_read_bounds(
+        plan.handle, int(block_size), _ptr(bounds), _ptr(page_table), _ptr(seq_lens), _ptr(block_indptr),
+        out.shape[0], _ptr(out), _stream(stream, plan))
+    if st:
+        raise AttnError(st, "attn_read_bounds")
+
+
+def _block_lists(plan: Plan, sparse: attn_sparse_t, block_idx) -> None:
+    if block_idx.numel() != plan.total_q * plan.kv_heads * sparse.num_blocks:
+        raise ValueError(f"block_idx has {block_idx.numel()} entries for {plan.total_q} tokens, "
+                         f"{plan.kv_heads} KV heads and {sparse.num_blocks} blocks")
+
+
+def attn_select_blocks(plan: Plan, sparse: attn_sparse_t, q, bounds, page_table, seq_lens, qo_indptr,
+                       block_idx, stream=None) -> None:
+    """Every new token's blocks into block_idx, int32 [total_q, Hkv, num_blocks]."""
+    _block_lists(plan, sparse, block_idx)
+    st = (_LIB or load()).attn_select_blocks(
+        plan.handle, sparse, _ptr(q), _ptr(bounds), _ptr(page_table), _ptr(seq_lens), _ptr(qo_indptr),
+        _ptr(block_idx), _stream(stream, plan))
+    if st:
+        raise AttnError(st, "attn_select_blocks")
+
+
+def attn_run_sparse(plan: Plan, sparse: attn_sparse_t, q, k_cache, v_cache, page_table, seq_lens, qo_indptr,
+                    block_idx, sinks, softmax_scale: float, k_scale: float, v_scale: float, out,
+                    lse_out=None, stream=None) -> None:
+    """Attention of every new token over the blocks of its lists."""
+    _block_lists(plan, sparse, block_idx)
+    st = (_LIB or load()).attn_run_sparse(
+        plan.handle, sparse, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens),
+        _ptr(qo_indptr), _ptr(block_idx), _ptr(sinks), float(softmax_scale), float(k_scale), float(v_scale),
+        _ptr(out), _ptr(lse_out), _stream(stream, plan))
+    if st:
+        raise AttnError(st, "attn_run_sparse")
 
 
 def attn_get_device_error(plan: Plan) -> int:

@@ -38,31 +38,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// K (d = 192 or 128) or V (d = 128) cache as a 3D tensor [slots][Hkv][d]; boxes of
-// `rows` consecutive slots of one head: 64 bf16 columns with 128-byte swizzle
-// (the tensor-core operand layout), or whole raw rows of `row_bytes` bytes (E4M3,
-// E2M1 with its scales; row_bytes = 0 for bf16) without swizzle.
-bool make_cache_map(CUtensorMap *map, const void *base, int row_bytes, int d, int hkv, int64_t slots,
-                    int rows) {
-  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
-  if (!fn) return false;
-  const bool raw = row_bytes > 0;
-  const cuuint64_t row = raw ? row_bytes : 2 * d;
-  const cuuint64_t dims[3] = {raw ? row : (cuuint64_t)d, (cuuint64_t)hkv, (cuuint64_t)slots};
-  const cuuint64_t strides[2] = {row, (cuuint64_t)hkv * row};
-  const cuuint32_t box[3] = {raw ? (cuuint32_t)row : 64u, 1u, (cuuint32_t)rows};
-  const cuuint32_t estr[3] = {1u, 1u, 1u};
-  CUresult r = fn(map, raw ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                  const_cast<void *>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  raw ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                  // 128-byte promotion: a 256-byte one pulls in part of the neighbouring
-                  // head's K row (rows are 384 bytes at offset g * 384), which measured
-                  // 2% slower on the batched decode
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
 // Staging scratch of prefill plans (K: d = 192, V: d = 128 16-bit values a
 // row) as a 2D tensor [rows][d]: boxes of 64 columns x 128 rows (one key tile
 // of one 64-column operand block) with 128-byte swizzle.
@@ -156,6 +131,34 @@ attn_status_t upload(attn_plan_s *p) {
 }
 
 }  // namespace
+
+namespace akp {
+// K (d = 192 or 128) or V (d = 128) cache as a 3D tensor [slots][Hkv][d]; boxes of
+// `rows` consecutive slots of one head: 64 bf16 columns with 128-byte swizzle
+// (the tensor-core operand layout), or whole raw rows of `row_bytes` bytes (E4M3,
+// E2M1 with its scales; row_bytes = 0 for bf16) without swizzle, or with the
+// 128-byte one where `swizzled` (rows of 128 bytes).
+bool make_cache_map(CUtensorMap *map, const void *base, int row_bytes, int d, int hkv, int64_t slots, int rows,
+                    bool swizzled) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+  if (!fn) return false;
+  const bool raw = row_bytes > 0;
+  const cuuint64_t row = raw ? row_bytes : 2 * d;
+  const cuuint64_t dims[3] = {raw ? row : (cuuint64_t)d, (cuuint64_t)hkv, (cuuint64_t)slots};
+  const cuuint64_t strides[2] = {row, (cuuint64_t)hkv * row};
+  const cuuint32_t box[3] = {raw ? (cuuint32_t)row : 64u, 1u, (cuuint32_t)rows};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  CUresult r = fn(map, raw ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+                  const_cast<void *>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  raw && !swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                  // 128-byte promotion: a 256-byte one pulls in part of the neighbouring
+                  // head's K row (rows are 384 bytes at offset g * 384), which measured
+                  // 2% slower on the batched decode
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+}  // namespace akp
 
 extern "C" {
 
@@ -307,8 +310,8 @@ static attn_status_t run_impl(attn_plan_t plan, int phases, bool allow_stage, co
     const int64_t slots = (int64_t)pr.num_pages * pr.page_size;
     // keys per box: a whole tile, or a unit of the register-operand 4-bit kernel
     const int rows = std::min(pr.page_size, hp.fp4_rows ? akp::kFp4UnitKeys : akp::kKeyTile);
-    if (!make_cache_map(&maps.k, k_cache, k_row, pr.head_dim_qk, pr.num_kv_heads, slots, rows) ||
-        !make_cache_map(&maps.v, v_cache, v_row, akp::kDv, pr.num_kv_heads, slots, rows))
+    if (!akp::make_cache_map(&maps.k, k_cache, k_row, pr.head_dim_qk, pr.num_kv_heads, slots, rows) ||
+        !akp::make_cache_map(&maps.v, v_cache, v_row, akp::kDv, pr.num_kv_heads, slots, rows))
       return ATTN_ERR_CUDA;
   }
   DeviceGuard guard(plan->device);

@@ -3,6 +3,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "plan.hpp"
 
 namespace akp {
@@ -41,6 +43,18 @@ struct RunArgs {
   int32_t *err;
   const uint8_t *stage_nan;  // NaN V blocks of each staged tile (4-bit prefill plans)
   int32_t replayed;      // the work list is rewritten by the device planner at every run
+};
+
+// A kernel's dynamic shared memory limit, raised on the first launch on each device.
+struct SmemLimit {
+  std::atomic<uint64_t> done{0};
+  cudaError_t raise(const void *kernel, int device, int bytes) {
+    const uint64_t bit = device < 64 ? 1ull << device : 0ull;
+    if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
+  }
 };
 
 // Launch `kernel` as a programmatic dependent of the stream's previous kernel:
@@ -116,11 +130,19 @@ attn_status_t run_paged_unstaged(attn_plan_t plan, const void *q, const void *k_
                                  float k_scale, float v_scale, void *out, float *lse_out,
                                  void *workspace, size_t workspace_bytes, void *stream);
 // New tokens' rows into the caches, rotated when `rope` is given (kv_rope.cu):
-// attn_append_kv_rope, and attn_append_kv of 4-bit caches (rope, q, q_out NULL).
-attn_status_t append_rows(attn_plan_t plan, const attn_rope_t *rope, const void *q, const void *k_new,
-                          const void *v_new, void *q_out, void *k_cache, void *v_cache,
+// attn_append_kv_rope, attn_append_kv_mrope (`axes` too, whose rope is `rope`), and
+// attn_append_kv of 4-bit caches (rope, axes, q, q_out NULL).
+attn_status_t append_rows(attn_plan_t plan, const attn_rope_t *rope, const attn_mrope_t *axes, const void *q,
+                          const void *k_new, const void *v_new, void *q_out, void *k_cache, void *v_cache,
                           const int32_t *page_table, const int32_t *seq_lens, const int32_t *qo_indptr,
                           float k_scale, float v_scale, void *stream);
+// Attention over selected blocks (select.cu, attn_sparse.cu): the checks both share, and
+// the longest request that a plan allows (lengths are clamped to it).
+attn_status_t check_sparse(const HostPlan &hp, const attn_sparse_t *s);
+int32_t longest_request(const HostPlan &hp);
+// A cache as 3D tensor [slots][Hkv][row], for boxes of `rows` slots of one head (api.cu).
+bool make_cache_map(CUtensorMap *map, const void *base, int row_bytes, int d, int hkv, int64_t slots, int rows,
+                    bool swizzled = false);
 // Log-sum-exp merge of multi-split blocks.
 cudaError_t launch_merge(const HostPlan &hp, const RunArgs &a, cudaStream_t stream);
 

@@ -130,7 +130,7 @@ extern "C" attn_status_t attn_append_kv(attn_plan_t plan, const void *k_new, con
   const akp::HostPlan &hp = plan->host;
   const attn_problem_t &pr = hp.prob;
   if (pr.kv_dtype == ATTN_KV_FP4_E2M1)          // a scale per 16 values: kv_rope.cu
-    return akp::append_rows(plan, nullptr, nullptr, k_new, v_new, nullptr, k_cache, v_cache, page_table,
+    return akp::append_rows(plan, nullptr, nullptr, nullptr, k_new, v_new, nullptr, k_cache, v_cache, page_table,
                             seq_lens, qo_indptr, k_scale, v_scale, stream);
   const int64_t total_q = hp.qo_indptr.back();
   if (total_q == 0) return ATTN_OK;

@@ -49,12 +49,19 @@
 #include "e2m1.cuh"
 #include "kernels.hpp"
 #include "plan.hpp"
+#include "requests.cuh"
+#include "sparse.cuh"
 
 namespace akp {
 namespace {
 
 constexpr int kAppendThreads = 256;
-enum { kNoRope = 0, kHalves = 1, kPairs = 2 };
+// what is rotated: nothing; pairs of dims half the rotated range apart, or of neighbours;
+// the same with every pair on an axis of its own
+enum { kNoRope = 0, kHalves = 1, kPairs = 2, kHalvesAxes = 3, kPairsAxes = 4 };
+__host__ __device__ constexpr bool halves(int rope) { return rope == kHalves || rope == kHalvesAxes; }
+__host__ __device__ constexpr bool by_axes(int rope) { return rope >= kHalvesAxes; }
+constexpr int kMaxAxes = 4;
 
 struct RopeAppendArgs {
   const uint16_t *q, *k_new, *v_new;
@@ -67,27 +74,11 @@ struct RopeAppendArgs {
   int32_t batch, hq, hkv, page_size, pt_stride, num_pages;
   int32_t max_pos, rot, rot_off;
   float k_scale, v_scale;
+  // positions of several axes: positions is [axes][tokens]; two bits a pair, its axis
+  int32_t axes;
+  const int32_t *position_delta;          // [batch], added to the tokens' own positions
+  uint32_t axis_bits[kDqk / 32];
 };
-
-// The request that holds flat row `t` of a prefix-sum array: the number of
-// entries indptr[1 .. batch] that are <= t.  All 32 lanes of a warp call it with
-// one t: whole blocks of 256 entries by bisection, then one round of loads.
-__device__ __forceinline__ int request_of(const int32_t *indptr, int batch, int64_t t) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = batch;               // the answer is in [lo, hi]
-  while (hi - lo > 256) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(indptr + mid + 1) <= t) lo = mid + 1; else hi = mid;
-  }
-  int n = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = lo + i * 32 + lane;
-    const bool le = e < hi && __ldg(indptr + e + 1) <= t;
-    n += __popc(__ballot_sync(0xffffffffu, le));
-  }
-  return lo + n;
-}
 
 // Paired fp32 arithmetic: a * b and a * b + c, two of each in one instruction.  (A
 // paired addition behind a paired product is contracted into one rounding by the
@@ -132,18 +123,20 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 // What a lane's chunk does under the rotation, for the token at hand.
 template <int ROPE, int NC>
 struct Turn {
+  static constexpr int N = halves(ROPE) ? 2 : 1;      // groups of four angles
   bool in = false;                // the chunk's dims are rotated
-  int partner = 0;                // kHalves: the lane with the other half's chunk
-  float c[ROPE == kHalves ? 8 : 4], s[ROPE == kHalves ? 8 : 4];
+  int partner = 0;                // halves: the lane with the other half's chunk
+  float c[4 * N], s[4 * N];
   int at = 0;                     // first cosine of the chunk
   float sign = 1.f;
+  uint32_t axis = 0;              // by axes: two bits an angle
 
   __device__ __forceinline__ void place(const RopeAppendArgs &a, int lane) {
     if (ROPE == kNoRope) return;
     const int half = a.rot >> 1, r = 8 * (lane % NC) - a.rot_off;
     in = r >= 0 && r < a.rot;
     partner = lane;
-    if (ROPE == kHalves) {
+    if (halves(ROPE)) {
       const bool first = r < half;
       at = first ? r : r - half;
       sign = first ? -1.f : 1.f;            // x1 c - x2 s, x2 c + x1 s
@@ -151,10 +144,11 @@ struct Turn {
     } else {
       at = r >> 1;
     }
+    // (a chunk's angles start at a multiple of 8, or of 4 for neighbours: one word)
+    if (by_axes(ROPE) && in) axis = a.axis_bits[at >> 4] >> (2 * (at & 15));
   }
   __device__ __forceinline__ void angles(const RopeAppendArgs &a, int64_t pos) {
     if (ROPE == kNoRope) return;
-    constexpr int N = ROPE == kHalves ? 2 : 1;
     const float *row = a.cos_sin + pos * a.rot + at;
 #pragma unroll
     for (int p = 0; p < N; ++p) {
@@ -167,11 +161,22 @@ struct Turn {
       s[4 * p] = sign * y.x, s[4 * p + 1] = sign * y.y, s[4 * p + 2] = sign * y.z, s[4 * p + 3] = sign * y.w;
     }
   }
+  // The same with a position per axis.
+  __device__ __forceinline__ void angles(const RopeAppendArgs &a, const int32_t (&pos)[kMaxAxes]) {
+#pragma unroll
+    for (int j = 0; j < 4 * N; ++j) {
+      const uint32_t ax = (axis >> (2 * j)) & 3u;
+      const int32_t p = ax == 0 ? pos[0] : ax == 1 ? pos[1] : ax == 2 ? pos[2] : pos[3];
+      const float *cos = a.cos_sin + (int64_t)p * a.rot + at + j;
+      c[j] = in ? __ldg(cos) : 0.f;
+      s[j] = in ? sign * __ldg(cos + (a.rot >> 1)) : 0.f;
+    }
+  }
   // v = the lane's chunk, rotated; every lane of the warp calls it (shuffles).
   // Products and sums are rounded one by one (a - b s = a + b (-s) exactly).
   __device__ __forceinline__ void apply(const uint4 raw, float (&v)[8]) const {
     unpack8(raw, v);
-    if (ROPE == kHalves) {
+    if (halves(ROPE)) {
       uint4 o;
       o.x = __shfl_sync(0xffffffffu, raw.x, partner);
       o.y = __shfl_sync(0xffffffffu, raw.y, partner);
@@ -187,7 +192,7 @@ struct Turn {
           v[j] = __fadd_rn(x.x, y.x);
           v[j + 1] = __fadd_rn(x.y, y.y);
         }
-    } else if (ROPE == kPairs) {
+    } else if (ROPE != kNoRope) {
       if (in)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -331,37 +336,6 @@ __device__ __forceinline__ uint32_t quantise8(const float (&v)[8], const Divisor
   return out;
 }
 
-// The request of consecutive rows of a prefix-sum array, in registers: looked up
-// once, then only when a row lies past its end.  `shift`: the position of row t in
-// its request is t + shift (the last row is the request's last key).
-struct Request {
-  int b = -1, first = 0, end = 0;      // rows [first, end)
-  int64_t shift = 0;
-  __device__ __forceinline__ void seek(const int32_t *indptr, const int32_t *seq_lens, int batch, int64_t row) {
-    if (b >= 0 && row < end) return;
-    if (batch <= 32) {                 // everything in one round of loads, a request a lane
-      const int lane = threadIdx.x & 31;
-      int lo = 0, hi = 0, len = 0;
-      if (lane < batch) {
-        lo = __ldg(indptr + lane);
-        hi = __ldg(indptr + lane + 1);
-        len = __ldg(seq_lens + lane);
-      }
-      b = __popc(__ballot_sync(0xffffffffu, lane < batch && hi <= row));
-      first = __shfl_sync(0xffffffffu, lo, b & 31);
-      end = __shfl_sync(0xffffffffu, hi, b & 31);
-      shift = (int64_t)__shfl_sync(0xffffffffu, len, b & 31) - end;
-      return;
-    }
-    b = request_of(indptr, batch, row);
-    if (b < batch) {
-      first = __ldg(indptr + b);
-      end = __ldg(indptr + b + 1);
-      shift = (int64_t)__ldg(seq_lens + b) - end;
-    }
-  }
-};
-
 // Rows of D values as a warp takes them: RPW rows a step, lane % NC the chunk.
 template <int D>
 struct Lanes {
@@ -479,7 +453,25 @@ __global__ void __launch_bounds__(kAppendThreads, 4) rope_append_kernel(const Ro
       continue;
     }
     const int64_t i = tok + rq.shift;
-    if (ROPE != kNoRope) {
+    if (by_axes(ROPE)) {
+      int32_t pos[kMaxAxes];
+      bool good = true;
+#pragma unroll
+      for (int ax = 0; ax < kMaxAxes; ++ax) {
+        int64_t p = 0;
+        if (ax < a.axes) {
+          p = a.positions ? (int64_t)__ldg(a.positions + (int64_t)ax * a.tokens + tok)
+                          : i + (a.position_delta ? __ldg(a.position_delta + rq.b) : 0);
+          good &= p >= 0 && p < a.max_pos;
+        }
+        pos[ax] = good ? (int32_t)p : 0;
+      }
+      if (!good) {                                  // as below
+        if (slice == 0 && lane == 0) atomicOr(a.err, 8);
+        continue;
+      }
+      turn.angles(a, pos);
+    } else if (ROPE != kNoRope) {
       const int64_t pos = a.positions ? (int64_t)__ldg(a.positions + tok) : i;
       if (pos < 0 || pos >= a.max_pos) {            // no row of the table: the token is skipped
         if (slice == 0 && lane == 0) atomicOr(a.err, 8);
@@ -654,8 +646,6 @@ __global__ void __launch_bounds__(kAppendThreads, 4) read_kernel(const ReadArgs 
   }
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 // Splits `rows` of `heads` rows of one kind each among the warps that all SMs hold
 // (four CTAs an SM): ranges of rows, and the warps that share a range's heads.  (A
 // step of 128-value rows takes two heads, so that with few rows some of the warps
@@ -692,8 +682,8 @@ bool scales_ok(int kv, float k, float v) {
 
 }  // namespace
 
-attn_status_t append_rows(attn_plan_t plan, const attn_rope_t *rope, const void *q, const void *k_new,
-                          const void *v_new, void *q_out, void *k_cache, void *v_cache,
+attn_status_t append_rows(attn_plan_t plan, const attn_rope_t *rope, const attn_mrope_t *axes, const void *q,
+                          const void *k_new, const void *v_new, void *q_out, void *k_cache, void *v_cache,
                           const int32_t *page_table, const int32_t *seq_lens, const int32_t *qo_indptr,
                           float k_scale, float v_scale, void *stream) {
   if (!plan || plan->device < 0) return ATTN_ERR_INVALID_ARG;
@@ -707,6 +697,13 @@ attn_status_t append_rows(attn_plan_t plan, const attn_rope_t *rope, const void 
     if (rope->rot_dim % 16 || rope->rot_offset % 8) return ATTN_ERR_UNSUPPORTED;
     if ((q == nullptr) != (q_out == nullptr) || !aligned16(rope->cos_sin) || !aligned16(q) || !aligned16(q_out))
       return ATTN_ERR_INVALID_ARG;
+  }
+  if (axes) {
+    if (axes->num_axes < 1 || axes->num_axes > kMaxAxes || !axes->pair_axis_host ||
+        (rope->positions && axes->position_delta))
+      return ATTN_ERR_INVALID_ARG;
+    for (int i = 0; i < rope->rot_dim / 2; ++i)
+      if (axes->pair_axis_host[i] >= axes->num_axes) return ATTN_ERR_INVALID_ARG;
   }
   if (!scales_ok(pr.kv_dtype, k_scale, v_scale)) return ATTN_ERR_INVALID_ARG;
   const int64_t total_q = hp.qo_indptr.back();
@@ -740,6 +737,12 @@ attn_status_t append_rows(attn_plan_t plan, const attn_rope_t *rope, const void 
     a.max_pos = rope->max_pos;
     a.rot = rope->rot_dim;
     a.rot_off = rope->rot_offset;
+    if (axes) {
+      a.axes = axes->num_axes;
+      a.position_delta = axes->position_delta;
+      for (int i = 0; i < rope->rot_dim / 2; ++i)
+        a.axis_bits[i / 16] |= (uint32_t)axes->pair_axis_host[i] << (2 * (i % 16));
+    }
     if (q) {
       a.q = static_cast<const uint16_t *>(q);
       a.q_out = static_cast<uint16_t *>(q_out);
@@ -754,9 +757,12 @@ attn_status_t append_rows(attn_plan_t plan, const attn_rope_t *rope, const void 
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const dim3 grid(sp.ctas);
   // (without a rotation only 4-bit caches come here: kv_append.cu)
-  const cudaError_t e = !rope               ? launch_append<ATTN_KV_FP4_E2M1, kNoRope>(a, pr.head_dim_qk, grid, st)
-                        : rope->interleaved ? launch_append_kv<kPairs>(a, pr.kv_dtype, pr.head_dim_qk, grid, st)
-                                            : launch_append_kv<kHalves>(a, pr.kv_dtype, pr.head_dim_qk, grid, st);
+  const int kv = pr.kv_dtype, dqk = pr.head_dim_qk;
+  const cudaError_t e = !rope               ? launch_append<ATTN_KV_FP4_E2M1, kNoRope>(a, dqk, grid, st)
+                        : rope->interleaved ? axes ? launch_append_kv<kPairsAxes>(a, kv, dqk, grid, st)
+                                                   : launch_append_kv<kPairs>(a, kv, dqk, grid, st)
+                        : axes              ? launch_append_kv<kHalvesAxes>(a, kv, dqk, grid, st)
+                                            : launch_append_kv<kHalves>(a, kv, dqk, grid, st);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
@@ -768,8 +774,18 @@ extern "C" attn_status_t attn_append_kv_rope(attn_plan_t plan, const attn_rope_t
                                              const int32_t *seq_lens, const int32_t *qo_indptr,
                                              float k_scale, float v_scale, void *stream) {
   if (!rope) return ATTN_ERR_INVALID_ARG;
-  return akp::append_rows(plan, rope, q, k_new, v_new, q_out, k_cache, v_cache, page_table, seq_lens,
+  return akp::append_rows(plan, rope, nullptr, q, k_new, v_new, q_out, k_cache, v_cache, page_table, seq_lens,
                           qo_indptr, k_scale, v_scale, stream);
+}
+
+extern "C" attn_status_t attn_append_kv_mrope(attn_plan_t plan, const attn_mrope_t *mrope, const void *q,
+                                              const void *k_new, const void *v_new, void *q_out,
+                                              void *k_cache, void *v_cache, const int32_t *page_table,
+                                              const int32_t *seq_lens, const int32_t *qo_indptr,
+                                              float k_scale, float v_scale, void *stream) {
+  if (!mrope) return ATTN_ERR_INVALID_ARG;
+  return akp::append_rows(plan, &mrope->rope, mrope, q, k_new, v_new, q_out, k_cache, v_cache, page_table,
+                          seq_lens, qo_indptr, k_scale, v_scale, stream);
 }
 
 extern "C" attn_status_t attn_read_kv(attn_plan_t plan, const void *k_cache, const void *v_cache,

@@ -1,0 +1,415 @@
+// attn_select_blocks: which blocks of the cache a new token attends to.
+//
+// For a token and KV head, with q^ the group's query rows in integers (|q^| <= 127, a
+// power of two apart from the bf16 row) and hi, lo a block's 8-bit bounds:
+//   d(h, c) = sum_d max(q^ hi, q^ lo) = q^+ . hi + q^- . lo,   q^+ = max(q^, 0), q^- = min(q^, 0),
+// a contraction of 2 Dqk whole numbers that every step of fp16 x fp16 -> fp32 MMAs holds
+// exactly (partial sums stay below 2^22), so that the order of summation plays no part
+// and equal scores are equal bits.  The score is the largest over the group's heads.
+//
+// A cluster of CTAs takes one token of one KV head.  A warp scores 8 blocks at a time:
+// lane (g, t) (g = lane / 4, t = lane % 4) reads 16-byte pieces t, t + 4, .. of the bounds
+// of block g straight into registers (the order of a contraction's index is free, so
+// that a piece feeds four MMAs) and widens them to fp16 there; the query rows wait in
+// shared memory as operand fragments.  Scores meet as ordered integers in the shared
+// memory of the cluster's first CTA, which finds the smallest one taken by a radix
+// select of 8 bits a pass and writes the list in order.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "attn_paged.h"
+#include "kernels.hpp"
+#include "plan.hpp"
+#include "requests.cuh"
+#include "sparse.cuh"
+
+namespace akp {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kMaxSmem = 224 * 1024;
+
+struct SelectArgs {
+  const uint16_t *q;
+  const uint8_t *bounds;
+  const int32_t *page_table, *seq_lens, *qo_indptr;
+  int32_t *block_idx, *err;
+  int32_t batch, hq, hkv, group, row_tiles, page_size, pt_stride, num_pages;
+  int32_t block, take, first, last, max_len, max_blocks;
+};
+
+// c (16 x 8, fp32) += a (16 x 16, fp16) . b (16 x 8, fp16)
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t max_h2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t min_h2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Four signed bytes -> four fp16 values: with the sign bit flipped, byte u = v + 128 is
+// the low byte of fp16 1024 + u.
+__device__ __forceinline__ void s8x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  w ^= 0x80808080u;
+  const __half2 bias = __half2half2(__ushort_as_half(0x6480));      // 1152
+  uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+  const __half2 x = __hsub2(*reinterpret_cast<__half2 *>(&a), bias);
+  const __half2 y = __hsub2(*reinterpret_cast<__half2 *>(&b), bias);
+  lo = *reinterpret_cast<const uint32_t *>(&x);
+  hi = *reinterpret_cast<const uint32_t *>(&y);
+}
+
+// fp32 -> an unsigned integer of the same order
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+
+template <int D>
+struct QTile {                         // 16 query rows as A fragments, and their factors
+  uint4 frag[D / 16][32];
+  float factor[16];                    // 2^(e_h - E); -1: no such row, or one that takes no part
+};
+
+// Row r of a token's query heads (r < group) as integers, D / 32 a lane in element order
+// of the fragments; returns its exponent, or INT_MIN for a row that takes no part.
+// Fragment order: k-step (j, s) holds for lane column t the dims 64 j + 16 t + 4 s + {0..3}.
+template <int D>
+__device__ __forceinline__ void stage_row(QTile<D> &tile, int r, const uint16_t *row, int lane, int *exps) {
+  // lane owns dims 4 (lane + 32 k) ..: piece p = dims / 4
+  constexpr int NP = D / 4, PL = (NP + 31) / 32;
+  uint2 w[PL];
+  float amax = 0.f;
+  bool odd = false;
+#pragma unroll
+  for (int k = 0; k < PL; ++k) {
+    const int p = lane + 32 * k;
+    w[k] = make_uint2(0u, 0u);
+    if (row && p < NP) w[k] = __ldg(reinterpret_cast<const uint2 *>(row) + p);
+    const uint32_t x[2] = {w[k].x, w[k].y};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float a = fabsf(__uint_as_float(x[i] << 16)), b = fabsf(__uint_as_float(x[i] & 0xFFFF0000u));
+      odd |= !(a < INFINITY) || !(b < INFINITY);
+      amax = fmaxf(amax, fmaxf(a, b));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  odd = __any_sync(0xffffffffu, odd) || !row;
+  const int e = odd ? 0 : min(code_exponent(amax), 121);
+  if (lane == 0) exps[r] = odd ? INT_MIN : e;
+  const float unit = odd ? 0.f : pow2(-e);
+#pragma unroll
+  for (int k = 0; k < PL; ++k) {
+    const int p = lane + 32 * k;
+    if (p >= NP) break;
+    float v[4] = {__uint_as_float(w[k].x << 16), __uint_as_float(w[k].x & 0xFFFF0000u),
+                  __uint_as_float(w[k].y << 16), __uint_as_float(w[k].y & 0xFFFF0000u)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = odd ? 0.f : fminf(fmaxf(rintf(v[i] * unit), -127.f), 127.f);
+    const __half2 lo = __floats2half2_rn(v[0], v[1]), hi = __floats2half2_rn(v[2], v[3]);
+    // dims 4p = 64 j + 16 t + 4 s: a lane (r % 8, t)'s words 0 (first pair), 2 (second), + 1 for rows 8..15
+    const int j = p / 16, t = p / 4 % 4, s = p % 4;
+    uint32_t *f = reinterpret_cast<uint32_t *>(&tile.frag[4 * j + s][(r & 7) * 4 + t]) + (r >> 3);
+    f[0] = *reinterpret_cast<const uint32_t *>(&lo);
+    f[2] = *reinterpret_cast<const uint32_t *>(&hi);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  QTile<D> *tiles = reinterpret_cast<QTile<D> *>(smem);                        // [row_tiles]
+  int *exps = reinterpret_cast<int *>(smem + a.row_tiles * sizeof(QTile<D>));  // [row_tiles * 16]
+  uint32_t *keys = reinterpret_cast<uint32_t *>(exps + a.row_tiles * 16);      // [max_blocks]
+  __shared__ int hist[256], sums[2][kWarps], pick[2];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tok = blockIdx.x / ranks, g = blockIdx.y;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  const int b = request_of(a.qo_indptr, a.batch, tok);
+  int32_t *out = a.block_idx + ((int64_t)tok * a.hkv + g) * a.take;
+  if (b >= a.batch) {                        // a row that qo_indptr does not hold (the whole cluster)
+    if (rank == 0) {
+      if (tid == 0) atomicOr(a.err, 4);
+      for (int k = tid; k < a.take; k += kThreads) out[k] = -1;
+    }
+    return;
+  }
+  const int q0 = __ldg(a.qo_indptr + b), n = __ldg(a.qo_indptr + b + 1) - q0;
+  const int L0 = __ldg(a.seq_lens + b), L = max(min(L0, a.max_len), n);
+  if (L != L0 && tid == 0 && rank == 0) atomicOr(a.err, 4);
+  const int own = (L - n + tok - q0) / a.block;             // the token's own block
+  if (own < a.take) {                                       // all of them
+    if (rank == 0)
+      for (int k = tid; k < a.take; k += kThreads) out[k] = k <= own ? k : -1;
+    return;
+  }
+  const int c_lo = a.first, c_hi = own - a.last + 1;        // the scored ones (take < own + 1: not empty
+                                                            // unless first + last == take)
+  uint32_t *dst = cluster.map_shared_rank(keys, 0);
+  // ---- the query rows
+  for (int r = warp; r < a.row_tiles * 16; r += kWarps) {
+    const uint16_t *row = r < a.group ? a.q + ((int64_t)tok * a.hq + g * a.group + r) * D : nullptr;
+    stage_row<D>(tiles[r >> 4], r & 15, row, lane, exps + (r & ~15));
+  }
+  __syncthreads();
+  for (int r = tid; r < a.row_tiles * 16; r += kThreads) {
+    int top = INT_MIN;
+    for (int i = 0; i < a.group; ++i) top = max(top, exps[i]);
+    tiles[r >> 4].factor[r & 15] = exps[r] == INT_MIN ? -1.f : ldexpf(1.f, exps[r] - top);
+  }
+  cluster.sync();                            // also: the first CTA's keys may be written from here on
+  // ---- scores
+  const int gq = lane >> 2, t = lane & 3;
+  const int per_page = a.page_size / a.block;
+  for (int c0 = c_lo + (rank * kWarps + warp) * 8; c0 < c_hi; c0 += ranks * kWarps * 8) {
+    const int c = min(c0 + gq, c_hi - 1);
+    const int32_t page = __ldg(a.page_table + (int64_t)b * a.pt_stride + c / per_page);
+    const bool bad = page < 0 || page >= a.num_pages;
+    if (bad && t == 0) atomicOr(a.err, 1);
+    const uint8_t *rec = a.bounds + (((int64_t)(bad ? 0 : page) * per_page + c % per_page) * a.hkv + g) *
+                                        bounds_row_bytes(D);
+    uint4 raw[2][D / 64];
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        raw[w][j] = make_uint4(0u, 0u, 0u, 0u);
+        if (!bad) raw[w][j] = __ldg(reinterpret_cast<const uint4 *>(rec + w * D) + 4 * j + t);
+      }
+    int e = 0;
+    if (!bad) e = (int8_t)__ldg(rec + 2 * D);
+    float best[2] = {-INFINITY, -INFINITY};
+    for (int rt = 0; rt < a.row_tiles; ++rt) {
+      float acc[2][4] = {};
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        const uint32_t up[4] = {raw[0][j].x, raw[0][j].y, raw[0][j].z, raw[0][j].w};
+        const uint32_t dn[4] = {raw[1][j].x, raw[1][j].y, raw[1][j].z, raw[1][j].w};
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const uint4 f = tiles[rt].frag[4 * j + s][lane];
+          uint32_t b0, b1;
+          const uint32_t pos[4] = {max_h2(f.x, 0u), max_h2(f.y, 0u), max_h2(f.z, 0u), max_h2(f.w, 0u)};
+          s8x4_to_f16(up[s], b0, b1);
+          mma16816(acc[0], pos, b0, b1);
+          const uint32_t neg[4] = {min_h2(f.x, 0u), min_h2(f.y, 0u), min_h2(f.z, 0u), min_h2(f.w, 0u)};
+          s8x4_to_f16(dn[s], b0, b1);
+          mma16816(acc[1], neg, b0, b1);
+        }
+      }
+      const float f0 = tiles[rt].factor[gq], f1 = tiles[rt].factor[gq + 8];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (f0 >= 0.f) best[x] = fmaxf(best[x], (acc[0][x] + acc[1][x]) * f0);
+        if (f1 >= 0.f) best[x] = fmaxf(best[x], (acc[0][2 + x] + acc[1][2 + x]) * f1);
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) best[x] = fmaxf(best[x], __shfl_xor_sync(0xffffffffu, best[x], o));
+      // column 2 t + x is block c0 + 2 t + x, whose exponent lane (2 t + x) * 4 holds
+      const int ec = __shfl_sync(0xffffffffu, e, (2 * t + x) * 4);
+      const int cc = c0 + 2 * t + x;
+      if (gq == 0 && cc < c_hi) dst[cc] = ordered(ec == kOddBlock ? INFINITY : best[x] * pow2(ec));
+    }
+  }
+  cluster.sync();
+  if (rank != 0) return;
+  // ---- the lists: forced blocks are above every score
+  for (int c = tid; c <= own; c += kThreads)
+    if (c < c_lo || c >= c_hi) keys[c] = 0xFFFFFFFFu;
+  const int total = own + 1;
+  uint32_t prefix = 0;
+  int want = a.take;                           // rank within the keys that share the prefix
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    __syncthreads();
+    hist[tid] = 0;
+    __syncthreads();
+    for (int c = tid; c < total; c += kThreads) {
+      const uint32_t k = keys[c];
+      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1);
+    }
+    __syncthreads();
+    if (warp == 0) {                           // from the highest bin down: lane owns 8 bins
+      int cnt[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        cnt[i] = hist[255 - (lane * 8 + i)];
+        sum += cnt[i];
+      }
+      int before = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
+      }
+      before -= sum;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (before < want && before + cnt[i] >= want) {
+          pick[0] = 255 - (lane * 8 + i);
+          pick[1] = want - before;
+        }
+        before += cnt[i];
+      }
+    }
+    __syncthreads();
+    prefix |= (uint32_t)pick[0] << shift;
+    want = pick[1];
+  }
+  // keys above `prefix` are in, and the first `want` equal to it; a warp takes a range
+  const int span = ((total + kWarps - 1) / kWarps + 31) & ~31;
+  const int w_lo = warp * span, w_hi = min(total, w_lo + span);
+  int above = 0, equal = 0;
+  for (int c = w_lo + lane; c < w_hi; c += 32) {
+    above += keys[c] > prefix;
+    equal += keys[c] == prefix;
+  }
+  above = __reduce_add_sync(0xffffffffu, above);
+  equal = __reduce_add_sync(0xffffffffu, equal);
+  if (lane == 0) {
+    sums[0][warp] = above;
+    sums[1][warp] = equal;
+  }
+  __syncthreads();
+  int eq_before = 0, at = 0;
+  for (int w = 0; w < warp; ++w) {
+    at += sums[0][w];
+    eq_before += sums[1][w];
+  }
+  at += min(eq_before, want);
+  for (int c = w_lo; c < w_hi; c += 32) {
+    const uint32_t k = c + lane < w_hi ? keys[c + lane] : 0u;
+    const bool is_eq = c + lane < w_hi && k == prefix;
+    const uint32_t below = (1u << lane) - 1u;
+    const uint32_t eq = __ballot_sync(0xffffffffu, is_eq);
+    const bool in = c + lane < w_hi && (k > prefix || (is_eq && eq_before + __popc(eq & below) < want));
+    const uint32_t m = __ballot_sync(0xffffffffu, in);
+    if (in) out[at + __popc(m & below)] = c + lane;
+    at += __popc(m);
+    eq_before += __popc(eq);
+  }
+}
+
+template <int D>
+size_t smem_of(int row_tiles, int max_blocks) {
+  return row_tiles * (sizeof(QTile<D>) + 16 * sizeof(int)) + (size_t)max_blocks * 4;
+}
+
+template <int D>
+cudaError_t launch(const SelectArgs &a, int64_t tokens, int num_sms, int device, cudaStream_t st) {
+  const size_t smem = smem_of<D>(a.row_tiles, a.max_blocks);
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(reinterpret_cast<const void *>(select_kernel<D>), device, kMaxSmem);
+  if (e != cudaSuccess) return e;
+  // CTAs of a cluster: while there are SMs for them, and 64 blocks for each
+  int ranks = 1;
+  while (ranks < 8 && tokens * a.hkv * ranks * 2 <= num_sms && a.max_blocks >= ranks * 2 * 64) ranks *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(tokens * ranks), (unsigned)a.hkv);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)ranks;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, select_kernel<D>, a);
+}
+
+}  // namespace
+
+attn_status_t check_sparse(const HostPlan &hp, const attn_sparse_t *s) {
+  if (!s) return ATTN_ERR_INVALID_ARG;
+  if (!block_size_ok(hp.prob, s->block_size)) return ATTN_ERR_UNSUPPORTED;
+  if (s->num_blocks < 1 || s->num_blocks > ATTN_SPARSE_MAX_TAKE || s->first_blocks < 0 || s->last_blocks < 1 ||
+      (int64_t)s->first_blocks + s->last_blocks > s->num_blocks || hp.prob.window > 0)
+    return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+int32_t longest_request(const HostPlan &hp) {
+  const int64_t slots = (int64_t)hp.prob.page_table_stride * hp.prob.page_size;
+  int32_t top = 0;
+  for (const int32_t L : hp.seq_lens) top = std::max(top, L);
+  return (int32_t)std::min<int64_t>(top, slots);
+}
+
+}  // namespace akp
+
+extern "C" attn_status_t attn_select_blocks(attn_plan_t plan, const attn_sparse_t *sparse, const void *q,
+                                            const void *bounds, const int32_t *page_table, const int32_t *seq_lens,
+                                            const int32_t *qo_indptr, int32_t *block_idx, void *stream) {
+  if (!plan || plan->device < 0) return ATTN_ERR_INVALID_ARG;
+  const akp::HostPlan &hp = plan->host;
+  const attn_problem_t &pr = hp.prob;
+  const attn_status_t ok = akp::check_sparse(hp, sparse);
+  if (ok != ATTN_OK) return ok;
+  akp::SelectArgs a{};
+  a.max_len = akp::longest_request(hp);
+  a.max_blocks = (a.max_len + sparse->block_size - 1) / sparse->block_size;
+  if (a.max_blocks > ATTN_SPARSE_MAX_BLOCKS) return ATTN_ERR_UNSUPPORTED;
+  const int64_t tokens = hp.qo_indptr.back();
+  if (tokens == 0) return ATTN_OK;
+  if (!q || !bounds || !page_table || !seq_lens || !qo_indptr || !block_idx || !akp::aligned16(q) ||
+      !akp::aligned16(bounds))
+    return ATTN_ERR_INVALID_ARG;
+  a.q = static_cast<const uint16_t *>(q);
+  a.bounds = static_cast<const uint8_t *>(bounds);
+  a.page_table = page_table;
+  a.seq_lens = seq_lens;
+  a.qo_indptr = qo_indptr;
+  a.block_idx = block_idx;
+  a.err = plan->dev.err;
+  a.batch = pr.batch;
+  a.hq = pr.num_q_heads;
+  a.hkv = pr.num_kv_heads;
+  a.group = hp.group;
+  a.row_tiles = (hp.group + 15) / 16;
+  a.page_size = pr.page_size;
+  a.pt_stride = pr.page_table_stride;
+  a.num_pages = pr.num_pages;
+  a.block = sparse->block_size;
+  a.take = sparse->num_blocks;
+  a.first = sparse->first_blocks;
+  a.last = sparse->last_blocks;
+  const size_t smem = pr.head_dim_qk == akp::kDqk ? akp::smem_of<akp::kDqk>(a.row_tiles, a.max_blocks)
+                                                  : akp::smem_of<akp::kDqkSym>(a.row_tiles, a.max_blocks);
+  if (smem > akp::kMaxSmem) return ATTN_ERR_UNSUPPORTED;
+  akp::DeviceGuard dev(plan->device);
+  if (!dev.ok) return ATTN_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = pr.head_dim_qk == akp::kDqk ? akp::launch<akp::kDqk>(a, tokens, hp.num_sms, plan->device, st)
+                                                    : akp::launch<akp::kDqkSym>(a, tokens, hp.num_sms, plan->device, st);
+  return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
+}

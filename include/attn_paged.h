@@ -336,6 +336,43 @@ attn_status_t attn_append_kv_rope(attn_plan_t plan, const attn_rope_t *rope, con
                                   float k_scale, float v_scale, void *stream);
 
 /*
+ * The rotation of attn_append_kv_mrope: positions of several axes, as tokens of
+ * images and videos have (time, height, width).
+ *   rope             cos_sin, max_pos, rot_dim, rot_offset and interleaved as above.
+ *                    rope.positions: device int32 [num_axes][total_q], contiguous, or
+ *                    NULL: every axis has the token's own position, plus
+ *                    position_delta[b] where that is given.
+ *   num_axes         1 to 4.
+ *   pair_axis_host   host uint8 [rot_dim / 2] (copied by the call): the axis that turns
+ *                    pair i, below num_axes.  Any assignment: consecutive sections,
+ *                    axes in turn, a table column used twice.
+ *   position_delta   device int32 [B], or NULL; NULL when positions are given.  With it a
+ *                    captured graph decodes behind a prompt whose images took fewer
+ *                    positions than tokens: seq_lens grows, the difference stays.
+ * Pair i of token tok uses cosine and sine i of row positions[pair_axis[i]][tok] of the
+ * table (what frequency column i has is the table's own affair).
+ */
+typedef struct {
+    attn_rope_t rope;
+    int32_t num_axes;
+    const uint8_t *pair_axis_host;
+    const int32_t *position_delta;
+} attn_mrope_t;
+
+/*
+ * attn_append_kv_rope with positions of several axes.  Arithmetic, rounding, q and
+ * q_out, bad page ids and lengths are as there; a token is skipped (bit 3) when any
+ * of its num_axes positions lies outside [0, max_pos).
+ * Errors: as attn_append_kv_rope; INVALID_ARG also for num_axes outside 1..4, a NULL
+ * pair_axis_host, an axis not below num_axes, positions together with position_delta.
+ */
+attn_status_t attn_append_kv_mrope(attn_plan_t plan, const attn_mrope_t *mrope, const void *q,
+                                   const void *k_new, const void *v_new, void *q_out,
+                                   void *k_cache, void *v_cache, const int32_t *page_table,
+                                   const int32_t *seq_lens, const int32_t *qo_indptr,
+                                   float k_scale, float v_scale, void *stream);
+
+/*
  * Read cached rows back as bf16, the values a cache of any type stands for.
  *   kv_indptr    device int32 [B+1], kv_indptr[0] = 0, non-decreasing: output
  *                rows [kv_indptr[b], kv_indptr[b+1]) are the last so many
@@ -356,6 +393,139 @@ attn_status_t attn_read_kv(attn_plan_t plan, const void *k_cache, const void *v_
                            const int32_t *page_table, const int32_t *seq_lens,
                            const int32_t *kv_indptr, int64_t rows, void *k_out, void *v_out,
                            float k_scale, float v_scale, void *stream);
+
+/*
+ * Attention over selected blocks.  A block is block_size consecutive positions
+ * [c * block_size, (c + 1) * block_size) of a request, inside one page.  A step is
+ *   attn_append_kv*      the new rows into the caches;
+ *   attn_update_bounds   bounds of the blocks that these rows complete;
+ *   attn_select_blocks   every new token's blocks, per KV head, by a cheap score;
+ *   attn_run_sparse      attention over them (instead of attn_run_paged).
+ * All four read lengths on the device, take any plan (replayable ones too) and can be
+ * captured together.
+ */
+#define ATTN_SPARSE_MAX_TAKE 256       /* num_blocks at most */
+#define ATTN_SPARSE_MAX_BLOCKS 49152   /* blocks of a request that are chosen among */
+
+/*
+ *   block_size      16, 32, 64 or 128; the plan's page_size is a multiple of it.
+ *   num_blocks      blocks per (token, KV head): 1 to ATTN_SPARSE_MAX_TAKE.
+ *   first_blocks, last_blocks   always among them: the request's first blocks, and the
+ *                   token's own block with the ones before it; last_blocks >= 1,
+ *                   first_blocks >= 0, together at most num_blocks.
+ */
+typedef struct {
+    int32_t block_size, num_blocks, first_blocks, last_blocks;
+} attn_sparse_t;
+
+/*
+ * Bytes of one block's bounds for one KV head: 400 for head_dim 192, 272 for 128.
+ * The bounds array belongs to the cache's pages, like the caches themselves:
+ * uint8 [num_pages][P / block_size][Hkv][bytes], 16-byte aligned, block c of request b
+ * at page_table[b][c * block_size / P].  A record is
+ *   int8 [head_dim]   upper codes: ceil(max_j k_j / 2^e),
+ *   int8 [head_dim]   lower codes: floor(min_j k_j / 2^e),
+ *   int8              e, the least exponent with max_j |k_j| <= 127 * 2^e (at least
+ *                     -126; 0 for a block of zeros); 127: the block holds an infinity
+ *                     or a NaN (codes 0),
+ *   zeros up to a multiple of 16,
+ * over the block's rows k_j as the cache holds them, without k_scale.  code * 2^e
+ * bounds every key of the block from above, resp. below.
+ * Errors: INVALID_ARG (bytes NULL), UNSUPPORTED (head dim).
+ */
+attn_status_t attn_bounds_row_bytes(int32_t head_dim, int32_t *bytes);
+
+/*
+ * Bounds of the blocks that cached rows complete, read from the K cache.
+ *   kv_indptr    device int32 [B+1] as for attn_read_kv: the last kv_indptr[b+1] -
+ *                kv_indptr[b] positions of request b are the new ones (qo_indptr after an
+ *                append; the lengths' prefix sums for a cache that has no bounds yet).
+ *   rows         kv_indptr[B]; rows past it set bit 2.
+ * Every block whose last position is one of them is written, from all its rows; other
+ * blocks' bounds stay.  A block that is overwritten (draft tokens rejected) is written
+ * again when it is complete again.  Positions before 0 or outside the page-table row are
+ * skipped (bit 2), page ids outside the pool likewise (bit 0).
+ * Runs on `stream`; no allocation, no synchronisation; can be captured.
+ * Errors: INVALID_ARG (also caches or bounds that are not 16-byte aligned), UNSUPPORTED
+ * (block size), CUDA.
+ */
+attn_status_t attn_update_bounds(attn_plan_t plan, int32_t block_size, const void *k_cache,
+                                 void *bounds, const int32_t *page_table,
+                                 const int32_t *seq_lens, const int32_t *kv_indptr,
+                                 int64_t rows, void *stream);
+
+/*
+ * Bounds read back as bf16 (exactly: 7 bits and an exponent).
+ *   block_indptr device int32 [B+1]: output rows [block_indptr[b], block_indptr[b+1]) are
+ *                the last so many complete blocks of request b, in order.
+ *   rows         block_indptr[B]; rows past it are written as zeros (bit 2).
+ *   out          bf16 [rows][Hkv][2][Dqk]: upper, then lower bounds; +inf and -inf for a
+ *                block that holds an infinity or a NaN.
+ * Blocks before 0 or outside the page-table row are written as zeros (bit 2), as are
+ * those of page ids outside the pool (bit 0).  Errors: as attn_update_bounds.
+ */
+attn_status_t attn_read_bounds(attn_plan_t plan, int32_t block_size, const void *bounds,
+                               const int32_t *page_table, const int32_t *seq_lens,
+                               const int32_t *block_indptr, int64_t rows, void *out,
+                               void *stream);
+
+/*
+ * The blocks that every new token attends to, one list per KV head for all query heads
+ * of its group.  For the token at position i, own block o = i / block_size, the blocks
+ * c <= o are the candidates.  The first first_blocks, and those with c > o - last_blocks,
+ * are taken; of the rest, those of the highest scores, equal ones by lowest index, up to
+ * num_blocks in all:
+ *   q^_h = the row of query head h in integers, round to nearest even of q_h / 2^(e_h),
+ *          e_h the least exponent with max |q_h| <= 127 * 2^(e_h) (in [-126, 121], 0 for
+ *          a row of zeros);
+ *   d(h, c) = sum over dims of max(q^_h * upper code, q^_h * lower code): an upper bound
+ *          on the scores of q^_h in the block;
+ *   score(c) = 2^(e_c) * max over the group's heads h of 2^(e_h - max e) * d(h, c).
+ * d is a whole number below 2^22, so that every term is exact in fp32 (short of under-
+ * or overflow, which are fp32's): equal inputs give equal lists on any plan and grid.  A
+ * block with an infinity or a NaN scores +inf.  A query head with one takes no part; with
+ * no head left all scores are equal.
+ *   bounds       of every complete block before the last_blocks of the request's last
+ *                token (only those are read).
+ *   block_idx    int32 [total_q][Hkv][num_blocks]: the list, ascending, then -1.
+ * Lengths below n_b, or above the longest of the plan's requests, are clamped (bit 2).
+ * Blocks on page ids outside the pool score as blocks of zeros (bit 0).
+ * q must be 16-byte aligned.  Runs on `stream`; no allocation, no synchronisation; can be
+ * captured.  Errors: INVALID_ARG (also a plan with window > 0), UNSUPPORTED (block
+ * size, or more than ATTN_SPARSE_MAX_BLOCKS blocks in the plan's longest request), CUDA.
+ */
+attn_status_t attn_select_blocks(attn_plan_t plan, const attn_sparse_t *sparse, const void *q,
+                                 const void *bounds, const int32_t *page_table,
+                                 const int32_t *seq_lens, const int32_t *qo_indptr,
+                                 int32_t *block_idx, void *stream);
+
+/*
+ * Attention of every new token over the blocks of its own lists: the operation at the top
+ * of this file with the visible keys j <= i whose block j / block_size is listed in
+ * block_idx[tok][g] for the head's KV head g.
+ *   block_idx    int32 [total_q][Hkv][num_blocks], as attn_select_blocks writes it or any
+ *                other choice: a list is a set, its order does not matter, an index met
+ *                twice counts once, negative entries are none.  Entries past the token's
+ *                own block are left out and set bit 4.  (sparse's first and last blocks
+ *                play no part here.)
+ *   others       as for attn_run_paged (q, out and the caches 16-byte aligned for every
+ *                cache type; any page_size that is a multiple of block_size; the plan's
+ *                window must be 0).
+ * A token whose list holds no block gets zeros and -inf (with sinks: the sink's own lse).
+ * Slots that a token does not see, invisible ones of a shared tile among them, do not
+ * reach its rows whatever they hold.  Arithmetic is that of the other kernels: bf16
+ * products for BF16 caches, fp16 with exactly scaled queries for the others, sums in
+ * fp32.  Lengths are clamped as by attn_select_blocks (bit 2); page ids outside the pool
+ * are read as rows of zeros (bit 0).  Needs no workspace.  Runs on `stream`; no
+ * allocation, no synchronisation; can be captured.
+ * Errors: INVALID_ARG, UNSUPPORTED (block size; num_pages * page_size > 2^31 - 65), CUDA.
+ */
+attn_status_t attn_run_sparse(attn_plan_t plan, const attn_sparse_t *sparse, const void *q,
+                              const void *k_cache, const void *v_cache,
+                              const int32_t *page_table, const int32_t *seq_lens,
+                              const int32_t *qo_indptr, const int32_t *block_idx,
+                              const float *sinks, float softmax_scale, float k_scale,
+                              float v_scale, void *out, float *lse_out, void *stream);
 
 /*
  * Size of the library-owned scratch used by attn_run_paged_no_workspace.
@@ -407,8 +577,9 @@ attn_status_t attn_plan_destroy(attn_plan_t plan);
  * kernel gave up after its time limit (the affected rows are not valid).
  * Bit 2: a run length outside a replayable plan's bounds (clamped), or an
  * appended or read position outside its page-table row (skipped, or read as
- * zeros).  Bit 3: a rotation position outside its table (skipped).  The workspace
- * argument is unused and may be NULL.
+ * zeros).  Bit 3: a rotation position outside its table (skipped).  Bit 4: a listed
+ * block past its token's own (left out).  The workspace argument is unused and may be
+ * NULL.
  */
 attn_status_t attn_get_device_error(attn_plan_t plan, void *workspace, int32_t *err);
 
