@@ -7,12 +7,14 @@
 // order either, and a block is always taken from all its rows when its last one arrives:
 // nothing is accumulated from step to step, and rejected drafts leave nothing behind.
 //
-// A CTA looks at a range of the new rows for one head, finds those that end a block, and
-// takes these blocks one after the other: a thread owns 8 dims of every RG-th row of the
-// block (16, 8 or 4 bytes a load), in 16-bit pairs (exact for every cache type: bf16, or
-// fp16 of E4M3 and E2M1 times its scale); the row groups meet in shared memory.  The
-// kernel reads each key once: what bounds it is memory for many blocks, and for a decode
-// step the launch and four dependent loads.
+// A warp takes one block of one head, heads of a block side by side (their rows are
+// neighbours in the cache): a lane owns 16 bytes of a row (8, 16 or 32 values) of every
+// RG-th row, in 16-bit pairs (exact for every cache type: bf16, or fp16 of E4M3 and E2M1
+// times its scale); the row groups meet by shuffle, so that nothing is shared and warps
+// never wait for one another.  Which block a warp takes follows from the requests'
+// counts of completed blocks, summed up 32 requests a step.  The kernel reads each key
+// once: what bounds it is memory for many blocks, and for a decode step the launch and a
+// chain of dependent loads.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -39,8 +41,8 @@ struct BoundsArgs {
   const int32_t *page_table, *seq_lens, *indptr;
   int32_t *err;
   uint16_t *out;                  // reading back
-  int32_t rows, rows_per_cta;     // flat rows (update: positions, reading: blocks)
-  int32_t batch, hkv, page_size, pt_stride, num_pages, block, per_page;
+  int32_t rows;                   // flat rows (update: positions, reading: blocks)
+  int32_t batch, hkv, page_size, pt_stride, num_pages, block;
 };
 
 template <int KV>
@@ -67,24 +69,37 @@ __device__ __forceinline__ float2 pair_values(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
-// Chunk ch (8 values) of a cached row as four 16-bit pairs.
+// How a warp takes rows of D values: VL values a lane (16 bytes of codes), NC lanes a
+// row, RG rows at a time.
 template <int KV, int D>
-__device__ __forceinline__ void load_chunk(const uint8_t *row, int ch, uint32_t (&w)[4]) {
-  if (KV == ATTN_KV_BF16) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(row) + ch);
-    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-  } else if (KV == ATTN_KV_FP8_E4M3) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row) + ch);
-    uint4 lo, hi;
-    e4m3x16_to_f16(make_uint4(v.x, v.y, 0u, 0u), lo, hi);
-    w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w;
-  } else {
-    const uint32_t codes = __ldg(reinterpret_cast<const uint32_t *>(row) + ch);
-    uint32_t s0, s1;
-    e4m3_scales_f16(__ldg(row + D / 2 + ch / 2), s0, s1);
-    e2m1x8_to_f16(codes, w);
+struct Rows {
+  static constexpr int VL = KV == ATTN_KV_BF16 ? 8 : KV == ATTN_KV_FP8_E4M3 ? 16 : 32, NP = VL / 2;
+  static constexpr int NC = D / VL, RG = 32 / NC;
+  // rows in flight per lane
+  static constexpr int kAhead = KV == ATTN_KV_FP4_E2M1 ? 4 : 8;
+};
+
+// A lane's piece of a row: the codes, and for 4-bit rows its two scales.
+template <int KV, int D>
+__device__ __forceinline__ void load_piece(const uint8_t *row, int ch, uint4 &raw, uint32_t &sc) {
+  raw = __ldg(reinterpret_cast<const uint4 *>(row) + ch);
+  if (KV == ATTN_KV_FP4_E2M1) sc = __ldg(reinterpret_cast<const uint16_t *>(row + D / 2) + ch);
+}
+template <int KV, int D>
+__device__ __forceinline__ void widen_piece(const uint4 raw, uint32_t sc, uint32_t (&w)[Rows<KV, D>::NP]) {
+  const uint32_t r[4] = {raw.x, raw.y, raw.z, raw.w};
+  if constexpr (KV == ATTN_KV_BF16) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = mul_f16x2(w[i], s0);
+    for (int i = 0; i < 4; ++i) w[i] = r[i];
+  } else if constexpr (KV == ATTN_KV_FP8_E4M3) {
+    uint4 lo, hi;
+    e4m3x16_to_f16(raw, lo, hi);
+    w[0] = lo.x, w[1] = lo.y, w[2] = lo.z, w[3] = lo.w, w[4] = hi.x, w[5] = hi.y, w[6] = hi.z, w[7] = hi.w;
+  } else {
+    uint4 o[4];
+    e2m1x32_to_f16(raw, sc, o);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[4 * i] = o[i].x, w[4 * i + 1] = o[i].y, w[4 * i + 2] = o[i].z, w[4 * i + 3] = o[i].w;
   }
 }
 
@@ -99,106 +114,176 @@ __device__ __forceinline__ int64_t slot_of(const BoundsArgs &a, int b, int64_t p
   return (int64_t)page * a.page_size + pos % a.page_size;
 }
 
-template <int KV, int D>
-__global__ void __launch_bounds__(kThreads) update_kernel(const BoundsArgs a) {
+// The request whose completed blocks hold block number j of all of them, and the number
+// of its block; false past the last.  All 32 lanes of a warp call it.  Blocks before
+// position 0 (a length that does not hold its rows) are none.
+__device__ __forceinline__ bool find_block(const BoundsArgs &a, int64_t j, int &b, int64_t &c, bool &odd) {
+  const int lane = threadIdx.x & 31;
+  int64_t base = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    const int r = b0 + lane;
+    int64_t first = 0, cnt = 0;
+    if (r < a.batch) {
+      const int64_t L = __ldg(a.seq_lens + r), m = (int64_t)__ldg(a.indptr + r + 1) - __ldg(a.indptr + r);
+      odd |= L < m;
+      first = max((int64_t)0, L - m) / a.block;
+      cnt = max((int64_t)0, max((int64_t)0, L) / a.block - first);
+    }
+    int64_t sum = cnt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, base + sum > j);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      b = b0 + l;
+      c = j - base - __shfl_sync(0xffffffffu, sum - cnt, l) + __shfl_sync(0xffffffffu, first, l);
+      return true;
+    }
+    base += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  return false;
+}
+
+// WIDE: the CTA's warps share a block's rows (few blocks: one round trip to memory for
+// each instead of several).
+template <int KV, int D, bool WIDE>
+__global__ void __launch_bounds__(kThreads, KV == ATTN_KV_FP4_E2M1 ? 2 : 4) update_kernel(const BoundsArgs a) {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  constexpr int NC = D / 8, RG = kThreads / NC, W = D / 2;      // chunks of a row, row groups, pairs
-  __shared__ int found;
-  __shared__ int64_t list[128];                                  // first slots of the blocks to take
-  __shared__ uint32_t part[RG][2][W];                            // [row group][hi, lo][pair]
-  __shared__ float top[kThreads / 32];
-  __shared__ int odd;                                            // an infinity or a NaN
-  const int tid = threadIdx.x, g = blockIdx.y;
-  if (tid == 0) found = 0;
-  __syncthreads();
-  const int64_t r0 = (int64_t)blockIdx.x * a.rows_per_cta;
-  if (tid < a.rows_per_cta && r0 + tid < a.rows) {
-    const int64_t row = r0 + tid;
-    const int b = request_of_row(a.indptr, a.batch, row);
+  using R = Rows<KV, D>;
+  constexpr int kWarps = kThreads / 32;
+  __shared__ uint32_t part[WIDE ? kWarps : 1][2][D / 2];         // [warp][hi, lo][pair]
+  const int lane = threadIdx.x & 31, ch = lane % R::NC, rg = lane / R::NC, warp = threadIdx.x >> 5;
+  const int64_t warps = (int64_t)gridDim.x * (WIDE ? 1 : kWarps);
+  const int64_t first_warp = WIDE ? blockIdx.x : (int64_t)blockIdx.x * kWarps + warp;
+  // rows that kv_indptr does not hold
+  if (first_warp == 0 && lane == 0 && __ldg(a.indptr + a.batch) < a.rows) atomicOr(a.err, 4);
+  for (int64_t unit = first_warp;; unit += warps) {
+    const int g = (int)(unit % a.hkv);
+    int b;
+    int64_t c;
+    bool odd_len = false;
+    const bool more = find_block(a, unit / a.hkv, b, c, odd_len);
+    if (odd_len && first_warp == 0) atomicOr(a.err, 4);
+    if (!more) break;
     int bad = 0;
-    if (b >= a.batch || row < __ldg(a.indptr)) {                 // a row that kv_indptr does not hold
-      bad = 4;
-    } else {
-      const int64_t pos = row + (int64_t)__ldg(a.seq_lens + b) - __ldg(a.indptr + b + 1);
-      if (pos < 0) {
-        bad = 4;
-      } else if ((pos + 1) % a.block == 0) {
-        const int64_t slot = slot_of(a, b, pos + 1 - a.block, bad);
-        if (slot >= 0) list[atomicAdd(&found, 1)] = slot;
-      }
+    const int64_t slot = slot_of(a, b, c * a.block, bad);
+    if (bad && g == 0 && lane == 0) atomicOr(a.err, bad);
+    if (slot < 0) continue;
+    const uint8_t *row = static_cast<const uint8_t *>(a.k_cache) + (slot * a.hkv + g) * kv_row_bytes(KV, D);
+    const int64_t step = (int64_t)a.hkv * kv_row_bytes(KV, D);
+    // every row group starts from row 0 .. RG - 1; the lanes past the last group repeat it
+    const int mine = min(rg, R::RG - 1);
+    // rows [r_lo, r_hi) are the warp's
+    const int r_lo = WIDE ? a.block / kWarps * warp : 0, r_hi = WIDE ? r_lo + a.block / kWarps : a.block;
+    uint32_t hi[R::NP], lo[R::NP];
+    {
+      uint4 raw;
+      uint32_t sc = 0u;
+      load_piece<KV, D>(row + min(r_lo + mine, r_hi - 1) * step, ch, raw, sc);
+      widen_piece<KV, D>(raw, sc, hi);
+#pragma unroll
+      for (int i = 0; i < R::NP; ++i) lo[i] = hi[i];
     }
-    if (bad) atomicOr(a.err, bad);
-  }
-  __syncthreads();
-  const int n = found;
-  for (int k = 0; k < n; ++k) {
-    const int64_t slot = list[k];
-    const int ch = tid % NC, rg = tid / NC;
-    uint32_t hi[4], lo[4];
-    if (rg < RG) {
-      const uint8_t *row = static_cast<const uint8_t *>(a.k_cache) + (slot * a.hkv + g) * kv_row_bytes(KV, D);
-      const int64_t step = (int64_t)a.hkv * kv_row_bytes(KV, D);
-      load_chunk<KV, D>(row + rg * step, ch, hi);
+#pragma unroll 1
+    for (int r0 = r_lo + mine + R::RG; r0 < r_hi; r0 += R::RG * R::kAhead) {
+      uint4 raw[R::kAhead];
+      uint32_t sc[R::kAhead];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) lo[i] = hi[i];
-#pragma unroll 4
-      for (int r = rg + RG; r < a.block; r += RG) {
-        uint32_t w[4];
-        load_chunk<KV, D>(row + r * step, ch, w);
+      for (int k = 0; k < R::kAhead; ++k) {
+        // (past the last row: that row again, which changes nothing)
+        load_piece<KV, D>(row + min(r0 + k * R::RG, r_hi - 1) * step, ch, raw[k], sc[k]);
+      }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+      for (int k = 0; k < R::kAhead; ++k) {
+        uint32_t w[R::NP];
+        widen_piece<KV, D>(raw[k], sc[k], w);
+#pragma unroll
+        for (int i = 0; i < R::NP; ++i) {
           hi[i] = max_pair<KV>(hi[i], w[i]);
           lo[i] = min_pair<KV>(lo[i], w[i]);
         }
       }
+    }
+    __syncwarp();
+    // the row groups meet in every lane
+    if (R::RG > 1) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        part[rg][0][4 * ch + i] = hi[i];
-        part[rg][1][4 * ch + i] = lo[i];
+      for (int i = 0; i < R::NP; ++i) {
+        uint32_t h = hi[i], l = lo[i];
+#pragma unroll
+        for (int k = 1; k < R::RG; ++k) {
+          const int from = (ch + R::NC * ((mine + k) % R::RG)) & 31;
+          h = max_pair<KV>(h, __shfl_sync(0xffffffffu, hi[i], from));
+          l = min_pair<KV>(l, __shfl_sync(0xffffffffu, lo[i], from));
+        }
+        hi[i] = h;
+        lo[i] = l;
       }
     }
-    if (tid == 0) odd = 0;
-    __syncthreads();
-    // thread tid: pair tid % W of hi (tid < W) or lo
-    const bool mine = tid < 2 * W;
-    float2 v = make_float2(0.f, 0.f);
-    if (mine) {
-      const int which = tid / W, w = tid % W;
-      uint32_t x = part[0][which][w];
+    if (WIDE) {
+      if (rg == 0)
 #pragma unroll
-      for (int r = 1; r < RG; ++r)
-        x = which ? min_pair<KV>(x, part[r][which][w]) : max_pair<KV>(x, part[r][which][w]);
-      v = pair_values<KV>(x);
+        for (int i = 0; i < R::NP; ++i) {
+          part[warp][0][ch * R::NP + i] = hi[i];
+          part[warp][1][ch * R::NP + i] = lo[i];
+        }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kWarps; ++k)
+#pragma unroll
+        for (int i = 0; i < R::NP; ++i) {
+          hi[i] = max_pair<KV>(hi[i], part[k][0][ch * R::NP + i]);
+          lo[i] = min_pair<KV>(lo[i], part[k][1][ch * R::NP + i]);
+        }
+      __syncthreads();
+      if (warp) continue;
     }
-    float t = fmaxf(fabsf(v.x), fabsf(v.y));
-    if (!(fabsf(v.x) < INFINITY) || !(fabsf(v.y) < INFINITY)) odd = 1;
+    float t = 0.f;
+    bool odd = false;                              // an infinity or a NaN
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-    if ((tid & 31) == 0) top[tid >> 5] = t;
-    __syncthreads();
-    float amax = top[0];
+    for (int i = 0; i < R::NP; ++i) {
+      const float2 x = pair_values<KV>(hi[i]), y = pair_values<KV>(lo[i]);
+      odd |= !(fabsf(x.x) < INFINITY) | !(fabsf(x.y) < INFINITY) | !(fabsf(y.x) < INFINITY) | !(fabsf(y.y) < INFINITY);
+      t = fmaxf(fmaxf(t, fmaxf(fabsf(x.x), fabsf(x.y))), fmaxf(fabsf(y.x), fabsf(y.y)));
+    }
+    odd = __any_sync(0xffffffffu, odd);
+    t = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(t)));      // (not negative)
+    const int e = odd ? kOddBlock : code_exponent(t);
+    uint8_t *rec = a.bounds + (slot / a.block * a.hkv + g) * bounds_row_bytes(D);   // pages hold whole blocks
+    if (rg == 0) {
+      const float unit_e = pow2(-e);
 #pragma unroll
-    for (int i = 1; i < kThreads / 32; ++i) amax = fmaxf(amax, top[i]);
-    const int e = odd ? kOddBlock : code_exponent(amax);
-    const int64_t entry = slot / a.block;        // pages hold whole blocks, in order
-    uint8_t *rec = a.bounds + (entry * a.hkv + g) * bounds_row_bytes(D);
-    if (mine) {
-      const int which = tid / W, w = tid % W;
-      const float unit = pow2(-e);
-      uint32_t codes = 0;
+      for (int which = 0; which < 2; ++which) {
+        uint32_t words[R::VL / 4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float x = i ? v.y : v.x;
-        // (a product that underflows keeps its side of zero)
-        int c = which ? min((int)floorf(x * unit), x < 0.f ? -1 : 127) : max((int)ceilf(x * unit), x > 0.f ? 1 : -127);
-        if (e == kOddBlock) c = 0;
-        codes |= (uint32_t)(c & 0xFF) << (8 * i);
+        for (int i = 0; i < R::VL / 4; ++i) {
+          words[i] = 0u;
+#pragma unroll
+          for (int p = 0; p < 4; ++p) {
+            const float2 v = pair_values<KV>(which ? lo[2 * i + p / 2] : hi[2 * i + p / 2]);
+            const float x = p & 1 ? v.y : v.x;
+            // 1.5 * 2^23 + x / 2^e rounded outwards once: the low byte is the code
+            const float y = which ? __fmaf_rd(x, unit_e, 12582912.f) : __fmaf_ru(x, unit_e, 12582912.f);
+            words[i] |= (__float_as_uint(y) & 0xFFu) << (8 * p);
+          }
+          if (odd) words[i] = 0u;
+        }
+        uint8_t *dst = rec + which * D + ch * R::VL;
+        if constexpr (R::VL == 8) {
+          *reinterpret_cast<uint2 *>(dst) = make_uint2(words[0], words[1]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < R::VL / 16; ++i)
+            reinterpret_cast<uint4 *>(dst)[i] =
+                make_uint4(words[4 * i], words[4 * i + 1], words[4 * i + 2], words[4 * i + 3]);
+        }
       }
-      reinterpret_cast<uint16_t *>(rec + which * D)[w] = (uint16_t)codes;
+      if (ch == 0) *reinterpret_cast<uint4 *>(rec + 2 * D) = make_uint4((uint32_t)(e & 0xFF), 0u, 0u, 0u);
     }
-    if (tid == 0) *reinterpret_cast<uint4 *>(rec + 2 * D) = make_uint4((uint32_t)(e & 0xFF), 0u, 0u, 0u);
-    __syncthreads();
   }
 }
 
@@ -266,11 +351,21 @@ BoundsArgs make_args(attn_plan_t plan, int32_t block_size, const int32_t *page_t
 }
 
 template <int D>
-cudaError_t launch_update(const BoundsArgs &a, int kv, dim3 grid, cudaStream_t st) {
+cudaError_t launch_update(const BoundsArgs &a, int kv, int64_t most, int num_sms, cudaStream_t st) {
+  // a warp a block and head; where there are SMs for it, a CTA
+  const int64_t per = kThreads / 32, room = (int64_t)num_sms * 4;
+  const bool wide = most <= room;
+  const dim3 grid((unsigned)std::min(wide ? most : (most + per - 1) / per, room)), block(kThreads);
   switch (kv) {
-    case ATTN_KV_BF16: return launch_dependent(update_kernel<ATTN_KV_BF16, D>, grid, dim3(kThreads), 0, st, a);
-    case ATTN_KV_FP8_E4M3: return launch_dependent(update_kernel<ATTN_KV_FP8_E4M3, D>, grid, dim3(kThreads), 0, st, a);
-    default: return launch_dependent(update_kernel<ATTN_KV_FP4_E2M1, D>, grid, dim3(kThreads), 0, st, a);
+    case ATTN_KV_BF16: 
+      return wide ? launch_dependent(update_kernel<ATTN_KV_BF16, D, true>, grid, block, 0, st, a)
+                  : launch_dependent(update_kernel<ATTN_KV_BF16, D, false>, grid, block, 0, st, a);
+    case ATTN_KV_FP8_E4M3: 
+      return wide ? launch_dependent(update_kernel<ATTN_KV_FP8_E4M3, D, true>, grid, block, 0, st, a)
+                  : launch_dependent(update_kernel<ATTN_KV_FP8_E4M3, D, false>, grid, block, 0, st, a);
+    default: 
+      return wide ? launch_dependent(update_kernel<ATTN_KV_FP4_E2M1, D, true>, grid, block, 0, st, a)
+                  : launch_dependent(update_kernel<ATTN_KV_FP4_E2M1, D, false>, grid, block, 0, st, a);
   }
 }
 
@@ -297,16 +392,13 @@ extern "C" attn_status_t attn_update_bounds(attn_plan_t plan, int32_t block_size
   akp::BoundsArgs a = akp::make_args(plan, block_size, page_table, seq_lens, kv_indptr, rows);
   a.k_cache = k_cache;
   a.bounds = static_cast<uint8_t *>(bounds);
-  // Rows a CTA looks at: at most a block's, so that the rows of one request end one
-  // block at most, and few enough to give every SM four CTAs.
-  const int64_t want = (int64_t)plan->host.num_sms * 4;
-  a.rows_per_cta = (int32_t)std::max<int64_t>(1, std::min<int64_t>(block_size, rows * pr.num_kv_heads / want));
-  const dim3 grid((unsigned)((rows + a.rows_per_cta - 1) / a.rows_per_cta), (unsigned)pr.num_kv_heads);
+  // blocks that the rows can complete, at most
+  const int64_t most = (rows / block_size + pr.batch) * pr.num_kv_heads;
   akp::DeviceGuard dev(plan->device);
   if (!dev.ok) return ATTN_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = pr.head_dim_qk == akp::kDqk ? akp::launch_update<akp::kDqk>(a, pr.kv_dtype, grid, st)
-                                                    : akp::launch_update<akp::kDqkSym>(a, pr.kv_dtype, grid, st);
+  const cudaError_t e = pr.head_dim_qk == akp::kDqk ? akp::launch_update<akp::kDqk>(a, pr.kv_dtype, most, plan->host.num_sms, st)
+                                                    : akp::launch_update<akp::kDqkSym>(a, pr.kv_dtype, most, plan->host.num_sms, st);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }
 
