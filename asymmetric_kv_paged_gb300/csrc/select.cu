@@ -27,7 +27,7 @@
 #include "kernels.hpp"
 #include "plan.hpp"
 #include "requests.cuh"
-#include "sparse.cuh"
+#include "select.cuh"
 
 namespace akp {
 namespace {
@@ -36,15 +36,6 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxSmem = 224 * 1024;
-
-struct SelectArgs {
-  const uint16_t *q;
-  const uint8_t *bounds;
-  const int32_t *page_table, *seq_lens, *qo_indptr;
-  int32_t *block_idx, *err;
-  int32_t batch, hq, hkv, group, row_tiles, page_size, pt_stride, num_pages;
-  int32_t block, take, first, last, max_len, max_blocks;
-};
 
 // c (16 x 8, fp32) += a (16 x 16, fp16) . b (16 x 8, fp16)
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -64,24 +55,6 @@ __device__ __forceinline__ uint32_t min_h2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("min.f16x2 %0, %1, %2;\n" : "=r"(d) : "r"(a), "r"(b));
   return d;
-}
-
-// Four signed bytes -> four fp16 values: with the sign bit flipped, byte u = v + 128 is
-// the low byte of fp16 1024 + u.
-__device__ __forceinline__ void s8x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
-  w ^= 0x80808080u;
-  const __half2 bias = __half2half2(__ushort_as_half(0x6480));      // 1152
-  uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
-  const __half2 x = __hsub2(*reinterpret_cast<__half2 *>(&a), bias);
-  const __half2 y = __hsub2(*reinterpret_cast<__half2 *>(&b), bias);
-  lo = *reinterpret_cast<const uint32_t *>(&x);
-  hi = *reinterpret_cast<const uint32_t *>(&y);
-}
-
-// fp32 -> an unsigned integer of the same order
-__device__ __forceinline__ uint32_t ordered(float x) {
-  const uint32_t u = __float_as_uint(x + 0.f);
-  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 template <int D>
@@ -409,6 +382,9 @@ extern "C" attn_status_t attn_select_blocks(attn_plan_t plan, const attn_sparse_
   akp::DeviceGuard dev(plan->device);
   if (!dev.ok) return ATTN_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  a.tokens = (int32_t)tokens;
+  if (akp::select_tc_fits(hp, a))
+    return akp::launch_select_tc(hp, a, plan->device, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
   const cudaError_t e = pr.head_dim_qk == akp::kDqk ? akp::launch<akp::kDqk>(a, tokens, hp.num_sms, plan->device, st)
                                                     : akp::launch<akp::kDqkSym>(a, tokens, hp.num_sms, plan->device, st);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;

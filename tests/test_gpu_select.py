@@ -58,6 +58,14 @@ CASES = [
     ([1000] * 300, [1] * 300, 16, 1, 64, 128, 64, 6, 1, 2),       # one CTA a token
     ([1500, 31, 800], [200, 31, 77], 16, 1, 32, 192, 32, 12, 1, 2),
     ([1100], [530], 32, 2, 16, 128, 16, 20, 0, 3),
+    # chunks of tokens: token tiles of 8, 4, 2, 1, 32, 128 tokens; lists that take all; several block tiles
+    ([5000], [700], 16, 1, 64, 192, 16, 30, 2, 2),
+    ([900, 700, 64, 1], [300, 411, 64, 1], 64, 2, 32, 192, 16, 9, 1, 1),
+    ([700], [333], 50, 1, 16, 128, 16, 9, 0, 1),
+    ([600], [333], 96, 1, 16, 192, 16, 9, 1, 2),
+    ([2100], [500], 12, 3, 48, 128, 16, 11, 1, 1),
+    ([600, 2500], [150, 600], 3, 3, 64, 192, 16, 25, 1, 3),
+    ([400], [390], 16, 2, 64, 192, 64, 7, 1, 1),
 ]
 
 
@@ -71,26 +79,28 @@ def test_lists(seq, n, hq, hkv, P, dqk, block, take, first, last):
     assert np.array_equal(got, P_.select(w, w.q, bounds, block, take, first, last))
 
 
-def test_scores_are_exact_at_the_codes_ends():
+@pytest.mark.parametrize("n", [2, 400])
+def test_scores_are_exact_at_the_codes_ends(n):
     """Every product at its largest: 192 * 127 * 127 in magnitude, apart by single units."""
-    w, dw = setup([4000], [2], 16, 1, 64)
+    w, dw = setup([4000], [n], 16, 1, 64)
     rng = np.random.default_rng(1)
     bounds = random_bounds(rng, w, 64).view(np.int8)
     bounds[..., :384] = rng.choice([-127, 126, 127], bounds.shape[:-1] + (384,))
     bounds[..., 192:384] = np.minimum(bounds[..., :192], bounds[..., 192:384])
     bounds[..., 384] = 0
-    q = W.bf16_bits(np.where(rng.random((2, 16, 192)) < 0.5, -127.0, 127.0).astype(np.float32))
+    q = W.bf16_bits(np.where(rng.random((n, 16, 192)) < 0.5, -127.0, 127.0).astype(np.float32))
     got = run(w, dw, q, bounds.view(np.uint8), 64, 9, 1, 1)
     assert np.array_equal(got, P_.select(w, q, bounds.view(np.uint8), 64, 9, 1, 1))
 
 
-def test_ties_take_the_lowest_index():
-    w, dw = setup([4000, 4000], [1, 3], 16, 2, 64)
+@pytest.mark.parametrize("n", [1, 200])
+def test_ties_take_the_lowest_index(n):
+    w, dw = setup([4096, 4096], [n, 3 * n], 16, 2, 64)
     bounds = random_bounds(np.random.default_rng(1), w, 64, spread=2)
     bounds[...] = bounds[:1]                                      # every block alike
     got = run(w, dw, w.q, bounds, 64, 10, 1, 2)
-    want = np.array([0, 1, 2, 3, 4, 5, 6, 7, 61, 62], np.int32)
-    assert (got == want).all()
+    assert np.array_equal(got, P_.select(w, w.q, bounds, 64, 10, 1, 2))
+    assert got[-1, 0].tolist() == [0, 1, 2, 3, 4, 5, 6, 7, 62, 63]
     few = bounds.view(np.int8).copy()                             # two values only, heads of zeros too
     few[::3, ..., 384] += 1
     q = w.q.copy()
@@ -99,8 +109,9 @@ def test_ties_take_the_lowest_index():
                           P_.select(w, q, few.view(np.uint8), 64, 10, 1, 2))
 
 
-def test_odd_blocks_and_odd_queries():
-    w, dw = setup([3000, 3000], [2, 1], 16, 2, 64)
+@pytest.mark.parametrize("n", [1, 120])
+def test_odd_blocks_and_odd_queries(n):
+    w, dw = setup([3000, 3000], [2 * n, n], 16, 2, 64)
     rng = np.random.default_rng(9)
     bounds = random_bounds(rng, w, 64).view(np.int8)
     for page in rng.choice(w.num_pages, w.num_pages // 4, replace=False):
