@@ -23,9 +23,10 @@ INCLUDE = os.path.join(ROOT, "include")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "attn_tc.cu", "attn_fp4.cu", "attn_prefill.cu", "merge.cu", "replan.cu", "no_workspace.cu", "kv_append.cu",
            "kv_stage.cu", "kv_rope.cu", "kv_bounds.cu", "select.cu", "select_tc.cu", "attn_sparse.cu",
+           "attn_sparse_tc.cu",
            "tc_selftest.cu", "planner.cpp"]
 HEADERS = ["plan.hpp", "replan.hpp", "kernels.hpp", "tc_common.cuh", "e4m3.cuh", "e2m1.cuh", "fp4_nan.cuh",
-           "requests.cuh", "sparse.cuh", "select.cuh", "stamps.cuh"]
+           "requests.cuh", "sparse.cuh", "select.cuh", "sparse_attn.cuh", "stamps.cuh"]
 
 
 def build_dir(stamps: bool = False) -> str:

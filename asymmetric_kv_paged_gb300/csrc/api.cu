@@ -15,6 +15,7 @@
 #include "kernels.hpp"
 #include "plan.hpp"
 #include "replan.hpp"
+#include "sparse_attn.cuh"
 
 namespace {
 
@@ -75,7 +76,10 @@ attn_status_t upload(attn_plan_s *p) {
   const size_t r_bytes = hp.replayable ? align256(hp.seq_lens.size() * sizeof(int32_t)) +
                                              2 * align256((hp.blocks.size() + 1) * sizeof(int32_t))
                                        : 0;
-  const size_t total = b_bytes + s_bytes + c_bytes + m_bytes + e_bytes + r_bytes + h_bytes + u_bytes + n_bytes;
+  const int64_t jobs = akp::sparse_jobs(hp);
+  const size_t j_bytes = jobs <= INT32_MAX ? align256((size_t)jobs * sizeof(int32_t)) : 0;
+  const size_t total =
+      b_bytes + s_bytes + c_bytes + m_bytes + e_bytes + r_bytes + h_bytes + u_bytes + j_bytes + n_bytes;
   uint8_t *base = nullptr;
   if (cudaMalloc(&base, total) != cudaSuccess) return ATTN_ERR_CUDA;
   p->dev.blocks = reinterpret_cast<akp::BlockDesc *>(base);
@@ -89,6 +93,7 @@ attn_status_t upload(attn_plan_s *p) {
     p->dev.stage_units = reinterpret_cast<akp::StageUnit *>(base + b_bytes + s_bytes + c_bytes +
                                                             m_bytes + e_bytes + r_bytes + h_bytes);
   if (n_bytes) p->dev.stage_nan = base + total - n_bytes;
+  if (j_bytes) p->dev.sparse_redo = reinterpret_cast<int32_t *>(base + total - n_bytes - j_bytes);
   if (hp.replayable) {
     uint8_t *r = base + b_bytes + s_bytes + c_bytes + m_bytes + e_bytes;
     p->dev.seq_bounds = reinterpret_cast<int32_t *>(r);

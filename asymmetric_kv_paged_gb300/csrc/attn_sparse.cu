@@ -18,6 +18,7 @@
 //   SHARED  eight neighbouring units, a warp each.  The loader merges their lists in
 //           ascending order, so that a block that several of them chose is fetched
 //           once; a warp skips the tiles that its unit has not chosen.
+//   REDO    the same for the jobs that attn_sparse_tc.cu has marked.
 //   SPLIT   (few units: decode, verify) one unit for all eight warps, each taking half
 //           of every fourth tile; a cluster of up to eight CTAs shares out the list.
 //           The warps' partial results meet in shared memory, the CTAs' through
@@ -46,7 +47,7 @@
 #include "e2m1.cuh"
 #include "kernels.hpp"
 #include "requests.cuh"
-#include "sparse.cuh"
+#include "sparse_attn.cuh"
 #include "tc_common.cuh"
 
 namespace akp {
@@ -60,21 +61,8 @@ constexpr int kRows = 16;                      // query rows of a unit
 constexpr int kTile = 64;                      // keys of a tile
 constexpr int kHalf = 32;                      // keys a warp takes at a time
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrow = 8.0f;                  // base-2 growth of a maximum before O is rescaled
 constexpr int kStride = 132;                   // floats per row of the partial results
-
-struct SparseArgs {
-  const uint16_t *q;
-  const int32_t *page_table, *seq_lens, *qo_indptr, *block_idx;
-  const float *sinks;
-  uint16_t *out;
-  float *lse;
-  int32_t *err;
-  float scale_log2, v_scale;
-  int32_t batch, hq, hkv, group, row_tiles, page_size, pt_stride, num_pages;
-  int32_t tokens, block, take, max_len;
-};
 
 template <int KV, int DQK>
 struct Tile {
@@ -420,21 +408,6 @@ struct Unit {
   }
 };
 
-// What a row's maximum and sum make of its output: the factor of O and the natural
-// log-sum-exp; sink2 in base 2.
-__device__ __forceinline__ float finish(float m, float l, float lift, float sink2, float v_scale, float &lse) {
-  const float lse2 = l == 0.f ? -INFINITY : m + log2f(l) - lift;
-  float f = l == 0.f ? 0.f : v_scale / l;
-  const float M = fmaxf(lse2, sink2);
-  lse = lse2 * kLn2;
-  if (sink2 != -INFINITY) {
-    const float w = exp2f(lse2 - M), Z = w + exp2f(sink2 - M);
-    f *= w / Z;
-    lse = (M + log2f(Z)) * kLn2;
-  }
-  return f;
-}
-
 // A unit's list as ascending blocks and the slots they start at (whole pool: a page id
 // outside it).  All 32 lanes of a warp call it; returns the number of blocks.
 __device__ __forceinline__ int prepare_list(const SparseArgs &a, const int32_t *idx, int b, int own, int32_t *list,
@@ -511,8 +484,11 @@ __device__ __forceinline__ int prepare_list(const SparseArgs &a, const int32_t *
   return cnt;
 }
 
-template <int KV, int DQK, bool SPLIT>
+enum { kShared = 0, kSplit = 1, kRedo = 2 };     // kRedo: the marked jobs of attn_sparse_tc.cu, as kShared
+
+template <int KV, int DQK, int MODE>
 __global__ void __launch_bounds__(kThreads, 1) sparse_kernel(const SparseArgs a, const __grid_constant__ TmaMaps maps) {
+  constexpr bool SPLIT = MODE == kSplit;
   using T = Tile<KV, DQK>;
   using U = Unit<KV, DQK>;
   constexpr int kUnits = SPLIT ? 1 : kWarps, kStages = T::kStages;
@@ -521,21 +497,46 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_kernel(const SparseArgs a,
   int32_t *lists = reinterpret_cast<int32_t *>(ring + T::kRing);       // [units][take] blocks, then slots
   __shared__ Shared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gq = lane >> 2, t = lane & 3;
-  const int g = blockIdx.y;
   const int ranks = SPLIT ? (int)cg::this_cluster().num_blocks() : 1;
   const int rank = SPLIT ? (int)cg::this_cluster().block_rank() : 0;
-  const int unit0 = SPLIT ? (int)blockIdx.x / ranks : (int)blockIdx.x * kWarps;
-  const int total_units = a.tokens * a.row_tiles;
+  int g = blockIdx.y;
+  int unit0 = SPLIT ? (int)blockIdx.x / ranks : (int)blockIdx.x * kWarps;
+  int total_units = a.tokens * a.row_tiles;
+  if (tid == 0) sh.abort = 0;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  int job = (int)blockIdx.x - (int)gridDim.x, job_left = 0;
+  for (bool again = false;; again = true) {
+  if (MODE != kRedo && again) break;
+  if (MODE == kRedo) {                       // the next eight units of a marked job
+    unit0 += kWarps;
+    while (--job_left < 0) {
+      for (job += gridDim.x; job < a.jobs && !__ldcg(a.redo + job);) job += gridDim.x;
+      if (job >= a.jobs) return;
+      SparseJob x;
+      if (!find_job(a, job, x, false)) continue;
+      g = x.g;
+      unit0 = x.tok0 * a.row_tiles;
+      total_units = (x.tok0 + x.ntok) * a.row_tiles;
+      job_left = (total_units - unit0 + kWarps - 1) / kWarps;
+    }
+    if (again) {
+      __syncthreads();
+      if (sh.abort) return;
+      if (tid == 0)
+        for (int s = 0; s < kStages; ++s) {
+          asm volatile("mbarrier.inval.shared::cta.b64 [%0];\n" ::"r"(tc::smem_u32(&sh.full[s])) : "memory");
+          asm volatile("mbarrier.inval.shared::cta.b64 [%0];\n" ::"r"(tc::smem_u32(&sh.empty[s])) : "memory");
+        }
+    }
+  }
   if (tid == 0) {
-    sh.abort = 0;
     for (int s = 0; s < kStages; ++s) {
       tc::mbar_init(&sh.full[s], 1);
       tc::mbar_init(&sh.empty[s], kWarps);
     }
     tc::fence_mbar_init();
   }
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   // ---- the units: their lists, their query rows
   U u;
   const int unit = SPLIT ? unit0 : unit0 + warp;
@@ -794,20 +795,23 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_kernel(const SparseArgs a,
     cluster.sync();                                   // (no CTA leaves while another reads from it)
   }
   if (tid == 0 && sh.abort) atomicOr(a.err, 2);
+  }
 }
 
-template <int KV, int DQK, bool SPLIT>
-cudaError_t launch_one(const SparseArgs &a, const TmaMaps &maps, int ranks, int device, cudaStream_t st) {
+template <int KV, int DQK, int MODE>
+cudaError_t launch_one(const SparseArgs &a, const TmaMaps &maps, int ranks, int num_sms, int device, cudaStream_t st) {
+  constexpr bool SPLIT = MODE == kSplit;
   using T = Tile<KV, DQK>;
   const size_t smem = 1024 + T::kRing + (size_t)(SPLIT ? 1 : kWarps) * a.take * 8;
-  auto kernel = sparse_kernel<KV, DQK, SPLIT>;
+  auto kernel = sparse_kernel<KV, DQK, MODE>;
   static SmemLimit limit;
   const cudaError_t e = limit.raise(reinterpret_cast<const void *>(kernel), device,
                                     1024 + T::kRing + (SPLIT ? 1 : kWarps) * ATTN_SPARSE_MAX_TAKE * 8);
   if (e != cudaSuccess) return e;
   const int units = a.tokens * a.row_tiles;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(SPLIT ? units * ranks : (units + kWarps - 1) / kWarps), (unsigned)a.hkv);
+  cfg.gridDim = MODE == kRedo ? dim3((unsigned)std::min(a.jobs, num_sms))
+                              : dim3((unsigned)(SPLIT ? units * ranks : (units + kWarps - 1) / kWarps), (unsigned)a.hkv);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -824,23 +828,31 @@ cudaError_t launch_one(const SparseArgs &a, const TmaMaps &maps, int ranks, int 
 }
 
 template <int KV, int DQK>
-cudaError_t launch_kv(const SparseArgs &a, const TmaMaps &maps, int num_sms, int device, cudaStream_t st) {
-  // One unit a CTA while that leaves no SM with two of them; its list over as many CTAs
-  // as there are SMs for (up to eight, with two tiles for each).
+cudaError_t launch_kv(const HostPlan &hp, const SparseArgs &a, const TmaMaps &maps, int device, cudaStream_t st) {
+  // One unit a CTA while that leaves no SM with more than four of them; its list over as
+  // many CTAs as there are SMs for (up to eight, with two tiles for each).
+  const int num_sms = hp.num_sms;
   const int64_t units = (int64_t)a.tokens * a.row_tiles * a.hkv;
-  if (units > 4 * num_sms) return launch_one<KV, DQK, false>(a, maps, 1, device, st);
+  if (units > 4 * num_sms) {
+    // chunks: jobs at least half full
+    if (a.redo && (int64_t)a.tokens * a.hkv * 2 >= (int64_t)a.jobs * a.job_tokens) {
+      const cudaError_t e = launch_sparse_tc(hp, a, maps, device, st);
+      return e != cudaSuccess ? e : launch_one<KV, DQK, kRedo>(a, maps, 1, num_sms, device, st);
+    }
+    return launch_one<KV, DQK, kShared>(a, maps, 1, num_sms, device, st);
+  }
   const int tiles = (int)((int64_t)a.take * a.block / kTile);
   int ranks = 1;
   while (ranks < 8 && units * ranks * 2 <= num_sms && ranks * 4 <= tiles) ranks *= 2;
-  return launch_one<KV, DQK, true>(a, maps, ranks, device, st);
+  return launch_one<KV, DQK, kSplit>(a, maps, ranks, num_sms, device, st);
 }
 
 template <int DQK>
-cudaError_t launch(int kv, const SparseArgs &a, const TmaMaps &maps, int num_sms, int device, cudaStream_t st) {
-  switch (kv) {
-    case ATTN_KV_BF16: return launch_kv<ATTN_KV_BF16, DQK>(a, maps, num_sms, device, st);
-    case ATTN_KV_FP8_E4M3: return launch_kv<ATTN_KV_FP8_E4M3, DQK>(a, maps, num_sms, device, st);
-    default: return launch_kv<ATTN_KV_FP4_E2M1, DQK>(a, maps, num_sms, device, st);
+cudaError_t launch(const HostPlan &hp, const SparseArgs &a, const TmaMaps &maps, int device, cudaStream_t st) {
+  switch (hp.prob.kv_dtype) {
+    case ATTN_KV_BF16: return launch_kv<ATTN_KV_BF16, DQK>(hp, a, maps, device, st);
+    case ATTN_KV_FP8_E4M3: return launch_kv<ATTN_KV_FP8_E4M3, DQK>(hp, a, maps, device, st);
+    default: return launch_kv<ATTN_KV_FP4_E2M1, DQK>(hp, a, maps, device, st);
   }
 }
 
@@ -870,6 +882,8 @@ extern "C" attn_status_t attn_run_sparse(attn_plan_t plan, const attn_sparse_t *
     return ATTN_ERR_INVALID_ARG;
   akp::SparseArgs a{};
   a.q = static_cast<const uint16_t *>(q);
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
   a.page_table = page_table;
   a.seq_lens = seq_lens;
   a.qo_indptr = qo_indptr;
@@ -893,6 +907,9 @@ extern "C" attn_status_t attn_run_sparse(attn_plan_t plan, const attn_sparse_t *
   a.block = sparse->block_size;
   a.take = sparse->num_blocks;
   a.max_len = akp::longest_request(hp);
+  a.job_tokens = akp::sparse_job_tokens(hp.group);
+  a.jobs = plan->dev.sparse_redo ? (int32_t)akp::sparse_jobs(hp) : 0;
+  a.redo = plan->dev.sparse_redo;
   const int box = std::min(sparse->block_size, akp::kTile);
   akp::TmaMaps maps{};
   if (!akp::make_cache_map(&maps.k, k_cache, raw ? akp::kv_row_bytes(pr.kv_dtype, pr.head_dim_qk) : 0, pr.head_dim_qk,
@@ -904,7 +921,7 @@ extern "C" attn_status_t attn_run_sparse(attn_plan_t plan, const attn_sparse_t *
   if (!dev.ok) return ATTN_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = pr.head_dim_qk == akp::kDqk
-                            ? akp::launch<akp::kDqk>(pr.kv_dtype, a, maps, hp.num_sms, plan->device, st)
-                            : akp::launch<akp::kDqkSym>(pr.kv_dtype, a, maps, hp.num_sms, plan->device, st);
+                            ? akp::launch<akp::kDqk>(hp, a, maps, plan->device, st)
+                            : akp::launch<akp::kDqkSym>(hp, a, maps, plan->device, st);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }

@@ -115,6 +115,7 @@ struct DevicePlan {
   MergeItem *merge_items = nullptr;
   StageUnit *stage_units = nullptr;
   uint8_t *stage_nan = nullptr;    // 4-bit prefill plans: written by each run's staging pass
+  int32_t *sparse_redo = nullptr;  // written by each run over selected blocks (sparse_attn.cuh)
   int32_t *err = nullptr;  // device error word
   // replayable plans only
   int32_t *seq_bounds = nullptr;   // [B]

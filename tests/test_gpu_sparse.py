@@ -69,6 +69,16 @@ CASES = [
     ("bf16", 192, [9000], [1], 128, 1, 64, 64, 140, False),        # a long list over a cluster
     ("fp8", 192, [4096], [2], 5, 1, 16, 16, 256, False),
     ("bf16", 192, [300] * 90, [3] * 90, 16, 2, 32, 32, 5, False),
+    # many requests of a token each, and a group of more rows than a tile: a warp a unit
+    ("bf16", 192, [200 + i for i in range(330)], [1] * 330, 16, 2, 64, 64, 3, True),
+    ("fp4", 128, [90 + i for i in range(700)], [1] * 700, 4, 1, 16, 16, 4, False),
+    ("fp8", 192, [400], [120], 130, 1, 64, 64, 3, False),
+    # several tiles of tokens, lists of every length, small blocks side by side in a tile
+    ("bf16", 192, [1500], [700], 16, 1, 16, 16, 40, True),
+    ("bf16", 128, [800, 650], [400, 600], 3, 1, 32, 32, 9, False),
+    ("fp8", 192, [1200], [900], 96, 1, 128, 128, 4, True),
+    ("fp4", 192, [900], [640], 1, 1, 64, 64, 6, False),
+    ("bf16", 192, [2000], [700], 2, 2, 64, 64, 20, False),
 ]
 
 
