@@ -1,24 +1,33 @@
 // attn_run_sparse for chunks of tokens, on tcgen05: neighbouring tokens together over the
 // union of their blocks.
 //
-// Neighbouring queries choose much the same blocks.  A CTA takes up to 2 x (128 / G)
-// consecutive tokens of one request and KV head as two Q tiles of 128 rows (token-major,
-// G heads a token), walks through the union of their lists in ascending order, 128 keys
-// a tile (two blocks of 64, one of 128, or four or eight smaller ones), and leaves out of
-// each row's softmax the blocks that its token did not list: their weights are zeros.  A
-// Q tile none of whose tokens listed a tile's blocks skips the tile.  What is multiplied
-// in vain is bounded by what has to be loaded anyway: a tile's 80 KB take about as long
-// from L2 as one Q tile's products with it.
+// Neighbouring queries choose much the same blocks.  A CTA takes up to 128 / G consecutive
+// tokens of one request and KV head as a Q tile of 128 rows (token-major, G heads a
+// token), walks through the union of their lists in ascending order, 128 keys a tile (two
+// blocks of 64, one of 128, or four or eight smaller ones), and leaves out of each row's
+// softmax the blocks that its token did not list: their weights are zeros.  What is
+// multiplied in vain is bounded by what has to be loaded anyway: a tile's 80 KB take
+// about as long from L2 as the Q tile's products with it.
 //
-// Roles, TMEM and the tile pipeline are those of attn_prefill.cu (512 threads):
-//   warps 0-3, 4-7  softmax and epilogue of Q tile 0 / 1 (row p in TMEM lane p)
-//   warps 8-11      Q rows; K and V tiles: TMA boxes of the paged cache (bf16), or rows
-//                   read by a thread per key, widened to fp16 and stored (8 and 4 bits)
-//   warps 12, 13    one thread each issues the MMAs of Q tile 0 / 1
-//   warp  14        merges the lists (a token a lane, four in turn) and looks the pages
-//                   up, some tiles ahead; a tile's blocks and who listed them go through
-//                   a ring of descriptors
-//   warp  15        completes the warpgroup
+// One chain S = Q.K^T, softmax, O += P.V spends most of its time waiting for its own parts.
+// Two chains share the Q tile: tile k belongs to chain k % 2, which has K and V buffers, S,
+// O and running maxima and sums of its own (the TMEM is full: 2 x 128 columns of S, 2 x 128
+// of O); at the end the two are merged, each chain's warps writing half the columns.  (Two
+// Q tiles of 128 rows on one chain each, over the union of all 256 rows' blocks as in
+// attn_prefill.cu, took 531 us on the case below: 96 KB of Q leave no room for the tiles
+// that only one of the two needs.)
+//
+// Roles (640 threads; the tile pipeline is that of attn_prefill.cu):
+//   warps 0-3, 4-7  Q rows, then softmax and epilogue of chain 0 / 1 (row p in TMEM lane p)
+//   warps 8-11      widen the K tiles of 8- and 4-bit caches to fp16, in place (the raw rows
+//                   arrive in the operand's own buffer, which they fill a half or a quarter)
+//   warps 12-15     the same for V tiles; zeros behind the request's end; whether the lists are
+//                   ascending
+//   warps 16, 17    one thread each issues the MMAs of chain 0 / 1
+//   warp  18        merges the lists (a token a lane, two in turn) and looks the pages up,
+//                   some tiles ahead; a tile's blocks and who listed them go through a ring
+//                   of descriptors
+//   warp  19        issues the tiles' TMA boxes (of the paged cache itself)
 //
 // Keys behind the request's end are zeroed in V tiles.  What else a row must not see (a NaN
 // or an infinity in a block that only its neighbours listed, or behind its token) could
@@ -29,6 +38,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "e2m1.cuh"
 #include "kernels.hpp"
@@ -40,36 +50,34 @@ namespace {
 
 constexpr int kPN = 128;                      // keys of a tile
 constexpr int kPM = kSparseTileRows;          // rows of a Q tile (MMA M)
-constexpr int kMmaWarp = 12, kMergeWarp = 14;
-constexpr int kPThreads = 16 * 32;
+constexpr int kMmaWarp = 16, kMergeWarp = 18;
+constexpr int kPThreads = 20 * 32, kLoadThreads = 128;
 constexpr int kTileBlk = 128 * 128;           // one 64-column block of a 128-row tile: 16 KB
 constexpr int kVStage = 2 * kTileBlk;
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;
-constexpr int kDescs = 6;                     // descriptors in the ring
+constexpr int kDescs = 8;                     // descriptors in the ring
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.0f;                 // base-2 growth of a maximum before O is rescaled
 
 template <int DQK>
 struct Lay {
   static constexpr int kQTile = DQK / 64 * kTileBlk, kKStage = DQK / 64 * kTileBlk;
-  static constexpr int kOffK = 2 * kQTile, kOffV = kOffK + 2 * kKStage;
-  static constexpr int kSmem = kOffV + kVStage + 1024;     // + room to align the base to 1024 B
+  static constexpr int kOffK = kQTile, kOffV = kOffK + 2 * kKStage;
+  static constexpr int kSmem = kOffV + 2 * kVStage + 1024;     // + room to align the base to 1024 B
   static_assert(kSmem + 2048 <= 227 * 1024, "shared memory layout too large");
 };
 
 // A tile: its pieces (blocks) in order.
 struct TileDesc {
   int32_t key0[8], slot[8];        // first key, first slot (the pool's size: read as zeros)
-  uint32_t tokens[8][4];           // the job's tokens that listed it
-  int32_t tiles;                   // bit t: some token of Q tile t did
+  uint8_t listed[64];              // of every token of the job, a bit per 16 keys: listed
   int32_t end;                     // no tile: the list has ended
-  int32_t edge;                    // keys that not every token of the job is past
-  int32_t pad;
+  int32_t edge;                    // bit 0: keys that not every token of the job is past; bit 1: behind the end
 };
 
 struct Bars {
   uint64_t desc_full[kDescs], desc_empty[kDescs];
-  uint64_t k_full[2], k_empty[2], v_full, v_empty, v_edge, q_full;
+  uint64_t k_raw[2], k_full[2], k_empty[2], v_raw[2], v_full[2], v_empty[2], load[2], q_full, merge;
   uint64_t s_full[2], p_hi[2], p_full[2], pv_done[2], done[2];
 };
 
@@ -98,25 +106,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
       : "memory");
 }
 
-// The power of two that a query row is multiplied by on its way to fp16 (attn_prefill.cu).
-template <int DQK>
-__device__ __forceinline__ int q_row_shift(const uint4 *row) {
-  uint32_t e = 0;
-#pragma unroll 1
-  for (int c0 = 0; c0 < DQK / 8; c0 += 8) {
-    uint4 v[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = __ldg(row + c0 + u);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) e = max(e, max((w[q] >> 7) & 0xFFu, (w[q] >> 23) & 0xFFu));
-    }
-  }
-  return min(141 - (int)e, 126);
-}
-
 template <int KV, int DQK>
 __global__ void __launch_bounds__(kPThreads, 1)
     sparse_tc_kernel(const SparseArgs a, const __grid_constant__ TmaMaps maps) {
@@ -129,6 +118,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   __shared__ TileDesc descs[kDescs];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag, odd_flag;
+  __shared__ float row_sc[kPM], row_m[2][kPM], row_l[2][kPM];     // the rows' score scales, the chains' results
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -141,312 +131,217 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     return;
   }
-  // the lists are ascending, their empty entries last, none past the token's own block
-  bool bad_list = false;
-  for (int i = tid; i < x.ntok * a.take; i += kPThreads) {
-    const int tt = i / a.take, k = i % a.take;
-    const int32_t *list = a.block_idx + ((int64_t)(x.tok0 + tt) * a.hkv + x.g) * a.take;
-    const int c = __ldg(list + k), next = k + 1 < a.take ? __ldg(list + k + 1) : -1;
-    bad_list |= (next >= 0 && (c < 0 || next <= c)) || c > (x.pos0 + tt) / a.block;
-  }
   if (tid == 0) {
     abort_flag = odd_flag = 0;
     for (int i = 0; i < kDescs; ++i) {
       tc::mbar_init(&bars.desc_full[i], 1);
-      tc::mbar_init(&bars.desc_empty[i], 14);     // softmax, load and issuing warps
+      tc::mbar_init(&bars.desc_empty[i], F16 ? 14 : 10);     // warps that read it: the loading ones, the chain's
     }
     for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&bars.k_raw[i], 1);
+      tc::mbar_init(&bars.v_raw[i], 1);
       tc::mbar_init(&bars.k_full[i], F16 ? 4 : 1);
-      tc::mbar_init(&bars.k_empty[i], 2);
+      tc::mbar_init(&bars.k_empty[i], 1);
+      tc::mbar_init(&bars.v_full[i], 4);
+      tc::mbar_init(&bars.v_empty[i], 1);
       tc::mbar_init(&bars.s_full[i], 1);
       tc::mbar_init(&bars.p_hi[i], 4);
       tc::mbar_init(&bars.p_full[i], 4);
       tc::mbar_init(&bars.pv_done[i], 1);
       tc::mbar_init(&bars.done[i], 1);
     }
-    tc::mbar_init(&bars.v_full, 4);
-    tc::mbar_init(&bars.v_empty, 2);
-    tc::mbar_init(&bars.v_edge, 1);
-    tc::mbar_init(&bars.q_full, 4);
+    tc::mbar_init(&bars.merge, 8);
+    tc::mbar_init(&bars.load[0], 4);
+    tc::mbar_init(&bars.load[1], 4);
+    tc::mbar_init(&bars.q_full, 8);
     tc::fence_mbar_init();
-  }
-  if (__syncthreads_or(bad_list)) {                // left to the other kernel
-    if (tid == 0) a.redo[job] = 1;
-    return;
   }
   if (warp == kMmaWarp) tc::tmem_alloc(&tmem_slot, kTmemCols);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = tmem_slot, sbase = tc::smem_u32(smem);
-  const int tile_tokens = a.job_tokens / 2;
   const int num_slots = a.num_pages * a.page_size;
   auto wait = [&](uint64_t *bar, uint32_t parity) { return tc::mbar_wait_warp(bar, parity, &abort_flag); };
   auto desc_wait = [&](int k) { return wait(&bars.desc_full[k % kDescs], (k / kDescs) & 1); };
   auto desc_done = [&](int k) { tc::mbar_arrive_warp(&bars.desc_empty[k % kDescs]); };
 
-  // Registers per warpgroup as in attn_prefill.cu: 168 + 168 + 120 + 56 = 4 x 128.
   if (warp >= 8 && warp < kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;\n" ::: "memory");
+    
     // ------------------------------------------------------------ load warps
-    const int lt = tid - 256;
-    // Q rows: row p of Q tile t is head p % G of token t * tile_tokens + p / G; others zero
+    const int lt = tid & 127;
+    const bool is_v = warp >= 12;
+    // Are the lists ascending, their empty entries last, none past the token's own block?
+    // Else the job is left to the other kernel.
+    if (is_v) {
+      bool bad = false;
 #pragma unroll 1
-    for (int rr = 0; rr < 2; ++rr) {
-      const int tt = rr * tile_tokens + lt / a.group;
-      const bool live = lt / a.group < tile_tokens && tt < x.ntok;
-      const uint4 *src = reinterpret_cast<const uint4 *>(
-          a.q + ((int64_t)(x.tok0 + (live ? tt : 0)) * a.hq + x.g * a.group + lt % a.group) * DQK);
-      const float f = F16 ? __int_as_float(((live ? q_row_shift<DQK>(src) : 0) + 127) << 23) : 1.f;
-#pragma unroll 1
-      for (int c0 = 0; c0 < DQK / 8; c0 += 8) {
-        uint4 v[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = live ? __ldg(src + c0 + u) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          uint32_t h[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-          if (F16)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              h[q] = pair16<false>(__uint_as_float(h[q] << 16) * f, __uint_as_float(h[q] & 0xFFFF0000u) * f);
-          *reinterpret_cast<uint4 *>(smem + rr * Y::kQTile + (c0 >> 3) * kTileBlk + tc::sw128_offset(lt, u)) =
-              make_uint4(h[0], h[1], h[2], h[3]);
-        }
+      for (int i = lt; i < x.ntok * a.take; i += kLoadThreads) {
+        const int tt = i / a.take, e = i % a.take;
+        const int32_t *list = a.block_idx + ((int64_t)(x.tok0 + tt) * a.hkv + x.g) * a.take;
+        const int c = __ldg(list + e), next = e + 1 < a.take ? __ldg(list + e + 1) : -1;
+        bad |= (next >= 0 && (c < 0 || next <= c)) || c > (x.pos0 + tt) / a.block;
       }
+      if (bad) odd_flag = 1;
     }
-    tc::fence_proxy_async_smem();
-    tc::mbar_arrive_warp(&bars.q_full);
-
-    if constexpr (F16) {
-      // Thread `lt` owns that key of every tile; the K stream runs one tile ahead of the V
-      // stream (attn_prefill.cu).
-      constexpr int KCH = E2M1 ? e2m1_row_bytes(DQK) / 16 : DQK / 16;
-      constexpr int VCH = E2M1 ? e2m1_row_bytes(kDv) / 16 : kDv / 16;
-      const uint8_t *kc = static_cast<const uint8_t *>(a.k_cache), *vc = static_cast<const uint8_t *>(a.v_cache);
-      auto put_row = [&](uint32_t base, const uint4 *src, int n) {
-        auto put = [&](int ch, uint4 v) {
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(
-                           base + (ch >> 3) * kTileBlk + tc::sw128_offset(lt, ch & 7)),
-                       "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                       : "memory");
-        };
-        if constexpr (E2M1) {
-          const uint32_t sc[4] = {src[n - 1].x, src[n - 1].y, src[n - 1].z, src[n - 1].w};
+    int synced = 0;
+    auto load_sync = [&]() {
+      tc::mbar_arrive_warp(&bars.load[is_v]);
+      return wait(&bars.load[is_v], synced++ & 1);
+    };
+    // A raw tile of ROWB-byte rows in its stage, widened in place: every thread holds its
+    // part in registers before any is written.  4-bit rows go by a row a thread (scales at
+    // the row's end; 112 and 80 bytes are an odd number of 16-byte banks), E4M3 by 16-byte
+    // pieces in order.  `dead(row)`: a key behind the request's end, zeros.
+    auto widen = [&](auto row_bytes, bool swizzled, uint8_t *tile, auto dead) -> bool {
+      constexpr int ROWB = decltype(row_bytes)::value, NCH = ROWB / 16;
+      uint4 r[NCH];
 #pragma unroll
-          for (int i = 0; i + 1 < n; ++i) {
-            uint4 w[4];
-            e2m1x32_to_f16(src[i], i & 1 ? sc[i >> 1] >> 16 : sc[i >> 1], w);
+      for (int i = 0; i < NCH; ++i) {
+        const int idx = E2M1 ? lt * NCH + i : lt + i * kLoadThreads;
+        const int row = idx / NCH, ch = idx % NCH;
+        r[i] = *reinterpret_cast<const uint4 *>(tile + row * ROWB + (swizzled ? ch ^ (row & 7) : ch) * 16);
+        if (dead(row)) r[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (!load_sync()) return false;
+      auto put = [&](int row, int ch, uint4 v) {
+        *reinterpret_cast<uint4 *>(tile + (ch >> 3) * kTileBlk + tc::sw128_offset(row, ch & 7)) = v;
+      };
+      if constexpr (E2M1) {
+        const uint32_t sc[4] = {r[NCH - 1].x, r[NCH - 1].y, r[NCH - 1].z, r[NCH - 1].w};
 #pragma unroll
-            for (int u = 0; u < 4; ++u) put(4 * i + u, w[u]);
-          }
-        } else {
+        for (int i = 0; i + 1 < NCH; ++i) {
+          uint4 w[4];
+          e2m1x32_to_f16(r[i], i & 1 ? sc[i >> 1] >> 16 : sc[i >> 1], w);
 #pragma unroll
-          for (int i = 0; i < n; ++i) {
-            uint4 lo, hi;
-            e4m3x16_to_f16(src[i], lo, hi);
-            put(2 * i, lo);
-            put(2 * i + 1, hi);
-          }
+          for (int u = 0; u < 4; ++u) put(lt, 4 * i + u, w[u]);
         }
-      };
-      // the thread's slot in tile k: -1 read as zeros; false: the list has ended
-      auto next = [&](int k, int64_t &slot, bool &more) -> bool {
-        if (!desc_wait(k)) return false;
-        const TileDesc &d = descs[k % kDescs];
-        more = !d.end;
-        const int p = lt / a.block, in = lt % a.block;
-        const int s = d.slot[p];
-        slot = s < num_slots && d.key0[p] + in < x.len ? s + in : -1;
-        desc_done(k);
-        return true;
-      };
-      uint4 kr[KCH], vr[VCH];
-      auto load = [&](uint4 *dst, int n, const uint8_t *cache, int64_t slot) {
-        const uint4 *row = reinterpret_cast<const uint4 *>(cache) + ((slot >= 0 ? slot : 0) * a.hkv + x.g) * n;
+      } else {
 #pragma unroll
-        for (int i = 0; i < n; ++i) dst[i] = slot >= 0 ? __ldg(row + i) : make_uint4(0u, 0u, 0u, 0u);
-      };
-      int64_t slot = -1;
-      bool more = false, ok = next(0, slot, more);
-      if (ok && more) load(kr, KCH, kc, slot);
-      for (int k = 0; ok; ++k) {
-        int64_t v_slot = -1;
-        const bool here = more;
-        if (here) {
-          const int s = k & 1;
-          if (k >= 2 && !(ok = wait(&bars.k_empty[s], ((k >> 1) - 1) & 1))) break;
-          put_row(sbase + Y::kOffK + s * Y::kKStage, kr, KCH);
-          tc::fence_proxy_async_smem();
+        for (int i = 0; i < NCH; ++i) {
+          const int idx = lt + i * kLoadThreads;
+          uint4 lo, hi;
+          e4m3x16_to_f16(r[i], lo, hi);
+          put(idx / NCH, 2 * (idx % NCH), lo);
+          put(idx / NCH, 2 * (idx % NCH) + 1, hi);
+        }
+      }
+      tc::fence_proxy_async_smem();
+      return true;
+    };
+    bool ok = F16 || is_v;                         // (bf16 K tiles need nothing)
+    for (int k = 0; ok; ++k) {
+      if (!(ok = desc_wait(k))) break;
+      const TileDesc &d = descs[k % kDescs];
+      const bool end = d.end != 0;
+      const bool tail = d.edge & 2;
+      bool dead = false;                           // the thread's key lies behind the request's end
+      if (tail) dead = d.key0[lt / a.block] + lt % a.block >= x.len;
+      uint32_t dead_rows[4] = {0u, 0u, 0u, 0u};
+      if (F16 && !E2M1 && tail) {                  // (pieces of other keys too)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 32 * i + lane;
+          const uint32_t m = __ballot_sync(0xffffffffu, d.key0[row / a.block] + row % a.block >= x.len);
+          dead_rows[i] = m;
+        }
+      }
+      desc_done(k);
+      if (end) break;
+      const int s = k & 1, phase = (k >> 1) & 1;
+      uint8_t *kt = smem + Y::kOffK + s * Y::kKStage, *vt = smem + Y::kOffV + s * kVStage;
+      if constexpr (F16) {
+        if (!is_v) {
+          if (!(ok = wait(&bars.k_raw[s], phase))) break;
+          if (!(ok = widen(std::integral_constant<int, kv_row_bytes(KV, DQK)>{}, false, kt, [](int) { return false; }))) break;
           tc::mbar_arrive_warp(&bars.k_full[s]);
-          v_slot = slot;
-          if (!(ok = next(k + 1, slot, more))) break;
-          if (more) load(kr, KCH, kc, slot);
+          continue;
         }
-        if (k >= 1) {
-          if (k >= 2 && !(ok = wait(&bars.v_empty, (k - 2) & 1))) break;
-          put_row(sbase + Y::kOffV, vr, VCH);
-          tc::fence_proxy_async_smem();
-          tc::mbar_arrive_warp(&bars.v_full);
-        }
-        if (!here) break;
-        load(vr, VCH, vc, v_slot);
       }
-    } else {
-      // Boxes of `rows` keys x 64 columns; lane i of warp 8 issues box i % nb of column block
-      // i / nb.
-      const int rows = min(a.block, 64), nb = kPN / rows;
-      const int col = lane / nb, box = lane % nb;
-      int v_slot = 0, dead = 0, v_dead = 0, v_tail = 0;
-      bool ok = true;
-      int issued_v = 0, issued_k = 0, edges = 0;
-      for (int k = 0; ok; ++k) {
-        if (!(ok = desc_wait(k))) break;
-        const TileDesc &d = descs[k % kDescs];
-        const bool more = !d.end;
-        const int at = box * rows, p = at / a.block;
-        const int slot = d.slot[p] + at % a.block;
-        // the thread's key lies behind the request's end; does any key of the tile?
-        dead = d.key0[lt / a.block] + lt % a.block >= x.len;
-        int tail = 0;
-        if (d.edge)
-          for (int i = 0; i < kPN / a.block; ++i) tail |= d.key0[i] + a.block > x.len;
-        desc_done(k);
-        if (more && warp == 8) {
-          const int s = k & 1;
-          if (k >= 2 && !(ok = wait(&bars.k_empty[s], ((k >> 1) - 1) & 1))) break;
-          if (lane == 0) tc::mbar_arrive_expect_tx(&bars.k_full[s], Y::kKStage);
-          __syncwarp();
-          if (col < DQK / 64)
-            tma_load_3d(sbase + Y::kOffK + s * Y::kKStage + col * kTileBlk + box * rows * 128, &maps.k, 64 * col, x.g,
-                        slot, &bars.k_full[s]);
-          __syncwarp();
-          ++issued_k;
-        }
-        if (k >= 1) {
-          if (k >= 2 && !(ok = wait(&bars.v_empty, (k - 2) & 1))) break;
-          uint64_t *bar = v_tail ? &bars.v_edge : &bars.v_full;
-          if (warp == 8) {
-            if (lane == 0) tc::mbar_arrive_expect_tx(bar, kVStage);
-            __syncwarp();
-            if (col < kDv / 64)
-              tma_load_3d(sbase + Y::kOffV + col * kTileBlk + box * rows * 128, &maps.v, 64 * col, x.g, v_slot, bar);
-            __syncwarp();
-            ++issued_v;
-          }
-          if (v_tail) {                            // zeros behind the request's end
-            if (!(ok = wait(&bars.v_edge, edges & 1))) break;
-            if (v_dead)
+      if (!(ok = wait(&bars.v_raw[s], phase))) break;
+      if constexpr (F16) {
+        // E4M3: a thread's pieces are of the rows lt / NCH + multiples of kLoadThreads / NCH
+        auto is_dead = [&](int row) {
+          if (E2M1) return dead;
+          const uint32_t w = row < 32 ? dead_rows[0] : row < 64 ? dead_rows[1] : row < 96 ? dead_rows[2] : dead_rows[3];
+          return (w >> (row & 31) & 1u) != 0u;
+        };
+        if (!(ok = widen(std::integral_constant<int, kv_row_bytes(KV, kDv)>{}, !E2M1, vt, is_dead))) break;
+      } else if (tail) {                           // zeros behind the request's end
+        if (dead)
 #pragma unroll
-              for (int ch = 0; ch < kDv / 8; ++ch)
-                *reinterpret_cast<uint4 *>(smem + Y::kOffV + (ch >> 3) * kTileBlk + tc::sw128_offset(lt, ch & 7)) =
-                    make_uint4(0u, 0u, 0u, 0u);
-            tc::fence_proxy_async_smem();
-            tc::mbar_arrive_warp(&bars.v_full);
-          } else if (warp != 8) {
-            tc::mbar_arrive_warp(&bars.v_full);
-          }
-          edges += v_tail;
-        }
-        if (!more) break;
-        v_slot = slot;
-        v_dead = dead;
-        v_tail = tail;
+          for (int ch = 0; ch < kDv / 8; ++ch)
+            *reinterpret_cast<uint4 *>(vt + (ch >> 3) * kTileBlk + tc::sw128_offset(lt, ch & 7)) = make_uint4(0u, 0u, 0u, 0u);
+        tc::fence_proxy_async_smem();
       }
-      if (abort_flag && warp == 8) {               // the copies in flight land before the CTA ends
-        int no_abort = 0;
-        for (int i = max(0, issued_k - 2); i < issued_k; ++i)
-          tc::mbar_wait(&bars.k_full[i & 1], (i >> 1) & 1, &no_abort, 100000000ull);
-        if (issued_v > 0) {
-          if (v_tail)
-            tc::mbar_wait(&bars.v_edge, (edges > 0 ? edges - 1 : 0) & 1, &no_abort, 100000000ull);
-          else
-            tc::mbar_wait(&bars.v_full, (issued_v - 1) & 1, &no_abort, 100000000ull);
-        }
-      }
+      tc::mbar_arrive_warp(&bars.v_full[s]);
     }
   } else if (warp >= kMmaWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n" ::: "memory");
     if (warp == kMergeWarp) {
       // ------------------------------------------------------------ the union of the lists
       const int pieces = kPN / a.block, per_page = a.page_size / a.block;
+      const uint32_t own = (uint32_t)((x.pos0 + x.ntok - 1) / a.block);
       // lane: tokens lane, lane + 32, ..; the entry at hand and the one behind it
-      const int32_t *next_at[4];
-      int left[4];
-      uint32_t cur[4], ahead[4];
+      const int32_t *next_at[2] = {a.block_idx, a.block_idx};
+      int left[2] = {0, 0};
+      uint32_t cur[2], ahead[2];
+      // (an empty entry is the largest number, and so is one past the job's last block)
+      auto entry = [&](int i) -> uint32_t {
+        if (left[i] <= 0) return 0xFFFFFFFFu;
+        --left[i];
+        const uint32_t c = (uint32_t)__ldg(next_at[i]++);
+        return c <= own ? c : 0xFFFFFFFFu;
+      };
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         const int tt = lane + 32 * i;
         next_at[i] = a.block_idx + ((int64_t)(x.tok0 + tt) * a.hkv + x.g) * a.take;
         left[i] = tt < x.ntok ? a.take : 0;
-        auto take = [&]() -> uint32_t {
-          if (left[i] <= 0) return 0xFFFFFFFFu;
-          --left[i];
-          return (uint32_t)__ldg(next_at[i]++);    // (an empty entry is the largest)
-        };
-        cur[i] = take();
-        ahead[i] = take();
+        cur[i] = entry(i);
+        ahead[i] = entry(i);
       }
-      bool ok = true, more = true;
-      for (int k = 0; more && ok; ++k) {
-        uint32_t block = 0xFFFFFFFFu, who[4] = {0u, 0u, 0u, 0u};
+      bool ok = true;
+      int ends = 0;                                // one for each chain
+      for (int k = 0; ok && ends < 2; ++k) {
+        uint32_t block = 0u, listed[2] = {0u, 0u};
         int found = 0;
+        const uint32_t groups = (1u << (a.block >> 4)) - 1u;
         for (int s = 0; s < pieces; ++s) {
-          const uint32_t least =
-              __reduce_min_sync(0xffffffffu, min(min(cur[0], cur[1]), min(cur[2], cur[3])));
-          if ((int32_t)least < 0) break;
-          uint32_t m[4];
+          const uint32_t least = __reduce_min_sync(0xffffffffu, min(cur[0], cur[1]));
+          if (least == 0xFFFFFFFFu) break;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool has = cur[i] == least;
-            m[i] = __ballot_sync(0xffffffffu, has);
-            if (has) {
+          for (int i = 0; i < 2; ++i)
+            if (cur[i] == least) {
+              listed[i] |= groups << (s * (a.block >> 4));
               cur[i] = ahead[i];
-              ahead[i] = 0xFFFFFFFFu;
-              if (left[i] > 0) {
-                --left[i];
-                ahead[i] = (uint32_t)__ldg(next_at[i]++);
-              }
+              ahead[i] = entry(i);
             }
-          }
-          if (lane == s) {
-            block = least;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) who[i] = m[i];
-          }
+          if (lane == s) block = least;
           ++found;
         }
-        more = found > 0;
-        int slot = num_slots;
-        const int key0 = lane < found ? (int)block * a.block : 0;
-        if (lane < found) {
+        ends += found == 0;
+        const bool in = lane < found;
+        int slot = num_slots, key0 = 0;
+        if (in) {
+          key0 = (int)block * a.block;
           const int32_t page = __ldg(a.page_table + (int64_t)x.b * a.pt_stride + (int)block / per_page);
           if (page >= 0 && page < a.num_pages)
             slot = page * a.page_size + (int)block % per_page * a.block;
           else
             atomicOr(a.err, 1);
         }
-        // Q tile 0: tokens below tile_tokens
-        uint32_t tiles = 0u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int cut = min(32, max(0, tile_tokens - 32 * i));
-          const uint32_t low = cut == 32 ? 0xFFFFFFFFu : (1u << cut) - 1u;
-          tiles |= (who[i] & low ? 1u : 0u) | (who[i] & ~low ? 2u : 0u);
-        }
-        tiles = __reduce_or_sync(0xffffffffu, tiles);
-        const bool edge = __any_sync(0xffffffffu, lane < found && key0 + a.block - 1 > x.pos0);
+        const int edge = (__any_sync(0xffffffffu, in && key0 + a.block - 1 > x.pos0) ? 1 : 0) |
+                         (__any_sync(0xffffffffu, in && key0 + a.block > x.len) ? 2 : 0);
         if (k >= kDescs && !(ok = wait(&bars.desc_empty[k % kDescs], (k / kDescs - 1) & 1))) break;
         TileDesc &d = descs[k % kDescs];
         if (lane < 8) {
           d.key0[lane] = key0;
           d.slot[lane] = slot;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) d.tokens[lane][i] = who[i];
         }
+        d.listed[lane] = (uint8_t)listed[0];
+        d.listed[lane + 32] = (uint8_t)listed[1];
         if (lane == 0) {
-          d.tiles = (int)tiles;
-          d.end = !more;
+          d.end = found == 0;
           d.edge = edge;
         }
         tc::mbar_arrive_warp(&bars.desc_full[k % kDescs]);
@@ -455,136 +350,196 @@ __global__ void __launch_bounds__(kPThreads, 1)
       // ------------------------------------------------------------ MMA issuers
       const int t = warp - kMmaWarp;
       const uint32_t id_s = tc::idesc_f16(F16 ? 0 : 1, 0, 0, kPM, kPN), id_pv = tc::idesc_f16(F16 ? 0 : 1, 0, 1, kPM, kDv);
-      const uint32_t q_smem = sbase + t * Y::kQTile, s_tmem = tmem + kPN * t, o_tmem = tmem + kTmemO + kDv * t;
-      int c = 0;                                   // tiles of this Q tile so far
-      bool ok = wait(&bars.q_full, 0);
-      for (int k = 0; ok; ++k) {
-        if (!(ok = desc_wait(k))) break;
-        const bool end = descs[k % kDescs].end != 0, mine = descs[k % kDescs].tiles >> t & 1;
-        desc_done(k);
-        if (end) break;
-        const int s = k & 1;
-        if (!(ok = wait(&bars.k_full[s], (k >> 1) & 1))) break;
-        if (lane == 0) {
-          if (mine) {
-            tc::tc_fence_after();
+      const uint32_t q_smem = sbase, s_tmem = tmem + kPN * t, o_tmem = tmem + kTmemO + kDv * t;
+      if (lane == 0) {
+        auto wait1 = [&](uint64_t *bar, uint32_t parity) { return tc::mbar_wait(bar, parity, &abort_flag); };
+        bool ok = wait1(&bars.q_full, 0);
+        for (int c = 0; ok; ++c) {                 // tile 2 c + t
+          const int ds = (2 * c + t) % kDescs;
+          if (!(ok = wait1(&bars.desc_full[ds], (2 * c + t) / kDescs & 1))) break;
+          const bool end = descs[ds].end != 0;
+          tc::mbar_arrive(&bars.desc_empty[ds]);
+          if (end) break;
+          if (!(ok = wait1(&bars.k_full[t], c & 1))) break;
+          tc::tc_fence_after();
 #pragma unroll
-            for (int kq = 0; kq < DQK / 16; ++kq) {
-              const uint32_t off = (kq & 3) * 32 + (kq >> 2) * kTileBlk;
-              const uint64_t ad = tc::smem_desc_sw128(q_smem + off, 16, 1024);
-              const uint64_t bd = tc::smem_desc_sw128(sbase + Y::kOffK + s * Y::kKStage + off, 16, 1024);
-              tc::mma_f16_ss(s_tmem, ad, bd, id_s, kq > 0 ? 1u : 0u);
-            }
-            tc::mma_commit(&bars.s_full[t]);
+          for (int kq = 0; kq < DQK / 16; ++kq) {
+            const uint32_t off = (kq & 3) * 32 + (kq >> 2) * kTileBlk;
+            const uint64_t ad = tc::smem_desc_sw128(q_smem + off, 16, 1024);
+            const uint64_t bd = tc::smem_desc_sw128(sbase + Y::kOffK + t * Y::kKStage + off, 16, 1024);
+            tc::mma_f16_ss(s_tmem, ad, bd, id_s, kq > 0 ? 1u : 0u);
           }
-          tc::mma_commit(&bars.k_empty[s]);
-        }
-        __syncwarp();
-        if (!(ok = wait(&bars.v_full, k & 1))) break;
-        if (mine) {
+          tc::mma_commit(&bars.s_full[t]);
+          tc::mma_commit(&bars.k_empty[t]);
+          if (!(ok = wait1(&bars.v_full[t], c & 1))) break;
           auto pv = [&](int kk, bool acc) {
-            const uint64_t bd = tc::smem_desc_sw128(sbase + Y::kOffV + kk * 16 * 128, kTileBlk, 1024);
-            tc::mma_f16_ts(o_tmem, s_tmem + kPN / 2 + kk * 8, bd, id_pv, acc ? 1u : 0u);
+            const uint64_t bd = tc::smem_desc_sw128(sbase + Y::kOffV + t * kVStage + kk * 16 * 128, kTileBlk, 1024);
+            tc::mma_f16_ts(o_tmem, s_tmem + 32 * (kk >> 1) + 8 * (kk & 1), bd, id_pv, acc ? 1u : 0u);
           };
-          if (!(ok = wait(&bars.p_hi[t], c & 1))) break;
-          if (lane == 0) {
-            tc::tc_fence_after();
+          if (!(ok = wait1(&bars.p_hi[t], c & 1))) break;
+          tc::tc_fence_after();
 #pragma unroll
-            for (int kk = kPN / 32; kk < kPN / 16; ++kk) pv(kk, c > 0 || kk > kPN / 32);
-          }
-          __syncwarp();
-          if (!(ok = wait(&bars.p_full[t], c & 1))) break;
-          if (lane == 0) {
-            tc::tc_fence_after();
+          for (int kk = kPN / 32; kk < kPN / 16; ++kk) pv(kk, c > 0 || kk > kPN / 32);
+          if (!(ok = wait1(&bars.p_full[t], c & 1))) break;
+          tc::tc_fence_after();
 #pragma unroll
-            for (int kk = 0; kk < kPN / 32; ++kk) pv(kk, true);
-            tc::mma_commit(&bars.pv_done[t]);
-          }
-          __syncwarp();
-          ++c;
+          for (int kk = 0; kk < kPN / 32; ++kk) pv(kk, true);
+          tc::mma_commit(&bars.pv_done[t]);
+          tc::mma_commit(&bars.v_empty[t]);
         }
-        if (lane == 0) tc::mma_commit(&bars.v_empty);
-        __syncwarp();
-      }
-      if (lane == 0) {                             // every MMA is complete before TMEM goes back
+        // every MMA is complete before TMEM goes back
         tc::mma_commit(&bars.done[t]);
         int no_abort = 0;
         tc::mbar_wait(&bars.done[t], 0, &no_abort, 100000000ull);
       }
-      __syncwarp();
+    } else {
+      // ------------------------------------------------------------ K and V tiles
+      // Boxes of `rows` keys of a 64-column block (bf16), or of whole rows: box i of a column
+      // block by lane col * boxes + i.
+      const int rows = min(a.block, 64), boxes = kPN / rows;
+      const int col = lane / boxes, box = lane % boxes;
+      constexpr int kKCols = F16 ? 1 : DQK / 64, kVCols = F16 ? 1 : kDv / 64;
+      constexpr uint32_t kKRow = F16 ? kv_row_bytes(KV, DQK) : 128, kVRow = F16 ? kv_row_bytes(KV, kDv) : 128;
+      uint64_t *k_bar = F16 ? bars.k_raw : bars.k_full;
+      int issued = 0;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        if (!(ok = desc_wait(k))) break;
+        const TileDesc &d = descs[k % kDescs];
+        const bool end = d.end != 0;
+        const int at = box * rows, slot = d.slot[at / a.block] + at % a.block;
+        desc_done(k);
+        if (end) break;
+        const int s = k & 1;
+        if (k >= 2 && !(ok = wait(&bars.k_empty[s], ((k >> 1) - 1) & 1))) break;
+        if (lane == 0) tc::mbar_arrive_expect_tx(&k_bar[s], kPN * kKRow * kKCols);
+        __syncwarp();
+        if (col < kKCols)
+          tma_load_3d(sbase + Y::kOffK + s * Y::kKStage + col * kTileBlk + at * kKRow, &maps.k, 64 * col, x.g, slot,
+                      &k_bar[s]);
+        __syncwarp();
+        ++issued;
+        if (k >= 2 && !(ok = wait(&bars.v_empty[s], ((k >> 1) - 1) & 1))) break;
+        if (lane == 0) tc::mbar_arrive_expect_tx(&bars.v_raw[s], kPN * kVRow * kVCols);
+        __syncwarp();
+        if (col < kVCols)
+          tma_load_3d(sbase + Y::kOffV + s * kVStage + col * kTileBlk + at * kVRow, &maps.v, 64 * col, x.g, slot,
+                      &bars.v_raw[s]);
+        __syncwarp();
+        ++issued;
+      }
+      if (!ok) {                                   // the copies in flight land before the CTA ends
+        int no_abort = 0;
+        for (int i = max(0, issued - 4); i < issued; ++i)
+          tc::mbar_wait(i & 1 ? &bars.v_raw[(i >> 1) & 1] : &k_bar[(i >> 1) & 1], (i >> 2) & 1, &no_abort, 100000000ull);
+      }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;\n" ::: "memory");
     // ------------------------------------------------------------ softmax + epilogue
     const int t = warp >> 2, wq = warp & 3;
     const int p = wq * 32 + lane;                  // row of the Q tile, TMEM lane
     const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
-    const uint32_t s_addr = tmem + lane_base + kPN * t, o_addr = tmem + lane_base + kTmemO + kDv * t;
-    const int tt = t * tile_tokens + p / a.group;
-    const bool valid = p / a.group < tile_tokens && tt < x.ntok;
+    const uint32_t s_addr = tmem + lane_base + kPN * t;
+    auto o_addr = [&](int chain) { return tmem + lane_base + kTmemO + kDv * chain; };
+    const int tt = p / a.group;
+    const bool valid = tt < x.ntok;
     const int head = x.g * a.group + p % a.group;
     const int pos = valid ? x.pos0 + tt : -1;
-    const uint32_t bit = valid ? 1u << (tt & 31) : 0u;
-    float sc = a.scale_log2;
-    if (F16 && valid)
-      sc = tc::row_score_scale(a.scale_log2,
-                               q_row_shift<DQK>(reinterpret_cast<const uint4 *>(
-                                   a.q + ((int64_t)(x.tok0 + tt) * a.hq + head) * DQK)));
+    // The warp's 16 rows into the operand tile, 16 bytes a lane: row r is head r % G of token
+    // r / G; others zeros.  8- and 4-bit caches: times the power of two that puts the row's
+    // largest |q| in [2^14, 2^15), in fp16 (attn_prefill.cu).
+    // (Rolled, the loads as asynchronous copies: a CTA runs this once, and its time was the
+    // fetching of unrolled code, 26 thousand cycles with the scaling.)
+    {
+      uint8_t *mine = smem + (lane >> 3) * kTileBlk;
+#pragma unroll 1
+      for (int r = warp * 16; r < warp * 16 + 16; ++r) {
+        const bool live = r / a.group < x.ntok;
+        const uint16_t *src =
+            a.q + ((int64_t)(x.tok0 + (live ? r / a.group : 0)) * a.hq + x.g * a.group + r % a.group) * DQK + lane * 8;
+        if (lane < DQK / 8)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
+                           tc::smem_u32(mine + tc::sw128_offset(r, lane & 7))),
+                       "l"(src), "r"(live ? 16 : 0)
+                       : "memory");
+      }
+      asm volatile("cp.async.wait_all;\n" ::: "memory");
+      if (F16) {
+#pragma unroll 1
+        for (int r = warp * 16; r < warp * 16 + 16; ++r) {
+          uint4 *at = reinterpret_cast<uint4 *>(mine + tc::sw128_offset(r, lane & 7));
+          const uint4 v = lane < DQK / 8 ? *at : make_uint4(0u, 0u, 0u, 0u);
+          uint32_t h[4] = {v.x, v.y, v.z, v.w}, e = 0u;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) e = max(e, max((h[q] >> 7) & 0xFFu, (h[q] >> 23) & 0xFFu));
+          const int sh = min(141 - (int)__reduce_max_sync(0xffffffffu, e), 126);
+          const float f = __int_as_float((sh + 127) << 23);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            h[q] = pair16<false>(__uint_as_float(h[q] << 16) * f, __uint_as_float(h[q] & 0xFFFF0000u) * f);
+          if (lane < DQK / 8) *at = make_uint4(h[0], h[1], h[2], h[3]);
+          if (lane == 0) row_sc[r] = tc::row_score_scale(a.scale_log2, sh);
+        }
+      }
+    }
+    tc::fence_proxy_async_smem();
+    tc::mbar_arrive_warp(&bars.q_full);
+    bool ok = wait(&bars.q_full, 0);               // the other warps' row_sc
+    const float sc = F16 && ok ? row_sc[p] : a.scale_log2;
     const int block_log2 = 31 - __clz(a.block);
     float m_run = -INFINITY, l_run = 0.f;
-    int c = 0;
-    bool ok = true;
-    for (int k = 0;; ++k) {
+    int c = 0;                                     // the chain's tiles so far
+    while (ok) {
+      const int k = 2 * c + t;
       if (!(ok = desc_wait(k))) break;
       const TileDesc &d = descs[k % kDescs];
-      const bool end = d.end != 0, mine = d.tiles >> t & 1, edge = d.edge != 0;
+      const bool end = d.end != 0, edge = d.edge & 1;
       // the eight groups of 16 keys: a bit each if listed, and (edge) how many keys are seen
-      uint32_t sel = 0u, lim[2] = {0u, 0u};
-      if (mine && !end) {
-#pragma unroll
+      const uint32_t sel = valid ? d.listed[tt & 63] : 0u;
+      uint64_t lim = 0u;
+      if (edge)
+#pragma unroll 1
         for (int g = 0; g < 8; ++g) {
-          const int pc = (g * 16) >> block_log2;
-          if (d.tokens[pc][(tt >> 5) & 3] & bit) {
-            sel |= 1u << g;
-            if (edge) lim[g >> 2] |= (uint32_t)min(16, max(0, pos + 1 - d.key0[pc] - ((g * 16) & (a.block - 1)))) << (8 * (g & 3));
-          }
+          const int n = pos + 1 - d.key0[(g * 16) >> block_log2] - ((g * 16) & (a.block - 1));
+          lim |= (uint64_t)(sel >> g & 1u ? min(16, max(0, n)) : 0) << (8 * g);
         }
-      }
       desc_done(k);
       if (end) break;
-      if (!mine) continue;
       if (!(ok = wait(&bars.s_full[t], c & 1))) break;
       tc::tc_fence_after();
-      uint32_t s[4][32];
-      tc::tmem_ld32(s_addr, s[0]);
-      tc::tmem_ld32(s_addr + 32, s[1]);
-      tc::tmem_ld32(s_addr + 64, s[2]);
-      tc::tmem_ld32(s_addr + 96, s[3]);
-      tc::tmem_wait_ld_regs64(s[0], s[1]);
-      tc::tmem_wait_ld_regs64(s[2], s[3]);
+      // Rolled over the tile's four 32-column chunks: the four roles share each scheduler's
+      // instruction cache, and this loop is what they wait for (unrolled, with the next chunk
+      // on its way, 5.3 thousand cycles a tile against 1.9).  Tiles with an edge: keys that the
+      // token does not see go to -inf first.  Groups of 16 that it did not list are left out of
+      // the maximum and get a weight of 2^-inf.
       if (edge) {
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t v[32];
+          tc::tmem_ld32(s_addr + 32 * q, v);
+          const uint32_t n0 = (uint32_t)(lim >> (16 * q)) & 31u, n1 = (uint32_t)(lim >> (16 * q + 8)) & 31u;
+          const uint32_t seen = ((1u << n0) - 1u) | ((1u << n1) - 1u) << 16;
+          tc::tmem_wait_ld_regs32(v);
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          const int n = (int)(lim[g >> 2] >> (8 * (g & 3)) & 31u);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            uint32_t &v = s[g >> 1][16 * (g & 1) + j];
-            v = j < n ? v : 0xFF800000u;
-          }
+          for (int j = 0; j < 32; ++j) v[j] = seen >> j & 1u ? v[j] : 0xFF800000u;
+          tc::tmem_st32(s_addr + 32 * q, v);
         }
+        tc::tmem_wait_st();
       }
-      // the listed groups' maximum
       float mx = -INFINITY;
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t here = sel >> (2 * q) & 3u;
+        if (!__any_sync(0xffffffffu, here != 0u)) continue;
+        uint32_t v[32];
+        tc::tmem_ld32(s_addr + 32 * q, v);
+        tc::tmem_wait_ld_regs32(v);
+        float g[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        float m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const uint32_t *v = &s[g >> 1][16 * (g & 1) + j];
-          m0 = tc::max3(m0, __uint_as_float(v[0]), __uint_as_float(v[1]));
-          m1 = tc::max3(m1, __uint_as_float(v[2]), __uint_as_float(v[3]));
-        }
-        if (sel >> g & 1u) mx = tc::max3(mx, m0, m1);
+        for (int j = 0; j < 32; j += 2)
+          g[j >> 4] = tc::max3(g[j >> 4], __uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+        if (here & 1u) mx = fmaxf(mx, g[0]);
+        if (here & 2u) mx = fmaxf(mx, g[1]);
       }
       const float m_tile = mx * sc;
       const bool need = m_tile > m_run + kGrow;    // also from -inf
@@ -597,84 +552,98 @@ __global__ void __launch_bounds__(kPThreads, 1)
 #pragma unroll 1
           for (int q = 0; q < kDv / 16; ++q) {
             uint32_t o[16];
-            tc::tmem_ld16(o_addr + q * 16, o);
+            tc::tmem_ld16(o_addr(t) + q * 16, o);
             tc::tmem_wait_ld_regs(o);
 #pragma unroll
             for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-            tc::tmem_st16(o_addr + q * 16, o);
+            tc::tmem_st16(o_addr(t) + q * 16, o);
           }
           tc::tmem_wait_st();
           l_run *= alpha;
         }
         if (need) m_run = m_tile;
       }
-      // P: key j's 16-bit value in the low or high half of column 64 + j / 2 of S; keys 64-127
-      // first.  A group that the row's token did not list gets zeros.
+      // P of a chunk's 32 keys (16-bit values, key j in a half of column j / 2) over the first
+      // half of its own columns; keys 64-127 first
       const float off = m_run == -INFINITY ? 0.f : kLift - m_run;
       float rs[2] = {0.f, 0.f};
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        const int q = i ^ 2;
+        const uint32_t here = sel >> (2 * q) & 3u;
+        uint32_t pk[16];
+        if (__any_sync(0xffffffffu, here != 0u)) {
+          uint32_t v[32];
+          tc::tmem_ld32(s_addr + 32 * q, v);
+          const float og[2] = {here & 1u ? off : -INFINITY, here & 2u ? off : -INFINITY};
+          tc::tmem_wait_ld_regs32(v);
 #pragma unroll
-      for (int half = 1; half >= 0; --half) {
-        const bool any = __any_sync(0xffffffffu, (sel >> (4 * half) & 15u) != 0u);
-#pragma unroll
-        for (int g = 4 * half; g < 4 * half + 4; ++g) {
-          uint32_t pk[8];
-          if (any) {
-            const float og = sel >> g & 1u ? off : -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 16; j += 2) {
-              const uint32_t *v = &s[g >> 1][16 * (g & 1) + j];
-              float y0, y1;
-              tc::ffma2(y0, y1, __uint_as_float(v[0]), __uint_as_float(v[1]), sc, og);
-              const float p0 = ex2(y0), p1 = ex2(y1);
-              tc::fadd2(rs[0], rs[1], p0, p1);
-              pk[j >> 1] = pair16<!F16>(p0, p1);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) pk[j] = 0u;
+          for (int j = 0; j < 32; j += 2) {
+            float y0, y1;
+            tc::ffma2(y0, y1, __uint_as_float(v[j]), __uint_as_float(v[j + 1]), sc, og[j >> 4]);
+            const float p0 = ex2(y0), p1 = ex2(y1);
+            tc::fadd2(rs[0], rs[1], p0, p1);
+            pk[j >> 1] = pair16<!F16>(p0, p1);
           }
-          tc::tmem_st8(s_addr + kPN / 2 + 8 * g, pk);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) pk[j] = 0u;
         }
-        tc::tmem_wait_st();
-        tc::tc_fence_before();
-        tc::mbar_arrive_warp(half ? &bars.p_hi[t] : &bars.p_full[t]);
+        tc::tmem_st16(s_addr + 32 * q, pk);
+        if (i & 1) {
+          tc::tmem_wait_st();
+          tc::tc_fence_before();
+          tc::mbar_arrive_warp(i == 1 ? &bars.p_hi[t] : &bars.p_full[t]);
+        }
       }
       l_run += rs[0] + rs[1];
       ++c;
     }
-    // ---------------- normalise and write the rows
+    // ---------------- the chains' results together; a warp writes half the columns
     if (ok && c > 0) ok = wait(&bars.pv_done[t], (c - 1) & 1);
+    bool odd = l_run != l_run;
+    // (a chain without a tile has nothing in its O, one that saw none of the row's blocks zeros)
+    row_m[t][p] = c > 0 ? m_run : -INFINITY;
+    row_l[t][p] = l_run;
+    tc::tc_fence_before();
+    tc::mbar_arrive_warp(&bars.merge);
+    if (ok) ok = wait(&bars.merge, 0);
     if (ok) {
       tc::tc_fence_after();
+      const float m0 = row_m[0][p], m1 = row_m[1][p], M = fmaxf(m0, m1);
+      const float w0 = m0 == -INFINITY ? 0.f : exp2f(m0 - M), w1 = m1 == -INFINITY ? 0.f : exp2f(m1 - M);
+      const float l = (w0 == 0.f ? 0.f : w0 * row_l[0][p]) + (w1 == 0.f ? 0.f : w1 * row_l[1][p]);
       float lse;
       const float sink2 = a.sinks && valid ? __ldg(a.sinks + head) * kLog2e : -INFINITY;
-      const float f = finish(m_run, l_run, kLift, sink2, a.v_scale, lse);
-      bool odd = l_run != l_run;
+      const float f = finish(M, l, kLift, sink2, a.v_scale, lse);
+      const float f0 = f * w0, f1 = f * w1;
       uint16_t *row = a.out + ((int64_t)(x.tok0 + (valid ? tt : 0)) * a.hq + head) * kDv;
 #pragma unroll 1
-      for (int q = 0; q < kDv / 32; ++q) {
-        uint32_t o[32];
-        if (c > 0) {
-          tc::tmem_ld32(o_addr + q * 32, o);
-          tc::tmem_wait_ld_regs32(o);
-        } else {
+      for (int q = 4 * t; q < 4 * t + 4; ++q) {
+        uint32_t o0[16], o1[16];
+        tc::tmem_ld16(o_addr(0) + q * 16, o0);
+        tc::tmem_ld16(o_addr(1) + q * 16, o1);
+        tc::tmem_wait_ld_regs(o0);
+        tc::tmem_wait_ld_regs(o1);
+        uint32_t w[8];
+        float sum = 0.f;                           // NaN if any of what counts is NaN or infinite
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = 0u;
-        }
-        if (!valid) continue;
+        for (int j = 0; j < 16; j += 2) {
+          float u[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint32_t w[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float v0 = __uint_as_float(o[8 * e + 2 * j]), v1 = __uint_as_float(o[8 * e + 2 * j + 1]);
-            odd |= !(fabsf(v0) < INFINITY) | !(fabsf(v1) < INFINITY);
-            w[j] = pair16<true>(v0 * f, v1 * f);
+          for (int y = 0; y < 2; ++y) {
+            const float u0 = w0 == 0.f ? 0.f : __uint_as_float(o0[j + y]), u1 = w1 == 0.f ? 0.f : __uint_as_float(o1[j + y]);
+            sum += 0.f * u0 + 0.f * u1;
+            u[y] = u0 * f0 + u1 * f1;
           }
-          reinterpret_cast<uint4 *>(row + q * 32)[e] = make_uint4(w[0], w[1], w[2], w[3]);
+          w[j >> 1] = pair16<true>(u[0], u[1]);
         }
+        odd |= sum != sum;
+        if (!valid) continue;
+        reinterpret_cast<uint4 *>(row + q * 16)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4 *>(row + q * 16)[1] = make_uint4(w[4], w[5], w[6], w[7]);
       }
-      if (valid && a.lse) a.lse[(int64_t)(x.tok0 + tt) * a.hq + head] = lse;
+      if (valid && a.lse && t == 0) a.lse[(int64_t)(x.tok0 + tt) * a.hq + head] = lse;
       if (valid && odd) odd_flag = 1;
     }
   }

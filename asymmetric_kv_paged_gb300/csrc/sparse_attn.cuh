@@ -88,7 +88,7 @@ __device__ __forceinline__ float finish(float m, float l, float lift, float sink
 // Tokens of a job for a group of `group` heads (0: the group is too large).
 constexpr int kSparseTileRows = 128;
 inline int sparse_job_tokens(int group) {
-  return group > kSparseTileRows ? 0 : 2 * (kSparseTileRows / group < 64 ? kSparseTileRows / group : 64);
+  return group > kSparseTileRows ? 0 : kSparseTileRows / group < 64 ? kSparseTileRows / group : 64;
 }
 inline int64_t sparse_jobs(const HostPlan &hp) {
   const int per = sparse_job_tokens(hp.group);
