@@ -34,7 +34,7 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxSmem = 224 * 1024;
 
 // c (16 x 8, fp32) += a (16 x 16, fp16) . b (16 x 8, fp16)
@@ -110,12 +110,12 @@ __device__ __forceinline__ void stage_row(QTile<D> &tile, int r, const uint16_t 
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   QTile<D> *tiles = reinterpret_cast<QTile<D> *>(smem);                        // [row_tiles]
   int *exps = reinterpret_cast<int *>(smem + a.row_tiles * sizeof(QTile<D>));  // [row_tiles * 16]
   uint32_t *keys = reinterpret_cast<uint32_t *>(exps + a.row_tiles * 16);      // [max_blocks]
-  __shared__ int hist[256], sums[2][kWarps], pick[2];
+  __shared__ int hist[256], sums[2][kWarps], pick[3];
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -140,9 +140,39 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
       for (int k = tid; k < a.take; k += kThreads) out[k] = k <= own ? k : -1;
     return;
   }
-  const int c_lo = a.first, c_hi = own - a.last + 1;        // the scored ones (take < own + 1: not empty
-                                                            // unless first + last == take)
+  const int c_lo = a.first, c_hi = own - a.last + 1;        // the scored ones (take < own + 1: there are some)
+  // the first CTA's keys may be written once all have started
+  asm volatile("barrier.cluster.arrive.aligned;\n" ::: "memory");
   uint32_t *dst = cluster.map_shared_rank(keys, 0);
+  // ---- a warp's bounds: 8 blocks at a time, on their way while the 8 before are at work,
+  // their pages one step ahead of them
+  const int gq = lane >> 2, t = lane & 3;
+  const int per_page = a.page_size / a.block, step = ranks * kWarps * 8;
+  struct Bounds {
+    uint4 raw[2][D / 64];
+    int e;
+  } ahead;
+  int c_at = c_lo + (rank * kWarps + warp) * 8;
+  int32_t page = 0;
+  auto look = [&](int c) { page = __ldg(a.page_table + (int64_t)b * a.pt_stride + min(c + gq, c_hi - 1) / per_page); };
+  auto fetch = [&](int c) {
+    c = min(c + gq, c_hi - 1);
+    const bool bad = page < 0 || page >= a.num_pages;
+    if (bad && t == 0) atomicOr(a.err, 1);
+    const uint8_t *rec = a.bounds + (((int64_t)(bad ? 0 : page) * per_page + c % per_page) * a.hkv + g) *
+                                        bounds_row_bytes(D);
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j)
+        ahead.raw[w][j] = bad ? make_uint4(0u, 0u, 0u, 0u) : __ldg(reinterpret_cast<const uint4 *>(rec + w * D) + 4 * j + t);
+    ahead.e = bad ? 0 : (int)(int8_t)__ldg(rec + 2 * D);
+  };
+  if (c_at < c_hi) {
+    look(c_at);
+    fetch(c_at);
+    look(c_at + step);
+  }
   // ---- the query rows
   for (int r = warp; r < a.row_tiles * 16; r += kWarps) {
     const uint16_t *row = r < a.group ? a.q + ((int64_t)tok * a.hq + g * a.group + r) * D : nullptr;
@@ -154,34 +184,22 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
     for (int i = 0; i < a.group; ++i) top = max(top, exps[i]);
     tiles[r >> 4].factor[r & 15] = exps[r] == INT_MIN ? -1.f : ldexpf(1.f, exps[r] - top);
   }
-  cluster.sync();                            // also: the first CTA's keys may be written from here on
+  __syncthreads();
+  asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
   // ---- scores
-  const int gq = lane >> 2, t = lane & 3;
-  const int per_page = a.page_size / a.block;
-  for (int c0 = c_lo + (rank * kWarps + warp) * 8; c0 < c_hi; c0 += ranks * kWarps * 8) {
-    const int c = min(c0 + gq, c_hi - 1);
-    const int32_t page = __ldg(a.page_table + (int64_t)b * a.pt_stride + c / per_page);
-    const bool bad = page < 0 || page >= a.num_pages;
-    if (bad && t == 0) atomicOr(a.err, 1);
-    const uint8_t *rec = a.bounds + (((int64_t)(bad ? 0 : page) * per_page + c % per_page) * a.hkv + g) *
-                                        bounds_row_bytes(D);
-    uint4 raw[2][D / 64];
-#pragma unroll
-    for (int w = 0; w < 2; ++w)
-#pragma unroll
-      for (int j = 0; j < D / 64; ++j) {
-        raw[w][j] = make_uint4(0u, 0u, 0u, 0u);
-        if (!bad) raw[w][j] = __ldg(reinterpret_cast<const uint4 *>(rec + w * D) + 4 * j + t);
-      }
-    int e = 0;
-    if (!bad) e = (int8_t)__ldg(rec + 2 * D);
+  for (; c_at < c_hi; c_at += step) {
+    const Bounds now = ahead;
+    if (c_at + step < c_hi) {
+      fetch(c_at + step);
+      look(c_at + 2 * step);
+    }
     float best[2] = {-INFINITY, -INFINITY};
     for (int rt = 0; rt < a.row_tiles; ++rt) {
       float acc[2][4] = {};
 #pragma unroll
       for (int j = 0; j < D / 64; ++j) {
-        const uint32_t up[4] = {raw[0][j].x, raw[0][j].y, raw[0][j].z, raw[0][j].w};
-        const uint32_t dn[4] = {raw[1][j].x, raw[1][j].y, raw[1][j].z, raw[1][j].w};
+        const uint32_t up[4] = {now.raw[0][j].x, now.raw[0][j].y, now.raw[0][j].z, now.raw[0][j].w};
+        const uint32_t dn[4] = {now.raw[1][j].x, now.raw[1][j].y, now.raw[1][j].z, now.raw[1][j].w};
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
           const uint4 f = tiles[rt].frag[4 * j + s][lane];
@@ -205,27 +223,58 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
     for (int x = 0; x < 2; ++x) {
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) best[x] = fmaxf(best[x], __shfl_xor_sync(0xffffffffu, best[x], o));
-      // column 2 t + x is block c0 + 2 t + x, whose exponent lane (2 t + x) * 4 holds
-      const int ec = __shfl_sync(0xffffffffu, e, (2 * t + x) * 4);
-      const int cc = c0 + 2 * t + x;
-      if (gq == 0 && cc < c_hi) dst[cc] = ordered(ec == kOddBlock ? INFINITY : best[x] * pow2(ec));
+      // column 2 t + x is block c_at + 2 t + x, whose exponent lane (2 t + x) * 4 holds
+      const int ec = __shfl_sync(0xffffffffu, now.e, (2 * t + x) * 4);
+      const int cc = c_at + 2 * t + x;
+      if (gq == 0 && cc < c_hi) dst[cc] = ordered(ec == kOddBlock ? INFINITY : best[x] * pow2(max(ec, -126)));
     }
   }
   cluster.sync();
   if (rank != 0) return;
-  // ---- the lists: forced blocks are above every score
-  for (int c = tid; c <= own; c += kThreads)
-    if (c < c_lo || c >= c_hi) keys[c] = 0xFFFFFFFFu;
-  const int total = own + 1;
-  uint32_t prefix = 0;
-  int want = a.take;                           // rank within the keys that share the prefix
-  for (int shift = 24; shift >= 0; shift -= 8) {
+  // ---- the list: a warp by itself where its registers hold the scores
+  const int total = own + 1, n_scored = c_hi - c_lo;
+  if (n_scored <= 32 * kHeld) {
+    if (warp == 0) pick_held(keys + c_lo, n_scored, a.take - (total - n_scored), c_lo, out + c_lo, lane);
+    for (int c = tid; c < c_lo; c += kThreads) out[c] = c;
+    for (int c = c_hi + tid; c <= own; c += kThreads) out[a.take - (total - c)] = c;
+    return;
+  }
+  // forced blocks are above every score
+  uint32_t least = 0xFFFFFFFFu, most = 0u;
+#pragma unroll 4
+  for (int c = c_lo + tid; c < c_hi; c += kThreads) {
+    least = min(least, keys[c]);
+    most = max(most, keys[c]);
+  }
+  least = __reduce_min_sync(0xffffffffu, least);
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) {
+    sums[0][warp] = (int)least;
+    sums[1][warp] = (int)most;
+  }
+  for (int c = tid; c < c_lo; c += kThreads) keys[c] = 0xFFFFFFFFu;
+  for (int c = c_hi + tid; c <= own; c += kThreads) keys[c] = 0xFFFFFFFFu;
+  __syncthreads();
+  for (int w = 0; w < kWarps; ++w) {
+    least = min(least, (uint32_t)sums[0][w]);
+    most = max(most, (uint32_t)sums[1][w]);
+  }
+  // The bits that all scores share need no pass; the others by 8 a pass, until all that share
+  // the prefix are in.
+  int bits = 32 - __clz(least ^ most);
+  uint32_t prefix = bits < 32 ? most >> bits << bits : 0u;
+  int want = a.take - (total - n_scored);      // rank within the scores that share the prefix
+  bool whole = want <= 0;
+  if (whole) prefix = 0xFFFFFFFFu;
+  while (bits > 0 && !whole) {
+    const int shift = max(bits - 8, 0);
     __syncthreads();
-    hist[tid] = 0;
+    if (tid < 256) hist[tid] = 0;
     __syncthreads();
-    for (int c = tid; c < total; c += kThreads) {
+#pragma unroll 4
+    for (int c = c_lo + tid; c < c_hi; c += kThreads) {
       const uint32_t k = keys[c];
-      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[(k >> shift) & 255u], 1);
+      if (bits == 32 || (k ^ prefix) >> bits == 0u) atomicAdd(&hist[(k >> shift) & ((1u << (bits - shift)) - 1u)], 1);
     }
     __syncthreads();
     if (warp == 0) {                           // from the highest bin down: lane owns 8 bins
@@ -247,6 +296,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
         if (before < want && before + cnt[i] >= want) {
           pick[0] = 255 - (lane * 8 + i);
           pick[1] = want - before;
+          pick[2] = want - before == cnt[i];
         }
         before += cnt[i];
       }
@@ -254,8 +304,15 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs a) {
     __syncthreads();
     prefix |= (uint32_t)pick[0] << shift;
     want = pick[1];
+    whole = pick[2] != 0;
+    bits = shift;
+  }
+  if (whole) {                                 // all from `prefix` on: above its predecessor
+    --prefix;
+    want = 0;
   }
   // keys above `prefix` are in, and the first `want` equal to it; a warp takes a range
+  __syncthreads();
   const int span = ((total + kWarps - 1) / kWarps + 31) & ~31;
   const int w_lo = warp * span, w_hi = min(total, w_lo + span);
   int above = 0, equal = 0;
@@ -298,11 +355,14 @@ template <int D>
 cudaError_t launch(const SelectArgs &a, int64_t tokens, int num_sms, int device, cudaStream_t st) {
   const size_t smem = smem_of<D>(a.row_tiles, a.max_blocks);
   static SmemLimit limit;
-  const cudaError_t e = limit.raise(reinterpret_cast<const void *>(select_kernel<D>), device, kMaxSmem);
+  const void *kernel = reinterpret_cast<const void *>(select_kernel<D>);
+  cudaError_t e = limit.raise(kernel, device, kMaxSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
-  // CTAs of a cluster: while there are SMs for them, and 64 blocks for each
+  // CTAs of a cluster: while there are SMs for them, and 64 blocks for each (16: more than
+  // every device has to offer; this one does)
   int ranks = 1;
-  while (ranks < 8 && tokens * a.hkv * ranks * 2 <= num_sms && a.max_blocks >= ranks * 2 * 64) ranks *= 2;
+  while (ranks < 16 && tokens * a.hkv * ranks * 2 <= num_sms && a.max_blocks >= ranks * 2 * 64) ranks *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(tokens * ranks), (unsigned)a.hkv);
   cfg.blockDim = dim3(kThreads);

@@ -37,6 +37,67 @@ __device__ __forceinline__ uint32_t ordered(float x) {
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
+// The `want` largest of n <= 32 * kHeld scores, equal ones by lowest index, as block
+// numbers first + index in ascending order; a warp, its scores in registers: the smallest
+// one taken is found bit by bit, until exactly `want` are not below it.
+constexpr int kHeld = 16;
+__device__ __forceinline__ void pick_held(const uint32_t *keys, int n, int want, int first, int32_t *out, int lane) {
+  if (want <= 0) return;
+  uint32_t k[kHeld];
+  uint32_t least = 0xFFFFFFFFu, most = 0u;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const int c = 32 * i + lane;
+    k[i] = 0u;                                    // (no score is 0)
+    if (c < n) {
+      k[i] = keys[c];
+      least = min(least, k[i]);
+    }
+    most = max(most, k[i]);
+  }
+  least = __reduce_min_sync(0xffffffffu, least);
+  most = __reduce_max_sync(0xffffffffu, most);
+  int bit = 31 - __clz(least ^ most);             // the first that differs (-1: none)
+  uint32_t from = bit < 0 ? most : bit == 31 ? 0u : most >> (bit + 1) << (bit + 1);
+  int count = n;                                  // scores >= from
+  for (; bit >= 0 && count != want; --bit) {
+    const uint32_t trial = from | 1u << bit;
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) c += k[i] >= trial;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (c >= want) {
+      from = trial;
+      count = c;
+    }
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  if (count == want) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      const bool in = k[i] >= from && 32 * i + lane < n;
+      const uint32_t m = __ballot_sync(0xffffffffu, in);
+      if (in) out[__popc(m & below)] = first + 32 * i + lane;
+      out += __popc(m);
+    }
+    return;
+  }
+  // several equal `from`, not all of which are in
+  int above = 0;
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) above += k[i] > from;
+  int ties = want - __reduce_add_sync(0xffffffffu, above);
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const uint32_t eq = __ballot_sync(0xffffffffu, k[i] == from);
+    const bool in = k[i] > from || (k[i] == from && __popc(eq & below) < ties);
+    const uint32_t m = __ballot_sync(0xffffffffu, in);
+    if (in) out[__popc(m & below)] = first + 32 * i + lane;
+    out += __popc(m);
+    ties -= __popc(eq);
+  }
+}
+
 // select_tc.cu: chunks of tokens.  False: the batch is not one for it.
 bool select_tc_fits(const HostPlan &hp, const SelectArgs &a);
 cudaError_t launch_select_tc(const HostPlan &hp, const SelectArgs &a, int device, cudaStream_t st);

@@ -55,6 +55,8 @@ CASES = [
     ([5000], [2], 21, 1, 48, 192, 16, 256, 3, 2),                 # two row tiles, the longest list
     ([257] * 40, [1] * 40, 8, 2, 64, 192, 64, 2, 1, 1),           # nothing but forced blocks
     ([40000], [1], 16, 2, 64, 192, 16, 64, 1, 1),                 # 2,500 blocks
+    ([40000], [2], 16, 1, 64, 128, 16, 3, 2, 1),                  # nothing but forced blocks of many
+    ([9000, 30000], [1, 1], 8, 1, 32, 192, 16, 17, 0, 2),         # 562 and 1,875
     ([1000] * 300, [1] * 300, 16, 1, 64, 128, 64, 6, 1, 2),       # one CTA a token
     ([1500, 31, 800], [200, 31, 77], 16, 1, 32, 192, 32, 12, 1, 2),
     ([1100], [530], 32, 2, 16, 128, 16, 20, 0, 3),
@@ -101,6 +103,11 @@ def test_ties_take_the_lowest_index(n):
     got = run(w, dw, w.q, bounds, 64, 10, 1, 2)
     assert np.array_equal(got, P_.select(w, w.q, bounds, 64, 10, 1, 2))
     assert got[-1, 0].tolist() == [0, 1, 2, 3, 4, 5, 6, 7, 62, 63]
+    w2, dw2 = setup([20000], [1], 16, 2, 16)                      # more than a warp holds
+    alike = random_bounds(np.random.default_rng(1), w2, 16, spread=2)
+    alike[...] = alike[:1]
+    got = run(w2, dw2, w2.q, alike, 16, 10, 1, 2)
+    assert got[0, 1].tolist() == [0, 1, 2, 3, 4, 5, 6, 7, 1248, 1249]
     few = bounds.view(np.int8).copy()                             # two values only, heads of zeros too
     few[::3, ..., 384] += 1
     q = w.q.copy()
