@@ -17,17 +17,16 @@
 // attn_prefill.cu, took 531 us on the case below: 96 KB of Q leave no room for the tiles
 // that only one of the two needs.)
 //
-// Roles (640 threads; the tile pipeline is that of attn_prefill.cu):
+// Roles (512 threads; the tile pipeline is that of attn_prefill.cu):
 //   warps 0-3, 4-7  Q rows, then softmax and epilogue of chain 0 / 1 (row p in TMEM lane p)
-//   warps 8-11      widen the K tiles of 8- and 4-bit caches to fp16, in place (the raw rows
-//                   arrive in the operand's own buffer, which they fill a half or a quarter)
-//   warps 12-15     the same for V tiles; zeros behind the request's end; whether the lists are
-//                   ascending
-//   warps 16, 17    one thread each issues the MMAs of chain 0 / 1
-//   warp  18        merges the lists (a token a lane, two in turn) and looks the pages up,
+//   warps 8-11      widen the tiles of 8- and 4-bit caches to fp16, in place (the raw rows
+//                   arrive in the operand's own buffer, which they fill a half or a quarter);
+//                   zeros behind the request's end; whether the lists are ascending
+//   warps 12, 13    one thread each issues the MMAs of chain 0 / 1
+//   warp  14        merges the lists (a token a lane, two in turn) and looks the pages up,
 //                   some tiles ahead; a tile's blocks and who listed them go through a ring
 //                   of descriptors
-//   warp  19        issues the tiles' TMA boxes (of the paged cache itself)
+//   warp  15        issues the tiles' TMA boxes (of the paged cache itself)
 //
 // Keys behind the request's end are zeroed in V tiles.  What else a row must not see (a NaN
 // or an infinity in a block that only its neighbours listed, or behind its token) could
@@ -50,8 +49,8 @@ namespace {
 
 constexpr int kPN = 128;                      // keys of a tile
 constexpr int kPM = kSparseTileRows;          // rows of a Q tile (MMA M)
-constexpr int kMmaWarp = 16, kMergeWarp = 18;
-constexpr int kPThreads = 20 * 32, kLoadThreads = 128;
+constexpr int kMmaWarp = 12, kMergeWarp = 14;
+constexpr int kPThreads = 16 * 32, kLoadThreads = 128;
 constexpr int kTileBlk = 128 * 128;           // one 64-column block of a 128-row tile: 16 KB
 constexpr int kVStage = 2 * kTileBlk;
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;
@@ -77,7 +76,7 @@ struct TileDesc {
 
 struct Bars {
   uint64_t desc_full[kDescs], desc_empty[kDescs];
-  uint64_t k_raw[2], k_full[2], k_empty[2], v_raw[2], v_full[2], v_empty[2], load[2], q_full, merge;
+  uint64_t k_raw[2], k_full[2], k_empty[2], v_raw[2], v_full[2], v_empty[2], load, q_full, merge;
   uint64_t s_full[2], p_hi[2], p_full[2], pv_done[2], done[2];
 };
 
@@ -131,11 +130,33 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     return;
   }
+  if (warp < 8) {
+    // The query rows into the operand tile, 16 a warp, 16 bytes a lane: row r is head r % G of
+    // token r / G; others zeros.  (Rolled, as asynchronous copies: a CTA runs this once, and
+    // unrolled its time was the fetching of its code.)
+    uint8_t *mine = smem + (lane >> 3) * kTileBlk;
+    int tt = warp * 16 / a.group, h = warp * 16 % a.group;
+#pragma unroll 1
+    for (int r = warp * 16; r < warp * 16 + 16; ++r) {
+      const bool live = tt < x.ntok;
+      const uint16_t *src =
+          a.q + ((int64_t)(x.tok0 + (live ? tt : 0)) * a.hq + x.g * a.group + (live ? h : 0)) * DQK + lane * 8;
+      if (lane < DQK / 8)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
+                         tc::smem_u32(mine + tc::sw128_offset(r, lane & 7))),
+                     "l"(src), "r"(live ? 16 : 0)
+                     : "memory");
+      if (++h == a.group) {
+        h = 0;
+        ++tt;
+      }
+    }
+  }
   if (tid == 0) {
     abort_flag = odd_flag = 0;
     for (int i = 0; i < kDescs; ++i) {
       tc::mbar_init(&bars.desc_full[i], 1);
-      tc::mbar_init(&bars.desc_empty[i], F16 ? 14 : 10);     // warps that read it: the loading ones, the chain's
+      tc::mbar_init(&bars.desc_empty[i], 10);     // warps that read it: the loading ones, the chain's
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bars.k_raw[i], 1);
@@ -151,8 +172,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       tc::mbar_init(&bars.done[i], 1);
     }
     tc::mbar_init(&bars.merge, 8);
-    tc::mbar_init(&bars.load[0], 4);
-    tc::mbar_init(&bars.load[1], 4);
+    tc::mbar_init(&bars.load, 4);
     tc::mbar_init(&bars.q_full, 8);
     tc::fence_mbar_init();
   }
@@ -167,13 +187,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
   auto desc_done = [&](int k) { tc::mbar_arrive_warp(&bars.desc_empty[k % kDescs]); };
 
   if (warp >= 8 && warp < kMmaWarp) {
-    
     // ------------------------------------------------------------ load warps
-    const int lt = tid & 127;
-    const bool is_v = warp >= 12;
+    const int lt = tid - 256;
     // Are the lists ascending, their empty entries last, none past the token's own block?
     // Else the job is left to the other kernel.
-    if (is_v) {
+    {
       bool bad = false;
 #pragma unroll 1
       for (int i = lt; i < x.ntok * a.take; i += kLoadThreads) {
@@ -186,8 +204,8 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     int synced = 0;
     auto load_sync = [&]() {
-      tc::mbar_arrive_warp(&bars.load[is_v]);
-      return wait(&bars.load[is_v], synced++ & 1);
+      tc::mbar_arrive_warp(&bars.load);
+      return wait(&bars.load, synced++ & 1);
     };
     // A raw tile of ROWB-byte rows in its stage, widened in place: every thread holds its
     // part in registers before any is written.  4-bit rows go by a row a thread (scales at
@@ -229,7 +247,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       tc::fence_proxy_async_smem();
       return true;
     };
-    bool ok = F16 || is_v;                         // (bf16 K tiles need nothing)
+    bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!(ok = desc_wait(k))) break;
       const TileDesc &d = descs[k % kDescs];
@@ -251,12 +269,9 @@ __global__ void __launch_bounds__(kPThreads, 1)
       const int s = k & 1, phase = (k >> 1) & 1;
       uint8_t *kt = smem + Y::kOffK + s * Y::kKStage, *vt = smem + Y::kOffV + s * kVStage;
       if constexpr (F16) {
-        if (!is_v) {
-          if (!(ok = wait(&bars.k_raw[s], phase))) break;
-          if (!(ok = widen(std::integral_constant<int, kv_row_bytes(KV, DQK)>{}, false, kt, [](int) { return false; }))) break;
-          tc::mbar_arrive_warp(&bars.k_full[s]);
-          continue;
-        }
+        if (!(ok = wait(&bars.k_raw[s], phase))) break;
+        if (!(ok = widen(std::integral_constant<int, kv_row_bytes(KV, DQK)>{}, false, kt, [](int) { return false; }))) break;
+        tc::mbar_arrive_warp(&bars.k_full[s]);
       }
       if (!(ok = wait(&bars.v_raw[s], phase))) break;
       if constexpr (F16) {
@@ -445,24 +460,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const bool valid = tt < x.ntok;
     const int head = x.g * a.group + p % a.group;
     const int pos = valid ? x.pos0 + tt : -1;
-    // The warp's 16 rows into the operand tile, 16 bytes a lane: row r is head r % G of token
-    // r / G; others zeros.  8- and 4-bit caches: times the power of two that puts the row's
-    // largest |q| in [2^14, 2^15), in fp16 (attn_prefill.cu).
-    // (Rolled, the loads as asynchronous copies: a CTA runs this once, and its time was the
-    // fetching of unrolled code, 26 thousand cycles with the scaling.)
+    // The warp's 16 rows have been on their way since the start; 8- and 4-bit caches: times the
+    // power of two that puts the row's largest |q| in [2^14, 2^15), in fp16 (attn_prefill.cu).
     {
       uint8_t *mine = smem + (lane >> 3) * kTileBlk;
-#pragma unroll 1
-      for (int r = warp * 16; r < warp * 16 + 16; ++r) {
-        const bool live = r / a.group < x.ntok;
-        const uint16_t *src =
-            a.q + ((int64_t)(x.tok0 + (live ? r / a.group : 0)) * a.hq + x.g * a.group + r % a.group) * DQK + lane * 8;
-        if (lane < DQK / 8)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(
-                           tc::smem_u32(mine + tc::sw128_offset(r, lane & 7))),
-                       "l"(src), "r"(live ? 16 : 0)
-                       : "memory");
-      }
       asm volatile("cp.async.wait_all;\n" ::: "memory");
       if (F16) {
 #pragma unroll 1
