@@ -365,9 +365,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
       // ------------------------------------------------------------ MMA issuers
       const int t = warp - kMmaWarp;
       const uint32_t id_s = tc::idesc_f16(F16 ? 0 : 1, 0, 0, kPM, kPN), id_pv = tc::idesc_f16(F16 ? 0 : 1, 0, 1, kPM, kDv);
-      const uint32_t q_smem = sbase, s_tmem = tmem + kPN * t, o_tmem = tmem + kTmemO + kDv * t;
+      const uint32_t s_tmem = tmem + kPN * t, o_tmem = tmem + kTmemO + kDv * t;
       if (lane == 0) {
         auto wait1 = [&](uint64_t *bar, uint32_t parity) { return tc::mbar_wait(bar, parity, &abort_flag); };
+        // (descriptors' addresses count 16 bytes: a step is one addition.  Each built anew, an MMA's
+        // issue took 97 cycles in place of the 47 to 66 that it runs.)
+        const uint64_t q_desc = tc::smem_desc_sw128(sbase, 16, 1024);
+        const uint64_t k_desc = tc::smem_desc_sw128(sbase + Y::kOffK + t * Y::kKStage, 16, 1024);
+        const uint64_t v_desc = tc::smem_desc_sw128(sbase + Y::kOffV + t * kVStage, kTileBlk, 1024);
         bool ok = wait1(&bars.q_full, 0);
         for (int c = 0; ok; ++c) {                 // tile 2 c + t
           const int ds = (2 * c + t) % kDescs;
@@ -379,17 +384,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
           tc::tc_fence_after();
 #pragma unroll
           for (int kq = 0; kq < DQK / 16; ++kq) {
-            const uint32_t off = (kq & 3) * 32 + (kq >> 2) * kTileBlk;
-            const uint64_t ad = tc::smem_desc_sw128(q_smem + off, 16, 1024);
-            const uint64_t bd = tc::smem_desc_sw128(sbase + Y::kOffK + t * Y::kKStage + off, 16, 1024);
-            tc::mma_f16_ss(s_tmem, ad, bd, id_s, kq > 0 ? 1u : 0u);
+            const uint32_t off = ((kq & 3) * 32 + (kq >> 2) * kTileBlk) / 16;
+            tc::mma_f16_ss(s_tmem, q_desc + off, k_desc + off, id_s, kq > 0 ? 1u : 0u);
           }
           tc::mma_commit(&bars.s_full[t]);
           tc::mma_commit(&bars.k_empty[t]);
           if (!(ok = wait1(&bars.v_full[t], c & 1))) break;
           auto pv = [&](int kk, bool acc) {
-            const uint64_t bd = tc::smem_desc_sw128(sbase + Y::kOffV + t * kVStage + kk * 16 * 128, kTileBlk, 1024);
-            tc::mma_f16_ts(o_tmem, s_tmem + 32 * (kk >> 1) + 8 * (kk & 1), bd, id_pv, acc ? 1u : 0u);
+            tc::mma_f16_ts(o_tmem, s_tmem + 32 * (kk >> 1) + 8 * (kk & 1), v_desc + kk * (16 * 128 / 16), id_pv,
+                           acc ? 1u : 0u);
           };
           if (!(ok = wait1(&bars.p_hi[t], c & 1))) break;
           tc::tc_fence_after();

@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_tc_kernel(const TcArgs ta)
       // the largest magnitude of each of the warp's 16 rows; lane i (and i + 16) keeps row i's
       const int r = w * 16 + (lane & 15);
       uint32_t mine = 0u;
-#pragma unroll
+#pragma unroll 4
       for (int i = 0; i < 16; ++i) {
         const uint4 v = in ? *reinterpret_cast<const uint4 *>(raw + (w * 16 + i) * Op<D>::kRow + lane * 16)
                            : make_uint4(0u, 0u, 0u, 0u);
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_tc_kernel(const TcArgs ta)
       for (int h = 0; h < 2; ++h) {
         if (staged > 0 && !wait(&bars.b_empty[h], (staged - 1) & 1)) return false;
         uint8_t *dst0 = smem + h * Op<D>::kHalf + (lane >> 3) * Op<D>::kColBlk;
-#pragma unroll 4
+#pragma unroll 1
         for (int i = 0; i < 8; ++i) {
           const int row = w * 8 + i;
           const int4 sc = *reinterpret_cast<const int4 *>(&scale_of[h * 64 + row]);
@@ -644,12 +644,12 @@ __global__ void __launch_bounds__(kThreads, 1) select_tc_kernel(const TcArgs ta)
             if (tile >= 2 && !(ok = wait(&bars.d_empty[d], ((tile >> 1) - 1) & 1))) break;
             tc::tc_fence_after();
             if (lane == 0) {
+              const uint64_t b_desc = tc::smem_desc_sw128(sbase + h * Op<D>::kHalf, 16, 1024);
+              const uint32_t d_tmem = tmem + Op<D>::kTmemD + 64 * d, a_tmem = tmem + j * Op<D>::kACols;
 #pragma unroll
-              for (int q = 0; q < 2 * D / 16; ++q) {
-                const uint64_t bd = tc::smem_desc_sw128(
-                    sbase + h * Op<D>::kHalf + (q >> 2) * Op<D>::kColBlk + (q & 3) * 32, 16, 1024);
-                tc::mma_f16_ts(tmem + Op<D>::kTmemD + 64 * d, tmem + j * Op<D>::kACols + 8 * q, bd, idesc, q > 0);
-              }
+              for (int q = 0; q < 2 * D / 16; ++q)      // (the descriptor's address counts 16 bytes)
+                tc::mma_f16_ts(d_tmem, a_tmem + 8 * q, b_desc + ((q >> 2) * Op<D>::kColBlk + (q & 3) * 32) / 16, idesc,
+                               q > 0);
               tc::mma_commit(&bars.d_full[d]);
               if (j + 1 == na) {
                 tc::mma_commit(&bars.b_empty[h]);
