@@ -543,9 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_kernel(const SparseArgs a,
   const int tok = unit / a.row_tiles, row0 = unit % a.row_tiles * kRows;       // the unit's first head
   const int rows = warp < kWarps && unit < total_units ? min(kRows, a.group - row0) : 0;
   if (warp < kWarps) {
-    const bool lists_it = !SPLIT || warp == 0;
-    if (rows > 0) u.load(a.q + ((int64_t)tok * a.hq + g * a.group + row0) * DQK, rows, a.scale_log2, lane);
-    if (lists_it) {
+    if (!SPLIT || warp == 0) {
       int cnt = 0, pos = -1, b = a.batch;
       if (rows > 0) {
         b = request_of(a.qo_indptr, a.batch, tok);
@@ -568,6 +566,9 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_kernel(const SparseArgs a,
     }
   }
   __syncthreads();
+  // after the lists: the loader's start waits for those, and their loads do not queue behind these
+  // (16 requests, 64 heads, 32 blocks of 64: 12.8 -> 12.3 us)
+  if (rows > 0) u.load(a.q + ((int64_t)tok * a.hq + g * a.group + row0) * DQK, rows, a.scale_log2, lane);
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ loader

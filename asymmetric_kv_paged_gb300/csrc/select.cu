@@ -122,17 +122,19 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectArgs a)
   const int tok = blockIdx.x / ranks, g = blockIdx.y;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  const int b = request_of(a.qo_indptr, a.batch, tok);
+  Request rq;
+  rq.seek(a.qo_indptr, a.seq_lens, a.batch, tok);
+  const int b = rq.b;
   int32_t *out = a.block_idx + ((int64_t)tok * a.hkv + g) * a.take;
-  if (b >= a.batch) {                        // a row that qo_indptr does not hold (the whole cluster)
+  if (b >= a.batch || tok < rq.first) {      // a row that qo_indptr does not hold (the whole cluster)
     if (rank == 0) {
       if (tid == 0) atomicOr(a.err, 4);
       for (int k = tid; k < a.take; k += kThreads) out[k] = -1;
     }
     return;
   }
-  const int q0 = __ldg(a.qo_indptr + b), n = __ldg(a.qo_indptr + b + 1) - q0;
-  const int L0 = __ldg(a.seq_lens + b), L = max(min(L0, a.max_len), n);
+  const int q0 = rq.first, n = rq.end - q0;
+  const int L0 = (int)(rq.shift + rq.end), L = max(min(L0, a.max_len), n);
   if (L != L0 && tid == 0 && rank == 0) atomicOr(a.err, 4);
   const int own = (L - n + tok - q0) / a.block;             // the token's own block
   if (own < a.take) {                                       // all of them
