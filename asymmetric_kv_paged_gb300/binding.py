@@ -460,6 +460,9 @@ def attn_read_bounds(plan: Plan, block_size: int, bounds, page_table, seq_lens, 
                      stream=None) -> None:
     """The bounds as bf16: the last block_indptr[b + 1] - block_indptr[b] complete blocks of
     every request b, into out [rows, Hkv, 2, Dqk] (upper, lower)."""
+    import torch
+    if out is not None:
+        _contiguous("out", out, torch.bfloat16)
     st = (_LIB or load()).attn_read_bounds(
         plan.handle, int(block_size), _ptr(bounds), _ptr(page_table), _ptr(seq_lens), _ptr(block_indptr),
         out.shape[0], _ptr(out), _stream(stream, plan))
@@ -468,6 +471,8 @@ def attn_read_bounds(plan: Plan, block_size: int, bounds, page_table, seq_lens, 
 
 
 def _block_lists(plan: Plan, sparse: attn_sparse_t, block_idx) -> None:
+    import torch
+    _contiguous("block_idx", block_idx, torch.int32)
     if block_idx.numel() != plan.total_q * plan.kv_heads * sparse.num_blocks:
         raise ValueError(f"block_idx has {block_idx.numel()} entries for {plan.total_q} tokens, "
                          f"{plan.kv_heads} KV heads and {sparse.num_blocks} blocks")

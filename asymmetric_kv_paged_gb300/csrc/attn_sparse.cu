@@ -547,10 +547,16 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_kernel(const SparseArgs a,
       int cnt = 0, pos = -1, b = a.batch;
       if (rows > 0) {
         b = request_of(a.qo_indptr, a.batch, tok);
-        if (b >= a.batch) {                         // a row that qo_indptr does not hold
+        int q0 = 0, n = 0;
+        if (b < a.batch) {
+          q0 = __ldg(a.qo_indptr + b);
+          n = __ldg(a.qo_indptr + b + 1) - q0;
+        }
+        // a row that qo_indptr does not hold, or a request longer than the plan's: left as it was
+        if (b >= a.batch || tok < q0 || n > a.max_len) {
+          b = a.batch;
           if (lane == 0) atomicOr(a.err, 4);
         } else {
-          const int q0 = __ldg(a.qo_indptr + b), n = __ldg(a.qo_indptr + b + 1) - q0;
           const int L0 = __ldg(a.seq_lens + b), L = max(min(L0, a.max_len), n);
           if (L != L0 && lane == 0) atomicOr(a.err, 4);
           pos = L - n + tok - q0;
@@ -694,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_kernel(const SparseArgs a,
   }
   auto sink_of = [&](int head) { return a.sinks ? __ldg(a.sinks + head) * kLog2e : -INFINITY; };
   if constexpr (!SPLIT) {
-    if (rows > 0) {
+    if (rows > 0 && sh.req[warp] < a.batch) {
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int r = gq + 8 * y;
@@ -769,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_kernel(const SparseArgs a,
     }
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
-    if (warp < kWarps) {
+    if (warp < kWarps && sh.req[0] < a.batch) {
       for (int r = rank + ranks * warp; r < rows; r += ranks * kWarps) {
         float M = -INFINITY, l = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);

@@ -1,6 +1,6 @@
 // attn_select_blocks: which blocks of the cache a new token attends to.
 //
-// For a token and KV head, with q^ the group's query rows in integers (|q^| <= 127, a
+// For a token and KV head, with q^ the group's query rows in integers (|q^| <= 128, a
 // power of two apart from the bf16 row) and hi, lo a block's 8-bit bounds:
 //   d(h, c) = sum_d max(q^ hi, q^ lo) = q^+ . hi + q^- . lo,   q^+ = max(q^, 0), q^- = min(q^, 0),
 // a contraction of 2 Dqk whole numbers that every step of fp16 x fp16 -> fp32 MMAs holds
@@ -99,7 +99,7 @@ __device__ __forceinline__ void stage_row(QTile<D> &tile, int r, const uint16_t 
     float v[4] = {__uint_as_float(w[k].x << 16), __uint_as_float(w[k].x & 0xFFFF0000u),
                   __uint_as_float(w[k].y << 16), __uint_as_float(w[k].y & 0xFFFF0000u)};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = odd ? 0.f : fminf(fmaxf(rintf(v[i] * unit), -127.f), 127.f);
+    for (int i = 0; i < 4; ++i) v[i] = odd ? 0.f : rintf(v[i] * unit);
     const __half2 lo = __floats2half2_rn(v[0], v[1]), hi = __floats2half2_rn(v[2], v[3]);
     // dims 4p = 64 j + 16 t + 4 s: a lane (r % 8, t)'s words 0 (first pair), 2 (second), + 1 for rows 8..15
     const int j = p / 16, t = p / 4 % 4, s = p % 4;
@@ -126,14 +126,13 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectArgs a)
   rq.seek(a.qo_indptr, a.seq_lens, a.batch, tok);
   const int b = rq.b;
   int32_t *out = a.block_idx + ((int64_t)tok * a.hkv + g) * a.take;
-  if (b >= a.batch || tok < rq.first) {      // a row that qo_indptr does not hold (the whole cluster)
-    if (rank == 0) {
-      if (tid == 0) atomicOr(a.err, 4);
-      for (int k = tid; k < a.take; k += kThreads) out[k] = -1;
-    }
+  const int q0 = rq.first, n = rq.end - q0;
+  // a row that qo_indptr does not hold, or a request longer than the plan's (the whole
+  // cluster): left as it was
+  if (b >= a.batch || tok < q0 || n > a.max_len) {
+    if (rank == 0 && tid == 0) atomicOr(a.err, 4);
     return;
   }
-  const int q0 = rq.first, n = rq.end - q0;
   const int L0 = (int)(rq.shift + rq.end), L = max(min(L0, a.max_len), n);
   if (L != L0 && tid == 0 && rank == 0) atomicOr(a.err, 4);
   const int own = (L - n + tok - q0) / a.block;             // the token's own block

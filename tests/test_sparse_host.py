@@ -55,6 +55,16 @@ def test_list_arrays_of_another_size_are_refused():
             B.attn_run_sparse(p, s, T, T, T, T, T, T, idx, None, 1.0, 1.0, 1.0, T)
 
 
+def test_list_arrays_of_another_type_or_order_are_refused():
+    p, s = host_plan(), B.make_sparse(64, 4)
+    for idx in (torch.zeros(3, 2, 4, dtype=torch.int64), torch.zeros(3, 2, 4),
+                torch.zeros(2, 3, 4, dtype=torch.int32).transpose(0, 1)):
+        with pytest.raises(ValueError):
+            B.attn_select_blocks(p, s, T, T, T, T, T, idx)
+        with pytest.raises(ValueError):
+            B.attn_run_sparse(p, s, T, T, T, T, T, T, idx, None, 1.0, 1.0, 1.0, T)
+
+
 def test_axes():
     assert B.mrope_axes([2, 3, 1]) == [0, 0, 1, 1, 1, 2]
     assert B.mrope_axes([2, 3, 1], in_turn=True) == [0, 1, 2, 0, 1, 1]
