@@ -15,14 +15,18 @@
 // 64, half a block of 128, or several smaller blocks), as TMA boxes in a ring that all
 // eight warps pass through in order, each waiting for every tile (so that no barrier
 // phase can be taken for another):
-//   SHARED  eight neighbouring units, a warp each.  The loader merges their lists in
-//           ascending order, so that a block that several of them chose is fetched
-//           once; a warp skips the tiles that its unit has not chosen.
-//   REDO    the same for the jobs that attn_sparse_tc.cu has marked.
-//   SPLIT   (few units: decode, verify) one unit for all eight warps, each taking half
-//           of every fourth tile; a cluster of up to eight CTAs shares out the list.
-//           The warps' partial results meet in shared memory, the CTAs' through
-//           distributed shared memory.
+//   SHARED  (groups of more than 128 heads) eight neighbouring units, a warp each.  The
+//           loader merges their lists in ascending order, so that a block that several of
+//           them chose is fetched once; a warp skips the tiles that its unit has not chosen.
+//   REDO    the same for the jobs that attn_sparse_tc.cu has marked; writes their marked
+//           rows.
+//   SPLIT   (decode, verify) one unit for all eight warps, each taking half of every
+//           fourth tile; a cluster of up to eight CTAs shares out the list.  The warps'
+//           partial results meet in shared memory, the CTAs' through distributed shared
+//           memory.
+// 32 requests (16/2 heads, 16 blocks of 64, bf16) take 12.3 us, 4 x 8 verified tokens of an
+// E4M3 cache 13.0: 42 MB at 3.4 TB/s on the first, behind a chain of dependent loads
+// (layout, list, pages, keys) and in front of a combine over the cluster.
 //
 // K fragments come from shared memory by ldmatrix (bf16), or as 16- or 8-byte pieces
 // that are widened in registers (E4M3, E2M1: the order of a contraction's index is free,
@@ -701,10 +705,21 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_kernel(const SparseArgs a,
   auto sink_of = [&](int head) { return a.sinks ? __ldg(a.sinks + head) * kLog2e : -INFINITY; };
   if constexpr (!SPLIT) {
     if (rows > 0 && sh.req[warp] < a.batch) {
+      bool write[2];                                  // REDO: the marked rows
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int r = gq + 8 * y;
-        if (r >= rows) continue;
+        write[y] = r < rows;
+        if (MODE == kRedo && write[y]) {
+          const uint16_t *at = a.out + ((int64_t)tok * a.hq + g * a.group + row0 + r) * kDv;
+          write[y] = __ldcg(at) == kMark || __ldcg(at + 64) == kMark;
+        }
+      }
+      __syncwarp();
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int r = gq + 8 * y;
+        if (!write[y]) continue;
         const int head = g * a.group + row0 + r;
         float lse;
         const float f = finish(u.m[y], u.l[y], U::kLift, sink_of(head), a.v_scale, lse);
@@ -836,18 +851,24 @@ cudaError_t launch_one(const SparseArgs &a, const TmaMaps &maps, int ranks, int 
 
 template <int KV, int DQK>
 cudaError_t launch_kv(const HostPlan &hp, const SparseArgs &a, const TmaMaps &maps, int device, cudaStream_t st) {
-  // One unit a CTA while that leaves no SM with more than four of them; its list over as
-  // many CTAs as there are SMs for (up to eight, with two tiles for each).
+  // With up to a unit for each SM: a unit a CTA, its list over as many CTAs as there are SMs
+  // for (up to eight, with two tiles for each).  With more, tiles of neighbouring tokens
+  // (attn_sparse_tc.cu) where they hold 1.5 units a job or more, however empty their 128
+  // rows: a job takes about as long as a unit, whose blocks it shares.  Measured at 4,000 to
+  // 8,000 tokens, 16 blocks of 64, 64/4 heads, bf16 (E4M3), us, a unit a CTA against tiles:
+  //   1,024 units of 1 token a request   163 (132)   160 (173)
+  //   1,024 units of 2 / 4 / 8           136 / 124 / 121   106 / 66 / 44
+  //   192 units of 2 / 8                 35 / 34 (35 / 35)   26 / 30 (32 / 39)
+  // A group of more than 128 heads fits no tile: its row tiles have one list, and eight
+  // units of a CTA share the blocks (256 heads, 64 tokens: 45 us, a unit a CTA 120; from about
+  // two units an SM on).
   const int num_sms = hp.num_sms;
   const int64_t units = (int64_t)a.tokens * a.row_tiles * a.hkv;
-  if (units > 4 * num_sms) {
-    // chunks: jobs at least half full
-    if (a.redo && (int64_t)a.tokens * a.hkv * 2 >= (int64_t)a.jobs * a.job_tokens) {
-      const cudaError_t e = launch_sparse_tc(hp, a, maps, device, st);
-      return e != cudaSuccess ? e : launch_one<KV, DQK, kRedo>(a, maps, 1, num_sms, device, st);
-    }
-    return launch_one<KV, DQK, kShared>(a, maps, 1, num_sms, device, st);
+  if (units > num_sms && a.jobs > 0 && 2 * units >= 3 * (int64_t)a.jobs) {
+    const cudaError_t e = launch_sparse_tc(hp, a, maps, device, st);
+    return e != cudaSuccess ? e : launch_one<KV, DQK, kRedo>(a, maps, 1, num_sms, device, st);
   }
+  if (a.group > kSparseTileRows && units > 2 * num_sms) return launch_one<KV, DQK, kShared>(a, maps, 1, num_sms, device, st);
   const int tiles = (int)((int64_t)a.take * a.block / kTile);
   int ranks = 1;
   while (ranks < 8 && units * ranks * 2 <= num_sms && ranks * 4 <= tiles) ranks *= 2;

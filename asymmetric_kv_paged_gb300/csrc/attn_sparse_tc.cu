@@ -5,9 +5,9 @@
 // tokens of one request and KV head as a Q tile of 128 rows (token-major, G heads a
 // token), walks through the union of their lists in ascending order, 128 keys a tile (two
 // blocks of 64, one of 128, or four or eight smaller ones), and leaves out of each row's
-// softmax the blocks that its token did not list: their weights are zeros.  What is
-// multiplied in vain is bounded by what has to be loaded anyway: a tile's 80 KB take
-// about as long from L2 as the Q tile's products with it.
+// softmax the blocks that its token did not list: their weights are zeros.  Multiplied in
+// vain is what the union has beyond a token's own list (2.8 times its length on the case
+// below), while a block is loaded once for all that listed it.
 //
 // One chain S = Q.K^T, softmax, O += P.V spends most of its time waiting for its own parts.
 // Two chains share the Q tile: tile k belongs to chain k % 2, which has K and V buffers, S,
@@ -16,6 +16,16 @@
 // Q tiles of 128 rows on one chain each, over the union of all 256 rows' blocks as in
 // attn_prefill.cu, took 531 us on the case below: 96 KB of Q leave no room for the tiles
 // that only one of the two needs.)
+//
+// 4096 tokens behind 26,000 (64/4 heads, 16 blocks of 64, bf16) take 484 us, with every unit
+// by itself (attn_sparse.cu) 822; dense attention of the same chunk takes about 3 ms.  The
+// 172 GFLOP of the listed keys would be 89 us at the tensor cores' rate.  A chain needs 4.4
+// thousand cycles a tile, half a tile's time as there are two: 12 + 8 MMAs of 66 cycles, 1.9
+// thousand cycles of softmax and the hand-offs between them; 10 of a CTA's 65 thousand cycles
+// pass before its first tile and 5 behind its last.  Two threads a row for the softmax gave
+// 479 us, a persistent form 504, spinning waits 495: the hand-offs remain, and no room in
+// shared memory or TMEM for a third chain.  4-bit caches (3 x 777 tokens, 12 blocks of 128):
+// 443 us, unit by unit 1403; there the widening of a tile by four warps is the chain's longest part.
 //
 // Roles (512 threads; the tile pipeline is that of attn_prefill.cu):
 //   warps 0-3, 4-7  Q rows, then softmax and epilogue of chain 0 / 1 (row p in TMEM lane p)
@@ -30,11 +40,13 @@
 //
 // Keys behind the request's end are zeroed in V tiles.  What else a row must not see (a NaN
 // or an infinity in a block that only its neighbours listed, or behind its token) could
-// still reach it as 0 * NaN: a job with any NaN or infinity in its sums, and one whose lists
-// are not ascending, is marked and done again by the kernel of attn_sparse.cu, unit by unit.
+// still reach it as 0 * NaN: rows with a NaN or an infinity in their sums are marked (so is
+// the job) and done again by the kernel of attn_sparse.cu, unit by unit.  Lists in any other order are searched
+// for their next entry instead of read on: the same tiles, the same bits.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <climits>
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -76,7 +88,7 @@ struct TileDesc {
 
 struct Bars {
   uint64_t desc_full[kDescs], desc_empty[kDescs];
-  uint64_t k_raw[2], k_full[2], k_empty[2], v_raw[2], v_full[2], v_empty[2], load, q_full, merge;
+  uint64_t k_raw[2], k_full[2], k_empty[2], v_raw[2], v_full[2], v_empty[2], load, checked, q_full, merge;
   uint64_t s_full[2], p_hi[2], p_full[2], pv_done[2], done[2];
 };
 
@@ -116,7 +128,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
   __shared__ Bars bars;
   __shared__ TileDesc descs[kDescs];
   __shared__ uint32_t tmem_slot;
-  __shared__ int abort_flag, odd_flag;
+  __shared__ int abort_flag, odd_flag, mixed_flag;
   __shared__ float row_sc[kPM], row_m[2][kPM], row_l[2][kPM];     // the rows' score scales, the chains' results
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
@@ -153,7 +165,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
   }
   if (tid == 0) {
-    abort_flag = odd_flag = 0;
+    abort_flag = odd_flag = mixed_flag = 0;
     for (int i = 0; i < kDescs; ++i) {
       tc::mbar_init(&bars.desc_full[i], 1);
       tc::mbar_init(&bars.desc_empty[i], 10);     // warps that read it: the loading ones, the chain's
@@ -173,6 +185,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
     }
     tc::mbar_init(&bars.merge, 8);
     tc::mbar_init(&bars.load, 4);
+    tc::mbar_init(&bars.checked, 4);
     tc::mbar_init(&bars.q_full, 8);
     tc::fence_mbar_init();
   }
@@ -190,17 +203,34 @@ __global__ void __launch_bounds__(kPThreads, 1)
     // ------------------------------------------------------------ load warps
     const int lt = tid - 256;
     // Are the lists ascending, their empty entries last, none past the token's own block?
-    // Else the job is left to the other kernel.
     {
-      bool bad = false;
+      // (a token a warp, the entries of up to eight tokens on their way together)
+      bool mixed = false, past = false;
+      const int lw = lt >> 5, blk = 31 - __clz(a.block);
+      for (int e0 = 0; e0 < a.take; e0 += 32) {
+        const int e = e0 + lane;
+        const int32_t *list = a.block_idx + ((int64_t)(x.tok0 + lw) * a.hkv + x.g) * a.take + e;
 #pragma unroll 1
-      for (int i = lt; i < x.ntok * a.take; i += kLoadThreads) {
-        const int tt = i / a.take, e = i % a.take;
-        const int32_t *list = a.block_idx + ((int64_t)(x.tok0 + tt) * a.hkv + x.g) * a.take;
-        const int c = __ldg(list + e), next = e + 1 < a.take ? __ldg(list + e + 1) : -1;
-        bad |= (next >= 0 && (c < 0 || next <= c)) || c > (x.pos0 + tt) / a.block;
+        for (int t0 = lw; t0 < x.ntok; t0 += 32) {
+          int c[8], next[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const bool in = t0 + 4 * i < x.ntok;
+            c[i] = in && e < a.take ? __ldg(list) : -1;
+            next[i] = in && e + 1 < a.take ? __ldg(list + 1) : -1;
+            list += (int64_t)4 * a.hkv * a.take;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            past |= c[i] > (x.pos0 + t0 + 4 * i) >> blk;
+            mixed |= next[i] >= 0 && (c[i] < 0 || next[i] <= c[i]);
+          }
+        }
       }
-      if (bad) odd_flag = 1;
+      if (past) atomicOr(a.err, 16);
+      mixed |= past;
+      if (mixed) mixed_flag = 1;
+      tc::mbar_arrive_warp(&bars.checked);
     }
     int synced = 0;
     auto load_sync = [&]() {
@@ -296,71 +326,93 @@ __global__ void __launch_bounds__(kPThreads, 1)
       // ------------------------------------------------------------ the union of the lists
       const int pieces = kPN / a.block, per_page = a.page_size / a.block;
       const uint32_t own = (uint32_t)((x.pos0 + x.ntok - 1) / a.block);
-      // lane: tokens lane, lane + 32, ..; the entry at hand and the one behind it
-      const int32_t *next_at[2] = {a.block_idx, a.block_idx};
-      int left[2] = {0, 0};
-      uint32_t cur[2], ahead[2];
-      // (an empty entry is the largest number, and so is one past the job's last block)
-      auto entry = [&](int i) -> uint32_t {
-        if (left[i] <= 0) return 0xFFFFFFFFu;
-        --left[i];
-        const uint32_t c = (uint32_t)__ldg(next_at[i]++);
-        return c <= own ? c : 0xFFFFFFFFu;
+      // Lists in ascending order are read on, others searched for their next entry.  False: the
+      // lists are not in order, and nothing has been passed on.
+      auto merge = [&](auto in_order) -> bool {
+        constexpr bool kInOrder = decltype(in_order)::value;
+        // lane: tokens lane, lane + 32, ..; the entry at hand and the one behind it
+        const int32_t *list[2] = {a.block_idx, a.block_idx};
+        uint32_t cur[2], ahead[2];
+        int left[2] = {0, 0};                      // entries unread; searched: the least block still to come
+        auto entry = [&](int i) -> uint32_t {      // (none: the largest number)
+          if (kInOrder) {
+            if (left[i] <= 0) return 0xFFFFFFFFu;
+            --left[i];
+            const uint32_t c = (uint32_t)__ldg(list[i]++);
+            return c <= own ? c : 0xFFFFFFFFu;     // (not past the job's last block)
+          }
+          const int tt = lane + 32 * i;
+          const uint32_t last = (uint32_t)((x.pos0 + tt) / a.block);
+          uint32_t best = 0xFFFFFFFFu;
+#pragma unroll 4
+          for (int e = 0; e < (tt < x.ntok ? a.take : 0); ++e) {
+            const uint32_t c = (uint32_t)__ldg(list[i] + e);
+            if (c >= (uint32_t)left[i] && c <= last) best = min(best, c);
+          }
+          left[i] = best == 0xFFFFFFFFu ? INT_MAX : (int)best + 1;
+          return best;
+        };
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int tt = lane + 32 * i;
+          list[i] = a.block_idx + ((int64_t)(x.tok0 + tt) * a.hkv + x.g) * a.take;
+          if (kInOrder) left[i] = tt < x.ntok ? a.take : 0;
+          cur[i] = entry(i);
+          ahead[i] = entry(i);
+        }
+        bool ok = true;
+        int ends = 0;                              // one for each chain
+        for (int k = 0; ok && ends < 2; ++k) {
+          uint32_t block = 0u, listed[2] = {0u, 0u};
+          int found = 0;
+          const uint32_t groups = (1u << (a.block >> 4)) - 1u;
+          for (int s = 0; s < pieces; ++s) {
+            const uint32_t least = __reduce_min_sync(0xffffffffu, min(cur[0], cur[1]));
+            if (least == 0xFFFFFFFFu) break;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              if (cur[i] == least) {
+                listed[i] |= groups << (s * (a.block >> 4));
+                cur[i] = ahead[i];
+                ahead[i] = entry(i);
+              }
+            if (lane == s) block = least;
+            ++found;
+          }
+          ends += found == 0;
+          const bool in = lane < found;
+          int slot = num_slots, key0 = 0;
+          if (in) {
+            key0 = (int)block * a.block;
+            const int32_t page = __ldg(a.page_table + (int64_t)x.b * a.pt_stride + (int)block / per_page);
+            if (page >= 0 && page < a.num_pages)
+              slot = page * a.page_size + (int)block % per_page * a.block;
+            else
+              atomicOr(a.err, 1);
+          }
+          const int edge = (__any_sync(0xffffffffu, in && key0 + a.block - 1 > x.pos0) ? 1 : 0) |
+                           (__any_sync(0xffffffffu, in && key0 + a.block > x.len) ? 2 : 0);
+          if (kInOrder && k == 0) {                // (asked first thing, it took 1% more)
+            if (!(ok = wait(&bars.checked, 0))) break;
+            if (mixed_flag) return false;
+          }
+          if (k >= kDescs && !(ok = wait(&bars.desc_empty[k % kDescs], (k / kDescs - 1) & 1))) break;
+          TileDesc &d = descs[k % kDescs];
+          if (lane < 8) {
+            d.key0[lane] = key0;
+            d.slot[lane] = slot;
+          }
+          d.listed[lane] = (uint8_t)listed[0];
+          d.listed[lane + 32] = (uint8_t)listed[1];
+          if (lane == 0) {
+            d.end = found == 0;
+            d.edge = edge;
+          }
+          tc::mbar_arrive_warp(&bars.desc_full[k % kDescs]);
+        }
+        return true;
       };
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int tt = lane + 32 * i;
-        next_at[i] = a.block_idx + ((int64_t)(x.tok0 + tt) * a.hkv + x.g) * a.take;
-        left[i] = tt < x.ntok ? a.take : 0;
-        cur[i] = entry(i);
-        ahead[i] = entry(i);
-      }
-      bool ok = true;
-      int ends = 0;                                // one for each chain
-      for (int k = 0; ok && ends < 2; ++k) {
-        uint32_t block = 0u, listed[2] = {0u, 0u};
-        int found = 0;
-        const uint32_t groups = (1u << (a.block >> 4)) - 1u;
-        for (int s = 0; s < pieces; ++s) {
-          const uint32_t least = __reduce_min_sync(0xffffffffu, min(cur[0], cur[1]));
-          if (least == 0xFFFFFFFFu) break;
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (cur[i] == least) {
-              listed[i] |= groups << (s * (a.block >> 4));
-              cur[i] = ahead[i];
-              ahead[i] = entry(i);
-            }
-          if (lane == s) block = least;
-          ++found;
-        }
-        ends += found == 0;
-        const bool in = lane < found;
-        int slot = num_slots, key0 = 0;
-        if (in) {
-          key0 = (int)block * a.block;
-          const int32_t page = __ldg(a.page_table + (int64_t)x.b * a.pt_stride + (int)block / per_page);
-          if (page >= 0 && page < a.num_pages)
-            slot = page * a.page_size + (int)block % per_page * a.block;
-          else
-            atomicOr(a.err, 1);
-        }
-        const int edge = (__any_sync(0xffffffffu, in && key0 + a.block - 1 > x.pos0) ? 1 : 0) |
-                         (__any_sync(0xffffffffu, in && key0 + a.block > x.len) ? 2 : 0);
-        if (k >= kDescs && !(ok = wait(&bars.desc_empty[k % kDescs], (k / kDescs - 1) & 1))) break;
-        TileDesc &d = descs[k % kDescs];
-        if (lane < 8) {
-          d.key0[lane] = key0;
-          d.slot[lane] = slot;
-        }
-        d.listed[lane] = (uint8_t)listed[0];
-        d.listed[lane + 32] = (uint8_t)listed[1];
-        if (lane == 0) {
-          d.end = found == 0;
-          d.edge = edge;
-        }
-        tc::mbar_arrive_warp(&bars.desc_full[k % kDescs]);
-      }
+      if (!merge(std::true_type{})) merge(std::false_type{});
     } else if (warp < kMergeWarp) {
       // ------------------------------------------------------------ MMA issuers
       const int t = warp - kMmaWarp;
@@ -648,7 +700,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
         reinterpret_cast<uint4 *>(row + q * 16)[1] = make_uint4(w[4], w[5], w[6], w[7]);
       }
       if (valid && a.lse && t == 0) a.lse[(int64_t)(x.tok0 + tt) * a.hq + head] = lse;
-      if (valid && odd) odd_flag = 1;
+      if (valid && odd) {                          // a mark on the row: no other row's output is NaN
+        row[64 * t] = kMark;
+        odd_flag = 1;
+      }
     }
   }
   tc::tc_fence_before();

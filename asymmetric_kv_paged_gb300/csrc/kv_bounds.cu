@@ -13,8 +13,12 @@
 // times its scale); the row groups meet by shuffle, so that nothing is shared and warps
 // never wait for one another.  Which block a warp takes follows from the requests'
 // counts of completed blocks, summed up 32 requests a step.  The kernel reads each key
-// once: what bounds it is memory for many blocks, and for a decode step the launch and a
-// chain of dependent loads.
+// once.  For a decode step (64 requests, 8 tokens each: 6.0 us, reading back 2.5) the launch
+// and a chain of dependent loads bound it.  All 17,000 records of a 4-bit cache (64 keys, 4
+// heads, 124 MB of keys) take 56 us, 2.2 TB/s: the widening of the nibbles fills the issue
+// slots' better half and its registers leave 34 KB in flight on an SM, four rows of 16 bytes
+// a lane ahead (a CTA a block with rounded codes by comparison: 60 us for the update and 121
+// in all with the reading, now 65).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -352,7 +356,8 @@ BoundsArgs make_args(attn_plan_t plan, int32_t block_size, const int32_t *page_t
 
 template <int D>
 cudaError_t launch_update(const BoundsArgs &a, int kv, int64_t most, int num_sms, cudaStream_t st) {
-  // a warp a block and head; where there are SMs for it, a CTA
+  // a warp a block and head; where there are SMs for it, a CTA (32 requests of 128 new tokens,
+  // 384 records at most: 7.7 us against 9.1; of 512, 1,152 records: 15.0 against 9.8)
   const int64_t per = kThreads / 32, room = (int64_t)num_sms * 4;
   const bool wide = most <= room;
   const dim3 grid((unsigned)std::min(wide ? most : (most + per - 1) / per, room)), block(kThreads);

@@ -12,8 +12,14 @@
 // of block g straight into registers (the order of a contraction's index is free, so
 // that a piece feeds four MMAs) and widens them to fp16 there; the query rows wait in
 // shared memory as operand fragments.  Scores meet as ordered integers in the shared
-// memory of the cluster's first CTA, which finds the smallest one taken by a radix
-// select of 8 bits a pass and writes the list in order.
+// memory of the cluster's first CTA, which finds the smallest one taken (by a warp bit by
+// bit up to 512 scores, else by a radix select of 8 bits a pass) and writes the list in order.
+//
+// 32 requests of 1,024 to 32,767 tokens (16/2 heads, blocks of 64): 8.9 us, one of 16,384
+// blocks (64/4 heads) 26 us, which the 26 MB of bounds would take 3.9 us to read: a chain
+// of dependent loads (layout, page, bounds), the cluster's barriers and the passes over the
+// scores by one CTA bound it, not the bandwidth.  Eight warps, no step ahead and clusters of
+// eight at most: 13.9 and 87 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

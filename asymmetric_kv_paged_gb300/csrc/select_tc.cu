@@ -25,8 +25,14 @@
 //   17     the query rows of the next token tile, as bulk copies
 // TMEM: A 2 x Dqk columns, D 128.  Every wait is bounded in time.
 //
-// The form with the tokens at rest and the bounds widened for every token tile took 316 us
-// for 4096 tokens (64/4 heads) over 470 blocks, a token a CTA (select.cu) 800.
+// 4096 tokens (64/4 heads) over 470 blocks take 150 us; with the tokens at rest and the
+// bounds widened for every token tile 316, a token a CTA (select.cu) 800.  Its 47 GFLOP
+// (94 with q^+ and q^- apart) are 49 us of the tensor cores, which are busy 28% of the time:
+// staging, epilogue, MMA issue and lists each need 7 to 9 thousand of a token tile's 11
+// thousand cycles, side by side on 54% of the issue slots.  Every CTA of a cluster
+// stages all query rows; to share that out is what is left.  Not kept: eight epilogue
+// warps (80 registers: 173 us), the rounding by packed bf16 FMAs (fewer instructions, the same
+// 150), the staging loops unrolled (153 to 157), scores by asynchronous remote stores (158).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -709,12 +715,19 @@ bool shape(const HostPlan &hp, const SelectArgs &a, TcArgs *t, int *ranks) {
       t->ns = n[1];
     }
   if (!t->nr) return false;
-  // token tiles at least half full, and enough of them that their bounds stay for a while
-  int64_t tiles = 0;
+  // Two tokens a request or more, which share its widened bounds however empty their tile
+  // (4,000 to 8,000 tokens, blocks of 64, 1,024 tokens x KV heads, us, select.cu against this:
+  // 16 heads a group 44 / 69, 44 / 40, 44 / 24 with 1, 2, 4 tokens a request; 64 heads 72 / 103,
+  // 70 / 48, 68 / 35), and more than two tokens x KV heads for each SM (one request, 256 tokens
+  // x KV heads 12.8 / 17.2, 384 18.0 / 17.2, 512 23.2 / 16.2).
+  int64_t tiles = 0, requests = 0;
   const auto &qo = hp.qo_indptr;
-  for (size_t b = 0; b + 1 < qo.size(); ++b) tiles += (qo[b + 1] - qo[b] + t->tile_tokens - 1) / t->tile_tokens;
+  for (size_t b = 0; b + 1 < qo.size(); ++b) {
+    tiles += (qo[b + 1] - qo[b] + t->tile_tokens - 1) / t->tile_tokens;
+    requests += qo[b + 1] > qo[b];
+  }
   const int64_t clusters = std::max(1, hp.num_sms / *ranks);
-  if ((int64_t)a.tokens * 2 < tiles * t->tile_tokens || (int64_t)a.tokens * a.hkv <= 2 * hp.num_sms) return false;
+  if (a.tokens < 2 * requests || (int64_t)a.tokens * a.hkv <= 2 * hp.num_sms) return false;
   // ranges of as many token tiles as give every cluster one
   t->range = (int32_t)std::max<int64_t>(1, (tiles * a.hkv + clusters - 1) / clusters);
   int64_t ranges = 0;

@@ -70,6 +70,10 @@ __device__ __forceinline__ bool find_job(const SparseArgs &a, int job, SparseJob
   return false;
 }
 
+// The mark of a row that attn_sparse_tc.cu leaves to the other kernel: a NaN as the first
+// value of either half of its output.
+constexpr uint16_t kMark = 0x7FFF;
+
 // What a row's maximum and sum make of its output: the factor of O and the natural
 // log-sum-exp; sink2 in base 2.
 __device__ __forceinline__ float finish(float m, float l, float lift, float sink2, float v_scale, float &lse) {

@@ -129,7 +129,10 @@ def test_blocks_past_the_own_one_are_left_out(n):
 @pytest.mark.parametrize("block", [16, 128])
 def test_unseen_slots_do_not_matter(kv, n, block):
     """Keys that a token does not see, and those only its neighbours chose, may be NaN: no bit
-    of its rows changes."""
+    of its rows changes; among the 300 tokens, where rows beside a NaN are summed anew in
+    another order, they stay where they were, as close to the 64-bit form as before (either
+    order is within assert_close's bound of it: the bound adds up every step's error in magnitude
+    and holds for any order)."""
     w, dw = setup(kv, [1000], [n], 16, 2, 128)
     rng = np.random.default_rng(3)
     lists = random_lists(rng, w, block, 5)
@@ -142,7 +145,11 @@ def test_unseen_slots_do_not_matter(kv, n, block):
             flat[int(P_.slots(w, 0, c))] = float("nan") if kv == "bf16" else 0x7F
     o2, l2 = run(w, dw, lists, block)
     same = slice(0, last + 1)
-    assert np.array_equal(o[same], o2[same]) and np.array_equal(l[same], l2[same])
+    if n == 2:
+        assert np.array_equal(o[same], o2[same]) and np.array_equal(l[same], l2[same])
+    ref = P_.attend(w, w.q, block, lists)                          # (of the caches without the NaNs)
+    for got in ((o, l), (o2, l2)):
+        P_.assert_close(got[0][same], got[1][same], [x[same] for x in ref], kv)
     sees = ((lists[last + 1:] == 2).any(-1)) | ((lists[last + 1:] == 999 // block).any(-1) &
                                                 (np.arange(last + 1, n) == n - 1)[:, None])
     assert np.array_equal(np.isnan(l2[last + 1:]).reshape(-1, 2, 8).all(-1), sees)
