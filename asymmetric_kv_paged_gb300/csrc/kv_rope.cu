@@ -13,6 +13,11 @@
 // to what the cache (or q_out) holds.  Dims that are not rotated keep their bits
 // in a bf16 cache and in q_out.
 //
+// By axes (attn_append_kv_mrope) the row of pair i's cosine and sine is that of the axis
+// which turns it, positions[axis(i)][token]: the axes are two bits a pair in the kernel's
+// arguments, a lane picks one of its up to four positions an angle and loads cosine and
+// sine one by one (one axis: four at a time).
+//
 // 4-bit rows (e2m1.cuh): y = x / tensor scale; per 16 values the block scale
 // is E4M3(max|y| / 6), nearest even, saturating at 448; the codes are
 // E2M1(y / block scale), nearest even, saturating at 6 (all zeros under a zero
@@ -37,6 +42,8 @@
 // 3.4 us, 4.5 with rotation and queries: the launch and four dependent loads.  Four
 // CTAs of 64 registers an SM: three of 80 took 55 us on the first, five 12.3 us on
 // the third; twice as many, shorter warps' shares 10.9 us on the third.
+// Three axes in turn, 4096 tokens of 64 and 4 heads to E4M3: 50 us against 45 with one
+// position (append and reading back); a decode step's 33 tokens 8.1 with the reading, in a graph.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -477,14 +477,14 @@ attn_status_t attn_read_bounds(attn_plan_t plan, int32_t block_size, const void 
  * num_blocks in all:
  *   q^_h = the row of query head h in integers, round to nearest even of q_h / 2^(e_h),
  *          e_h the least exponent with max |q_h| <= 127 * 2^(e_h) (in [-126, 121], 0 for
- *          a row of zeros);
+ *          a row of zeros), so that |q^| <= 128;
  *   d(h, c) = sum over dims of max(q^_h * upper code, q^_h * lower code): an upper bound
  *          on the scores of q^_h in the block;
  *   score(c) = 2^(e_c) * max over the group's heads h of 2^(e_h - max e) * d(h, c).
  * d is a whole number below 2^22, so that every term is exact in fp32 (short of under-
  * or overflow, which are fp32's): equal inputs give equal lists on any plan and grid.  A
  * block with an infinity or a NaN scores +inf.  A query head with one takes no part; with
- * no head left all scores are equal.
+ * no head left all other blocks' scores are equal.
  *   bounds       of every complete block before the last_blocks of the request's last
  *                token (only those are read).
  *   block_idx    int32 [total_q][Hkv][num_blocks]: the list, ascending, then -1.
@@ -492,7 +492,9 @@ attn_status_t attn_read_bounds(attn_plan_t plan, int32_t block_size, const void 
  * Blocks on page ids outside the pool score as blocks of zeros (bit 0).
  * q must be 16-byte aligned.  Runs on `stream`; no allocation, no synchronisation; can be
  * captured.  Errors: INVALID_ARG (also a plan with window > 0), UNSUPPORTED (block
- * size, or more than ATTN_SPARSE_MAX_BLOCKS blocks in the plan's longest request), CUDA.
+ * size, more than ATTN_SPARSE_MAX_BLOCKS blocks in the plan's longest request, or more
+ * than 224 KB for 4 bytes a block of it and 6.2 KB (head_dim 128: 4.2) for each 16 heads
+ * of a group), CUDA.
  */
 attn_status_t attn_select_blocks(attn_plan_t plan, const attn_sparse_t *sparse, const void *q,
                                  const void *bounds, const int32_t *page_table,
@@ -513,11 +515,13 @@ attn_status_t attn_select_blocks(attn_plan_t plan, const attn_sparse_t *sparse, 
  *                window must be 0).
  * A token whose list holds no block gets zeros and -inf (with sinks: the sink's own lse).
  * Slots that a token does not see, invisible ones of a shared tile among them, do not
- * reach its rows whatever they hold.  Arithmetic is that of the other kernels: bf16
+ * reach its rows whatever they hold (in a chunk of tokens, rows beside a NaN or an
+ * infinity are summed anew, in another order).  Arithmetic is that of the other kernels: bf16
  * products for BF16 caches, fp16 with exactly scaled queries for the others, sums in
  * fp32.  Lengths are clamped as by attn_select_blocks (bit 2); page ids outside the pool
- * are read as rows of zeros (bit 0).  Needs no workspace.  Runs on `stream`; no
- * allocation, no synchronisation; can be captured.
+ * are read as rows of zeros (bit 0).  Needs no workspace; like the runs of attn_run_paged,
+ * those of one plan must be ordered on one stream.  Runs on `stream`; no allocation, no
+ * synchronisation; can be captured.
  * Errors: INVALID_ARG, UNSUPPORTED (block size; num_pages * page_size > 2^31 - 65), CUDA.
  */
 attn_status_t attn_run_sparse(attn_plan_t plan, const attn_sparse_t *sparse, const void *q,
