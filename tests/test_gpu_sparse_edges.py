@@ -259,3 +259,39 @@ def test_shifts_out_of_every_range_skip_their_tokens():
                            dw.qo_indptr)
     assert B.attn_get_device_error(dw.plan) == 8
     assert (q_out == 7).all((1, 2)).tolist() == [True, True, False]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "fp4"])
+def test_rows_beside_nans_of_a_mixed_batch(kv):
+    """Decode requests beside a chunk of tokens, sinks, lists in any order, one value of a block NaN:
+    the dims of the rows that list it, and the other rows stay close to the 64-bit form; without
+    lse_out the same bits."""
+    from asymmetric_kv_paged_gb300 import binding as B
+    seq, n = [900] * 40 + [700], [1] * 40 + [250]
+    w, dw = sparse_setup(kv, seq, n, 16, 2, 64, sinks=True)
+    lists = random_lists(np.random.default_rng(3), w, 64, 6)
+    lists = np.random.default_rng(4).permuted(lists, axis=-1)
+    ref = P_.attend(w, w.q, 64, lists, w.sinks)
+    flat = dw.v_cache.view(-1, *dw.v_cache.shape[2:])
+    slot = int(P_.slots(w, 40, 3 * 64 + 5))                        # key 197 of the chunk's request, head 1
+    if kv == "fp4":
+        flat[slot, 1, 64] = 0x7F                                   # the scale of dims 0 to 15
+    else:
+        flat[slot, 1, 7] = float("nan") if kv == "bf16" else 0x7F
+    dims = slice(0, 16) if kv == "fp4" else slice(7, 8)
+    o, l = attend(w, dw, lists, 64)
+    hit = (lists[:, 1] == 3).any(-1) & (np.arange(w.total_q) >= 40)
+    assert 20 < hit.sum() < 240
+    assert np.isnan(o[hit, 8:, dims]).all() and not np.isnan(o[~hit]).any() and not np.isnan(o[:, :8]).any()
+    rows = np.ones((w.total_q, 16), bool)
+    rows[hit, 8:] = False
+    P_.assert_close(o[rows], l[rows], [x[rows] for x in ref], kv)
+    clean = np.ones(128, bool)
+    clean[dims] = False
+    tol = [x[hit, 8:][..., clean] if x.ndim == 3 else x[hit, 8:] for x in ref]
+    P_.assert_close(o[hit, 8:][..., clean], l[hit, 8:], tol, kv)
+    out = torch.empty(w.total_q, 16, 128, dtype=BF, device="cuda")
+    B.attn_run_sparse(dw.plan, B.make_sparse(64, 6, 0, 1), dw.q, dw.k_cache, dw.v_cache, dw.page_table, dw.seq_lens,
+                      dw.qo_indptr, device(lists), dw.sinks, w.softmax_scale, w.k_scale, w.v_scale, out)
+    assert np.array_equal(out.double().cpu().numpy(), o, equal_nan=True)
+    assert B.attn_get_device_error(dw.plan) == 0
