@@ -772,9 +772,9 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_kernel(const SparseArgs a,
         for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sh.m[w][r]);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float f = sh.m[w][r] == -INFINITY ? 0.f : exp2f(sh.m[w][r] - M);
+          if (sh.m[w][r] == -INFINITY) continue;      // (nothing seen)
+          const float f = exp2f(sh.m[w][r] - M);      // (0 for a warp far below the others, whose NaN stays one)
           const float4 v = *reinterpret_cast<const float4 *>(part + (w * kRows + r) * kStride + 4 * lane);
-          if (f == 0.f) continue;                     // (nothing seen: no product with what it holds)
           l += f * sh.l[w][r];
           acc.x += f * v.x;
           acc.y += f * v.y;
