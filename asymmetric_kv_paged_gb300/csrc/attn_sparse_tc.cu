@@ -667,8 +667,10 @@ __global__ void __launch_bounds__(kPThreads, 1)
     if (ok) {
       tc::tc_fence_after();
       const float m0 = row_m[0][p], m1 = row_m[1][p], M = fmaxf(m0, m1);
-      const float w0 = m0 == -INFINITY ? 0.f : exp2f(m0 - M), w1 = m1 == -INFINITY ? 0.f : exp2f(m1 - M);
-      const float l = (w0 == 0.f ? 0.f : w0 * row_l[0][p]) + (w1 == 0.f ? 0.f : w1 * row_l[1][p]);
+      // (a chain far below the other has a weight of 0 and counts all the same: its NaN is the row's)
+      const bool saw0 = m0 != -INFINITY, saw1 = m1 != -INFINITY;
+      const float w0 = saw0 ? exp2f(m0 - M) : 0.f, w1 = saw1 ? exp2f(m1 - M) : 0.f;
+      const float l = (saw0 ? w0 * row_l[0][p] : 0.f) + (saw1 ? w1 * row_l[1][p] : 0.f);
       float lse;
       const float sink2 = a.sinks && valid ? __ldg(a.sinks + head) * kLog2e : -INFINITY;
       const float f = finish(M, l, kLift, sink2, a.v_scale, lse);
@@ -688,7 +690,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           float u[2];
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
-            const float u0 = w0 == 0.f ? 0.f : __uint_as_float(o0[j + y]), u1 = w1 == 0.f ? 0.f : __uint_as_float(o1[j + y]);
+            const float u0 = saw0 ? __uint_as_float(o0[j + y]) : 0.f, u1 = saw1 ? __uint_as_float(o1[j + y]) : 0.f;
             sum += 0.f * u0 + 0.f * u1;
             u[y] = u0 * f0 + u1 * f1;
           }

@@ -1,7 +1,7 @@
 """attn_run_sparse: a visible NaN whose key's neighbours weigh nothing still reaches its row.
 
-Keys of one stretch score 0, all others a few hundred: where a row's results of several warps
-or CTAs meet, the stretch's share is 2^-300 or less of the row's, 0 in fp32.  A NaN
+Keys of one stretch score 0, all others a few hundred: where a row's results of several warps,
+CTAs or chains of tiles meet, the stretch's share is 2^-300 or less of the row's, 0 in fp32.  A NaN
 in it is still the row's (a NaN score makes the whole row NaN, a NaN in a V row its dims)."""
 import numpy as np
 import pytest
@@ -79,3 +79,13 @@ def test_decode(kv, cache, take, half, whole):
     stretch = np.arange(32 * half, 32 * half + 32)
     w, clean = build(kv, 64 * take, 1, stretch, stretch if whole else stretch[13:14], cache, 192)
     check(w, kv, np.broadcast_to(np.arange(take, dtype=np.int32), (1, 2, take)).copy(), clean, cache)
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("cache", ["k", "v"])
+@pytest.mark.parametrize("tiles", [(1,), (0, 2)])
+def test_chunk(kv, cache, tiles):
+    """Tiles of two blocks, every second one a chain's: one chain's keys score 0, one of them NaN."""
+    n, take = 300, 6
+    stretch = np.concatenate([np.arange(128 * t, 128 * t + 128) for t in tiles])
+    w, clean = build(kv, 64 * take + n, n, stretch, stretch[77:78], cache, 192 if kv != "fp8" else 128)
+    check(w, kv, np.broadcast_to(np.arange(take, dtype=np.int32), (n, 2, take)).copy(), clean, cache)
