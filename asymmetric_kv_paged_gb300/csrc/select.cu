@@ -11,7 +11,9 @@
 // lane (g, t) (g = lane / 4, t = lane % 4) reads 16-byte pieces t, t + 4, .. of the bounds
 // of block g straight into registers (the order of a contraction's index is free, so
 // that a piece feeds four MMAs) and widens them to fp16 there; the query rows wait in
-// shared memory as operand fragments.  Scores meet as ordered integers in the shared
+// shared memory as operand fragments.  A row's factor 2^(e_h - max e) is applied as two powers
+// of two, the first of which keeps every whole number exact, so that the product is rounded
+// once however far the heads lie apart.  Scores meet as ordered integers in the shared
 // memory of the cluster's first CTA, which finds the smallest one taken (by a warp bit by
 // bit up to 512 scores, else by a radix select of 8 bits a pass) and writes the list in order.
 //
@@ -63,10 +65,14 @@ __device__ __forceinline__ uint32_t min_h2(uint32_t a, uint32_t b) {
   return d;
 }
 
+// The smallest factor that is one multiplication: from 2^-122 on a whole number times it is a
+// normal fp32; what is left of it (2^-125 at least) is multiplied behind it.
+constexpr int kLeastLog2 = -122;
+
 template <int D>
 struct QTile {                         // 16 query rows as A fragments, and their factors
   uint4 frag[D / 16][32];
-  float factor[16];                    // 2^(e_h - E); -1: no such row, or one that takes no part
+  float factor[16];                    // 2^(e_h - E), at least 2^kLeastLog2; -1: no such row, or one that takes no part
 };
 
 // Row r of a token's query heads (r < group) as integers, D / 32 a lane in element order
@@ -122,6 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectArgs a)
   int *exps = reinterpret_cast<int *>(smem + a.row_tiles * sizeof(QTile<D>));  // [row_tiles * 16]
   uint32_t *keys = reinterpret_cast<uint32_t *>(exps + a.row_tiles * 16);      // [max_blocks]
   __shared__ int hist[256], sums[2][kWarps], pick[3];
+  __shared__ int top_exp, far_apart;      // E, and whether a factor is below 2^kLeastLog2
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -181,6 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectArgs a)
     look(c_at + step);
   }
   // ---- the query rows
+  if (tid == 0) far_apart = 0;
   for (int r = warp; r < a.row_tiles * 16; r += kWarps) {
     const uint16_t *row = r < a.group ? a.q + ((int64_t)tok * a.hq + g * a.group + r) * D : nullptr;
     stage_row<D>(tiles[r >> 4], r & 15, row, lane, exps + (r & ~15));
@@ -189,7 +197,10 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectArgs a)
   for (int r = tid; r < a.row_tiles * 16; r += kThreads) {
     int top = INT_MIN;
     for (int i = 0; i < a.group; ++i) top = max(top, exps[i]);
-    tiles[r >> 4].factor[r & 15] = exps[r] == INT_MIN ? -1.f : ldexpf(1.f, exps[r] - top);
+    const bool in = exps[r] != INT_MIN;
+    tiles[r >> 4].factor[r & 15] = in ? pow2(max(exps[r] - top, kLeastLog2)) : -1.f;
+    if (r == 0) top_exp = top;
+    if (in && exps[r] - top < kLeastLog2) far_apart = 1;
   }
   __syncthreads();
   asm volatile("barrier.cluster.wait.aligned;\n" ::: "memory");
@@ -220,10 +231,20 @@ __global__ void __launch_bounds__(kThreads, 1) select_kernel(const SelectArgs a)
         }
       }
       const float f0 = tiles[rt].factor[gq], f1 = tiles[rt].factor[gq + 8];
+      float s[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s[x] = (acc[0][x] + acc[1][x]) * (x < 2 ? f0 : f1);
+      if (far_apart) {
+        const int *e = exps + rt * 16 + gq;
+        const float r0 = f0 < 0.f ? 1.f : pow2(min(e[0] - top_exp - kLeastLog2, 0));
+        const float r1 = f1 < 0.f ? 1.f : pow2(min(e[8] - top_exp - kLeastLog2, 0));
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[x] *= x < 2 ? r0 : r1;
+      }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        if (f0 >= 0.f) best[x] = fmaxf(best[x], (acc[0][x] + acc[1][x]) * f0);
-        if (f1 >= 0.f) best[x] = fmaxf(best[x], (acc[0][2 + x] + acc[1][2 + x]) * f1);
+        if (f0 >= 0.f) best[x] = fmaxf(best[x], s[x]);
+        if (f1 >= 0.f) best[x] = fmaxf(best[x], s[2 + x]);
       }
     }
 #pragma unroll

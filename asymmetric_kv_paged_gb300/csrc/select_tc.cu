@@ -8,7 +8,7 @@
 // their maximum without a shuffle.  A row that is missing or takes no part repeats one
 // that does, which leaves the maximum as it is.  Rows carry their factor 2^(e_h - max e)
 // in the fp16 integers (exact down to 2^-16; what is left of smaller ones is multiplied
-// to the scores).
+// to the scores, as two powers of two where one would round twice or vanish).
 //
 // The bounds stay and the tokens stream by: a cluster of CTAs shares out the blocks of
 // one (request, KV head), two tiles of 128 for each CTA, widened once into tensor memory,
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_tc_kernel(const TcArgs ta)
   // integers, and whether there are any
   __shared__ int exps[kN];
   __shared__ __align__(16) RowScale scale_of[kN];
-  __shared__ float resid_of[2][kN];
+  __shared__ float resid_of[2][2][kN];
   __shared__ int spread[2];
   __shared__ uint32_t home[kN / 4];              // where a token's scores go (buffer 0)
   __shared__ __align__(16) int hist[kPickWarps][256];
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) select_tc_kernel(const TcArgs ta)
             for (int i = 0; i < 64; ++i) v[i] = __uint_as_float(x[i / 32][i % 32]);
             if (odd_factors) {
 #pragma unroll
-              for (int i = 0; i < 64; ++i) v[i] *= resid_of[rb][64 * h + i];
+              for (int i = 0; i < 64; ++i) v[i] = v[i] * resid_of[rb][0][64 * h + i] * resid_of[rb][1][64 * h + i];
             }
             // maxima of 4, 8, .. columns side by side
 #pragma unroll
@@ -350,7 +350,6 @@ __global__ void __launch_bounds__(kThreads, 1) select_tc_kernel(const TcArgs ta)
     auto stage = [&](const Item &x, int k_tile) -> bool {
       const int tokens = min(ta.tile_tokens, x.ntok - k_tile * ta.tile_tokens);
       const int qb = staged % ta.nr, rb = staged & 1;
-      float *resid = resid_of[rb];
       if (staged >= 2 && !wait(&bars.r_empty[rb], ((staged >> 1) - 1) & 1)) return false;
       if (!wait(&bars.raw_full[qb], (staged / ta.nr) & 1)) return false;
       const uint8_t *raw = smem + 2 * Op<D>::kHalf + qb * Op<D>::kRaw;
@@ -397,7 +396,9 @@ __global__ void __launch_bounds__(kThreads, 1) select_tc_kernel(const TcArgs ta)
       const int from = odd ? first : r;
       const int ef = from == INT_MAX ? 0 : odd ? exps[from] : e, k = from == INT_MAX ? 0 : top - ef;
       if (lane < 16) {
-        resid[r] = k > 16 ? ldexpf(1.f, 16 - k) : 1.f;
+        // (a whole number times 2^-122 is a normal fp32, still exact: one rounding, with the rest)
+        resid_of[rb][0][r] = pow2(min(16 - min(k, 122), 0));
+        resid_of[rb][1][r] = pow2(min(122 - k, 0));
         if (k > 16) spread[rb] = 1;
         const __half2 sh2 = __float2half2_rn(pow2(-min(k, 16)));
         scale_of[r] = RowScale{pow2(-ef), *reinterpret_cast<const uint32_t *>(&sh2), from == INT_MAX ? -1 : from, 0};

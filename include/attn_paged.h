@@ -481,8 +481,9 @@ attn_status_t attn_read_bounds(attn_plan_t plan, int32_t block_size, const void 
  *   d(h, c) = sum over dims of max(q^_h * upper code, q^_h * lower code): an upper bound
  *          on the scores of q^_h in the block;
  *   score(c) = 2^(e_c) * max over the group's heads h of 2^(e_h - max e) * d(h, c).
- * d is a whole number below 2^22, so that every term is exact in fp32 (short of under-
- * or overflow, which are fp32's): equal inputs give equal lists on any plan and grid.  A
+ * d is a whole number below 2^22, so that every term is exact in fp32, short of under-
+ * or overflow: the product with 2^(e_h - max e), then the largest one's with 2^(e_c), are
+ * each rounded to fp32 once.  Equal inputs give equal lists on any plan and grid.  A
  * block with an infinity or a NaN scores +inf.  A query head with one takes no part; with
  * no head left all other blocks' scores are equal.
  *   bounds       of every complete block before the last_blocks of the request's last
