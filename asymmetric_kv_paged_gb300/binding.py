@@ -174,6 +174,11 @@ class Plan:
         self.total_q = _total_q(problem)         # new tokens of the whole batch
         self.batch = problem.batch
         self.kv_heads = problem.num_kv_heads
+        self.head_dim_qk = problem.head_dim_qk
+        # bytes of a bounds array, per block size that the pages hold whole
+        page = problem.num_pages * problem.num_kv_heads * attn_bounds_row_bytes(problem.head_dim_qk)
+        self.bounds_bytes = {b: page * (problem.page_size // b) for b in (16, 32, 64, 128)
+                             if problem.page_size % b == 0}
         self._keep = keep
 
     def destroy(self) -> None:
@@ -445,10 +450,23 @@ def attn_bounds_row_bytes(head_dim: int) -> int:
     return n.value
 
 
+def _bounds_array(plan: Plan, block_size: int, bounds) -> None:
+    """Records of another block size, type or order than the call's would be read or written past
+    the array's end.  (A missing array, another block size and a host plan the library refuses.)"""
+    import torch
+    need = plan.bounds_bytes.get(block_size)
+    if bounds is None or need is None or plan.device < 0:
+        return
+    if bounds.dtype != torch.uint8 or not bounds.is_contiguous() or bounds.numel() < need:
+        raise ValueError(f"bounds must be contiguous uint8 of {need} bytes for blocks of {block_size}, "
+                         f"not {bounds.dtype} {tuple(bounds.shape)}")
+
+
 def attn_update_bounds(plan: Plan, block_size: int, k_cache, bounds, page_table, seq_lens, kv_indptr,
                        rows: int, stream=None) -> None:
     """Bounds of the blocks that the last kv_indptr[b + 1] - kv_indptr[b] positions of every
     request b complete; rows = kv_indptr[batch]."""
+    _bounds_array(plan, block_size, bounds)
     st = (_LIB or load()).attn_update_bounds(
         plan.handle, int(block_size), _ptr(k_cache), _ptr(bounds), _ptr(page_table), _ptr(seq_lens),
         _ptr(kv_indptr), int(rows), _stream(stream, plan))
@@ -461,8 +479,12 @@ def attn_read_bounds(plan: Plan, block_size: int, bounds, page_table, seq_lens, 
     """The bounds as bf16: the last block_indptr[b + 1] - block_indptr[b] complete blocks of
     every request b, into out [rows, Hkv, 2, Dqk] (upper, lower)."""
     import torch
-    if out is not None:
-        _contiguous("out", out, torch.bfloat16)
+    if out is None:
+        raise ValueError("out is missing")
+    _contiguous("out", out, torch.bfloat16)
+    if out.numel() != out.shape[0] * plan.kv_heads * 2 * plan.head_dim_qk:
+        raise ValueError(f"out must be [rows, {plan.kv_heads}, 2, {plan.head_dim_qk}], not {tuple(out.shape)}")
+    _bounds_array(plan, block_size, bounds)
     st = (_LIB or load()).attn_read_bounds(
         plan.handle, int(block_size), _ptr(bounds), _ptr(page_table), _ptr(seq_lens), _ptr(block_indptr),
         out.shape[0], _ptr(out), _stream(stream, plan))
@@ -482,6 +504,7 @@ def attn_select_blocks(plan: Plan, sparse: attn_sparse_t, q, bounds, page_table,
                        block_idx, stream=None) -> None:
     """Every new token's blocks into block_idx, int32 [total_q, Hkv, num_blocks]."""
     _block_lists(plan, sparse, block_idx)
+    _bounds_array(plan, sparse.block_size, bounds)
     st = (_LIB or load()).attn_select_blocks(
         plan.handle, sparse, _ptr(q), _ptr(bounds), _ptr(page_table), _ptr(seq_lens), _ptr(qo_indptr),
         _ptr(block_idx), _stream(stream, plan))
