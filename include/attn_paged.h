@@ -455,12 +455,14 @@ attn_status_t attn_update_bounds(attn_plan_t plan, int32_t block_size, const voi
                                  int64_t rows, void *stream);
 
 /*
- * Bounds read back as bf16 (exactly: 7 bits and an exponent).
+ * Bounds read back as bf16 (exactly: 7 bits and an exponent, short of overflow: in a block
+ * with max |k| above 127 * 2^121 a code of +-64 stands for +-2^128, past the largest bf16,
+ * and reads back as the infinity, which bounds the key as well).
  *   block_indptr device int32 [B+1]: output rows [block_indptr[b], block_indptr[b+1]) are
  *                the last so many complete blocks of request b, in order.
  *   rows         block_indptr[B]; rows past it are written as zeros (bit 2).
- *   out          bf16 [rows][Hkv][2][Dqk]: upper, then lower bounds; +inf and -inf for a
- *                block that holds an infinity or a NaN.
+ *   out          bf16 [rows][Hkv][2][Dqk]: upper, then lower bounds; +inf and -inf in all
+ *                dims for a block that holds an infinity or a NaN.
  * Blocks before 0 or outside the page-table row are written as zeros (bit 2), as are
  * those of page ids outside the pool (bit 0).  Errors: as attn_update_bounds.
  */
