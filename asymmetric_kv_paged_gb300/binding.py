@@ -24,7 +24,7 @@ ATTN_KV_FP4_E2M1 = 2
 EXPORTED = ("attn_plan", "attn_run_paged", "attn_run_phase", "attn_plan_destroy", "attn_get_device_error",
             "attn_status_string", "attn_plan_host", "attn_plan_info", "attn_plan_blocks",
             "attn_plan_segments", "attn_plan_cta_heads", "attn_plan_stage_units",
-            "attn_plan_merge_ctas",
+            "attn_plan_merge_ctas", "attn_plan_select_ctas",
             "attn_debug_tc_gemm", "attn_debug_stamps",
             "attn_run_paged_no_workspace",
             "attn_append_kv", "attn_append_kv_rope", "attn_read_kv", "attn_kv_row_bytes",
@@ -111,6 +111,7 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     L.attn_update_bounds.argtypes = [vp, ctypes.c_int32] + [vp] * 5 + [ctypes.c_int64, vp]
     L.attn_read_bounds.argtypes = [vp, ctypes.c_int32] + [vp] * 4 + [ctypes.c_int64, vp, vp]
     L.attn_select_blocks.argtypes = [vp, ctypes.POINTER(attn_sparse_t)] + [vp] * 7
+    L.attn_plan_select_ctas.argtypes = [vp, ctypes.POINTER(attn_sparse_t), i32p]
     L.attn_run_sparse.argtypes = [vp, ctypes.POINTER(attn_sparse_t)] + [vp] * 8 + [ctypes.c_float] * 3 + [vp] * 3
     L.attn_plan_destroy.argtypes = [vp]
     L.attn_get_device_error.argtypes = [vp, vp, i32p]
@@ -576,6 +577,15 @@ def attn_plan_merge_ctas(plan: Plan) -> int:
     n = ctypes.c_int32(0)
     _check(load().attn_plan_merge_ctas(ctypes.c_void_p(plan.handle), ctypes.byref(n)),
            "attn_plan_merge_ctas")
+    return n.value
+
+
+def attn_plan_select_ctas(plan: Plan, sparse: attn_sparse_t) -> int:
+    """CTAs of a cluster of the kernel that selects blocks for chunks of tokens (0: the plan's
+    tokens are taken one by one)."""
+    n = ctypes.c_int32(0)
+    _check(load().attn_plan_select_ctas(ctypes.c_void_p(plan.handle), sparse, ctypes.byref(n)),
+           "attn_plan_select_ctas")
     return n.value
 
 

@@ -426,7 +426,47 @@ int32_t longest_request(const HostPlan &hp) {
   return (int32_t)std::min<int64_t>(top, slots);
 }
 
+// What a selection has of its plan, and whether its longest request may have so many blocks.
+static attn_status_t plan_args(const HostPlan &hp, const attn_sparse_t *sparse, SelectArgs *a) {
+  const attn_status_t ok = check_sparse(hp, sparse);
+  if (ok != ATTN_OK) return ok;
+  const attn_problem_t &pr = hp.prob;
+  a->max_len = longest_request(hp);
+  a->max_blocks = (a->max_len + sparse->block_size - 1) / sparse->block_size;
+  if (a->max_blocks > ATTN_SPARSE_MAX_BLOCKS) return ATTN_ERR_UNSUPPORTED;
+  a->batch = pr.batch;
+  a->hq = pr.num_q_heads;
+  a->hkv = pr.num_kv_heads;
+  a->group = hp.group;
+  a->row_tiles = (hp.group + 15) / 16;
+  a->page_size = pr.page_size;
+  a->pt_stride = pr.page_table_stride;
+  a->num_pages = pr.num_pages;
+  a->block = sparse->block_size;
+  a->take = sparse->num_blocks;
+  a->first = sparse->first_blocks;
+  a->last = sparse->last_blocks;
+  a->tokens = hp.qo_indptr.back();
+  return ATTN_OK;
+}
+
+static bool fits_smem(const HostPlan &hp, const SelectArgs &a) {
+  return (hp.prob.head_dim_qk == kDqk ? smem_of<kDqk>(a.row_tiles, a.max_blocks)
+                                      : smem_of<kDqkSym>(a.row_tiles, a.max_blocks)) <= kMaxSmem;
+}
+
 }  // namespace akp
+
+extern "C" attn_status_t attn_plan_select_ctas(attn_plan_t plan, const attn_sparse_t *sparse, int32_t *ctas) {
+  if (!plan || !ctas) return ATTN_ERR_INVALID_ARG;
+  *ctas = 0;
+  akp::SelectArgs a{};
+  const attn_status_t ok = akp::plan_args(plan->host, sparse, &a);
+  if (ok != ATTN_OK || a.tokens == 0) return ok;
+  if (!akp::fits_smem(plan->host, a)) return ATTN_ERR_UNSUPPORTED;
+  *ctas = akp::select_tc_ranks(plan->host, a);
+  return ATTN_OK;
+}
 
 extern "C" attn_status_t attn_select_blocks(attn_plan_t plan, const attn_sparse_t *sparse, const void *q,
                                             const void *bounds, const int32_t *page_table, const int32_t *seq_lens,
@@ -434,14 +474,9 @@ extern "C" attn_status_t attn_select_blocks(attn_plan_t plan, const attn_sparse_
   if (!plan || plan->device < 0) return ATTN_ERR_INVALID_ARG;
   const akp::HostPlan &hp = plan->host;
   const attn_problem_t &pr = hp.prob;
-  const attn_status_t ok = akp::check_sparse(hp, sparse);
-  if (ok != ATTN_OK) return ok;
   akp::SelectArgs a{};
-  a.max_len = akp::longest_request(hp);
-  a.max_blocks = (a.max_len + sparse->block_size - 1) / sparse->block_size;
-  if (a.max_blocks > ATTN_SPARSE_MAX_BLOCKS) return ATTN_ERR_UNSUPPORTED;
-  const int64_t tokens = hp.qo_indptr.back();
-  if (tokens == 0) return ATTN_OK;
+  const attn_status_t ok = akp::plan_args(hp, sparse, &a);
+  if (ok != ATTN_OK || a.tokens == 0) return ok;
   if (!q || !bounds || !page_table || !seq_lens || !qo_indptr || !block_idx || !akp::aligned16(q) ||
       !akp::aligned16(bounds))
     return ATTN_ERR_INVALID_ARG;
@@ -452,28 +487,13 @@ extern "C" attn_status_t attn_select_blocks(attn_plan_t plan, const attn_sparse_
   a.qo_indptr = qo_indptr;
   a.block_idx = block_idx;
   a.err = plan->dev.err;
-  a.batch = pr.batch;
-  a.hq = pr.num_q_heads;
-  a.hkv = pr.num_kv_heads;
-  a.group = hp.group;
-  a.row_tiles = (hp.group + 15) / 16;
-  a.page_size = pr.page_size;
-  a.pt_stride = pr.page_table_stride;
-  a.num_pages = pr.num_pages;
-  a.block = sparse->block_size;
-  a.take = sparse->num_blocks;
-  a.first = sparse->first_blocks;
-  a.last = sparse->last_blocks;
-  const size_t smem = pr.head_dim_qk == akp::kDqk ? akp::smem_of<akp::kDqk>(a.row_tiles, a.max_blocks)
-                                                  : akp::smem_of<akp::kDqkSym>(a.row_tiles, a.max_blocks);
-  if (smem > akp::kMaxSmem) return ATTN_ERR_UNSUPPORTED;
+  if (!akp::fits_smem(hp, a)) return ATTN_ERR_UNSUPPORTED;
   akp::DeviceGuard dev(plan->device);
   if (!dev.ok) return ATTN_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  a.tokens = (int32_t)tokens;
-  if (akp::select_tc_fits(hp, a))
+  if (akp::select_tc_ranks(hp, a))
     return akp::launch_select_tc(hp, a, plan->device, st) == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
-  const cudaError_t e = pr.head_dim_qk == akp::kDqk ? akp::launch<akp::kDqk>(a, tokens, hp.num_sms, plan->device, st)
-                                                    : akp::launch<akp::kDqkSym>(a, tokens, hp.num_sms, plan->device, st);
+  const cudaError_t e = pr.head_dim_qk == akp::kDqk ? akp::launch<akp::kDqk>(a, a.tokens, hp.num_sms, plan->device, st)
+                                                    : akp::launch<akp::kDqkSym>(a, a.tokens, hp.num_sms, plan->device, st);
   return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA;
 }

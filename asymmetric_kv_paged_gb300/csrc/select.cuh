@@ -98,8 +98,8 @@ __device__ __forceinline__ void pick_held(const uint32_t *keys, int n, int want,
   }
 }
 
-// select_tc.cu: chunks of tokens.  False: the batch is not one for it.
-bool select_tc_fits(const HostPlan &hp, const SelectArgs &a);
+// select_tc.cu: chunks of tokens.  CTAs of a cluster there; 0: the batch is not one for it.
+int select_tc_ranks(const HostPlan &hp, const SelectArgs &a);
 cudaError_t launch_select_tc(const HostPlan &hp, const SelectArgs &a, int device, cudaStream_t st);
 
 }  // namespace akp

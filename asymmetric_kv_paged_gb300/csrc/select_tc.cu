@@ -764,10 +764,10 @@ cudaError_t launch(const TcArgs &t, int ranks, int num_sms, int device, cudaStre
 
 }  // namespace
 
-bool select_tc_fits(const HostPlan &hp, const SelectArgs &a) {
+int select_tc_ranks(const HostPlan &hp, const SelectArgs &a) {
   TcArgs t{};
   int ranks;
-  return shape(hp, a, &t, &ranks);
+  return shape(hp, a, &t, &ranks) ? ranks : 0;
 }
 
 cudaError_t launch_select_tc(const HostPlan &hp, const SelectArgs &a, int device, cudaStream_t st) {

@@ -653,6 +653,13 @@ attn_status_t attn_plan_stage_units(attn_plan_t plan, int32_t *count, int32_t *u
  * only known on the device).  Errors: INVALID_ARG.
  */
 attn_status_t attn_plan_merge_ctas(attn_plan_t plan, int32_t *ctas);
+/*
+ * attn_plan_select_ctas reports in *ctas which kernel attn_select_blocks launches: for
+ * chunks of tokens, whose clusters share a request's blocks out over *ctas CTAs (1 to 8),
+ * or (0) the one that takes every token by itself.  Errors: INVALID_ARG and UNSUPPORTED as
+ * attn_select_blocks.
+ */
+attn_status_t attn_plan_select_ctas(attn_plan_t plan, const attn_sparse_t *sparse, int32_t *ctas);
 attn_status_t attn_plan_replayable_host(const attn_problem_t *bounds, int32_t num_sms,
                                         attn_plan_t *plan);
 attn_status_t attn_plan_replan_host(attn_plan_t plan, const int32_t *seq_lens_host,
