@@ -410,6 +410,8 @@ def make_mrope(cos_sin, rot_dim: int, pair_axis, positions=None, position_delta=
 def mrope_axes(sections, in_turn: bool = False) -> list:
     """pair_axis for sections[a] pairs of each axis a: one section after the other, or the
     axes in turn until each has had its pairs."""
+    if any(n < 0 for n in sections):
+        raise ValueError(f"sections must not be negative: {list(sections)}")
     if not in_turn:
         return [a for a, n in enumerate(sections) for _ in range(n)]
     left, out = list(sections), []
