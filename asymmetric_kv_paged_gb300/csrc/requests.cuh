@@ -55,14 +55,4 @@ struct Request {
   }
 };
 
-// request_of for threads that ask for rows of their own: a bisection each.
-__device__ __forceinline__ int request_of_row(const int32_t *indptr, int batch, int64_t t) {
-  int lo = 0, hi = batch;               // the answer is in [lo, hi]
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(indptr + mid + 1) <= t) lo = mid + 1; else hi = mid;
-  }
-  return lo;
-}
-
 }  // namespace akp
