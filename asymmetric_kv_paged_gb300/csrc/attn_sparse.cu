@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 1) sparse_kernel(const SparseArgs a,
   }
   __syncthreads();
   // after the lists: the loader's start waits for those, and their loads do not queue behind these
-  // (16 requests, 64 heads, 32 blocks of 64: 12.8 -> 12.3 us)
+  // (32 requests, 16/2 heads, 16 blocks of 64: 12.8 -> 12.3 us)
   if (rows > 0) u.load(a.q + ((int64_t)tok * a.hq + g * a.group + row0) * DQK, rows, a.scale_log2, lane);
 
   if (warp == kWarps) {
@@ -855,10 +855,19 @@ cudaError_t launch_kv(const HostPlan &hp, const SparseArgs &a, const TmaMaps &ma
   // for (up to eight, with two tiles for each).  With more, tiles of neighbouring tokens
   // (attn_sparse_tc.cu) where they hold 1.5 units a job or more, however empty their 128
   // rows: a job takes about as long as a unit, whose blocks it shares.  Measured at 4,000 to
-  // 8,000 tokens, 16 blocks of 64, 64/4 heads, bf16 (E4M3), us, a unit a CTA against tiles:
-  //   1,024 units of 1 token a request   163 (132)   160 (173)
-  //   1,024 units of 2 / 4 / 8           136 / 124 / 121   106 / 66 / 44
-  //   192 units of 2 / 8                 35 / 34 (35 / 35)   26 / 30 (32 / 39)
+  // 8,000 tokens, 16 blocks of 64, 64/4 heads, us, a unit a CTA against tiles:
+  //                                      bf16        E4M3        4-bit
+  //   1,024 units of 1 token a request   163 / 161   133 / 172   143 / 170
+  //   1,024 units of 2                   138 / 107   129 / 115   139 / 114
+  //   1,024 units of 4                   126 / 67    128 / 71    138 / 71
+  //   1,024 units of 8                   122 / 44    126 / 47    137 / 47
+  //   192 units of 2                     35 / 27     35 / 32     38 / 32
+  //   192 units of 8                     35 / 31     35 / 39     38 / 39
+  // (24 jobs of eight tokens leave most SMs idle: there the rule costs E4M3 4 us.)  The more
+  // neighbours' lists differ, the longer a job's union: 4,096 tokens in a row take 485 (E4M3
+  // 624, 4-bit 632) us with lists alike for 16 tokens, 43 blocks a job of eight tokens, and
+  // 886 (1,166, 1,187) with independent ones, 97 blocks; a unit a CTA 1,870 (1,941, 2,101)
+  // whatever the lists.
   // A group of more than 128 heads fits no tile: its row tiles have one list, and eight
   // units of a CTA share the blocks (256 heads, 64 tokens: 45 us, a unit a CTA 120; from about
   // two units an SM on).

@@ -17,15 +17,17 @@
 // attn_prefill.cu, took 531 us on the case below: 96 KB of Q leave no room for the tiles
 // that only one of the two needs.)
 //
-// 4096 tokens behind 26,000 (64/4 heads, 16 blocks of 64, bf16) take 488 us, with every unit
-// by itself (attn_sparse.cu) 822; dense attention of the same chunk takes about 3 ms.  The
-// 172 GFLOP of the listed keys would be 89 us at the tensor cores' rate.  A chain needs 4.4
-// thousand cycles a tile, half a tile's time as there are two: 12 + 8 MMAs of 66 cycles, 1.9
+// 4096 tokens behind 26,000 (64/4 heads, 16 blocks of 64, bf16) take 485 us, with every unit
+// by itself (attn_sparse.cu) 1,870, with eight neighbouring units of register operands a CTA
+// 822; dense attention of the same chunk takes about 3 ms.  That is with lists that stay alike
+// for 16 tokens, from a job's first token on (43 blocks a job); shifted by 4 tokens (52 blocks)
+// it takes 546, with lists independent from token to token (97) 886.  The 172 GFLOP of the
+// listed keys would be 89 us at the tensor cores' rate.  A chain needs 4.4 thousand cycles a tile, half a tile's time as there are two: 12 + 8 MMAs of 66 cycles, 1.9
 // thousand cycles of softmax and the hand-offs between them; 10 of a CTA's 65 thousand cycles
 // pass before its first tile and 5 behind its last.  Two threads a row for the softmax gave
 // 479 us (of 481 then), a persistent form 504, spinning waits 495: the hand-offs remain, and no room in
 // shared memory or TMEM for a third chain.  4-bit caches (3 x 777 tokens, 12 blocks of 128):
-// 439 us, unit by unit 1403; there the widening of a tile by four warps is the chain's longest part.
+// 435 us, unit by unit 2,810; there the widening of a tile by four warps is the chain's longest part.
 //
 // Roles (512 threads; the tile pipeline is that of attn_prefill.cu):
 //   warps 0-3, 4-7  Q rows, then softmax and epilogue of chain 0 / 1 (row p in TMEM lane p)

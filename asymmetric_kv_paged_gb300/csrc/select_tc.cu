@@ -25,6 +25,11 @@
 //   17     the query rows of the next token tile, as bulk copies
 // TMEM: A 2 x Dqk columns, D 128.  Every wait is bounded in time.
 //
+// Up to 512 scored blocks a list is found in one warp's registers; beyond that by radix passes
+// of one warp over the scores, and with larger clusters, which have room for fewer tokens a CTA,
+// fewer of its four warps have a list to make.  4096 tokens (64/4 heads) over 500 blocks 150 us,
+// 514 422, 768 659, 1,024 763, 1,500 1,939, 2,047 3,194.
+//
 // 4096 tokens (64/4 heads) over 470 blocks take 150 us; with the tokens at rest and the
 // bounds widened for every token tile 316, a token a CTA (select.cu) 800.  Its 47 GFLOP
 // (94 with q^+ and q^- apart) are 49 us of the tensor cores, which are busy 28% of the time:
@@ -706,6 +711,10 @@ bool shape(const HostPlan &hp, const SelectArgs &a, TcArgs *t, int *ranks) {
   t->gp_log2 = 0;
   while ((1 << t->gp_log2) < t->gp) ++t->gp_log2;
   t->tile_tokens = kN / t->gp;
+  // Eight CTAs a cluster at most, 2,048 scored blocks of the plan's longest request.  At that
+  // limit both kernels take the same time (4,096 tokens, 64/4 heads: 2,047 blocks 3,194 us here,
+  // 2,050 3,311 token by token, then in proportion: 4,096 6,068, 8,192 11,494).  A replayable
+  // plan's bounds decide: 470 blocks under a bound of 2,047 take 1,061 us, of 8,192 1,171.
   *ranks = std::max(1, (a.max_blocks - a.first + kSpan - 1) / kSpan);
   if (*ranks > kMaxRanks) return false;
   constexpr int kChoices[4][2] = {{2, 2}, {1, 2}, {2, 1}, {1, 1}};

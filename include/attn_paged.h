@@ -498,6 +498,11 @@ attn_status_t attn_read_bounds(attn_plan_t plan, int32_t block_size, const void 
  * size, more than ATTN_SPARSE_MAX_BLOCKS blocks in the plan's longest request, or more
  * than 224 KB for 4 bytes a block of it and 6.2 KB (head_dim 128: 4.2) for each 16 heads
  * of a group), CUDA.
+ * Chunks of tokens share the reading and scoring of their request's blocks while the plan's
+ * longest request (a replayable plan's longest bound) has at most 2,048 blocks behind the
+ * first ones and a group at most 128 heads; past either, and for single tokens, every token
+ * is taken by itself.  4,096 tokens, 64/4 heads: 0.15 ms over 500 blocks, 3.2 over 2,047,
+ * 11.5 over 8,192.
  */
 attn_status_t attn_select_blocks(attn_plan_t plan, const attn_sparse_t *sparse, const void *q,
                                  const void *bounds, const int32_t *page_table,
@@ -517,6 +522,9 @@ attn_status_t attn_select_blocks(attn_plan_t plan, const attn_sparse_t *sparse, 
  *                cache type; any page_size that is a multiple of block_size; the plan's
  *                window must be 0).
  * A token whose list holds no block gets zeros and -inf (with sinks: the sink's own lse).
+ * Neighbouring tokens of a chunk are taken together over the union of their lists, so that
+ * its time grows with what they do not share (4,096 tokens, 16 blocks of 64: 0.49 ms with
+ * lists alike for 16 tokens, 0.89 with lists independent from token to token).
  * Slots that a token does not see, invisible ones of a shared tile among them, do not
  * reach its rows whatever they hold (in a chunk of tokens, rows beside a NaN or an
  * infinity are summed anew, in another order).  Arithmetic is that of the other kernels: bf16
